@@ -14,7 +14,7 @@ own = False
 DEV = "cuda"
 TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
 LR, BETA1, BETA2, EPS, DECAY = 3e-4, 0.9, 0.95, 1e-8, 0.1
-STEP, SEED, MAX_NORM = 1000, 1234567, 1.0
+STEP, SEED = 1000, 1234567
 BLOCK = 128   # elements that share a scale of an 8-bit state
 
 
@@ -67,7 +67,7 @@ def draw(rng):
         param = rng.choice(("fp32", "bf16", "fp16", "mixed"))
         grad = rng.choice(("same", "fp32"))
         master = param in ("bf16", "fp16") and rng.random() < 0.4
-        c = dict(op="adamw", param=param, grad=grad, master=master, state=state, clip=rng.random() < 0.5)
+        c = dict(op="adamw", param=param, grad=grad, master=master, state=state, clip=state == 8 or rng.random() < 0.5)
         kind = rng.choice(("one", "gpt", "layer", "small"))
         if kind == "one":
             c.update(list="one", n=_log(rng, 1000, 1 << 27))
@@ -163,14 +163,18 @@ def _prepare_adamw(case, seed):
             c["m"] = _normal(n, 3e-4, torch.float32, gen)
             c["v"] = _normal(n, 1.0, torch.float32, gen).exp_().mul_(3e-7)
         else:
+            # the blocks' largest values lie between the powers of two, where a last-bit
+            # difference does not choose another scale
             nb = sum(-(-s // BLOCK) for s in sizes)
-            c["m"] = _normal(n, 60.0, torch.float32, gen).clamp_(-250, 250).to(torch.float8_e4m3fn)
-            c["v"] = _normal(n, 0.6, torch.float32, gen).exp_().mul_(40).clamp_(0.05, 250).to(torch.float8_e4m3fn)
+            c["m"] = _normal(n, 90.0, torch.float32, gen).clamp_(-240, 240).to(torch.float8_e4m3fn)
+            c["v"] = _normal(n, 0.6, torch.float32, gen).exp_().mul_(50).clamp_(0.05, 240).to(torch.float8_e4m3fn)
             c["m_scale"] = torch.randint(107, 111, (nb,), dtype=torch.uint8, device=DEV, generator=gen)
             c["v_scale"] = torch.randint(109, 112, (nb,), dtype=torch.uint8, device=DEV, generator=gen)
         classes.append(c)
     s = {"op": "adamw", "state": case["state"], "classes": classes, "sq_total": total.reshape(1),
-         "max_norm": MAX_NORM if case["clip"] else 0.0,
+         # a clip that is at work: every gradient is scaled by about 1/e, so that sums of
+         # 8-bit states and 16-bit gradients do not fall exactly on powers of two
+         "max_norm": math.sqrt(float(total)) / math.e if case["clip"] else 0.0,
          "groups": torch.tensor([[LR, BETA1, BETA2, EPS, DECAY], [LR, BETA1, BETA2, EPS, 0.0]],
                                 dtype=torch.float64, device=DEV)}
     if own:
@@ -426,7 +430,7 @@ def _exact_adamw(case, seed):
     s = _prepare_adamw(case, seed)
     clip = 1.0
     if case["clip"]:
-        clip = min(1.0, MAX_NORM / (math.sqrt(float(s["sq_total"])) + 1e-6))
+        clip = min(1.0, s["max_norm"] / (math.sqrt(float(s["sq_total"])) + 1e-6))
     t, out, first = STEP + 1, [], 0
     for c in s["classes"]:
         sizes, n = c["sizes"], c["param"].numel()
