@@ -412,6 +412,114 @@ int32_t sdc_confirm_verdict(const uint64_t* d_witness, const uint64_t* d_retry,
                             void* d_ws, uint64_t ws_bytes, int32_t* h_verdict,
                             sdc_stream_t stream);
 
+/* ---- the optimizer step --------------------------------------------------
+ * [BLOG] runs Check 1 before the optimizer step (a step whose gradients hold
+ * NaN/Inf is not taken) and Check 3 after it (the weights' fingerprints).
+ * sdc_adamw_step is the step between them: it takes sdc_sqnorm's results on
+ * the device as its gate and its clip, so neither needs the host, and it can
+ * write the new weights' rows in the pass that computes them. */
+
+/* One tensor of the step; all pointers to device memory, contiguous, element
+ * i of each belonging to element i of the others, none overlapping another.
+ *   param       numel weights of param_dtype (SDC_F32, SDC_BF16 or SDC_F16).
+ *   grad        gradients of grad_dtype (one of the same three, need not be
+ *               param_dtype); NULL: the tensor and its states are left alone.
+ *   exp_avg, exp_avg_sq
+ *               the moving averages m and v.  state_dtype SDC_F32: fp32 values.
+ *               SDC_FP8_E4M3: e4m3 codes, m = code * 2^(s-127) and
+ *               sqrt(v) = code * 2^(s-127) with s the scale byte of the
+ *               element's block of 128 (blocks count from the tensor's start).
+ *               All-zero codes and scale bytes are the state before any step.
+ *   master      fp32 weights behind a 16-bit param: the step is computed on
+ *               them and param receives them rounded (param is only written);
+ *               NULL: param itself is updated.  Must be NULL for SDC_F32.
+ *   exp_avg_scale, exp_avg_sq_scale
+ *               ceil(numel / 128) scale bytes each for SDC_FP8_E4M3 states, else NULL.
+ *   group       index of its parameter group. */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* master;
+  uint8_t* exp_avg_scale;
+  uint8_t* exp_avg_sq_scale;
+  uint64_t numel;
+  uint32_t param_dtype;
+  uint32_t grad_dtype;
+  uint32_t state_dtype;
+  uint32_t group;
+} sdc_adamw_tensor;
+
+/* Hyperparameters of a parameter group, in device memory: the caller may
+ * change them between steps (a learning-rate schedule), also between replays
+ * of a captured step.  0 <= beta < 1, eps > 0. */
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+} sdc_adamw_group;
+
+/* The step's control block, in device memory, owned by the caller:
+ *   step        steps taken so far (bias correction uses step + 1)
+ *   skipped     steps not taken
+ *   seed        of the random bits that round 8-bit states
+ *   grad_scale  (written) the factor the last call multiplied gradients by
+ *   skip        (written) 1 when the last call did not take the step
+ * A step with 8-bit states depends on nothing but its inputs, this block and
+ * the elements' places in the list: a replay gives the same bits. */
+typedef struct {
+  uint64_t step, skipped, seed;
+  float grad_scale;
+  uint32_t skip;
+} sdc_adamw_control;
+
+/* Host summary of a step's plan, filled by sdc_adamw_plan_build. */
+typedef struct {
+  uint64_t magic, n_tensors, n_groups, n_items, n_split, n_slots, total_elems, plan_bytes;
+  uint64_t n_block[12], n_wave[12]; /* work items by kernel class */
+} sdc_adamw_info;
+
+/* Device bytes of the plan of h_tensors[0..n) with n_groups groups (1..65536).
+ * Host only.  Errors as sdc_adamw_plan_build's argument checks. */
+int32_t sdc_adamw_plan_bytes(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
+                             uint64_t* h_bytes);
+
+/* Packs the list into d_plan (plan_bytes bytes of device memory, 16-byte
+ * aligned, owned by the caller).  The plan keeps the pointers and holds the
+ * step's scratch: steps of one plan must not overlap in time.  SYNCHRONOUS.
+ * Errors: SDC_ERR_INVALID (NULL, a group out of range, a master of an fp32
+ * param, scale bytes that do not go with the state type), SDC_ERR_DTYPE,
+ * SDC_ERR_ALIGN (a pointer not aligned to its element), SDC_ERR_RANGE (2^31
+ * tensors, 2^48 elements), SDC_ERR_WORKSPACE, SDC_ERR_HIP. */
+int32_t sdc_adamw_plan_build(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
+                             void* d_plan, uint64_t plan_bytes, sdc_adamw_info* h_info,
+                             sdc_stream_t stream);
+
+/* One AdamW step over the list (decoupled weight decay), in fp32:
+ *   norm = sqrt(*d_sq_total) * grad_scale
+ *   g = grad * grad_scale * (max_norm > 0 ? min(1, max_norm / (norm + 1e-6)) : 1)
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps),  t = step + 1
+ * 16-bit weights are rounded to nearest, ties to even; 8-bit states are drawn
+ * from their two neighbours (expected m, and expected v, kept).
+ *   d_sq_total  sdc_sqnorm's total over the gradients; NULL: none (then
+ *               max_norm must be 0).
+ *   d_flag      sdc_sqnorm's flag; NULL: none.
+ *   max_norm    0: no clip.      grad_scale  finite, above 0 (1: none).
+ *   d_rows      n_tensors rows (16-byte aligned), or NULL: the new weights'
+ *               fingerprint rows, those of sdc_fingerprint_plan over the
+ *               params (zero-extended patterns).  They describe the values the
+ *               step computed: a later scan that differs shows that memory
+ *               changed after it.
+ * When *d_flag is not 0 or *d_sq_total rounded to fp32 is not finite, no
+ * weight and no state changes, `skipped` counts the call and `step` stays;
+ * rows are still written.  ASYNCHRONOUS on stream, capturable.
+ * Errors: SDC_ERR_INVALID, SDC_ERR_PLAN, SDC_ERR_ALIGN, SDC_ERR_HIP. */
+int32_t sdc_adamw_step(void* d_plan, const sdc_adamw_info* h_info, const sdc_adamw_group* d_groups,
+                       sdc_adamw_control* d_control, const double* d_sq_total,
+                       const uint32_t* d_flag, double max_norm, double grad_scale,
+                       sdc_row* d_rows, sdc_stream_t stream);
+
 /* ---- measurement ----------------------------------------------------------- */
 
 /* Streaming-read reference (no passage of the pages defines it: it measures

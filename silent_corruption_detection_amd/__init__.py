@@ -7,6 +7,7 @@ raises ImportError when the library has not been built; there is no fallback.
 
 Function names are those of the C ABI.
 """
+import contextlib
 import ctypes
 import os
 import threading
@@ -25,6 +26,7 @@ __all__ = [
     "sdc_tensor_ws_bytes", "sdc_tensor_split_host", "sdc_fingerprint_tensor",
     "sdc_fingerprint_tensor_noalloc",
     "sdc_read_sum_ws_bytes", "sdc_read_sum",
+    "AdamwPlan", "sdc_adamw_plan_build", "sdc_adamw_control", "sdc_adamw_step",
 ]
 
 # The in-tree build; SDC_LIB_PATH may name another build of the same sources
@@ -76,6 +78,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
     P, U64, U32, I32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int32
+    F64 = ctypes.c_double
     sig = {
         "sdc_plan_bytes": [P, U64, U64, P],
         "sdc_plan_build": [P, U64, U64, P, U64, P, P],
@@ -99,6 +102,9 @@ def _load():
         "sdc_confirm_verdict": [P, P, P, P, U64, P, U64, P, P],
         "sdc_read_sum_ws_bytes": [U64, P],
         "sdc_read_sum": [P, U64, P, U64, P, P],
+        "sdc_adamw_plan_bytes": [P, U64, U32, P],
+        "sdc_adamw_plan_build": [P, U64, U32, P, U64, P, P],
+        "sdc_adamw_step": [P, P, P, P, P, P, F64, F64, P, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -211,6 +217,14 @@ def _scan_stream(stream, device, made):
         for t in made:
             t.record_stream(stream)
     return stream.cuda_stream
+
+
+def _device_guard(device):
+    """Context in which `device` is the current device (launches and pointers
+    belong to the current one); free when it already is."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _on_device(t, device):
@@ -680,3 +694,164 @@ def sdc_sqnorm(plan, sq=None, total=None, flag=None, stream=None):
                            ctypes.c_void_p(flag.data_ptr()), _stream_handle(stream, dev)),
            "sdc_sqnorm")
     return sq[:plan.n_tensors], total, flag
+
+
+# ---- the optimizer step ----------------------------------------------------------
+class _AdamwInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in
+                ("magic", "n_tensors", "n_groups", "n_items", "n_split", "n_slots", "total_elems",
+                 "plan_bytes")] + [("n_block", ctypes.c_uint64 * 12), ("n_wave", ctypes.c_uint64 * 12)]
+
+
+# sdc_adamw_tensor as a numpy record
+_ADAMW_DESC = np.dtype([(n, "<u8") for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master",
+                                             "exp_avg_scale", "exp_avg_sq_scale", "numel")]
+                       + [(n, "<u4") for n in ("param_dtype", "grad_dtype", "state_dtype", "group")])
+_ADAMW_STATE = {torch.float32: F32, torch.float8_e4m3fn: FP8_E4M3}
+_STATE_BLOCK = 128
+
+
+class AdamwPlan:
+    """A built AdamW plan: the device buffer, the host summary and the tensors
+    the step reads and writes."""
+
+    def __init__(self, buf, info, tensors, device):
+        self.buf, self.info, self.tensors, self.device = buf, info, tensors, device
+
+    @property
+    def n_tensors(self):
+        return self.info.n_tensors
+
+    @property
+    def n_groups(self):
+        return self.info.n_groups
+
+    @property
+    def total_elems(self):
+        return self.info.total_elems
+
+
+def _adamw_column(table, col, tensors, n, name, check):
+    """Fills pointer column `col` from a list of n tensors (None allowed)."""
+    if tensors is None:
+        return []
+    if len(tensors) != n:
+        raise ValueError(f"{name} has {len(tensors)} entries for {n} params")
+    for k, t in enumerate(tensors):
+        if t is None:
+            continue
+        check(k, t)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{k}] is not contiguous (a plan reads and writes it in place)")
+        table[col][k] = t.data_ptr() if t.numel() else 0
+    return [t for t in tensors if t is not None]
+
+
+def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None,
+                         exp_avg_sq_scale=None, group=None, n_groups=1, stream=None):
+    """Plan of an AdamW step over a tensor list (synchronous; see
+    sdc_adamw_plan_build in include/sdc.h).
+
+    params, grads, exp_avg, exp_avg_sq: lists of device tensors of one numel
+    each; a grad of None leaves its tensor alone.  States are fp32, or
+    torch.float8_e4m3fn with the uint8 scale bytes of each block of 128
+    elements in exp_avg_scale / exp_avg_sq_scale (ceil(numel / 128) entries;
+    None where the state is fp32).  master: fp32 weights behind 16-bit params
+    (None: the param itself is updated).  group: parameter group of each
+    tensor.  The plan keeps the tensors' addresses: gradients have to stay
+    where they are (zero them in place)."""
+    n = len(params)
+    if not n:
+        raise ValueError("the list is empty")
+    table = np.zeros(n, dtype=_ADAMW_DESC)
+    dev = None
+    for k, p in enumerate(params):
+        if p.get_device() < 0:
+            raise ValueError(f"params[{k}] is not on a GPU")
+        if dev is None:
+            dev = _cuda_device(p.get_device())
+        if _TORCH_DTYPE.get(p.dtype) not in (F32, BF16, F16):
+            raise TypeError(f"params[{k}]: unsupported dtype {p.dtype}")
+        if exp_avg[k].dtype not in _ADAMW_STATE if k < len(exp_avg) and exp_avg[k] is not None else True:
+            raise TypeError(f"exp_avg[{k}] must be float32 or float8_e4m3fn")
+        table["numel"][k] = p.numel()
+        table["param_dtype"][k] = _TORCH_DTYPE[p.dtype]
+        table["grad_dtype"][k] = _TORCH_DTYPE[p.dtype]
+        table["state_dtype"][k] = _ADAMW_STATE[exp_avg[k].dtype]
+
+    def same(name, dtypes, numel=lambda k: params[k].numel()):
+        def check(k, t):
+            if not _on_device(t, dev):
+                raise ValueError(f"{name}[{k}] must be on {dev}, not {t.device}")
+            if t.dtype not in dtypes(k):
+                raise TypeError(f"{name}[{k}]: unsupported dtype {t.dtype}")
+            if t.numel() != numel(k):
+                raise ValueError(f"{name}[{k}] has {t.numel()} elements, needs {numel(k)}")
+        return check
+
+    floats = (torch.float32, torch.bfloat16, torch.float16)
+    blocks = same("a scale", lambda k: (torch.uint8,), lambda k: -(-params[k].numel() // _STATE_BLOCK))
+    keep = _adamw_column(table, "param", params, n, "params", same("params", lambda k: floats))
+    keep += _adamw_column(table, "grad", grads, n, "grads", same("grads", lambda k: floats))
+    keep += _adamw_column(table, "exp_avg", exp_avg, n, "exp_avg", same("exp_avg", lambda k: (exp_avg[k].dtype,)))
+    keep += _adamw_column(table, "exp_avg_sq", exp_avg_sq, n, "exp_avg_sq",
+                          same("exp_avg_sq", lambda k: (exp_avg[k].dtype,)))
+    keep += _adamw_column(table, "master", master, n, "master", same("master", lambda k: (torch.float32,)))
+    keep += _adamw_column(table, "exp_avg_scale", exp_avg_scale, n, "exp_avg_scale", blocks)
+    keep += _adamw_column(table, "exp_avg_sq_scale", exp_avg_sq_scale, n, "exp_avg_sq_scale", blocks)
+    for k, g in enumerate(grads):
+        if g is not None:
+            table["grad_dtype"][k] = _TORCH_DTYPE[g.dtype]
+    if group is not None:
+        if len(group) != n or min(group) < 0:
+            raise ValueError(f"group needs {n} indices, none negative")
+        table["group"] = group
+    h = ctypes.c_void_p(table.ctypes.data)
+    nbytes = ctypes.c_uint64(0)
+    _check(_lib.sdc_adamw_plan_bytes(h, n, n_groups, ctypes.byref(nbytes)), "sdc_adamw_plan_bytes")
+    buf = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    info = _AdamwInfo()
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, [buf])
+        _check(_lib.sdc_adamw_plan_build(h, n, n_groups, buf.data_ptr(), buf.numel(), ctypes.byref(info), s),
+               "sdc_adamw_plan_build")
+    return AdamwPlan(buf, info, keep, dev)
+
+
+def sdc_adamw_control(device="cuda", step=0, seed=0):
+    """A step's control block: int64 [4] device tensor (steps taken, steps
+    skipped, seed, and the last call's gradient factor and skip word)."""
+    if step < 0 or not 0 <= seed < 1 << 63:
+        raise ValueError("step and seed must not be negative (seed below 2^63)")
+    return torch.tensor([step, 0, seed, 0], dtype=torch.int64, device=device)
+
+
+def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0, grad_scale=1.0,
+                   rows=None, stream=None):
+    """One AdamW step over the plan's list, in place (asynchronous; see
+    sdc_adamw_step in include/sdc.h).
+
+    groups: float64 [n_groups, 5] device tensor of (lr, beta1, beta2, eps,
+    weight_decay), which may change between steps.  control: the block of
+    sdc_adamw_control.  sq_total, flag: sdc_sqnorm's results over the
+    gradients; a set flag or a total that is not finite in fp32 leaves weights
+    and states alone.  max_norm: clips the gradients to that norm (needs
+    sq_total).  grad_scale: factor of the gradients (and of their norm).
+    rows: an int64 [n_tensors, 4] device tensor that receives the new weights'
+    fingerprint rows."""
+    dev = plan.device
+    _arg(groups, "groups", torch.float64, 5 * plan.info.n_groups, dev)
+    _arg(control, "control", torch.int64, 4, dev)
+    if sq_total is not None:
+        _arg(sq_total, "sq_total", torch.float64, 1, dev)
+    if flag is not None:
+        _arg(flag, "flag", torch.int32, 1, dev)
+    if rows is not None:
+        _arg(rows, "rows", torch.int64, 4 * plan.n_tensors, dev)
+    with _device_guard(dev):
+        _check(_lib.sdc_adamw_step(
+            plan.buf.data_ptr(), ctypes.byref(plan.info), groups.data_ptr(), control.data_ptr(),
+            None if sq_total is None else sq_total.data_ptr(), None if flag is None else flag.data_ptr(),
+            max_norm, grad_scale, None if rows is None else rows.data_ptr(), _stream_handle(stream, dev)),
+            "sdc_adamw_step")
+    return rows

@@ -1,0 +1,268 @@
+// adamw.hip -- the AdamW step over a tensor list for gfx950: the plan, the
+// gate that decides on the device whether and how the step is taken, and the
+// merge of the fingerprint rows.  The update kernels are in adamw_device.h.
+//
+// A step is one launch for the gate, one for each kernel class in the list
+// (usually one or two), and, where rows are asked for, one merge.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "adamw_device.h"
+
+namespace sdc {
+namespace {
+
+// The gate: skip, clip and bias corrections, one thread per parameter group,
+// so nothing of a step waits for the host.  In double: beta^t for t in the
+// thousands loses digits in fp32.
+__global__ void __launch_bounds__(64) adamw_gate_kernel(sdc_adamw_control* control,
+                                                        const sdc_adamw_group* __restrict__ groups,
+                                                        uint32_t n_groups,
+                                                        const double* __restrict__ sq_total,
+                                                        const uint32_t* __restrict__ flag,
+                                                        double max_norm, double grad_scale,
+                                                        AdamwGate* __restrict__ gate,
+                                                        AdamwCoef* __restrict__ coef) {
+  const uint64_t done = control->step, seed = control->seed;
+  const double total = sq_total ? *sq_total : 0.0;
+  const bool skip = (flag && *flag != 0) || !__builtin_isfinite((float)total);
+  const uint64_t t = done + (skip ? 0 : 1);
+  __syncthreads();  // every thread has read the control block
+  if (threadIdx.x == 0) {
+    double scale = grad_scale;
+    if (max_norm > 0.0) scale *= fmin(1.0, max_norm / (sqrt(total) * grad_scale + 1e-6));
+    if (skip) control->skipped += 1;
+    control->step = t;
+    control->grad_scale = (float)scale;
+    control->skip = skip;
+    constexpr uint32_t kSeed = 0x9E3779B1u, kStep = 0x85157AF5u;
+    *gate = AdamwGate{(float)scale, skip, (uint32_t)seed * kSeed + (uint32_t)t * kStep,
+                      (uint32_t)(seed >> 32) * kSeed + (uint32_t)(t >> 32) * kStep + 0x6C8E9CF5u};
+  }
+  for (uint32_t k = threadIdx.x; k < n_groups; k += 64) {
+    const sdc_adamw_group g = groups[k];
+    coef[k] = AdamwCoef{(float)g.beta1, (float)(1.0 - g.beta1), (float)g.beta2, (float)(1.0 - g.beta2),
+                        (float)(g.lr / (1.0 - pow(g.beta1, (double)t))),
+                        (float)(1.0 / sqrt(1.0 - pow(g.beta2, (double)t))), (float)g.eps,
+                        (float)(1.0 - g.lr * g.weight_decay)};
+  }
+}
+
+// Rows of the tensors of several items (or of none), one wave each.
+__global__ void __launch_bounds__(kBlock) adamw_merge_kernel(const PlanSplit* __restrict__ split,
+                                                             uint32_t n_split,
+                                                             const sdc_row* __restrict__ partials,
+                                                             sdc_row* __restrict__ rows) {
+  const uint32_t e = wave_item_index();
+  if (e >= n_split) return;
+  const PlanSplit sp = split[e];
+  const uint32_t l = threadIdx.x & 63u;
+  Lane ln = merge_slots(partials + sp.first, sp.count, l);
+  wave_reduce(ln);
+  if (l == 0) store_row(rows + sp.row, ln, ln.w);
+}
+
+struct Layout {
+  uint64_t n_items = 0, n_split = 0, n_slots = 0, total_elems = 0, chunk = 0;
+  uint64_t n_block[kAdamwClasses] = {}, n_wave[kAdamwClasses] = {};
+  AdamwOffsets off{};
+};
+
+bool float_dtype(uint32_t d) { return d == SDC_F32 || d == SDC_BF16 || d == SDC_F16; }
+
+bool aligned(const void* p, uint32_t es) { return reinterpret_cast<uintptr_t>(p) % es == 0; }
+
+int32_t check_tensor(const sdc_adamw_tensor& t, uint32_t n_groups) {
+  if (!float_dtype(t.param_dtype) || !float_dtype(t.grad_dtype)) return SDC_ERR_DTYPE;
+  if (t.state_dtype != SDC_F32 && t.state_dtype != SDC_FP8_E4M3) return SDC_ERR_DTYPE;
+  if (t.group >= n_groups) return SDC_ERR_INVALID;
+  if (t.numel >= 1ull << 48) return SDC_ERR_RANGE;
+  if (t.numel == 0) return SDC_OK;
+  const bool eight = t.state_dtype == SDC_FP8_E4M3;
+  if (!t.param || !t.exp_avg || !t.exp_avg_sq) return SDC_ERR_INVALID;
+  if (eight != (t.exp_avg_scale != nullptr) || eight != (t.exp_avg_sq_scale != nullptr))
+    return SDC_ERR_INVALID;
+  if (t.master && t.param_dtype == SDC_F32) return SDC_ERR_INVALID;
+  if (!aligned(t.param, element_size(t.param_dtype)) || !aligned(t.grad, element_size(t.grad_dtype)) ||
+      !aligned(t.master, 4) || !aligned(t.exp_avg, eight ? 1 : 4) || !aligned(t.exp_avg_sq, eight ? 1 : 4))
+    return SDC_ERR_ALIGN;
+  return SDC_OK;
+}
+
+uint32_t class_of(const sdc_adamw_tensor& t) {
+  const uint32_t p = t.param_dtype == SDC_F32 ? 0u : t.master ? 2u : 1u;
+  const uint32_t g = (t.grad_dtype == SDC_F32 || !t.grad) ? 0u : 1u;
+  return adamw_class(p, g, t.state_dtype == SDC_FP8_E4M3);
+}
+
+int32_t layout_adamw(const sdc_adamw_tensor* t, uint64_t n, uint32_t n_groups, Layout* L) {
+  if ((n > 0 && t == nullptr) || n_groups == 0 || n_groups > 65536) return SDC_ERR_INVALID;
+  if (n >= 1ull << 31) return SDC_ERR_RANGE;
+  constexpr int kCand = 6;  // 65536 .. 2048 elements
+  static_assert((kAdamwChunkMax >> (kCand - 1)) == kAdamwChunkMin, "candidate chunks");
+  uint64_t count[kCand] = {};
+  for (uint64_t k = 0; k < n; ++k) {
+    if (int32_t st = check_tensor(t[k], n_groups)) return st;
+    L->total_elems += t[k].numel;
+    if (L->total_elems >= 1ull << 48) return SDC_ERR_RANGE;
+    for (int c = 0; c < kCand; ++c) count[c] += (t[k].numel + (kAdamwChunkMax >> c) - 1) / (kAdamwChunkMax >> c);
+  }
+  L->chunk = kAdamwChunkMin;
+  for (int c = 0; c < kCand; ++c)
+    if (count[c] >= kAdamwMinItems) {
+      L->chunk = kAdamwChunkMax >> c;
+      break;
+    }
+  for (uint64_t k = 0; k < n; ++k) {
+    const uint64_t items = (t[k].numel + L->chunk - 1) / L->chunk;
+    L->n_items += items;
+    if (L->n_items > kMaxGrid) return SDC_ERR_RANGE;
+    if (items != 1) {
+      L->n_split += 1;
+      L->n_slots += items;
+    }
+    if (items == 0) continue;
+    const uint32_t c = class_of(t[k]);
+    if (t[k].numel <= kAdamwWaveElems) L->n_wave[c] += 1;
+    else L->n_block[c] += items;
+  }
+  L->off = adamw_offsets(n, n_groups, L->n_items, L->n_split, L->n_slots);
+  return SDC_OK;
+}
+
+void pack_adamw(const sdc_adamw_tensor* t, uint64_t n, const Layout& L, std::vector<unsigned char>& img) {
+  img.assign(L.off.partials, 0);
+  AdamwDesc* desc = reinterpret_cast<AdamwDesc*>(img.data() + L.off.desc);
+  AdamwItem* items = reinterpret_cast<AdamwItem*>(img.data() + L.off.items);
+  PlanSplit* split = reinterpret_cast<PlanSplit*>(img.data() + L.off.split);
+  uint64_t block[kAdamwClasses], wave[kAdamwClasses], at = 0, first = 0, slot = 0, ns = 0;
+  for (uint32_t c = 0; c < kAdamwClasses; ++c) {
+    block[c] = at;
+    wave[c] = at + L.n_block[c];
+    at += L.n_block[c] + L.n_wave[c];
+  }
+  for (uint64_t k = 0; k < n; ++k) {
+    const sdc_adamw_tensor& x = t[k];
+    desc[k] = AdamwDesc{x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.master, x.exp_avg_scale,
+                        x.exp_avg_sq_scale, first, x.group, x.param_dtype, x.grad_dtype, 0};
+    first += x.numel;
+    const uint64_t count = (x.numel + L.chunk - 1) / L.chunk;
+    if (count != 1) split[ns++] = PlanSplit{(uint32_t)k, (uint32_t)slot, (uint32_t)count, 0};
+    if (count == 0) continue;
+    const uint32_t c = class_of(x);
+    uint64_t& next = x.numel <= kAdamwWaveElems ? wave[c] : block[c];
+    for (uint64_t s = 0; s < x.numel; s += L.chunk)
+      items[next++] = AdamwItem{s, (uint32_t)std::min<uint64_t>(L.chunk, x.numel - s), (uint32_t)k,
+                                count == 1 ? 0u : (uint32_t)slot++, count == 1, 0};
+  }
+}
+
+void fill_info(const Layout& L, uint64_t n, uint32_t n_groups, sdc_adamw_info* h) {
+  h->magic = kAdamwMagic;
+  h->n_tensors = n;
+  h->n_groups = n_groups;
+  h->n_items = L.n_items;
+  h->n_split = L.n_split;
+  h->n_slots = L.n_slots;
+  h->total_elems = L.total_elems;
+  h->plan_bytes = L.off.end;
+  for (uint32_t c = 0; c < kAdamwClasses; ++c) {
+    h->n_block[c] = L.n_block[c];
+    h->n_wave[c] = L.n_wave[c];
+  }
+}
+
+bool adamw_info_ok(const sdc_adamw_info* h) {
+  if (h->magic != kAdamwMagic || h->n_items > kMaxGrid || h->n_split > h->n_tensors ||
+      h->n_tensors >= 1ull << 31 || h->n_groups == 0 || h->n_groups > 65536 || h->n_slots > h->n_items)
+    return false;
+  uint64_t items = 0;
+  for (uint32_t c = 0; c < kAdamwClasses; ++c) {
+    if (h->n_block[c] > kMaxGrid || h->n_wave[c] > kMaxGrid) return false;
+    items += h->n_block[c] + h->n_wave[c];
+  }
+  return items == h->n_items &&
+         h->plan_bytes >= adamw_offsets(h->n_tensors, h->n_groups, h->n_items, h->n_split, h->n_slots).end;
+}
+
+}  // namespace
+}  // namespace sdc
+
+using namespace sdc;
+
+extern "C" int32_t sdc_adamw_plan_bytes(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
+                                        uint64_t* h_bytes) {
+  if (h_bytes == nullptr) return SDC_ERR_INVALID;
+  Layout L;
+  if (int32_t st = layout_adamw(h_tensors, n, n_groups, &L)) return st;
+  *h_bytes = L.off.end;
+  return SDC_OK;
+}
+
+extern "C" int32_t sdc_adamw_plan_build(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
+                                        void* d_plan, uint64_t plan_bytes, sdc_adamw_info* h_info,
+                                        sdc_stream_t stream) {
+  if (d_plan == nullptr || h_info == nullptr) return SDC_ERR_INVALID;
+  Layout L;
+  int32_t st = layout_adamw(h_tensors, n, n_groups, &L);
+  if (st) return st;
+  if (plan_bytes < L.off.end) return SDC_ERR_WORKSPACE;
+  if (!aligned(d_plan, 16)) return SDC_ERR_ALIGN;
+  std::vector<unsigned char> img;
+  try {
+    pack_adamw(h_tensors, n, L, img);
+  } catch (...) {
+    return SDC_ERR_RANGE;  // host allocation failed
+  }
+  hipStream_t s = as_stream(stream);
+  st = hip_status(hipMemcpyAsync(d_plan, img.data(), img.size(), hipMemcpyHostToDevice, s));
+  if (st) return st;
+  st = hip_status(hipStreamSynchronize(s));
+  if (st) return st;
+  fill_info(L, n, n_groups, h_info);
+  return SDC_OK;
+}
+
+extern "C" int32_t sdc_adamw_step(void* d_plan, const sdc_adamw_info* h_info,
+                                  const sdc_adamw_group* d_groups, sdc_adamw_control* d_control,
+                                  const double* d_sq_total, const uint32_t* d_flag, double max_norm,
+                                  double grad_scale, sdc_row* d_rows, sdc_stream_t stream) {
+  if (d_plan == nullptr || h_info == nullptr || d_groups == nullptr || d_control == nullptr)
+    return SDC_ERR_INVALID;
+  if (!adamw_info_ok(h_info)) return SDC_ERR_PLAN;
+  if (!(max_norm >= 0.0) || (max_norm > 0.0 && d_sq_total == nullptr) || !(grad_scale > 0.0) ||
+      !std::isfinite(max_norm) || !std::isfinite(grad_scale))
+    return SDC_ERR_INVALID;
+  if (!aligned(d_groups, 8) || !aligned(d_control, 8) || !aligned(d_sq_total, 8) || !aligned(d_flag, 4) ||
+      !aligned(d_rows, 16))
+    return SDC_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  unsigned char* base = static_cast<unsigned char*>(d_plan);
+  const AdamwOffsets o = adamw_offsets(h_info->n_tensors, h_info->n_groups, h_info->n_items,
+                                       h_info->n_split, h_info->n_slots);
+  AdamwGate* gate = reinterpret_cast<AdamwGate*>(base + o.gate);
+  AdamwCoef* coef = reinterpret_cast<AdamwCoef*>(base + o.coef);
+  hipLaunchKernelGGL(adamw_gate_kernel, dim3(1), dim3(64), 0, s, d_control, d_groups,
+                     (uint32_t)h_info->n_groups, d_sq_total, d_flag, max_norm, grad_scale, gate, coef);
+  int32_t st = launch_status();
+  if (st) return st;
+  AdamwArgs a{gate, coef, reinterpret_cast<const AdamwDesc*>(base + o.desc),
+              reinterpret_cast<const AdamwItem*>(base + o.items), 0, 0,
+              reinterpret_cast<sdc_row*>(base + o.partials), d_rows};
+  for (uint32_t c = 0; c < kAdamwClasses; ++c) {
+    a.n_block = (uint32_t)h_info->n_block[c];
+    a.n_wave = (uint32_t)h_info->n_wave[c];
+    if (a.n_block + a.n_wave == 0) continue;
+    st = (c & 1) ? launch_adamw8(c, a, s) : launch_adamw32(c, a, s);
+    if (st) return st;
+    a.items += a.n_block + a.n_wave;
+  }
+  if (d_rows && h_info->n_split) {
+    hipLaunchKernelGGL(adamw_merge_kernel, dim3((uint32_t)((h_info->n_split + kWaves - 1) / kWaves)),
+                       dim3(kBlock), 0, s, reinterpret_cast<const PlanSplit*>(base + o.split),
+                       (uint32_t)h_info->n_split, a.partials, d_rows);
+    return launch_status();
+  }
+  return SDC_OK;
+}

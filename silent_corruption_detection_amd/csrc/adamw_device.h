@@ -1,0 +1,574 @@
+// adamw_device.h -- device and plan definitions of the AdamW step over a
+// tensor list (the optimizer step that the weight check of AWS Machine
+// Learning Blog, "Detecting and recovering from silent data corruption on
+// Amazon SageMaker HyperPod", section "Check 3", runs after).
+#pragma once
+
+#include "fingerprint_device.h"
+
+namespace sdc {
+
+constexpr uint64_t kAdamwMagic = 0x31766D6164414453ull;  // "SDAdamv1", little-endian
+
+// A tensor is cut into items of kAdamwChunkMin .. kAdamwChunkMax elements (a
+// power of two, so an item starts on a 128-element block of an 8-bit state),
+// each updated by one workgroup; tensors of up to kAdamwWaveElems elements
+// are items of one wave.  The largest chunk that still gives kAdamwMinItems
+// items is taken.  A lane of a chunk sees at most 65536 / 1024 = 64 vectors
+// of 4 elements, so 16-bit patterns sum in 32 bits.
+constexpr uint64_t kAdamwChunkMin = 2048, kAdamwChunkMax = 65536;
+constexpr uint64_t kAdamwMinItems = 4096;
+constexpr uint64_t kAdamwWaveElems = 2048;
+
+// Elements that share one scale byte of an 8-bit state.
+constexpr uint32_t kStateBlock = 128;
+
+// Kernel classes by the widths of what they stream: param 0 fp32, 1 16-bit,
+// 2 16-bit with fp32 master weights; grad 0 fp32, 1 16-bit; state 0 fp32,
+// 1 8-bit.
+constexpr uint32_t kAdamwClasses = 12;
+constexpr uint32_t adamw_class(uint32_t param, uint32_t grad, uint32_t state) {
+  return (param * 2 + grad) * 2 + state;
+}
+
+struct AdamwDesc {
+  void* param;
+  const void* grad;  // null: the tensor is left as it is
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* master;
+  uint8_t* exp_avg_scale;
+  uint8_t* exp_avg_sq_scale;
+  uint64_t first;  // elements of the list before this tensor (the random bits' counter)
+  uint32_t group;
+  uint32_t param_dtype, grad_dtype;
+  uint32_t pad;
+};
+static_assert(sizeof(AdamwDesc) == 80, "AdamW descriptor layout");
+
+struct AdamwItem {
+  uint64_t start;   // first element
+  uint32_t len;     // elements
+  uint32_t tensor;  // descriptor, and row, of the tensor
+  uint32_t slot;    // partial-row slot (tensors of several items)
+  uint32_t whole;   // 1: the item is the whole tensor and stores its row
+  uint64_t pad;
+};
+static_assert(sizeof(AdamwItem) == 32, "AdamW item layout");
+
+// What the gate of a step leaves for its items: the factor of the gradients,
+// whether the step is skipped, and the keys of its random bits.
+struct AdamwGate {
+  float scale;
+  uint32_t skip;
+  uint32_t k0, k1;
+};
+
+struct AdamwCoef {
+  float beta1, omb1, beta2, omb2;  // omb = 1 - beta
+  float size;                      // lr / (1 - beta1^t)
+  float rbc2;                      // 1 / sqrt(1 - beta2^t)
+  float eps, decay;                // decay = 1 - lr * weight_decay
+};
+static_assert(sizeof(AdamwCoef) == 32, "AdamW coefficients");
+
+// Device plan: [AdamwGate][coefficients x n_groups][descriptors x n_tensors]
+// [items][split entries] (pad to 256) [partial rows].
+struct AdamwOffsets {
+  uint64_t gate, coef, desc, items, split, partials, end;
+};
+
+inline AdamwOffsets adamw_offsets(uint64_t n_tensors, uint64_t n_groups, uint64_t n_items,
+                                  uint64_t n_split, uint64_t n_slots) {
+  AdamwOffsets o;
+  o.gate = 0;
+  o.coef = 64;
+  o.desc = o.coef + n_groups * sizeof(AdamwCoef);
+  o.items = o.desc + n_tensors * sizeof(AdamwDesc);
+  o.items = (o.items + 31) / 32 * 32;
+  o.split = o.items + n_items * sizeof(AdamwItem);
+  o.partials = (o.split + n_split * sizeof(PlanSplit) + 255) / 256 * 256;
+  o.end = o.partials + n_slots * sizeof(sdc_row);
+  return o;
+}
+
+struct AdamwArgs {
+  const AdamwGate* gate;
+  const AdamwCoef* coef;
+  const AdamwDesc* desc;
+  const AdamwItem* items;  // of the class: n_block workgroup items, then n_wave wave items
+  uint32_t n_block, n_wave;
+  sdc_row* partials;
+  sdc_row* rows;  // null: no rows
+};
+
+// Launches the class's items (csrc/adamw32.hip, csrc/adamw8.hip).
+int32_t launch_adamw32(uint32_t cls, const AdamwArgs& a, hipStream_t s);
+int32_t launch_adamw8(uint32_t cls, const AdamwArgs& a, hipStream_t s);
+
+namespace {
+
+// Vectors at any element alignment: the hardware's global accesses need no
+// more (they split only where a vector crosses a cache line).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+// W dwords at p, streamed (every byte of the step is touched once).
+template <int W>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[W]) {
+  const unsigned char* c = (const unsigned char*)p;
+  if constexpr (W >= 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const u32x4_any v = __builtin_nontemporal_load((const SDC_GLOBAL u32x4_any*)(c + 4 * i));
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  } else if constexpr (W == 2) {
+    const u32x2_any v = __builtin_nontemporal_load((const SDC_GLOBAL u32x2_any*)c);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = __builtin_nontemporal_load((const SDC_GLOBAL u32_any*)c);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[W]) {
+  unsigned char* c = (unsigned char*)p;
+  if constexpr (W >= 4) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const u32x4_any v = {w[i], w[i + 1], w[i + 2], w[i + 3]};
+      __builtin_nontemporal_store(v, (SDC_GLOBAL u32x4_any*)(c + 4 * i));
+    }
+  } else if constexpr (W == 2) {
+    const u32x2_any v = {w[0], w[1]};
+    __builtin_nontemporal_store(v, (SDC_GLOBAL u32x2_any*)c);
+  } else {
+    __builtin_nontemporal_store(w[0], (SDC_GLOBAL u32_any*)c);
+  }
+}
+
+// One vector of E elements of ES bytes as packed little-endian words.  n: how
+// many of them the tensor still has from here (E or more for all but its last
+// vector, 0 or less past its end, whose vectors read as zero).
+template <int E, int ES>
+struct Vec {
+  static constexpr int W = E * ES / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const void* base, uint64_t at, int n) {
+    const unsigned char* p = (const unsigned char*)base + at * ES;
+    zero();
+    if (n >= E) {
+      load_words<W>(p, w);
+    } else if (n > 0) {
+#pragma unroll
+      for (int k = 0; k < E - 1; ++k)
+        if (k < n) w[k * ES / 4] |= (uint32_t)load_elem<ES>(p + k * ES) << (8 * ((k * ES) & 3));
+    }
+  }
+  // zeroes the elements from n on
+  __device__ __forceinline__ void cut(int n) {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k >= n) w[k * ES / 4] &= ES == 4 ? 0u : ~(((1u << (8 * ES & 31)) - 1u) << (8 * ((k * ES) & 3)));
+  }
+  __device__ __forceinline__ void store(void* base, uint64_t at, int n) const {
+    unsigned char* p = (unsigned char*)base + at * ES;
+    if (n >= E) {
+      store_words<W>(p, w);
+    } else if (n > 0) {
+#pragma unroll
+      for (int k = 0; k < E - 1; ++k)
+        if (k < n) {
+          const uint32_t x = w[k * ES / 4] >> (8 * ((k * ES) & 3));
+          if constexpr (ES == 4) *(SDC_GLOBAL uint32_t*)(p + k * 4) = x;
+          else if constexpr (ES == 2) *(SDC_GLOBAL uint16_t*)(p + k * 2) = (uint16_t)x;
+          else *(SDC_GLOBAL uint8_t*)(p + k) = (uint8_t)x;
+        }
+    }
+  }
+};
+
+__device__ __forceinline__ float bf16_to_float(uint32_t h) { return __uint_as_float(h << 16); }
+__device__ __forceinline__ float f16_to_float(uint32_t h) {
+  return (float)__builtin_bit_cast(_Float16, (unsigned short)h);
+}
+
+// Round to nearest, ties to even: the rounding of torch's own casts, off by at
+// most half a step.  NaN stays NaN (quieted).
+__device__ __forceinline__ uint32_t float_to_bf16(float x) {
+  const __bf16 b = (__bf16)x;
+  return __builtin_bit_cast(unsigned short, b);
+}
+__device__ __forceinline__ uint32_t float_to_f16(float x) {
+  const _Float16 h = (_Float16)x;
+  return __builtin_bit_cast(unsigned short, h);
+}
+
+template <int E, int ES>
+__device__ __forceinline__ void to_floats(const Vec<E, ES>& v, bool half, float (&f)[E]) {
+  if constexpr (ES == 4) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) f[k] = __uint_as_float(v.w[k]);
+  } else if (half) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) f[k] = f16_to_float((v.w[k / 2] >> (16 * (k & 1))) & 0xFFFFu);
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      f[k] = (k & 1) ? __uint_as_float(v.w[k / 2] & 0xFFFF0000u) : bf16_to_float(v.w[k / 2]);
+  }
+}
+
+template <int E, int ES>
+__device__ __forceinline__ void from_floats(const float (&f)[E], bool half, Vec<E, ES>& v) {
+  if constexpr (ES == 4) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) v.w[k] = __float_as_uint(f[k]);
+  } else if (half) {
+#pragma unroll
+    for (int k = 0; k < E; k += 2) v.w[k / 2] = float_to_f16(f[k]) | (float_to_f16(f[k + 1]) << 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; k += 2) v.w[k / 2] = float_to_bf16(f[k]) | (float_to_bf16(f[k + 1]) << 16);
+  }
+}
+
+// Fingerprint of the new weights while they are in registers: the lane's
+// sums over its vectors of E elements, vector i of the item being lane
+// i % LANES's, as in the scan: a = sum x, c = sum k x (k: slot in the vector),
+// q = the running sum of a after each vector.
+template <int E, int ES>
+struct RowAcc {
+  typedef std::conditional_t<(ES == 2), uint32_t, uint64_t> sum_t;
+  sum_t a = 0, c = 0;
+  uint64_t q = 0;
+  uint32_t x = 0, nf = 0;
+  __device__ __forceinline__ void add(const Vec<E, ES>& v, uint32_t m2, uint32_t k2) {
+#pragma unroll
+    for (int i = 0; i < Vec<E, ES>::W; ++i) {
+      const uint32_t d = v.w[i];
+      if constexpr (ES == 2) {
+        a = udot2(d, 0x00010001u, a);
+        c = udot2(d, (uint32_t)((2 * i + 1) << 16 | (2 * i)), c);
+        nf += (uint32_t)__builtin_popcount(((d & m2) + k2) & 0x80008000u);
+      } else {
+        a += d;
+        c += (uint64_t)i * d;
+        nf += ((d & 0x7F800000u) + 0x00800000u) >> 31;
+      }
+      x ^= d;
+    }
+    q += a;
+  }
+  // T: vectors of the lane, those past the end counted as zero vectors
+  __device__ __forceinline__ Lane lane(uint32_t l, uint32_t lanes, uint64_t T) const {
+    Lane ln;
+    ln.s = a;
+    ln.w = (uint64_t)(1u + E * l) * a + (uint64_t)(lanes * E) * (T * a - q) + c;
+    ln.x = x;
+    ln.nf = nf;
+    return ln;
+  }
+};
+
+__device__ __forceinline__ void store_row(sdc_row* dst, const Lane& ln, uint64_t w) {
+  ulonglong2* d = reinterpret_cast<ulonglong2*>(dst);
+  d[0] = ulonglong2{ln.s, w};
+  d[1] = ulonglong2{ln.x, ln.nf};
+}
+
+// One step of one element, in fp32: m, v and the weight p of the gradient g
+// (scaled already); returns sqrt(v).  The quotient takes the hardware's
+// reciprocal, and EXACT false also its square root (each off by about one unit
+// in the last place, which moves the update, not the weight, by 2^-23 of
+// itself).  EXACT: every operation of m, v and sqrt(v) is rounded on its own,
+// so the 8-bit codes drawn from them follow bit for bit from the formulas,
+// whoever computes them.
+template <bool EXACT>
+__device__ __forceinline__ float adamw_element(const AdamwCoef& c, float g, float& m, float& v, float& p) {
+  float r;
+  if constexpr (EXACT) {
+    {
+#pragma clang fp contract(off)
+      m = m * c.beta1 + g * c.omb1;
+      v = v * c.beta2 + (g * g) * c.omb2;
+    }
+    r = __builtin_sqrtf(v);
+  } else {
+    m = __builtin_fmaf(c.beta1, m, c.omb1 * g);
+    v = __builtin_fmaf(c.beta2, v, c.omb2 * (g * g));
+    r = __builtin_amdgcn_sqrtf(v);
+  }
+  const float q = m * __builtin_amdgcn_rcpf(__builtin_fmaf(r, c.rbc2, c.eps));
+  p = __builtin_fmaf(-c.size, q, p * c.decay);
+  return r;
+}
+
+// The two streams of state of E elements of an item.
+template <int E>
+struct State32 {
+  Vec<E, 4> m, v;
+  __device__ __forceinline__ void load(const AdamwDesc& d, uint64_t at, int n) {
+    m.load(d.exp_avg, at, n);
+    v.load(d.exp_avg_sq, at, n);
+  }
+  template <class F>
+  __device__ __forceinline__ void update(F&& element, uint64_t, const AdamwGate&) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      float mk = __uint_as_float(m.w[k]), vk = __uint_as_float(v.w[k]);
+      element(k, mk, vk);
+      m.w[k] = __float_as_uint(mk);
+      v.w[k] = __float_as_uint(vk);
+    }
+  }
+  __device__ __forceinline__ void store(const AdamwDesc& d, uint64_t at, int n) const {
+    m.store(d.exp_avg, at, n);
+    v.store(d.exp_avg_sq, at, n);
+  }
+};
+
+// Largest value over groups of G (16 or 32) adjacent lanes, in all of them.
+template <int G>
+__device__ __forceinline__ uint32_t group_umax(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));  // mirrored in 8
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));  // mirrored in 16
+  if constexpr (G == 32) x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+  return x;
+}
+
+// States in 8 bits.  A block of 128 elements of the tensor shares the power
+// of two 2^(s-127), s = max(exponent field of the block's largest magnitude
+// - 7, 1): the largest lands in [128, 256), so rounding up never reaches
+// e4m3's NaN.  m is held as e4m3 codes of m / 2^(s-127), v as those of
+// sqrt(v) / 2^(s-127) (a square root halves the range of exponents that 8
+// bits have to span).  e4m3 has the bits of an fp32 number 2^-120 times as
+// large, cut to 3 mantissa bits, subnormals included.
+//
+// Codes are 1/8 to 1/16 apart, a step moves a state by 1 - beta (0.1 .. 0.001)
+// of itself: rounding to nearest would never move v.  So each code is drawn
+// from its two neighbours with the element's random bits, for m so that the
+// expected value is m, for sqrt(v) so that the expected square is v; the
+// moving averages then stay unbiased.  A v above zero is never held as zero
+// (the quotient would be m / eps).  NaN and Inf become NaN.
+template <int E>
+struct State8 {
+  static constexpr int kLanes = kStateBlock / E;  // lanes of a block
+  Vec<E, 1> m, v;
+  uint32_t ms, vs;  // scale bytes
+  __device__ __forceinline__ void load(const AdamwDesc& d, uint64_t at, int n) {
+    m.load(d.exp_avg, at, n);
+    v.load(d.exp_avg_sq, at, n);
+    ms = vs = 0;
+    if (n > 0) {
+      ms = ((const SDC_GLOBAL uint8_t*)d.exp_avg_scale)[at / kStateBlock];
+      vs = ((const SDC_GLOBAL uint8_t*)d.exp_avg_sq_scale)[at / kStateBlock];
+    }
+  }
+  static __device__ __forceinline__ uint32_t hash(uint32_t lo, uint32_t hi_key, uint32_t k0) {
+    // Two multiply-xorshift rounds; multipliers and shifts of least bias from
+    // the search published by C. Wellons ("Prospecting for Hash Functions").
+    uint32_t a = lo + k0;
+    a = (a ^ (a >> 16)) * 0x7FEB352Du;
+    a ^= hi_key;
+    a = (a ^ (a >> 15)) * 0x846CA68Bu;
+    return a ^ (a >> 16);
+  }
+  template <class F>
+  __device__ __forceinline__ void update(F&& element, uint64_t index, const AdamwGate& gate) {
+    const float md = __uint_as_float(ms << 23), vd = __uint_as_float(vs << 23);  // scale byte 0: zeros
+    float mf[E], rf[E];
+    uint32_t mtop = 0, rtop = 0, live = 0;
+#pragma unroll
+    for (int k = 0; k < E; k += 2) {
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      const f2 a = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], true)
+                           : __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], false);
+      const f2 b = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], true)
+                           : __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], false);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mk = a[j] * md, rk = b[j] * vd, vk = rk * rk;
+        rf[k + j] = element(k + j, mk, vk);
+        mf[k + j] = mk;
+        live |= (vk > 0.0f ? 1u : 0u) << (k + j);
+        mtop = max(mtop, __float_as_uint(mk) & 0x7FFFFFFFu);
+        rtop = max(rtop, __float_as_uint(rf[k + j]) & 0x7FFFFFFFu);
+      }
+    }
+    mtop = group_umax<kLanes>(mtop);
+    rtop = group_umax<kLanes>(rtop);
+    ms = (uint32_t)max((int)(mtop >> 23) - 7, 1);
+    vs = (uint32_t)max((int)(rtop >> 23) - 7, 1);
+    const int me = 7 - (int)ms, ve = 127 - (int)vs;  // 2^me: to e4m3's place in fp32; 2^ve: to units
+    const uint32_t lo0 = (uint32_t)index, hi0 = (uint32_t)(index >> 32);
+    const uint32_t hk0 = gate.k1 + hi0 * 0x2C1B3C6Du, hk1 = hk0 + 0x2C1B3C6Du;
+    m.zero();
+    v.zero();
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const uint32_t lo = lo0 + k;
+      const uint32_t h = hash(lo, lo < lo0 ? hk1 : hk0, gate.k0);
+      const float y = __builtin_amdgcn_ldexpf(__builtin_fabsf(mf[k]), me);
+      uint32_t cm = (__float_as_uint(y) + ((h & 0xFFFFu) << 4) + 8u) >> 20;
+      cm = min(cm, 0x7Fu) | ((__float_as_uint(mf[k]) >> 24) & 0x80u);
+      const float t = __builtin_amdgcn_ldexpf(rf[k], ve);
+      uint32_t cr = __float_as_uint(__builtin_amdgcn_ldexpf(t, -120)) >> 20;
+      const float lo_r = __builtin_amdgcn_ldexpf(__uint_as_float(cr << 20), 120);
+      const float hi_r = __builtin_amdgcn_ldexpf(__uint_as_float((cr + 1u) << 20), 120);
+      const float u = __builtin_fmaf((float)(h >> 16), 0x1p-16f, 0x1p-17f);
+      {
+#pragma clang fp contract(off)
+        const float lo_v = lo_r * lo_r;  // 4-bit numbers: their squares and u times the difference are exact
+        cr += u * (hi_r * hi_r - lo_v) < t * t - lo_v ? 1u : 0u;
+      }
+      cr = min(max(cr, (live >> k) & 1u), 0x7Fu);
+      m.w[k / 4] |= cm << (8 * (k & 3));
+      v.w[k / 4] |= cr << (8 * (k & 3));
+    }
+  }
+  __device__ __forceinline__ void store(const AdamwDesc& d, uint64_t at, int n) const {
+    m.store(d.exp_avg, at, n);
+    v.store(d.exp_avg_sq, at, n);
+    if (n > 0 && at % kStateBlock == 0) {
+      ((SDC_GLOBAL uint8_t*)d.exp_avg_scale)[at / kStateBlock] = (uint8_t)ms;
+      ((SDC_GLOBAL uint8_t*)d.exp_avg_sq_scale)[at / kStateBlock] = (uint8_t)vs;
+    }
+  }
+};
+
+template <uint32_t PARAM, uint32_t GRAD, uint32_t STATE, bool ROWS>
+struct AdamwCfg {
+  static constexpr int kParamBytes = PARAM == 0 ? 4 : 2;
+  static constexpr int kGradBytes = GRAD == 0 ? 4 : 2;
+  static constexpr bool kMaster = PARAM == 2;
+  static constexpr bool kRows = ROWS;
+  static constexpr bool kExact = STATE == 1;
+  // Elements per lane and vector: 16 bytes of the widest stream.
+  static constexpr int E = (STATE == 0 || PARAM != 1 || GRAD == 0) ? 4 : 8;
+  static constexpr int U = 8 / E;  // vectors per lane and round
+  typedef std::conditional_t<STATE == 0, State32<E>, State8<E>> State;
+};
+
+// One item by LANES lanes (256: a workgroup, 64: a wave).
+template <class Cfg, uint32_t LANES>
+__device__ __forceinline__ void adamw_item(const AdamwArgs& a, const AdamwItem& it, uint32_t l) {
+  constexpr int E = Cfg::E, U = Cfg::U;
+  const AdamwDesc& d = a.desc[it.tensor];
+  const AdamwGate gate = *a.gate;
+  const AdamwCoef coef = a.coef[d.group];
+  const bool phalf = d.param_dtype == SDC_F16, ghalf = d.grad_dtype == SDC_F16;
+  const bool skip = gate.skip != 0 || d.grad == nullptr;
+  const uint32_t m2 = phalf ? 0x7C007C00u : 0x7F807F80u, k2 = phalf ? 0x04000400u : 0x00800080u;
+  if (skip && !Cfg::kRows) return;
+  RowAcc<E, Cfg::kParamBytes> acc;
+  uint32_t T = 0;
+  // One round of U vectors per lane from vector v0.  FULL: every lane's
+  // vectors are whole, so all loads are issued with no branch between them.
+  const auto round = [&](uint32_t v0, auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    const auto left = [&](uint32_t j) { return FULL ? E : (int)it.len - (int)j; };
+    if (skip) {  // the weights stay: their row alone
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t j = (v0 + u * LANES + l) * E;
+        Vec<E, Cfg::kParamBytes> p;
+        p.load(d.param, it.start + j, left(j));
+        acc.add(p, m2, k2);
+      }
+      return;
+    }
+    Vec<E, Cfg::kParamBytes> p[U];
+    Vec<E, Cfg::kGradBytes> g[U];
+    Vec<E, 4> mw[U];
+    typename Cfg::State st[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = (v0 + u * LANES + l) * E;
+      g[u].load(d.grad, it.start + j, left(j));
+      if constexpr (Cfg::kMaster) mw[u].load(d.master, it.start + j, left(j));
+      else p[u].load(d.param, it.start + j, left(j));
+      st[u].load(d, it.start + j, left(j));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = (v0 + u * LANES + l) * E;
+      float gf[E], pf[E];
+      to_floats(g[u], ghalf, gf);
+      if constexpr (Cfg::kMaster) to_floats(mw[u], false, pf);
+      else to_floats(p[u], phalf, pf);
+      st[u].update(
+          [&](int k, float& m, float& v) { return adamw_element<Cfg::kExact>(coef, gf[k] * gate.scale, m, v, pf[k]); },
+          d.first + it.start + j, gate);
+      if constexpr (Cfg::kMaster) {
+        from_floats(pf, false, mw[u]);
+        mw[u].store(d.master, it.start + j, left(j));
+      }
+      from_floats(pf, phalf, p[u]);
+      if (Cfg::kRows && !FULL) p[u].cut(left(j));
+      p[u].store(d.param, it.start + j, left(j));
+      st[u].store(d, it.start + j, left(j));
+      if constexpr (Cfg::kRows) acc.add(p[u], m2, k2);
+    }
+  };
+  for (uint32_t v0 = 0; v0 * E < it.len; v0 += LANES * U, T += U) {
+    if ((v0 + LANES * U) * E <= it.len) round(v0, std::true_type());
+    else round(v0, std::false_type());
+  }
+  if constexpr (Cfg::kRows) {
+    Lane ln = acc.lane(l, LANES, T);
+    if constexpr (LANES == 64) wave_reduce(ln);
+    else block_reduce(ln);
+    if (l != 0) return;
+    ln.x = finish_xor<TypeTag<Cfg::kParamBytes, false, kChkNone>>(ln.x);
+    store_row(it.whole ? a.rows + it.tensor : a.partials + it.slot, ln, ln.w + it.start * ln.s);
+  }
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(kBlock) adamw_kernel(const AdamwArgs a) {
+  if (blockIdx.x < a.n_block) {
+    adamw_item<Cfg, kBlock>(a, a.items[blockIdx.x], threadIdx.x);
+    return;
+  }
+  const uint32_t w =
+      __builtin_amdgcn_readfirstlane((blockIdx.x - a.n_block) * kWaves + (threadIdx.x >> 6));
+  if (w < a.n_wave) adamw_item<Cfg, 64>(a, a.items[a.n_block + w], threadIdx.x & 63u);
+}
+
+template <uint32_t PARAM, uint32_t GRAD, uint32_t STATE>
+int32_t launch_adamw_class(const AdamwArgs& a, hipStream_t s) {
+  const dim3 grid(a.n_block + (a.n_wave + kWaves - 1) / kWaves), block(kBlock);
+  if (a.rows)
+    hipLaunchKernelGGL((adamw_kernel<AdamwCfg<PARAM, GRAD, STATE, true>>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((adamw_kernel<AdamwCfg<PARAM, GRAD, STATE, false>>), grid, block, 0, s, a);
+  return launch_status();
+}
+
+template <uint32_t STATE>
+int32_t launch_adamw_state(uint32_t cls, const AdamwArgs& a, hipStream_t s) {
+  switch (cls / 2) {
+    case 0: return launch_adamw_class<0, 0, STATE>(a, s);
+    case 1: return launch_adamw_class<0, 1, STATE>(a, s);
+    case 2: return launch_adamw_class<1, 0, STATE>(a, s);
+    case 3: return launch_adamw_class<1, 1, STATE>(a, s);
+    case 4: return launch_adamw_class<2, 0, STATE>(a, s);
+    default: return launch_adamw_class<2, 1, STATE>(a, s);
+  }
+}
+
+}  // namespace
+}  // namespace sdc
