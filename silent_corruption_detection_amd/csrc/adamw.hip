@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kBlock) adamw_merge_kernel(const PlanSplit* __
 }
 
 struct Layout {
-  uint64_t n_items = 0, n_split = 0, n_slots = 0, total_elems = 0, chunk = 0;
+  uint64_t n_items = 0, n_split = 0, n_slots = 0, total_elems = 0;
   uint64_t n_block[kAdamwClasses] = {}, n_wave[kAdamwClasses] = {};
   AdamwOffsets off{};
 };
@@ -96,26 +96,27 @@ uint32_t class_of(const sdc_adamw_tensor& t) {
   return adamw_class(p, g, t.state_dtype == SDC_FP8_E4M3);
 }
 
+// Elements of a tensor with fp32 states past the 16-byte boundary at or below
+// its exp_avg: its first item is that much shorter, so that the others start
+// on a boundary.
+uint64_t shift_of(const sdc_adamw_tensor& t) {
+  return t.state_dtype == SDC_FP8_E4M3 ? 0 : (reinterpret_cast<uintptr_t>(t.exp_avg) >> 2) & 3;
+}
+
+uint64_t items_of(const sdc_adamw_tensor& t) {
+  return t.numel ? (t.numel + shift_of(t) + kAdamwItemElems - 1) / kAdamwItemElems : 0;
+}
+
+bool of_wave(const sdc_adamw_tensor& t) { return t.numel + shift_of(t) <= kAdamwWaveElems; }
+
 int32_t layout_adamw(const sdc_adamw_tensor* t, uint64_t n, uint32_t n_groups, Layout* L) {
   if ((n > 0 && t == nullptr) || n_groups == 0 || n_groups > 65536) return SDC_ERR_INVALID;
   if (n >= 1ull << 31) return SDC_ERR_RANGE;
-  constexpr int kCand = 6;  // 65536 .. 2048 elements
-  static_assert((kAdamwChunkMax >> (kCand - 1)) == kAdamwChunkMin, "candidate chunks");
-  uint64_t count[kCand] = {};
   for (uint64_t k = 0; k < n; ++k) {
     if (int32_t st = check_tensor(t[k], n_groups)) return st;
     L->total_elems += t[k].numel;
     if (L->total_elems >= 1ull << 48) return SDC_ERR_RANGE;
-    for (int c = 0; c < kCand; ++c) count[c] += (t[k].numel + (kAdamwChunkMax >> c) - 1) / (kAdamwChunkMax >> c);
-  }
-  L->chunk = kAdamwChunkMin;
-  for (int c = 0; c < kCand; ++c)
-    if (count[c] >= kAdamwMinItems) {
-      L->chunk = kAdamwChunkMax >> c;
-      break;
-    }
-  for (uint64_t k = 0; k < n; ++k) {
-    const uint64_t items = (t[k].numel + L->chunk - 1) / L->chunk;
+    const uint64_t items = items_of(t[k]);
     L->n_items += items;
     if (L->n_items > kMaxGrid) return SDC_ERR_RANGE;
     if (items != 1) {
@@ -124,7 +125,7 @@ int32_t layout_adamw(const sdc_adamw_tensor* t, uint64_t n, uint32_t n_groups, L
     }
     if (items == 0) continue;
     const uint32_t c = class_of(t[k]);
-    if (t[k].numel <= kAdamwWaveElems) L->n_wave[c] += 1;
+    if (of_wave(t[k])) L->n_wave[c] += 1;
     else L->n_block[c] += items;
   }
   L->off = adamw_offsets(n, n_groups, L->n_items, L->n_split, L->n_slots);
@@ -147,14 +148,16 @@ void pack_adamw(const sdc_adamw_tensor* t, uint64_t n, const Layout& L, std::vec
     desc[k] = AdamwDesc{x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.master, x.exp_avg_scale,
                         x.exp_avg_sq_scale, first, x.group, x.param_dtype, x.grad_dtype, 0};
     first += x.numel;
-    const uint64_t count = (x.numel + L.chunk - 1) / L.chunk;
+    const uint64_t count = items_of(x);
     if (count != 1) split[ns++] = PlanSplit{(uint32_t)k, (uint32_t)slot, (uint32_t)count, 0};
     if (count == 0) continue;
     const uint32_t c = class_of(x);
-    uint64_t& next = x.numel <= kAdamwWaveElems ? wave[c] : block[c];
-    for (uint64_t s = 0; s < x.numel; s += L.chunk)
-      items[next++] = AdamwItem{s, (uint32_t)std::min<uint64_t>(L.chunk, x.numel - s), (uint32_t)k,
-                                count == 1 ? 0u : (uint32_t)slot++, count == 1, 0};
+    uint64_t& next = of_wave(x) ? wave[c] : block[c];
+    for (uint64_t s = 0, len = kAdamwItemElems - shift_of(x); s < x.numel; s += len, len = kAdamwItemElems) {
+      const uint64_t left = x.numel - s;
+      items[next++] = AdamwItem{s, (uint32_t)std::min(len, left), (uint32_t)k, count == 1 ? 0u : (uint32_t)slot++,
+                                count == 1, 0};
+    }
   }
 }
 

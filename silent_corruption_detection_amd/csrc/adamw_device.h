@@ -10,14 +10,13 @@ namespace sdc {
 
 constexpr uint64_t kAdamwMagic = 0x31766D6164414453ull;  // "SDAdamv1", little-endian
 
-// A tensor is cut into items of kAdamwChunkMin .. kAdamwChunkMax elements (a
-// power of two, so an item starts on a 128-element block of an 8-bit state),
-// each updated by one workgroup; tensors of up to kAdamwWaveElems elements
-// are items of one wave.  The largest chunk that still gives kAdamwMinItems
-// items is taken.  A lane of a chunk sees at most 65536 / 1024 = 64 vectors
-// of 4 elements, so 16-bit patterns sum in 32 bits.
-constexpr uint64_t kAdamwChunkMin = 2048, kAdamwChunkMax = 65536;
-constexpr uint64_t kAdamwMinItems = 4096;
+// A tensor is cut into items of one round of loads of a workgroup each (a
+// multiple of the 128-element block of an 8-bit state); tensors of up to
+// kAdamwWaveElems elements are items of one wave.  One round, because what
+// hides the memory's latency here is the number of waves that load: longer
+// items measured 4921 / 5130 / 5200 us at 4096 / 16384 / 65536 elements, this size
+// 4826 us (0.96B fp32 weights).
+constexpr uint64_t kAdamwItemElems = 2048;
 constexpr uint64_t kAdamwWaveElems = 2048;
 
 // Elements that share one scale byte of an 8-bit state.
@@ -108,11 +107,31 @@ int32_t launch_adamw8(uint32_t cls, const AdamwArgs& a, hipStream_t s);
 
 namespace {
 
+// Loads through the constant address space: what the plan holds does not
+// change while a step's kernels run, so uniform reads of it are scalar loads
+// that stores in between do not repeat.
+template <class T>
+__device__ __forceinline__ T load_const(const T* p) {
+  struct Words {
+    uint32_t w[sizeof(T) / 4];
+  } x;
+#pragma unroll
+  for (uint32_t i = 0; i < sizeof(T) / 4; ++i) x.w[i] = ((const __attribute__((address_space(4))) uint32_t*)p)[i];
+  return __builtin_bit_cast(T, x);
+}
+
+// An item's streams, each from the item's first element on.
+struct AdamwStreams {
+  unsigned char *param, *exp_avg, *exp_avg_sq, *master, *exp_avg_scale, *exp_avg_sq_scale;
+  const unsigned char* grad;
+};
+
 // Vectors at any element alignment: the hardware's global accesses need no
 // more (they split only where a vector crosses a cache line).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // W dwords at p, streamed (every byte of the step is touched once).
 template <int W>
@@ -153,9 +172,9 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[W]) {
   }
 }
 
-// One vector of E elements of ES bytes as packed little-endian words.  n: how
-// many of them the tensor still has from here (E or more for all but its last
-// vector, 0 or less past its end, whose vectors read as zero).
+// One vector of E elements of ES bytes as packed little-endian words, of
+// which those from `lo` on and below `hi` are the item's (0 and E: all of
+// them; hi <= lo: none).  The others read as zero and are not written.
 template <int E, int ES>
 struct Vec {
   static constexpr int W = E * ES / 4;
@@ -164,37 +183,43 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0u;
   }
-  __device__ __forceinline__ void load(const void* base, uint64_t at, int n) {
-    const unsigned char* p = (const unsigned char*)base + at * ES;
-    zero();
-    if (n >= E) {
+  __device__ __forceinline__ void load(const unsigned char* base, uint32_t at, int lo, int hi) {
+    const unsigned char* p = base + at * ES;
+    if (lo <= 0 && hi >= E) {
       load_words<W>(p, w);
-    } else if (n > 0) {
-#pragma unroll
-      for (int k = 0; k < E - 1; ++k)
-        if (k < n) w[k * ES / 4] |= (uint32_t)load_elem<ES>(p + k * ES) << (8 * ((k * ES) & 3));
+      return;
     }
-  }
-  // zeroes the elements from n on
-  __device__ __forceinline__ void cut(int n) {
+    zero();
+    if (lo >= hi) return;
+    // element loads from addresses held inside the range, all in flight together
+    uint32_t x[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = (uint32_t)load_elem<ES>(p + min(max(k, lo), hi - 1) * ES);
 #pragma unroll
     for (int k = 0; k < E; ++k)
-      if (k >= n) w[k * ES / 4] &= ES == 4 ? 0u : ~(((1u << (8 * ES & 31)) - 1u) << (8 * ((k * ES) & 3)));
+      if (k >= lo && k < hi) w[k * ES / 4] |= x[k] << (8 * ((k * ES) & 3));
   }
-  __device__ __forceinline__ void store(void* base, uint64_t at, int n) const {
-    unsigned char* p = (unsigned char*)base + at * ES;
-    if (n >= E) {
-      store_words<W>(p, w);
-    } else if (n > 0) {
+  // zeroes the elements below lo and from hi on
+  __device__ __forceinline__ void cut(int lo, int hi) {
 #pragma unroll
-      for (int k = 0; k < E - 1; ++k)
-        if (k < n) {
-          const uint32_t x = w[k * ES / 4] >> (8 * ((k * ES) & 3));
-          if constexpr (ES == 4) *(SDC_GLOBAL uint32_t*)(p + k * 4) = x;
-          else if constexpr (ES == 2) *(SDC_GLOBAL uint16_t*)(p + k * 2) = (uint16_t)x;
-          else *(SDC_GLOBAL uint8_t*)(p + k) = (uint8_t)x;
-        }
+    for (int k = 0; k < E; ++k)
+      if (k < lo || k >= hi)
+        w[k * ES / 4] &= ES == 4 ? 0u : ~(((1u << (8 * ES & 31)) - 1u) << (8 * ((k * ES) & 3)));
+  }
+  __device__ __forceinline__ void store(unsigned char* base, uint32_t at, int lo, int hi) const {
+    unsigned char* p = base + at * ES;
+    if (lo <= 0 && hi >= E) {
+      store_words<W>(p, w);
+      return;
     }
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (k >= lo && k < hi) {
+        const uint32_t x = w[k * ES / 4] >> (8 * ((k * ES) & 3));
+        if constexpr (ES == 4) *(SDC_GLOBAL uint32_t*)(p + k * 4) = x;
+        else if constexpr (ES == 2) *(SDC_GLOBAL uint16_t*)(p + k * 2) = (uint16_t)x;
+        else *(SDC_GLOBAL uint8_t*)(p + k) = (uint8_t)x;
+      }
   }
 };
 
@@ -270,11 +295,12 @@ struct RowAcc {
     }
     q += a;
   }
-  // T: vectors of the lane, those past the end counted as zero vectors
-  __device__ __forceinline__ Lane lane(uint32_t l, uint32_t lanes, uint64_t T) const {
+  // T: vectors of the lane, those past the end counted as zero vectors; shift:
+  // places before the item's first element in its first vector
+  __device__ __forceinline__ Lane lane(uint32_t l, uint32_t lanes, uint64_t T, uint32_t shift) const {
     Lane ln;
     ln.s = a;
-    ln.w = (uint64_t)(1u + E * l) * a + (uint64_t)(lanes * E) * (T * a - q) + c;
+    ln.w = ((uint64_t)(1u + E * l) - shift) * a + (uint64_t)(lanes * E) * (T * a - q) + c;
     ln.x = x;
     ln.nf = nf;
     return ln;
@@ -287,13 +313,27 @@ __device__ __forceinline__ void store_row(sdc_row* dst, const Lane& ln, uint64_t
   d[1] = ulonglong2{ln.x, ln.nf};
 }
 
+// The fp32 number nearest to sqrt(v), for v = 0, v >= 2^-96, Inf or NaN (below,
+// within one unit in the last place): the hardware's root s is off by at most
+// one unit, and the signs of v - s s' for s' its neighbours below and above
+// tell which of the three it is (each an fma, exact in sign as long as it
+// does not underflow).
+__device__ __forceinline__ float sqrt_nearest(float v) {
+  const float s = __builtin_amdgcn_sqrtf(v);
+  const float below = __uint_as_float(__float_as_uint(s) - 1u), above = __uint_as_float(__float_as_uint(s) + 1u);
+  float r = s;
+  if (__builtin_fmaf(-below, s, v) <= 0.0f) r = below;
+  if (__builtin_fmaf(-above, s, v) > 0.0f) r = above;
+  return r;
+}
+
 // One step of one element, in fp32: m, v and the weight p of the gradient g
 // (scaled already); returns sqrt(v).  The quotient takes the hardware's
 // reciprocal, and EXACT false also its square root (each off by about one unit
 // in the last place, which moves the update, not the weight, by 2^-23 of
 // itself).  EXACT: every operation of m, v and sqrt(v) is rounded on its own,
-// so the 8-bit codes drawn from them follow bit for bit from the formulas,
-// whoever computes them.
+// so the 8-bit codes drawn from them follow from the formulas, whoever
+// computes them.
 template <bool EXACT>
 __device__ __forceinline__ float adamw_element(const AdamwCoef& c, float g, float& m, float& v, float& p) {
   float r;
@@ -303,7 +343,7 @@ __device__ __forceinline__ float adamw_element(const AdamwCoef& c, float g, floa
       m = m * c.beta1 + g * c.omb1;
       v = v * c.beta2 + (g * g) * c.omb2;
     }
-    r = __builtin_sqrtf(v);
+    r = sqrt_nearest(v);
   } else {
     m = __builtin_fmaf(c.beta1, m, c.omb1 * g);
     v = __builtin_fmaf(c.beta2, v, c.omb2 * (g * g));
@@ -318,12 +358,12 @@ __device__ __forceinline__ float adamw_element(const AdamwCoef& c, float g, floa
 template <int E>
 struct State32 {
   Vec<E, 4> m, v;
-  __device__ __forceinline__ void load(const AdamwDesc& d, uint64_t at, int n) {
-    m.load(d.exp_avg, at, n);
-    v.load(d.exp_avg_sq, at, n);
+  __device__ __forceinline__ void load(const AdamwStreams& d, uint32_t at, int lo, int hi) {
+    m.load(d.exp_avg, at, lo, hi);
+    v.load(d.exp_avg_sq, at, lo, hi);
   }
-  template <class F>
-  __device__ __forceinline__ void update(F&& element, uint64_t, const AdamwGate&) {
+  template <class F, class G>
+  __device__ __forceinline__ void update(F&& element, G&& done, uint64_t, const AdamwGate&, bool) {
 #pragma unroll
     for (int k = 0; k < E; ++k) {
       float mk = __uint_as_float(m.w[k]), vk = __uint_as_float(v.w[k]);
@@ -331,10 +371,11 @@ struct State32 {
       m.w[k] = __float_as_uint(mk);
       v.w[k] = __float_as_uint(vk);
     }
+    done();
   }
-  __device__ __forceinline__ void store(const AdamwDesc& d, uint64_t at, int n) const {
-    m.store(d.exp_avg, at, n);
-    v.store(d.exp_avg_sq, at, n);
+  __device__ __forceinline__ void store(const AdamwStreams& d, uint32_t at, int lo, int hi) const {
+    m.store(d.exp_avg, at, lo, hi);
+    v.store(d.exp_avg_sq, at, lo, hi);
   }
 };
 
@@ -368,11 +409,11 @@ struct State8 {
   static constexpr int kLanes = kStateBlock / E;  // lanes of a block
   Vec<E, 1> m, v;
   uint32_t ms, vs;  // scale bytes
-  __device__ __forceinline__ void load(const AdamwDesc& d, uint64_t at, int n) {
-    m.load(d.exp_avg, at, n);
-    v.load(d.exp_avg_sq, at, n);
+  __device__ __forceinline__ void load(const AdamwStreams& d, uint32_t at, int lo, int hi) {
+    m.load(d.exp_avg, at, lo, hi);
+    v.load(d.exp_avg_sq, at, lo, hi);
     ms = vs = 0;
-    if (n > 0) {
+    if (hi > 0) {
       ms = ((const SDC_GLOBAL uint8_t*)d.exp_avg_scale)[at / kStateBlock];
       vs = ((const SDC_GLOBAL uint8_t*)d.exp_avg_sq_scale)[at / kStateBlock];
     }
@@ -386,63 +427,83 @@ struct State8 {
     a = (a ^ (a >> 15)) * 0x846CA68Bu;
     return a ^ (a >> 16);
   }
-  template <class F>
-  __device__ __forceinline__ void update(F&& element, uint64_t index, const AdamwGate& gate) {
+  template <class F, class G>
+  __device__ __forceinline__ void update(F&& element, G&& done, uint64_t index, const AdamwGate& gate, bool wraps) {
     const float md = __uint_as_float(ms << 23), vd = __uint_as_float(vs << 23);  // scale byte 0: zeros
-    float mf[E], rf[E];
-    uint32_t mtop = 0, rtop = 0, live = 0;
+    float mf[E], rf[E], mtop = 0.0f, rtop = 0.0f;  // NaNs are left out of the largest
 #pragma unroll
     for (int k = 0; k < E; k += 2) {
-      typedef float f2 __attribute__((ext_vector_type(2)));
-      const f2 a = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], true)
-                           : __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], false);
-      const f2 b = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], true)
-                           : __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], false);
+      const f32x2 a = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)m.w[k / 4], false);
+      const f32x2 b = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], true)
+                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)v.w[k / 4], false);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float mk = a[j] * md, rk = b[j] * vd, vk = rk * rk;
-        rf[k + j] = element(k + j, mk, vk);
-        mf[k + j] = mk;
-        live |= (vk > 0.0f ? 1u : 0u) << (k + j);
-        mtop = max(mtop, __float_as_uint(mk) & 0x7FFFFFFFu);
-        rtop = max(rtop, __float_as_uint(rf[k + j]) & 0x7FFFFFFFu);
+        const float rk = b[j] * vd;
+        float vk = rk * rk;
+        mf[k + j] = a[j] * md;
+        rf[k + j] = element(k + j, mf[k + j], vk);
+        mtop = __builtin_fmaxf(mtop, __builtin_fabsf(mf[k + j]));
+        rtop = __builtin_fmaxf(rtop, rf[k + j]);
       }
     }
-    mtop = group_umax<kLanes>(mtop);
-    rtop = group_umax<kLanes>(rtop);
-    ms = (uint32_t)max((int)(mtop >> 23) - 7, 1);
-    vs = (uint32_t)max((int)(rtop >> 23) - 7, 1);
-    const int me = 7 - (int)ms, ve = 127 - (int)vs;  // 2^me: to e4m3's place in fp32; 2^ve: to units
-    const uint32_t lo0 = (uint32_t)index, hi0 = (uint32_t)(index >> 32);
-    const uint32_t hk0 = gate.k1 + hi0 * 0x2C1B3C6Du, hk1 = hk0 + 0x2C1B3C6Du;
-    m.zero();
-    v.zero();
+    ms = scale_byte(group_umax<kLanes>(__float_as_uint(mtop)));
+    vs = scale_byte(group_umax<kLanes>(__float_as_uint(rtop)));
+    done();  // the weights are final: stored before the codes are drawn
+    const uint32_t hk = gate.k1 + (uint32_t)(index >> 32) * 0x2C1B3C6Du;
+    // `wraps` is uniform: whether the low word of the element counter wraps inside the item
+    if (wraps) codes<true>(mf, rf, (uint32_t)index, hk, gate.k0);
+    else codes<false>(mf, rf, (uint32_t)index, hk, gate.k0);
+  }
+  // The codes of the E new m and sqrt(v) with the scale bytes ms and vs.
+  template <bool WRAPS>
+  __device__ __forceinline__ void codes(const float (&mf)[E], const float (&rf)[E], uint32_t lo0, uint32_t hk,
+                                        uint32_t k0) {
+    const float mu = __uint_as_float((254u - ms) << 23), ru = __uint_as_float((254u - vs) << 23);  // 1 / 2^(s-127)
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const uint32_t lo = lo0 + k;
-      const uint32_t h = hash(lo, lo < lo0 ? hk1 : hk0, gate.k0);
-      const float y = __builtin_amdgcn_ldexpf(__builtin_fabsf(mf[k]), me);
-      uint32_t cm = (__float_as_uint(y) + ((h & 0xFFFFu) << 4) + 8u) >> 20;
-      cm = min(cm, 0x7Fu) | ((__float_as_uint(mf[k]) >> 24) & 0x80u);
-      const float t = __builtin_amdgcn_ldexpf(rf[k], ve);
-      uint32_t cr = __float_as_uint(__builtin_amdgcn_ldexpf(t, -120)) >> 20;
-      const float lo_r = __builtin_amdgcn_ldexpf(__uint_as_float(cr << 20), 120);
-      const float hi_r = __builtin_amdgcn_ldexpf(__uint_as_float((cr + 1u) << 20), 120);
-      const float u = __builtin_fmaf((float)(h >> 16), 0x1p-16f, 0x1p-17f);
-      {
+    for (int w = 0; w < E / 4; ++w) {
+      uint32_t h[4], cm = 0, cv = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * w + i;
+        const uint32_t lo = lo0 + k;
+        h[i] = hash(lo, (WRAPS && lo < lo0) ? hk + 0x2C1B3C6Du : hk, k0);
+        const float t = rf[k] * ru;
+        uint32_t c = __float_as_uint(__builtin_amdgcn_ldexpf(t, -120)) >> 20;
+        const f32x2 r = __builtin_amdgcn_cvt_pk_f32_fp8((int)(c * 257u + 256u), false);  // codes c, c + 1
+        const float u = __builtin_fmaf((float)(h[i] >> 16), 0x1p-16f, 0x1p-17f);
+        {
 #pragma clang fp contract(off)
-        const float lo_v = lo_r * lo_r;  // 4-bit numbers: their squares and u times the difference are exact
-        cr += u * (hi_r * hi_r - lo_v) < t * t - lo_v ? 1u : 0u;
+          // 4-bit numbers: their squares, the difference and u times it are exact
+          const float lo_v = r.x * r.x;
+          const float gap = u * __builtin_fmaf(r.y, r.y, -lo_v);
+          c += gap < t * t - lo_v ? 1u : 0u;
+        }
+        c = umed3(c, min(__float_as_uint(rf[k]), 1u), 0x7Fu);  // c in 1 .. 0x7F, or 0 for a zero
+        cv |= c << (8 * i);
       }
-      cr = min(max(cr, (live >> k) & 1u), 0x7Fu);
-      m.w[k / 4] |= cm << (8 * (k & 3));
-      v.w[k / 4] |= cr << (8 * (k & 3));
+      // m: the hardware's stochastic rounding adds the seed below the kept
+      // bits and cuts; here 16 random bits and a half of the next
+      cm = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(mf[4 * w] * mu, (h[0] << 16) | 0x8000u, (int)cm, 0);
+      cm = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(mf[4 * w + 1] * mu, (h[1] << 16) | 0x8000u, (int)cm, 1);
+      cm = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(mf[4 * w + 2] * mu, (h[2] << 16) | 0x8000u, (int)cm, 2);
+      cm = (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(mf[4 * w + 3] * mu, (h[3] << 16) | 0x8000u, (int)cm, 3);
+      m.w[w] = cm;
+      v.w[w] = cv;
     }
   }
-  __device__ __forceinline__ void store(const AdamwDesc& d, uint64_t at, int n) const {
-    m.store(d.exp_avg, at, n);
-    v.store(d.exp_avg_sq, at, n);
-    if (n > 0 && at % kStateBlock == 0) {
+  static __device__ __forceinline__ uint32_t umed3(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("v_med3_u32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    return (uint32_t)max((int)(top >> 23) - 7, 1);
+  }
+  __device__ __forceinline__ void store(const AdamwStreams& d, uint32_t at, int lo, int hi) const {
+    m.store(d.exp_avg, at, lo, hi);
+    v.store(d.exp_avg_sq, at, lo, hi);
+    if (hi > 0 && at % kStateBlock == 0) {
       ((SDC_GLOBAL uint8_t*)d.exp_avg_scale)[at / kStateBlock] = (uint8_t)ms;
       ((SDC_GLOBAL uint8_t*)d.exp_avg_sq_scale)[at / kStateBlock] = (uint8_t)vs;
     }
@@ -455,6 +516,7 @@ struct AdamwCfg {
   static constexpr int kGradBytes = GRAD == 0 ? 4 : 2;
   static constexpr bool kMaster = PARAM == 2;
   static constexpr bool kRows = ROWS;
+  static constexpr bool kState8 = STATE == 1;
   static constexpr bool kExact = STATE == 1;
   // Elements per lane and vector: 16 bytes of the widest stream.
   static constexpr int E = (STATE == 0 || PARAM != 1 || GRAD == 0) ? 4 : 8;
@@ -466,69 +528,103 @@ struct AdamwCfg {
 template <class Cfg, uint32_t LANES>
 __device__ __forceinline__ void adamw_item(const AdamwArgs& a, const AdamwItem& it, uint32_t l) {
   constexpr int E = Cfg::E, U = Cfg::U;
-  const AdamwDesc& d = a.desc[it.tensor];
-  const AdamwGate gate = *a.gate;
-  const AdamwCoef coef = a.coef[d.group];
-  const bool phalf = d.param_dtype == SDC_F16, ghalf = d.grad_dtype == SDC_F16;
-  const bool skip = gate.skip != 0 || d.grad == nullptr;
+  const AdamwDesc desc = load_const(a.desc + it.tensor);
+  const AdamwGate gate = load_const(a.gate);
+  const AdamwCoef coef = load_const(a.coef + desc.group);
+  // fp32 states: vectors are counted from the 16-byte boundary at or below the
+  // item's first element of exp_avg (a tensor's later items start on one), so
+  // that lists packed at odd offsets stream aligned: the other fp32 streams
+  // usually share the offset.
+  const uint32_t shift =
+      Cfg::kState8 ? 0u : ((uint32_t)((uintptr_t)desc.exp_avg >> 2) + (uint32_t)it.start) & 3u;
+  const uint64_t from = it.start - shift;
+  AdamwStreams d;
+  d.param = (unsigned char*)desc.param + from * Cfg::kParamBytes;
+  d.grad = (const unsigned char*)desc.grad + from * Cfg::kGradBytes;
+  d.exp_avg = (unsigned char*)desc.exp_avg + from * (Cfg::kState8 ? 1 : 4);
+  d.exp_avg_sq = (unsigned char*)desc.exp_avg_sq + from * (Cfg::kState8 ? 1 : 4);
+  d.master = (unsigned char*)desc.master + from * 4;
+  d.exp_avg_scale = desc.exp_avg_scale + from / kStateBlock;
+  d.exp_avg_sq_scale = desc.exp_avg_sq_scale + from / kStateBlock;
+  const uint64_t first = desc.first + it.start;
+  const bool phalf = desc.param_dtype == SDC_F16, ghalf = desc.grad_dtype == SDC_F16;
+  const bool skip = gate.skip != 0 || desc.grad == nullptr;
+  const bool wraps = (uint32_t)first + it.len < it.len;
   const uint32_t m2 = phalf ? 0x7C007C00u : 0x7F807F80u, k2 = phalf ? 0x04000400u : 0x00800080u;
   if (skip && !Cfg::kRows) return;
   RowAcc<E, Cfg::kParamBytes> acc;
-  uint32_t T = 0;
-  // One round of U vectors per lane from vector v0.  FULL: every lane's
-  // vectors are whole, so all loads are issued with no branch between them.
-  const auto round = [&](uint32_t v0, auto full) {
-    constexpr bool FULL = decltype(full)::value;
-    const auto left = [&](uint32_t j) { return FULL ? E : (int)it.len - (int)j; };
-    if (skip) {  // the weights stay: their row alone
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t j = (v0 + u * LANES + l) * E;
-        Vec<E, Cfg::kParamBytes> p;
-        p.load(d.param, it.start + j, left(j));
-        acc.add(p, m2, k2);
-      }
-      return;
-    }
+  // A round: U vectors per lane from vector v0.  FULL: every lane's vectors
+  // are whole, so all loads are issued with no branch between them.
+  struct Round {
     Vec<E, Cfg::kParamBytes> p[U];
     Vec<E, Cfg::kGradBytes> g[U];
     Vec<E, 4> mw[U];
     typename Cfg::State st[U];
+  };
+  constexpr uint32_t kRound = LANES * U;
+  const uint32_t end = it.len + shift, rounds = (end + kRound * E - 1) / (kRound * E);
+  const auto lo = [&](uint32_t j, auto full) { return decltype(full)::value ? 0 : (int)shift - (int)j; };
+  const auto hi = [&](uint32_t j, auto full) { return decltype(full)::value ? E : (int)end - (int)j; };
+  const auto load = [&](Round& r, uint32_t v0, auto full) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t j = (v0 + u * LANES + l) * E;
-      g[u].load(d.grad, it.start + j, left(j));
-      if constexpr (Cfg::kMaster) mw[u].load(d.master, it.start + j, left(j));
-      else p[u].load(d.param, it.start + j, left(j));
-      st[u].load(d, it.start + j, left(j));
+      r.g[u].load(d.grad, j, lo(j, full), hi(j, full));
+      if constexpr (Cfg::kMaster) r.mw[u].load(d.master, j, lo(j, full), hi(j, full));
+      else r.p[u].load(d.param, j, lo(j, full), hi(j, full));
+      r.st[u].load(d, j, lo(j, full), hi(j, full));
     }
+  };
+  const auto step = [&](Round& r, uint32_t v0, auto full) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t j = (v0 + u * LANES + l) * E;
       float gf[E], pf[E];
-      to_floats(g[u], ghalf, gf);
-      if constexpr (Cfg::kMaster) to_floats(mw[u], false, pf);
-      else to_floats(p[u], phalf, pf);
-      st[u].update(
-          [&](int k, float& m, float& v) { return adamw_element<Cfg::kExact>(coef, gf[k] * gate.scale, m, v, pf[k]); },
-          d.first + it.start + j, gate);
-      if constexpr (Cfg::kMaster) {
-        from_floats(pf, false, mw[u]);
-        mw[u].store(d.master, it.start + j, left(j));
-      }
-      from_floats(pf, phalf, p[u]);
-      if (Cfg::kRows && !FULL) p[u].cut(left(j));
-      p[u].store(d.param, it.start + j, left(j));
-      st[u].store(d, it.start + j, left(j));
-      if constexpr (Cfg::kRows) acc.add(p[u], m2, k2);
+      to_floats(r.g[u], ghalf, gf);
+      if constexpr (Cfg::kMaster) to_floats(r.mw[u], false, pf);
+      else to_floats(r.p[u], phalf, pf);
+      r.st[u].update(
+          [&](int k, float& m, float& v) {
+            return adamw_element<Cfg::kExact>(coef, gf[k] * gate.scale, m, v, pf[k]);
+          },
+          [&]() {
+            if constexpr (Cfg::kMaster) {
+              from_floats(pf, false, r.mw[u]);
+              r.mw[u].store(d.master, j, lo(j, full), hi(j, full));
+            }
+            from_floats(pf, phalf, r.p[u]);
+            if (Cfg::kRows && !decltype(full)::value) r.p[u].cut(lo(j, full), hi(j, full));
+            r.p[u].store(d.param, j, lo(j, full), hi(j, full));
+            if constexpr (Cfg::kRows) acc.add(r.p[u], m2, k2);
+          },
+          first - shift + j, gate, wraps);
+      r.st[u].store(d, j, lo(j, full), hi(j, full));
     }
   };
-  for (uint32_t v0 = 0; v0 * E < it.len; v0 += LANES * U, T += U) {
-    if ((v0 + LANES * U) * E <= it.len) round(v0, std::true_type());
-    else round(v0, std::false_type());
+  const std::true_type whole;
+  const std::false_type part;
+  const uint32_t T = rounds * U;
+  if (skip) {  // the weights stay: their row alone
+    for (uint32_t i = 0; i < T; ++i) {
+      const uint32_t j = (i * LANES + l) * E;
+      Vec<E, Cfg::kParamBytes> p;
+      p.load(d.param, j, lo(j, part), hi(j, part));
+      acc.add(p, m2, k2);
+    }
+  } else {
+    for (uint32_t i = 0; i < rounds; ++i) {
+      Round r;
+      if ((i > 0 || shift == 0) && (i + 1) * kRound * E <= end) {
+        load(r, i * kRound, whole);
+        step(r, i * kRound, whole);
+      } else {
+        load(r, i * kRound, part);
+        step(r, i * kRound, part);
+      }
+    }
   }
   if constexpr (Cfg::kRows) {
-    Lane ln = acc.lane(l, LANES, T);
+    Lane ln = acc.lane(l, LANES, T, shift);
     if constexpr (LANES == 64) wave_reduce(ln);
     else block_reduce(ln);
     if (l != 0) return;
@@ -540,12 +636,12 @@ __device__ __forceinline__ void adamw_item(const AdamwArgs& a, const AdamwItem& 
 template <class Cfg>
 __global__ void __launch_bounds__(kBlock) adamw_kernel(const AdamwArgs a) {
   if (blockIdx.x < a.n_block) {
-    adamw_item<Cfg, kBlock>(a, a.items[blockIdx.x], threadIdx.x);
+    adamw_item<Cfg, kBlock>(a, load_const(a.items + blockIdx.x), threadIdx.x);
     return;
   }
   const uint32_t w =
       __builtin_amdgcn_readfirstlane((blockIdx.x - a.n_block) * kWaves + (threadIdx.x >> 6));
-  if (w < a.n_wave) adamw_item<Cfg, 64>(a, a.items[a.n_block + w], threadIdx.x & 63u);
+  if (w < a.n_wave) adamw_item<Cfg, 64>(a, load_const(a.items + (a.n_block + w)), threadIdx.x & 63u);
 }
 
 template <uint32_t PARAM, uint32_t GRAD, uint32_t STATE>
