@@ -520,6 +520,67 @@ int32_t sdc_adamw_step(void* d_plan, const sdc_adamw_info* h_info, const sdc_ada
                        const uint32_t* d_flag, double max_norm, double grad_scale,
                        sdc_row* d_rows, sdc_stream_t stream);
 
+/* ---- the loss of a linear head ----------------------------------------------
+ * [BLOG] "Check 2" compares a replay's loss bits and gradient fingerprints with
+ * the original's; [AEGIS] item 4 compares a recomputed result with the
+ * original's fingerprint.  The cross entropy of a linear head over a large
+ * vocabulary is where both meet: its gradient recomputes the logits, which are
+ * never kept in memory, so their fingerprint is taken where they are computed.
+ * Results are bit-reproducible on one kind of device. */
+
+/* A linear head and the rows it is applied to.
+ *   x       n rows of d elements of dtype (SDC_BF16 or SDC_F16), x_stride
+ *           elements apart.          w   vocab rows likewise, w_stride apart.
+ *   target  n indices; one outside [0, vocab) (for example -100) marks a row
+ *           without a target: its loss is 0 and it gives no gradient, whatever
+ *           x holds there.
+ *   flags   0. */
+typedef struct {
+  const void* x;
+  const void* w;
+  const int64_t* target;
+  uint64_t n, d, vocab;
+  uint64_t x_stride, w_stride;
+  uint32_t dtype;
+  uint32_t flags;
+} sdc_head;
+
+/* Device workspace bytes of sdc_cross_entropy (h_bytes) and
+ * sdc_cross_entropy_grad (h_grad_bytes); either may be NULL.  The gradient's
+ * holds one piece of the vocabulary (about 512 MiB, or 4096 rows' worth where
+ * that is more) and fp32 sums of dx.  Host only.  Errors: SDC_ERR_INVALID
+ * (NULL x, w or target, d or vocab 0, a stride below d, flags), SDC_ERR_DTYPE,
+ * SDC_ERR_ALIGN (an element, or target, not aligned), SDC_ERR_RANGE (2^24
+ * rows of x or w, d 2^20, a stride of 2^40). */
+int32_t sdc_cross_entropy_ws_bytes(const sdc_head* h_head, uint64_t* h_bytes, uint64_t* h_grad_bytes);
+
+/* z = x w^T in fp32; per row n
+ *   d_lse[n]   log sum_v exp z_nv
+ *   d_loss[n]  d_lse[n] - z_n,target (0 without a target)
+ *   *d_total   the losses' sum (added in double in a fixed order, rounded once)
+ *   *d_count   rows with a target (NULL allowed)
+ *   d_row      NULL, or (16-byte aligned) the fingerprint row of the n x vocab
+ *              fp32 logits, row-major, as a scan of them in memory would give it.
+ * d_ws: 16-byte aligned, not reused before the call's work has completed.
+ * ASYNCHRONOUS on stream.  Errors as sdc_cross_entropy_ws_bytes, and
+ * SDC_ERR_WORKSPACE, SDC_ERR_HIP. */
+int32_t sdc_cross_entropy(const sdc_head* h_head, void* d_ws, uint64_t ws_bytes, float* d_loss,
+                          float* d_lse, float* d_total, uint64_t* d_count, sdc_row* d_row,
+                          sdc_stream_t stream);
+
+/* Gradient of *d_total times *d_grad (one float): with dz = (exp(z - lse) -
+ * onehot) * *d_grad, zero in rows without a target,
+ *   d_dx = dz w  (n x d, contiguous)      d_dw = dz^T x  (vocab x d, contiguous)
+ * both of the head's dtype, summed in fp32 from dz rounded to that type's
+ * precision.  d_lse: the forward pass'.  d_row: as there, of the recomputed
+ * logits; with d_ref (the forward pass' row) a difference under col_mask adds 1
+ * to *d_mismatch (required then; the caller clears it).
+ * ASYNCHRONOUS on stream.  Errors as sdc_cross_entropy. */
+int32_t sdc_cross_entropy_grad(const sdc_head* h_head, const float* d_lse, const float* d_grad,
+                               void* d_ws, uint64_t ws_bytes, void* d_dx, void* d_dw,
+                               const sdc_row* d_ref, uint32_t col_mask, sdc_row* d_row,
+                               uint32_t* d_mismatch, sdc_stream_t stream);
+
 /* ---- measurement ----------------------------------------------------------- */
 
 /* Streaming-read reference (no passage of the pages defines it: it measures

@@ -27,6 +27,7 @@ __all__ = [
     "sdc_fingerprint_tensor_noalloc",
     "sdc_read_sum_ws_bytes", "sdc_read_sum",
     "AdamwPlan", "sdc_adamw_plan_build", "sdc_adamw_control", "sdc_adamw_step",
+    "sdc_cross_entropy_ws_bytes", "sdc_cross_entropy", "sdc_cross_entropy_grad",
 ]
 
 # The in-tree build; SDC_LIB_PATH may name another build of the same sources
@@ -102,6 +103,9 @@ def _load():
         "sdc_confirm_verdict": [P, P, P, P, U64, P, U64, P, P],
         "sdc_read_sum_ws_bytes": [U64, P],
         "sdc_read_sum": [P, U64, P, U64, P, P],
+        "sdc_cross_entropy_ws_bytes": [P, P, P],
+        "sdc_cross_entropy": [P, P, U64, P, P, P, P, P, P],
+        "sdc_cross_entropy_grad": [P, P, P, P, U64, P, P, P, U32, P, P, P],
         "sdc_adamw_plan_bytes": [P, U64, U32, P],
         "sdc_adamw_plan_build": [P, U64, U32, P, U64, P, P],
         "sdc_adamw_step": [P, P, P, P, P, P, F64, F64, P, P],
@@ -855,3 +859,131 @@ def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0
             max_norm, grad_scale, None if rows is None else rows.data_ptr(), _stream_handle(stream, dev)),
             "sdc_adamw_step")
     return rows
+
+
+# ---- the loss of a linear head -----------------------------------------------------
+class _Head(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("target", ctypes.c_void_p),
+                ("n", ctypes.c_uint64), ("d", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("x_stride", ctypes.c_uint64), ("w_stride", ctypes.c_uint64),
+                ("dtype", ctypes.c_uint32), ("flags", ctypes.c_uint32)]
+
+
+def _head_rows(t, name):
+    """A 2-D tensor with contiguous rows as the library takes it (a copy where
+    the rows are not)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
+    if t.get_device() < 0:
+        raise ValueError(f"{name} is not on a GPU")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        t = t.contiguous()
+    return t
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _head(x, w, target):
+    """(sdc_head, device, tensors it points into)"""
+    x, w = _head_rows(x, "x"), _head_rows(w, "w")
+    dev = _cuda_device(x.get_device())
+    if w.dtype != x.dtype or w.shape[1] != x.shape[1]:
+        raise ValueError(f"w must be {x.dtype} with rows of {x.shape[1]}, is {w.dtype} {tuple(w.shape)}")
+    if not _on_device(w, dev):
+        raise ValueError(f"w must be on {dev}, not {w.device}")
+    _arg(target, "target", torch.int64, x.shape[0], dev)
+    if target.numel() != x.shape[0]:
+        raise ValueError(f"target has {target.numel()} entries for {x.shape[0]} rows")
+    return (_Head(x.data_ptr(), w.data_ptr(), target.data_ptr(), x.shape[0], x.shape[1], w.shape[0],
+                  _row_stride(x), _row_stride(w), _TORCH_DTYPE[x.dtype], 0), dev, [x, w])
+
+
+def sdc_cross_entropy_ws_bytes(x, w, target):
+    """(forward, gradient) workspace bytes of the cross entropy of this head."""
+    h, _, _ = _head(x, w, target)
+    f, g = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(_lib.sdc_cross_entropy_ws_bytes(ctypes.byref(h), ctypes.byref(f), ctypes.byref(g)),
+           "sdc_cross_entropy_ws_bytes")
+    return f.value, g.value
+
+
+def _head_ws(ws, h, dev, grad):
+    need = ctypes.c_uint64(0)
+    args = (None, ctypes.byref(need)) if grad else (ctypes.byref(need), None)
+    _check(_lib.sdc_cross_entropy_ws_bytes(ctypes.byref(h), *args), "sdc_cross_entropy_ws_bytes")
+    if ws is None:
+        return torch.empty(need.value, dtype=torch.uint8, device=dev), True
+    return _arg(ws, "ws", torch.uint8, need.value, dev), False
+
+
+def sdc_cross_entropy(x, w, target, count=None, row=None, ws=None, stream=None):
+    """(loss [n], lse [n], total [1]), fp32: the softmax cross entropy of the
+    logits x w^T, which are not kept (asynchronous; see include/sdc.h).
+
+    x: [n, d], w: [vocab, d], bfloat16 or float16, rows contiguous (any row
+    stride).  target: int64 [n]; an index outside [0, vocab) marks a row without
+    a target.  count: an int64 [1] tensor that receives the rows with one.  row:
+    an int64 [1, 4] tensor that receives the fp32 logits' fingerprint row.  ws: a
+    uint8 workspace (sdc_cross_entropy_ws_bytes), else one is allocated."""
+    h, dev, keep = _head(x, w, target)
+    n = x.shape[0]
+    loss = torch.empty(n, dtype=torch.float32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    total = torch.empty(1, dtype=torch.float32, device=dev)
+    if count is not None:
+        _arg(count, "count", torch.int64, 1, dev)
+    if row is not None:
+        _arg(row, "row", torch.int64, 4, dev)
+    ws, made_ws = _head_ws(ws, h, dev, grad=False)
+    made = [loss, lse, total] + ([ws] if made_ws else []) + [t for t in keep if t is not x and t is not w]
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_cross_entropy(ctypes.byref(h), ws.data_ptr(), ws.numel(), loss.data_ptr(),
+                                      lse.data_ptr(), total.data_ptr(),
+                                      None if count is None else count.data_ptr(),
+                                      None if row is None else row.data_ptr(), s), "sdc_cross_entropy")
+    return loss, lse, total
+
+
+def sdc_cross_entropy_grad(x, w, target, lse, grad, dx=None, dw=None, row=None, ref=None, mismatch=None,
+                           col_mask=COL_ALL, ws=None, stream=None):
+    """(dx, dw): the gradient of the total loss times `grad` (an fp32 [1]
+    tensor), from the logits computed again (asynchronous; see include/sdc.h).
+
+    lse: the forward pass'.  dx, dw: contiguous outputs of x's and w's shape and
+    dtype (allocated by default).  row: receives the recomputed logits'
+    fingerprint row.  ref, mismatch: the forward pass' row and an int32 [1]
+    counter that a difference under col_mask adds 1 to."""
+    h, dev, keep = _head(x, w, target)
+    n, d, vocab = x.shape[0], x.shape[1], w.shape[0]
+    _arg(lse, "lse", torch.float32, n, dev)
+    _arg(grad, "grad", torch.float32, 1, dev)
+    made = [t for t in keep if t is not x and t is not w]
+    if dx is None:
+        dx = torch.empty((n, d), dtype=x.dtype, device=dev)
+        made.append(dx)
+    _arg(dx, "dx", x.dtype, n * d, dev)
+    if dw is None:
+        dw = torch.empty((vocab, d), dtype=x.dtype, device=dev)
+        made.append(dw)
+    _arg(dw, "dw", x.dtype, vocab * d, dev)
+    if ref is not None and row is None:
+        row = torch.empty((1, 4), dtype=torch.int64, device=dev)
+        made.append(row)
+    if row is not None:
+        _arg(row, "row", torch.int64, 4, dev)
+    ref_p, mis_p = _ref_args(ref, mismatch, dev)
+    ws, made_ws = _head_ws(ws, h, dev, grad=True)
+    if made_ws:
+        made.append(ws)
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_cross_entropy_grad(ctypes.byref(h), lse.data_ptr(), grad.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), dx.data_ptr(), dw.data_ptr(), ref_p, col_mask,
+                                           None if row is None else row.data_ptr(), mis_p, s),
+               "sdc_cross_entropy_grad")
+    return dx, dw

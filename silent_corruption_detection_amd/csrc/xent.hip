@@ -1,0 +1,783 @@
+// xent.hip -- softmax cross entropy of a linear head over a large vocabulary,
+// and its gradient, without keeping the logits, for gfx950.
+//
+//   z = x W^T   lse_n = log sum_v exp z_nv   loss_n = lse_n - z_n,target(n)
+//   dz = (exp(z - lse) - onehot) * grad      dx = dz W      dW = dz^T x
+//
+// These are the two ends of a replayed step (AWS Machine Learning Blog,
+// "Detecting and recovering from silent data corruption on Amazon SageMaker
+// HyperPod", section "Check 2": a replay's row starts with the loss bits), and
+// the gradient recomputes the logits, which is the case of AEGIS' recompute
+// check (review page, section "core method", item 4) whose original is never
+// in memory: both passes can fingerprint the logits while they are in
+// registers.
+//
+// Forward: one launch of 256 x 256 logit tiles, each leaving its columns'
+// running maximum and sum of exponentials, one that merges a row's tiles and
+// takes the target's logit, one for the total.  The tiles are computed as
+// z^T (vocabulary down, tokens across), which puts 32 logits of one token
+// into each lane: a token's maximum and sum need two shuffles.
+// Gradient: the vocabulary in pieces; per piece the logit tiles again, whose
+// epilogue writes dz (16-bit, once by token and once by vocabulary row), then
+// two matrix products.  dx is summed over pieces and splits in fp32 in a
+// fixed order.  Bound by the matrix cores: 2 N V d operations forward, 6 N V d
+// for the gradient.
+#include <algorithm>
+
+#include "fingerprint_device.h"
+#include "gemm_device.h"
+
+namespace sdc {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr uint32_t kStageRow = kTile + 8;  // 16-bit elements of a staged row, padded off the banks
+constexpr uint32_t kStageLds = kTile * kStageRow * 2;
+static_assert(kStageLds >= kGemmLds && kStageLds <= 160u * 1024u, "the staging area holds the buffers");
+
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+
+__device__ __forceinline__ bool has_target(int64_t t, uint64_t vocab) { return (uint64_t)t < vocab; }
+
+// exp(m - M) of a running maximum m <= M, also where both are the same infinity
+__device__ __forceinline__ float rescale(float m, float M) {
+  return m == M ? 1.0f : __builtin_amdgcn_exp2f((m - M) * kLog2e);
+}
+
+// ---- packing and transposing operands ------------------------------------------
+// Copies the R x C matrix src (rows `stride` bytes apart, elements at any even
+// address) to copy [R][c_pad] (zeros from column C on) and / or its transpose
+// to tr [C][r_pad] (zeros from column R on).  mask: rows whose target is
+// outside [0, vocab) are zeros in the transpose, whatever they hold.
+struct PackArgs {
+  const unsigned char* src;
+  uint64_t stride;
+  uint32_t R, C, c_pad, r_pad;
+  uint16_t *copy, *tr;
+  const int64_t* mask;
+  uint64_t vocab;
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+  constexpr uint32_t kT = 64, kRow = kT + 8;
+  __shared__ __align__(16) uint16_t tile[kT * kRow];
+  const uint32_t c0 = blockIdx.y * kT, r0 = blockIdx.x * kT, t = threadIdx.x;
+#pragma unroll
+  for (uint32_t h = 0; h < 2; ++h) {
+    const uint32_t lr = (t >> 3) + 32u * h, r = r0 + lr, c = c0 + (t & 7u) * 8u;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (r < a.R && c < a.C) {
+      const unsigned char* p = a.src + (uint64_t)r * a.stride + (uint64_t)c * 2u;
+      if (VEC) {
+        v = *reinterpret_cast<const u32x4*>(p);
+      } else {
+        uint32_t e[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k)
+          e[k] = c + k < a.C ? *reinterpret_cast<const uint16_t*>(p + 2u * k) : 0u;
+        v = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+      }
+      if (a.copy) *reinterpret_cast<u32x4*>(a.copy + (uint64_t)r * a.c_pad + c) = v;
+      if (a.mask && !has_target(a.mask[r], a.vocab)) v = u32x4{0u, 0u, 0u, 0u};
+    } else if (a.copy && r < a.R && c < a.c_pad) {
+      *reinterpret_cast<u32x4*>(a.copy + (uint64_t)r * a.c_pad + c) = v;
+    }
+    *reinterpret_cast<u32x4*>(tile + lr * kRow + (t & 7u) * 8u) = v;
+  }
+  if (!a.tr) return;
+  __syncthreads();
+#pragma unroll
+  for (uint32_t h = 0; h < 2; ++h) {
+    const uint32_t lc = (t >> 3) + 32u * h, c = c0 + lc, lr = (t & 7u) * 8u;
+    if (c >= a.C || r0 + lr >= a.r_pad) continue;
+    uint32_t e[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) e[k] = tile[(lr + k) * kRow + lc];
+    *reinterpret_cast<u32x4*>(a.tr + (uint64_t)c * a.r_pad + r0 + lr) =
+        u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+  }
+}
+
+int32_t launch_pack(const PackArgs& a, hipStream_t s) {
+  const bool vec = a.C % 8 == 0 && a.stride % 16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
+  const uint32_t cols = a.copy ? a.c_pad : a.C, rows = a.tr ? a.r_pad : a.R;
+  const dim3 grid((rows + 63) / 64, (cols + 63) / 64);
+  if (vec) hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(256), 0, s, a);
+  return launch_status();
+}
+
+// ---- logit tiles ------------------------------------------------------------------
+struct LogitArgs {
+  Operand w, x;            // rows of the vocabulary (from v0 on), rows of tokens
+  uint32_t K;              // elements of a row that count
+  uint32_t v0;             // vocabulary index of w's first row
+  uint32_t nt;             // token tiles
+  uint32_t n_tiles, xcds;
+  uint64_t vocab;
+  // forward: [token][tile] maxima and sums
+  float2* part;
+  uint32_t n_vt;
+  // gradient
+  const int64_t* target;
+  const float* lse;
+  uint16_t *dz, *dzt;      // [n_pad][v_pad] and [w.rows][n_pad]
+  uint32_t n_pad, v_pad;
+  // fingerprint of the logits: one partial row per tile, or null
+  sdc_row* rows;
+};
+
+// The tile's part of the fingerprint row of the fp32 logits [N][V].
+__device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitArgs& a, uint32_t m0,
+                                         uint32_t n0, sdc_row* out) {
+  const Place at;
+  Lane ln;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = n0 + at.col(j);
+    if (n >= a.x.rows) continue;
+    uint64_t s = 0, ws = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (m0 + at.row(i) + r >= a.w.rows) continue;
+        const uint32_t x = __float_as_uint(acc[i][j][r]);
+        s += x;
+        ws += (uint64_t)(i * 16 + r) * x;
+        ln.x ^= x;
+        ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+      }
+    ln.s += s;
+    ln.w += ws + ((uint64_t)n * a.vocab + a.v0 + m0 + at.row(0) + 1u) * s;
+  }
+  wave_reduce(ln);
+  __shared__ uint64_t waves[4][8];
+  const uint32_t wave = threadIdx.x >> 6;
+  if (at.lane == 0) {
+    waves[0][wave] = ln.s;
+    waves[1][wave] = ln.w;
+    waves[2][wave] = ln.x;
+    waves[3][wave] = ln.nf;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      ln.s += waves[0][i];
+      ln.w += waves[1][i];
+      ln.x ^= waves[2][i];
+      ln.nf += waves[3][i];
+    }
+    ulonglong2* d = reinterpret_cast<ulonglong2*>(out);
+    d[0] = ulonglong2{ln.s, ln.w};
+    d[1] = ulonglong2{ln.x, ln.nf};
+  }
+}
+
+template <class T, bool ROW>
+__global__ void __launch_bounds__(kGemmBlock) logit_lse_kernel(const LogitArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
+  const uint32_t m0 = vt * kTile, n0 = (id % a.nt) * kTile;
+  f32x4 acc[8][4];
+  gemm_tile<T>(a.w, a.x, m0, n0, 0, a.K, a.K, lds, acc);
+  const Place at;
+  float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (m0 + at.row(i) + r < a.w.rows) m = __builtin_fmaxf(m, acc[i][j][r]);
+    m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+    m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+    const float c = (__builtin_isinf(m) ? 0.0f : m) * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (m0 + at.row(i) + r < a.w.rows)
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (at.lane < 16) half[at.wm * kTile + at.col(j)] = float2{m, s};
+  }
+  __syncthreads();
+  if (threadIdx.x < kTile && n0 + threadIdx.x < a.x.rows) {
+    const float2 p = half[threadIdx.x], q = half[kTile + threadIdx.x];
+    const float M = __builtin_fmaxf(p.x, q.x);
+    a.part[(uint64_t)(n0 + threadIdx.x) * a.n_vt + vt] =
+        float2{M, p.y * rescale(p.x, M) + q.y * rescale(q.x, M)};
+  }
+  if constexpr (ROW) tile_row(acc, a, m0, n0, a.rows + id);
+}
+
+// dz of the tile, in 16 bits (rounded to nearest: off by half a step of its
+// own size, which the products average out), 0 for rows without a target and
+// in the padding.
+template <class T, bool ROW>
+__global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
+  const uint32_t m0 = (id / a.nt) * kTile, n0 = (id % a.nt) * kTile;
+  f32x4 acc[8][4];
+  gemm_tile<T>(a.w, a.x, m0, n0, 0, a.K, a.K, lds, acc);
+  const Place at;
+  if constexpr (ROW) tile_row(acc, a, m0, n0, a.rows + id);
+  uint16_t* st = reinterpret_cast<uint16_t*>(lds);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = n0 + at.col(j);
+    const int64_t t = n < a.x.rows ? a.target[n] : -1;
+    const bool live = has_target(t, a.vocab);
+    const float c = live ? a.lse[n] * kLog2e : 0.0f;
+    // the target's row among those of acc[0][j][0] on, or far off
+    const uint64_t hit = live ? (uint64_t)t - (a.v0 + m0 + at.row(0)) : ~0ull;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
+        p = (p - (hit == (uint64_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
+        b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
+        acc[i][j][r] = __uint_as_float(b[r]);  // kept for the transposed store
+      }
+      *reinterpret_cast<uint2*>(st + at.col(j) * kStageRow + at.row(i)) =
+          uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+    }
+  }
+  __syncthreads();
+  const uint32_t t = threadIdx.x, ch = (t & 31u) * 8u;
+#pragma unroll 4
+  for (uint32_t k = t >> 5; k < kTile; k += 16) {
+    const uint32_t n = n0 + k, v = m0 + ch;
+    if (n < a.n_pad && v < a.v_pad)
+      *reinterpret_cast<u32x4*>(a.dz + (uint64_t)n * a.v_pad + v) =
+          *reinterpret_cast<const u32x4*>(st + k * kStageRow + ch);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        st[(at.row(i) + r) * kStageRow + at.col(j)] = (uint16_t)__float_as_uint(acc[i][j][r]);
+  __syncthreads();
+#pragma unroll 4
+  for (uint32_t k = t >> 5; k < kTile; k += 16) {
+    const uint32_t v = m0 + k, n = n0 + ch;
+    if (v < a.w.rows && n < a.n_pad)
+      *reinterpret_cast<u32x4*>(a.dzt + (uint64_t)v * a.n_pad + n) =
+          *reinterpret_cast<const u32x4*>(st + k * kStageRow + ch);
+  }
+}
+
+// ---- dx and dW --------------------------------------------------------------------
+struct DxArgs {
+  Operand wt, dz;      // [d][v_pad], [n_pad][v_pad]
+  uint32_t v_pad, chunk;
+  uint32_t N, d, nt, n_tiles, xcds;
+  float* part;         // [splits][N][d]
+  uint32_t first;      // 1: the first piece stores, later ones add
+};
+
+template <class T>
+__global__ void __launch_bounds__(kGemmBlock) dx_kernel(const DxArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
+  const uint32_t n0 = (id % a.nt) * kTile, rest = id / a.nt, md = (a.d + kTile - 1) / kTile;
+  const uint32_t m0 = (rest % md) * kTile, split = rest / md;
+  const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.v_pad);
+  if (k0 >= k1 && !a.first) return;
+  f32x4 acc[8][4];
+  if (k0 < k1) {
+    gemm_tile<T>(a.wt, a.dz, m0, n0, k0, k1, a.v_pad, lds, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const Place at;
+  float* out = a.part + (uint64_t)split * a.N * a.d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = n0 + at.col(j);
+    if (n >= a.N) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t m = m0 + at.row(i);
+      float* p = out + (uint64_t)n * a.d + m;
+      if (a.d % 4 == 0) {
+        if (m < a.d) {
+          f32x4* q = reinterpret_cast<f32x4*>(p);
+          *q = a.first ? acc[i][j] : *q + acc[i][j];
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (m + r < a.d) p[r] = a.first ? acc[i][j][r] : p[r] + acc[i][j][r];
+      }
+    }
+  }
+}
+
+// dx = grad * the splits' sum, in split order; 0 for rows without a target.
+template <class T>
+__global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict__ part, uint32_t splits,
+                                                        uint32_t N, uint32_t d,
+                                                        const int64_t* __restrict__ target, uint64_t vocab,
+                                                        const float* __restrict__ grad,
+                                                        uint16_t* __restrict__ dx) {
+  const uint32_t n = blockIdx.x;
+  const bool live = has_target(target[n], vocab);
+  const float g = *grad * (1.0f / T::kDzScale);
+  for (uint32_t c = blockIdx.y * 1024u + threadIdx.x; c < d && c < (blockIdx.y + 1) * 1024u; c += 256) {
+    float s = 0.0f;
+    if (live)
+      for (uint32_t k = 0; k < splits; ++k) s += part[((uint64_t)k * N + n) * d + c];
+    dx[(uint64_t)n * d + c] = (uint16_t)T::bits(live ? s * g : 0.0f);
+  }
+}
+
+struct DwArgs {
+  Operand xt, dzt;     // [d][n_pad], [piece rows][n_pad]
+  uint32_t n_pad, d, md, n_tiles, xcds;
+  const float* grad;
+  uint16_t* dw;        // of the piece's first row
+};
+
+template <class T>
+__global__ void __launch_bounds__(kGemmBlock) dw_kernel(const DwArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
+  const uint32_t m0 = (id % a.md) * kTile, n0 = (id / a.md) * kTile;
+  f32x4 acc[8][4];
+  gemm_tile<T>(a.xt, a.dzt, m0, n0, 0, a.n_pad, a.n_pad, lds, acc);
+  const Place at;
+  const float g = *a.grad * (1.0f / T::kDzScale);
+  uint16_t* st = reinterpret_cast<uint16_t*>(lds);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = T::bits(acc[i][j][r] * g);
+      *reinterpret_cast<uint2*>(st + at.col(j) * kStageRow + at.row(i)) =
+          uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+    }
+  __syncthreads();
+  const uint32_t t = threadIdx.x, ch = (t & 31u) * 8u;
+#pragma unroll 4
+  for (uint32_t k = t >> 5; k < kTile; k += 16) {
+    const uint32_t v = n0 + k, c = m0 + ch;
+    if (v >= a.dzt.rows || c >= a.d) continue;
+    uint16_t* p = a.dw + (uint64_t)v * a.d + c;
+    const uint16_t* s = st + k * kStageRow + ch;
+    if (c + 8u <= a.d) {
+      *reinterpret_cast<u32x4_at2*>(p) = *reinterpret_cast<const u32x4*>(s);
+    } else {
+      for (uint32_t e = 0; c + e < a.d; ++e) p[e] = s[e];
+    }
+  }
+}
+
+// ---- row results -------------------------------------------------------------------
+// One wave per token: merges its tiles' maxima and sums, and the target's
+// logit as a plain dot product (fp32, a fixed order).
+template <class T>
+__global__ void __launch_bounds__(kBlock) lse_kernel(const float2* __restrict__ part, uint32_t n_vt,
+                                                     uint32_t N, uint32_t d, const unsigned char* x,
+                                                     uint64_t x_stride, const unsigned char* w,
+                                                     uint64_t w_stride, const int64_t* __restrict__ target,
+                                                     uint64_t vocab, float* __restrict__ loss,
+                                                     float* __restrict__ lse) {
+  const uint32_t n = wave_item_index(), l = threadIdx.x & 63u;
+  if (n >= N) return;
+  float m = -__builtin_inff(), s = 0.0f;
+  for (uint32_t k = l; k < n_vt; k += 64) {
+    const float2 p = part[(uint64_t)n * n_vt + k];
+    const float M = __builtin_fmaxf(m, p.x);
+    s = s * rescale(m, M) + p.y * rescale(p.x, M);
+    m = M;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const float pm = __shfl_xor(m, off), ps = __shfl_xor(s, off), M = __builtin_fmaxf(m, pm);
+    s = s * rescale(m, M) + ps * rescale(pm, M);
+    m = M;
+  }
+  const float r = m + kLn2 * __builtin_amdgcn_logf(s);
+  const int64_t t = target[n];
+  float dot = 0.0f;
+  if (has_target(t, vocab)) {
+    const uint16_t* a = reinterpret_cast<const uint16_t*>(x + (uint64_t)n * x_stride);
+    const uint16_t* b = reinterpret_cast<const uint16_t*>(w + (uint64_t)t * w_stride);
+    for (uint32_t k = l; k < d; k += 64) dot = __builtin_fmaf(T::value(a[k]), T::value(b[k]), dot);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
+  }
+  if (l == 0) {
+    lse[n] = r;
+    loss[n] = has_target(t, vocab) ? r - dot : 0.0f;
+  }
+}
+
+// total = sum of the losses (in double, thread t adding t, t + 1024, ..., then
+// a fixed tree; rounded once to fp32), count = rows with a target.
+__global__ void __launch_bounds__(1024) loss_total_kernel(const float* __restrict__ loss,
+                                                          const int64_t* __restrict__ target, uint32_t N,
+                                                          uint64_t vocab, float* __restrict__ total,
+                                                          uint64_t* __restrict__ count) {
+  double s = 0.0;
+  uint32_t c = 0;
+  for (uint32_t k = threadIdx.x; k < N; k += 1024) {
+    s += loss[k];
+    c += has_target(target[k], vocab);
+  }
+  __shared__ double sw[16];
+  __shared__ uint32_t cw[16];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    s += __shfl_xor(s, off);
+    c += __shfl_xor(c, off);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    sw[threadIdx.x >> 6] = s;
+    cw[threadIdx.x >> 6] = c;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < 16; ++i) {
+    s += sw[i];
+    c += cw[i];
+  }
+  *total = (float)s;
+  if (count) *count = c;
+}
+
+// The logits' row from its tiles' rows; with ref, a difference under col_mask
+// adds 1 to *mismatch.
+__global__ void __launch_bounds__(64) logit_row_kernel(const sdc_row* __restrict__ parts, uint32_t n,
+                                                       const sdc_row* __restrict__ ref, uint32_t col_mask,
+                                                       sdc_row* __restrict__ out,
+                                                       uint32_t* __restrict__ mismatch) {
+  Lane ln = merge_slots(parts, n, threadIdx.x);
+  wave_reduce(ln);
+  if (threadIdx.x != 0) return;
+  const sdc_row r = {ln.s, ln.w, ln.x, ln.nf};
+  if (ref) {
+    const sdc_row o = *ref;
+    const bool differs = ((col_mask & SDC_COL_SUM) && r.sum != o.sum) ||
+                         ((col_mask & SDC_COL_WSUM) && r.wsum != o.wsum) ||
+                         ((col_mask & SDC_COL_XOR) && r.xorsum != o.xorsum) ||
+                         ((col_mask & SDC_COL_NONFINITE) && r.nonfinite != o.nonfinite);
+    if (differs) atomicAdd(mismatch, 1u);
+  }
+  *out = r;
+}
+
+__global__ void __launch_bounds__(256) zero16_kernel(uint16_t* p, uint64_t n) {
+  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) p[i] = 0;
+}
+
+// ---- host ----------------------------------------------------------------------------
+constexpr uint64_t kPieceBytes = 512ull << 20;  // of the gradient's workspace that grows with the piece
+
+constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+
+struct Head {
+  uint32_t N, d, V, d_pad, n_pad;
+  bool copy;             // the operands need an aligned copy
+  uint32_t piece;        // vocabulary rows of a piece
+  uint32_t pieces;
+  uint32_t splits;       // of dx's sum over a piece
+  uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
+};
+
+uint32_t tiles(uint64_t n) { return (uint32_t)((n + kTile - 1) / kTile); }
+
+int32_t check_head(const sdc_head* h) {
+  if (h == nullptr) return SDC_ERR_INVALID;
+  if (h->dtype != SDC_BF16 && h->dtype != SDC_F16) return SDC_ERR_DTYPE;
+  if (h->d == 0 || h->vocab == 0 || h->flags != 0) return SDC_ERR_INVALID;
+  if (h->n > 0 && (h->x == nullptr || h->target == nullptr)) return SDC_ERR_INVALID;
+  if (h->w == nullptr || h->x_stride < h->d || h->w_stride < h->d) return SDC_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(h->x) % 2 || reinterpret_cast<uintptr_t>(h->w) % 2 ||
+      reinterpret_cast<uintptr_t>(h->target) % 8)
+    return SDC_ERR_ALIGN;
+  if (h->n >= 1ull << 24 || h->d >= 1ull << 20 || h->vocab >= 1ull << 24 || h->x_stride >= 1ull << 40 ||
+      h->w_stride >= 1ull << 40 || (uint64_t)tiles(h->n) * (tiles(h->vocab) + 4096) >= 1ull << 31)
+    return SDC_ERR_RANGE;
+  return SDC_OK;
+}
+
+// GRAD: the sizes of the gradient's pieces; else those of the forward pass,
+// which needs pieces only for its copies.
+Head plan_head(const sdc_head* h, bool grad) {
+  Head p;
+  p.N = (uint32_t)h->n;
+  p.d = (uint32_t)h->d;
+  p.V = (uint32_t)h->vocab;
+  p.d_pad = (uint32_t)up(h->d, 8);
+  p.n_pad = (uint32_t)up(h->n, 64);
+  p.copy = h->d % 8 || h->x_stride % 8 || h->w_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16 ||
+           reinterpret_cast<uintptr_t>(h->w) % 16;
+  // A piece takes kPieceBytes of workspace, in steps of 4096 rows (16 tiles:
+  // with 16 token tiles a whole number of waves over 256 CUs).
+  uint64_t piece = up(p.V, 64);
+  const uint64_t col = (p.copy ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.d + 4ull * p.n_pad : 0);
+  if (col && col * piece > kPieceBytes)
+    piece = std::min<uint64_t>(piece, std::max<uint64_t>(kPieceBytes / col / 4096, 1) * 4096);
+  p.piece = (uint32_t)piece;
+  p.pieces = (uint32_t)((p.V + piece - 1) / piece);
+  const uint32_t dx_tiles = tiles(p.N) * tiles(p.d);
+  p.splits = std::max(1u, std::min(dx_tiles ? 256u / dx_tiles : 1u, tiles(piece)));
+  p.n_tiles = 0;
+  for (uint32_t k = 0; k < p.pieces; ++k)
+    p.n_tiles += tiles(std::min<uint64_t>(piece, p.V - k * piece)) * tiles(p.N);
+  return p;
+}
+
+struct Layout {
+  uint64_t part, rows, xc, wc, xt, wt, dz, dzt, dxp, end;
+};
+
+Layout layout_head(const Head& p, bool grad) {
+  Layout o;
+  uint64_t at = 0;
+  const auto take = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at = up(at + bytes, 256);
+    return here;
+  };
+  o.rows = take(32ull * p.n_tiles);
+  o.xc = take(p.copy ? 2ull * p.N * p.d_pad : 0);
+  o.wc = take(p.copy ? 2ull * p.piece * p.d_pad : 0);
+  o.part = o.xt = o.wt = o.dz = o.dzt = o.dxp = at;
+  if (grad) {
+    o.xt = take(2ull * p.d * p.n_pad);
+    o.wt = take(2ull * p.d * p.piece);
+    o.dz = take(2ull * p.n_pad * p.piece);
+    o.dzt = take(2ull * p.piece * p.n_pad);
+    o.dxp = take(4ull * p.splits * p.N * p.d);
+  } else {
+    o.part = take(8ull * p.N * tiles(p.V) + 8ull * p.N * p.pieces);
+  }
+  o.end = std::max<uint64_t>(at, 256);
+  return o;
+}
+
+template <class F>
+int32_t for_type(uint32_t dtype, F&& f) {
+  return dtype == SDC_BF16 ? f(Bf16()) : f(Fp16());
+}
+
+// Operands of a piece, copied where they are not aligned.
+int32_t piece_operands(const sdc_head* h, const Head& p, const Layout& o, unsigned char* ws, uint32_t v0,
+                       uint32_t rows, LogitArgs* a, hipStream_t s) {
+  const unsigned char* w = static_cast<const unsigned char*>(h->w) + 2ull * v0 * h->w_stride;
+  if (p.copy) {
+    int32_t st;
+    if (v0 == 0 &&
+        (st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, p.d_pad, 0,
+                                   reinterpret_cast<uint16_t*>(ws + o.xc), nullptr, nullptr, 0}, s)))
+      return st;
+    if ((st = launch_pack(PackArgs{w, 2 * h->w_stride, rows, p.d, p.d_pad, 0,
+                                   reinterpret_cast<uint16_t*>(ws + o.wc), nullptr, nullptr, 0}, s)))
+      return st;
+    a->x = Operand{ws + o.xc, 2ull * p.d_pad, p.N};
+    a->w = Operand{ws + o.wc, 2ull * p.d_pad, rows};
+  } else {
+    a->x = Operand{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N};
+    a->w = Operand{w, 2 * h->w_stride, rows};
+  }
+  a->K = p.copy ? p.d_pad : p.d;
+  a->v0 = v0;
+  a->nt = tiles(p.N);
+  a->n_tiles = tiles(rows) * a->nt;
+  a->vocab = p.V;
+  return SDC_OK;
+}
+
+int32_t merge_logit_row(const Layout& o, const Head& p, unsigned char* ws, const sdc_row* ref, uint32_t mask,
+                        sdc_row* row, uint32_t* mismatch, hipStream_t s) {
+  hipLaunchKernelGGL(logit_row_kernel, dim3(1), dim3(64), 0, s, reinterpret_cast<const sdc_row*>(ws + o.rows),
+                     p.n_tiles, ref, mask, row, mismatch);
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace sdc
+
+using namespace sdc;
+
+extern "C" int32_t sdc_cross_entropy_ws_bytes(const sdc_head* h, uint64_t* h_bytes, uint64_t* h_grad_bytes) {
+  int32_t st = check_head(h);
+  if (st) return st;
+  if (h_bytes) *h_bytes = layout_head(plan_head(h, false), false).end;
+  if (h_grad_bytes) *h_grad_bytes = layout_head(plan_head(h, true), true).end;
+  return SDC_OK;
+}
+
+extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_bytes, float* d_loss,
+                                     float* d_lse, float* d_total, uint64_t* d_count, sdc_row* d_row,
+                                     sdc_stream_t stream) {
+  int32_t st = check_head(h);
+  if (st) return st;
+  if (d_total == nullptr || d_ws == nullptr || (h->n > 0 && (d_loss == nullptr || d_lse == nullptr)))
+    return SDC_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(d_ws) % 16 || reinterpret_cast<uintptr_t>(d_row) % 16) return SDC_ERR_ALIGN;
+  const Head p = plan_head(h, false);
+  const Layout o = layout_head(p, false);
+  if (ws_bytes < o.end) return SDC_ERR_WORKSPACE;
+  DeviceShape dev;
+  if ((st = current_device_shape(&dev))) return st;
+  hipStream_t s = as_stream(stream);
+  unsigned char* ws = static_cast<unsigned char*>(d_ws);
+  if (p.N > 0) {
+    LogitArgs a = {};
+    a.xcds = dev.xcds;
+    a.part = reinterpret_cast<float2*>(ws + o.part);
+    sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
+    a.n_vt = 0;
+    for (uint32_t k = 0; k < p.pieces; ++k) a.n_vt += tiles(std::min(p.piece, p.V - k * p.piece));
+    for (uint32_t k = 0; k < p.pieces; ++k) {
+      const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0);
+      if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
+      a.rows = d_row ? rows : nullptr;
+      st = for_type(h->dtype, [&](auto t) {
+        typedef decltype(t) T;
+        if (d_row)
+          hipLaunchKernelGGL((logit_lse_kernel<T, true>), dim3(a.n_tiles), dim3(kGemmBlock), kGemmLds, s, a);
+        else
+          hipLaunchKernelGGL((logit_lse_kernel<T, false>), dim3(a.n_tiles), dim3(kGemmBlock), kGemmLds, s, a);
+        return launch_status();
+      });
+      if (st) return st;
+      rows += a.n_tiles;
+      a.part += tiles(n);
+    }
+    st = for_type(h->dtype, [&](auto t) {
+      typedef decltype(t) T;
+      hipLaunchKernelGGL(lse_kernel<T>, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s,
+                         reinterpret_cast<const float2*>(ws + o.part), a.n_vt, p.N, p.d,
+                         static_cast<const unsigned char*>(h->x), 2 * h->x_stride,
+                         static_cast<const unsigned char*>(h->w), 2 * h->w_stride, h->target, h->vocab, d_loss,
+                         d_lse);
+      return launch_status();
+    });
+    if (st) return st;
+  }
+  hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, s, d_loss, h->target, p.N, h->vocab, d_total,
+                     d_count);
+  if ((st = launch_status())) return st;
+  if (d_row) return merge_logit_row(o, p, ws, nullptr, 0, d_row, nullptr, s);
+  return SDC_OK;
+}
+
+extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse, const float* d_grad, void* d_ws,
+                                          uint64_t ws_bytes, void* d_dx, void* d_dw, const sdc_row* d_ref,
+                                          uint32_t col_mask, sdc_row* d_row, uint32_t* d_mismatch,
+                                          sdc_stream_t stream) {
+  int32_t st = check_head(h);
+  if (st) return st;
+  if (d_grad == nullptr || d_ws == nullptr || d_dw == nullptr ||
+      (h->n > 0 && (d_lse == nullptr || d_dx == nullptr)))
+    return SDC_ERR_INVALID;
+  if (d_ref != nullptr && (d_row == nullptr || d_mismatch == nullptr || col_mask == 0 || (col_mask & ~15u)))
+    return SDC_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(d_ws) % 16 || reinterpret_cast<uintptr_t>(d_row) % 16 ||
+      reinterpret_cast<uintptr_t>(d_ref) % 16 || reinterpret_cast<uintptr_t>(d_dx) % 2 ||
+      reinterpret_cast<uintptr_t>(d_dw) % 2 || reinterpret_cast<uintptr_t>(d_lse) % 4 ||
+      reinterpret_cast<uintptr_t>(d_grad) % 4)
+    return SDC_ERR_ALIGN;
+  const Head p = plan_head(h, true);
+  const Layout o = layout_head(p, true);
+  if (ws_bytes < o.end) return SDC_ERR_WORKSPACE;
+  DeviceShape dev;
+  if ((st = current_device_shape(&dev))) return st;
+  hipStream_t s = as_stream(stream);
+  unsigned char* ws = static_cast<unsigned char*>(d_ws);
+  if (p.N == 0) {
+    hipLaunchKernelGGL(zero16_kernel, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(d_dw),
+                       (uint64_t)p.V * p.d);
+    if ((st = launch_status())) return st;
+    return d_row ? merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s) : SDC_OK;
+  }
+  // x^T once, without the rows that have no target
+  st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, 0, p.n_pad, nullptr,
+                            reinterpret_cast<uint16_t*>(ws + o.xt), h->target, h->vocab}, s);
+  if (st) return st;
+  LogitArgs a = {};
+  a.xcds = dev.xcds;
+  a.target = h->target;
+  a.lse = d_lse;
+  a.dz = reinterpret_cast<uint16_t*>(ws + o.dz);
+  a.dzt = reinterpret_cast<uint16_t*>(ws + o.dzt);
+  a.n_pad = p.n_pad;
+  sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
+  float* dxp = reinterpret_cast<float*>(ws + o.dxp);
+  for (uint32_t k = 0; k < p.pieces; ++k) {
+    const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0), v_pad = (uint32_t)up(n, 64);
+    if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
+    st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->w) + 2ull * v0 * h->w_stride, 2 * h->w_stride, n,
+                              p.d, 0, v_pad, nullptr, reinterpret_cast<uint16_t*>(ws + o.wt), nullptr, 0}, s);
+    if (st) return st;
+    a.v_pad = v_pad;
+    a.rows = d_row ? rows : nullptr;
+    rows += a.n_tiles;
+    DxArgs x;
+    x.wt = Operand{ws + o.wt, 2ull * v_pad, p.d};
+    x.dz = Operand{ws + o.dz, 2ull * v_pad, p.n_pad};
+    x.v_pad = v_pad;
+    x.chunk = (uint32_t)up((v_pad + p.splits - 1) / p.splits, kTileK);
+    x.N = p.N;
+    x.d = p.d;
+    x.nt = tiles(p.N);
+    x.n_tiles = x.nt * tiles(p.d) * p.splits;
+    x.xcds = dev.xcds;
+    x.part = dxp;
+    x.first = k == 0;
+    DwArgs w;
+    w.xt = Operand{ws + o.xt, 2ull * p.n_pad, p.d};
+    w.dzt = Operand{ws + o.dzt, 2ull * p.n_pad, n};
+    w.n_pad = p.n_pad;
+    w.d = p.d;
+    w.md = tiles(p.d);
+    w.n_tiles = w.md * tiles(n);
+    w.xcds = dev.xcds;
+    w.grad = d_grad;
+    w.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
+    st = for_type(h->dtype, [&](auto t) {
+      typedef decltype(t) T;
+      if (d_row)
+        hipLaunchKernelGGL((logit_dz_kernel<T, true>), dim3(a.n_tiles), dim3(kGemmBlock), kStageLds, s, a);
+      else
+        hipLaunchKernelGGL((logit_dz_kernel<T, false>), dim3(a.n_tiles), dim3(kGemmBlock), kStageLds, s, a);
+      if (int32_t e = launch_status()) return e;
+      hipLaunchKernelGGL(dx_kernel<T>, dim3(x.n_tiles), dim3(kGemmBlock), kGemmLds, s, x);
+      if (int32_t e = launch_status()) return e;
+      hipLaunchKernelGGL(dw_kernel<T>, dim3(w.n_tiles), dim3(kGemmBlock), kStageLds, s, w);
+      return launch_status();
+    });
+    if (st) return st;
+  }
+  st = for_type(h->dtype, [&](auto t) {
+    typedef decltype(t) T;
+    hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 1023) / 1024), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
+                       h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));
+    return launch_status();
+  });
+  if (st) return st;
+  if (d_row) return merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s);
+  return SDC_OK;
+}
