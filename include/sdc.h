@@ -547,8 +547,8 @@ typedef struct {
 
 /* Device workspace bytes of sdc_cross_entropy (h_bytes) and
  * sdc_cross_entropy_grad (h_grad_bytes); either may be NULL.  The gradient's
- * holds one piece of the vocabulary (about 512 MiB, or 4096 rows' worth where
- * that is more) and fp32 sums of dx.  Host only.  Errors: SDC_ERR_INVALID
+ * holds dz of one piece of the vocabulary (up to 256 MiB, or 256 rows' worth
+ * where that is more), a copy of x and fp32 sums of dx.  Host only.  Errors: SDC_ERR_INVALID
  * (NULL x, w or target, d or vocab 0, a stride below d, flags), SDC_ERR_DTYPE,
  * SDC_ERR_ALIGN (an element, or target, not aligned), SDC_ERR_RANGE (2^24
  * rows of x or w, d 2^20, a stride of 2^40). */

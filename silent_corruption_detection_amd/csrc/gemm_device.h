@@ -1,16 +1,24 @@
 // gemm_device.h -- the matrix-product tile of the cross-entropy head for
-// gfx950: C[m][n] = sum_k A[m][k] B[n][k] for 16-bit A and B whose rows are
-// contiguous in k, accumulated in fp32 by MFMA.
+// gfx950: C[m][n] = sum_k A(m, k) B(n, k) for 16-bit operands whose rows are
+// contiguous either in k or, "k-major", in m (n), accumulated in fp32 by MFMA.
 //
 // A workgroup of 8 waves computes 256 x 256 of C; wave (wm, wn), wm = 0..1,
 // wn = 0..3, holds rows 128 wm .. and columns 64 wn .. of it as 8 x 4 tiles of
 // 16 x 16 (128 accumulator registers).  k advances 64 at a time through two
 // LDS buffers of 64 KiB: the next buffer is filled by direct global-to-LDS
 // loads (16 bytes a lane, no registers) while the current one is multiplied.
-// Within a 128-byte row of a buffer the eight 16-byte chunks are permuted by
-// the row's low three bits, so that the 16 rows x 16 bytes an MFMA operand
-// reads at once fall on different banks; direct loads write LDS in lane order,
-// so the permutation is made in the addresses they read.
+// Direct loads write LDS in lane order, so the permutations below, which keep
+// the lanes of one LDS read on different banks, are made in the addresses they
+// read from.
+//   rows along k: 256 rows of 128 bytes; the eight 16-byte chunks of a row are
+//     permuted by its low three bits.  An operand register group is one
+//     16-byte read per lane.
+//   k-major: 64 rows of 512 bytes; the sixteen 32-byte granules (16 columns) of
+//     row k are permuted by f(k) = k & 3 | (k >> 3 & 3) << 2, which differs
+//     over the 16 rows that one transposing read takes.  A group is two
+//     transposing 8-byte reads (each gives a lane four k of its column), which
+//     is what spares transposed copies of the weights, the inputs and dz.
+// Measured alone on random data at 4096 x 50304 x 2048: 742 us (1140 TFLOP/s).
 #pragma once
 
 #include "scan_device.h"
@@ -58,11 +66,12 @@ struct Fp16 {
   }
 };
 
-// An operand: `rows` rows of K elements, `stride` bytes apart, 16-byte aligned.
+// An operand with `rows` rows (of C's index, or, k-major, of k), `stride` bytes
+// apart, each of `cols` elements; 16-byte aligned, cols a multiple of 8.
 struct Operand {
   const unsigned char* p;
   uint64_t stride;
-  uint32_t rows;
+  uint32_t rows, cols;
 };
 
 // Where a thread's accumulators stand in the tile: element r of acc[i][j] is
@@ -76,63 +85,130 @@ struct Place {
 };
 
 #define SDC_LDS __attribute__((address_space(3)))
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Sum over k in [k0, k1) (k0 and the operands' chunks of 8 aligned; k from K on
-// reads as zero) of the tile at row m0 of A and row n0 of B.  Rows past the
-// operands' last are read as that row: their results mean nothing.
-template <class T>
+// 16 bytes per lane from src to LDS at base + 16 * lane (base uniform).  Written
+// as an instruction of its own: the compiler otherwise waits for all loads in
+// flight before every transposing read of LDS, whichever buffer it reads.  It
+// has no output register; gemm_tile waits for it with vmcnt(0).  m0 is a
+// register the compiler reserves and writes right before each use of its own.
+__device__ __forceinline__ void load_to_lds(const unsigned char* src, uint32_t base) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(base), "v"(src)
+      : "memory");
+}
+
+// One operand's side of the tile: its loads into LDS, step after step, and its
+// reads.
+template <class T, bool KMAJOR>
+struct Side {
+  const unsigned char* p[4];  // of the thread's loads of the next step
+  uint64_t step;              // bytes from one step to the next
+  uint32_t limit;             // k from here on reads as zero
+  uint32_t k_in;              // k of the thread's first load within a step
+  uint32_t off;               // of the lane's LDS reads
+
+  // at0: first row of C's index; base: LDS row (rows along k) or granule
+  // (k-major) of the wave's first group.  Rows along k past the operand's last
+  // are read as the last, columns past a k-major one's last as its last eight.
+  __device__ __forceinline__ void init(const Operand& o, uint32_t at0, uint32_t base, uint32_t k0) {
+    const uint32_t t = threadIdx.x, lane = t & 63u;
+    if constexpr (KMAJOR) {
+      limit = o.rows;
+      k_in = t >> 5;
+      step = o.stride * kTileK;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        const uint32_t k = i * 16u + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
+        const uint32_t col = at0 + ((((t & 31u) >> 1) ^ f) * 16u) + (t & 1u) * 8u;
+        p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)min(col, o.cols - 8u) * 2u;
+      }
+      const uint32_t g = lane >> 4, r = (lane >> 2) & 3u, f = r | g << 2;
+      off = (8u * g + r) * 512u + ((base ^ f) << 5) + (lane & 3u) * 8u;
+    } else {
+      limit = o.cols;
+      const uint32_t q = (t & 7u) ^ ((t >> 3) & 7u);
+      k_in = q * 8u;
+      step = kTileK * 2u;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        p[i] = o.p + (uint64_t)min(at0 + i * 64u + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
+      off = (base + (lane & 15u)) * 128u + (((lane >> 4) ^ (lane & 7u)) << 4);
+    }
+  }
+  // Loads the 32 KiB of step k into LDS at byte `dst`; called step by step.
+  __device__ __forceinline__ void fill(uint32_t k, uint32_t dst) {
+    const uint32_t base = dst + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u) * 16u;
+    if (k + kTileK <= limit) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * 8192u);
+    } else {
+      const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * 8192u);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) p[i] += step;
+  }
+  // Group i (16 rows of C's index) of k 32 s .. of the step in LDS at `src`.
+  __device__ __forceinline__ typename T::frag read(const unsigned char* src, int i, uint32_t s) const {
+    if constexpr (KMAJOR) {
+      const unsigned char* q = src + (off ^ ((uint32_t)i << 5)) + s * 16384u;
+      union {
+        s16x4 half[2];
+        typename T::frag all;
+      } u;
+      u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)q);
+      u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + 2048));
+      return u.all;
+    } else {
+      return *reinterpret_cast<const typename T::frag*>(src + (off ^ (s * 64u)) + i * 2048);
+    }
+  }
+};
+
+// Sum over k in [k0, k1) (k0 a multiple of 64) of the tile at row m0 of A's
+// index and n0 of B's.  What the tile holds past either's last means nothing.
+template <class T, bool AK, bool BK>
 __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
-                                          uint32_t k0, uint32_t k1, uint32_t K, unsigned char* lds,
-                                          f32x4 (&acc)[8][4]) {
+                                          uint32_t k0, uint32_t k1, unsigned char* lds, f32x4 (&acc)[8][4]) {
   typedef typename T::frag frag;
   const Place at;
-  const uint32_t t = threadIdx.x;
-  // loads: thread t fills chunk t & 7 of rows t / 8 + 64 i of each operand
-  const uint32_t q = (t & 7u) ^ ((t >> 3) & 7u);
-  const unsigned char *pa[4], *pb[4];
-#pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) {
-    pa[i] = A.p + (uint64_t)min(m0 + i * 64u + (t >> 3), A.rows - 1u) * A.stride + q * 16u;
-    pb[i] = B.p + (uint64_t)min(n0 + i * 64u + (t >> 3), B.rows - 1u) * B.stride + q * 16u;
-  }
-  const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
-  const auto fill = [&](uint32_t k, uint32_t buf) {
-    SDC_LDS unsigned char* base =
-        (SDC_LDS unsigned char*)(lds + buf * kBufBytes + (t & ~63u) * 16u);
-    const bool in = k + q * 8u < K;
-#pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) {
-      __builtin_amdgcn_global_load_lds(
-          (const SDC_GLOBAL uint32_t*)(in ? pa[i] + (uint64_t)k * 2u : zero),
-          (SDC_LDS uint32_t*)(base + i * 8192u), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(
-          (const SDC_GLOBAL uint32_t*)(in ? pb[i] + (uint64_t)k * 2u : zero),
-          (SDC_LDS uint32_t*)(base + 32768u + i * 8192u), 16, 0, 0);
-    }
-  };
-  // operand reads: row lane & 15 of a 16-row group, chunk 4 s + lane / 16 of its 8
-  const uint32_t off = (at.lane & 15u) * 128u + (((at.lane >> 4) ^ (at.lane & 7u)) << 4);
+  Side<T, AK> sa;
+  Side<T, BK> sb;
+  sa.init(A, m0, AK ? at.wm * 8u : at.wm * 128u, k0);
+  sb.init(B, n0, BK ? at.wn * 4u : at.wn * 64u, k0);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const auto fill = [&](uint32_t k, uint32_t buf) {
+    sa.fill(k, lds0 + buf * kBufBytes);
+    sb.fill(k, lds0 + buf * kBufBytes + kBufBytes / 2);
+  };
   fill(k0, 0);
   uint32_t buf = 0;
   for (uint32_t k = k0; k < k1; k += kTileK, buf ^= 1u) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // own loads have landed, own reads of the other buffer are done
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
     asm volatile("" ::: "memory");
     if (k + kTileK < k1) fill(k + kTileK, buf ^ 1u);
-    const unsigned char* sa = lds + buf * kBufBytes + at.wm * 16384u;
-    const unsigned char* sb = lds + buf * kBufBytes + 32768u + at.wn * 8192u;
+    const unsigned char* la = lds + buf * kBufBytes;
+    const unsigned char* lb = la + kBufBytes / 2;
 #pragma unroll
     for (uint32_t s = 0; s < 2; ++s) {
-      const uint32_t o = off ^ (s * 64u);
       frag a[8], b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const frag*>(sb + j * 2048 + o);
+      for (int j = 0; j < 4; ++j) b[j] = sb.read(lb, j, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const frag*>(sa + i * 2048 + o);
+      for (int i = 0; i < 8; ++i) a[i] = sa.read(la, i, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll

@@ -18,9 +18,8 @@
 // z^T (vocabulary down, tokens across), which puts 32 logits of one token
 // into each lane: a token's maximum and sum need two shuffles.
 // Gradient: the vocabulary in pieces; per piece the logit tiles again, whose
-// epilogue writes dz (16-bit, once by token and once by vocabulary row), then
-// two matrix products.  dx is summed over pieces and splits in fp32 in a
-// fixed order.  Bound by the matrix cores: 2 N V d operations forward, 6 N V d
+// epilogue writes dz (16-bit), then the two products of dz in one launch.  dx
+// is summed over pieces and splits in fp32 in a fixed order.  Bound by the matrix cores: 2 N V d operations forward, 6 N V d
 // for the gradient.
 #include <algorithm>
 
@@ -44,30 +43,27 @@ __device__ __forceinline__ float rescale(float m, float M) {
   return m == M ? 1.0f : __builtin_amdgcn_exp2f((m - M) * kLog2e);
 }
 
-// ---- packing and transposing operands ------------------------------------------
+// ---- copies of operands ---------------------------------------------------------
 // Copies the R x C matrix src (rows `stride` bytes apart, elements at any even
-// address) to copy [R][c_pad] (zeros from column C on) and / or its transpose
-// to tr [C][r_pad] (zeros from column R on).  mask: rows whose target is
-// outside [0, vocab) are zeros in the transpose, whatever they hold.
+// address) to dst [R][c_pad], zeros from column C on.  mask: rows whose target
+// is outside [0, vocab) become zeros, whatever they hold.
 struct PackArgs {
   const unsigned char* src;
   uint64_t stride;
-  uint32_t R, C, c_pad, r_pad;
-  uint16_t *copy, *tr;
+  uint32_t R, C, c_pad;
+  uint16_t* dst;
   const int64_t* mask;
   uint64_t vocab;
 };
 
 template <bool VEC>
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
-  constexpr uint32_t kT = 64, kRow = kT + 8;
-  __shared__ __align__(16) uint16_t tile[kT * kRow];
-  const uint32_t c0 = blockIdx.y * kT, r0 = blockIdx.x * kT, t = threadIdx.x;
-#pragma unroll
-  for (uint32_t h = 0; h < 2; ++h) {
-    const uint32_t lr = (t >> 3) + 32u * h, r = r0 + lr, c = c0 + (t & 7u) * 8u;
+  const uint32_t per = a.c_pad / 8;
+  const uint64_t n = (uint64_t)a.R * per;
+  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) {
+    const uint32_t r = (uint32_t)(i / per), c = (uint32_t)(i % per) * 8u;
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (r < a.R && c < a.C) {
+    if (!a.mask || has_target(a.mask[r], a.vocab)) {
       const unsigned char* p = a.src + (uint64_t)r * a.stride + (uint64_t)c * 2u;
       if (VEC) {
         v = *reinterpret_cast<const u32x4*>(p);
@@ -78,31 +74,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
           e[k] = c + k < a.C ? *reinterpret_cast<const uint16_t*>(p + 2u * k) : 0u;
         v = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
       }
-      if (a.copy) *reinterpret_cast<u32x4*>(a.copy + (uint64_t)r * a.c_pad + c) = v;
-      if (a.mask && !has_target(a.mask[r], a.vocab)) v = u32x4{0u, 0u, 0u, 0u};
-    } else if (a.copy && r < a.R && c < a.c_pad) {
-      *reinterpret_cast<u32x4*>(a.copy + (uint64_t)r * a.c_pad + c) = v;
     }
-    *reinterpret_cast<u32x4*>(tile + lr * kRow + (t & 7u) * 8u) = v;
-  }
-  if (!a.tr) return;
-  __syncthreads();
-#pragma unroll
-  for (uint32_t h = 0; h < 2; ++h) {
-    const uint32_t lc = (t >> 3) + 32u * h, c = c0 + lc, lr = (t & 7u) * 8u;
-    if (c >= a.C || r0 + lr >= a.r_pad) continue;
-    uint32_t e[8];
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) e[k] = tile[(lr + k) * kRow + lc];
-    *reinterpret_cast<u32x4*>(a.tr + (uint64_t)c * a.r_pad + r0 + lr) =
-        u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+    *reinterpret_cast<u32x4*>(a.dst + (uint64_t)r * a.c_pad + c) = v;
   }
 }
 
 int32_t launch_pack(const PackArgs& a, hipStream_t s) {
   const bool vec = a.C % 8 == 0 && a.stride % 16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
-  const uint32_t cols = a.copy ? a.c_pad : a.C, rows = a.tr ? a.r_pad : a.R;
-  const dim3 grid((rows + 63) / 64, (cols + 63) / 64);
+  const uint64_t n = (uint64_t)a.R * (a.c_pad / 8);
+  const dim3 grid((uint32_t)std::min<uint64_t>((n + 255) / 256, 8192));
   if (vec) hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(256), 0, s, a);
   return launch_status();
@@ -111,7 +91,7 @@ int32_t launch_pack(const PackArgs& a, hipStream_t s) {
 // ---- logit tiles ------------------------------------------------------------------
 struct LogitArgs {
   Operand w, x;            // rows of the vocabulary (from v0 on), rows of tokens
-  uint32_t K;              // elements of a row that count
+  uint32_t K;              // elements of a row
   uint32_t v0;             // vocabulary index of w's first row
   uint32_t nt;             // token tiles
   uint32_t n_tiles, xcds;
@@ -122,8 +102,8 @@ struct LogitArgs {
   // gradient
   const int64_t* target;
   const float* lse;
-  uint16_t *dz, *dzt;      // [n_pad][v_pad] and [w.rows][n_pad]
-  uint32_t n_pad, v_pad;
+  uint16_t* dz;            // [x.rows][v_pad]
+  uint32_t v_pad;
   // fingerprint of the logits: one partial row per tile, or null
   sdc_row* rows;
 };
@@ -182,7 +162,7 @@ __global__ void __launch_bounds__(kGemmBlock) logit_lse_kernel(const LogitArgs a
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
   const uint32_t m0 = vt * kTile, n0 = (id % a.nt) * kTile;
   f32x4 acc[8][4];
-  gemm_tile<T>(a.w, a.x, m0, n0, 0, a.K, a.K, lds, acc);
+  gemm_tile<T, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
   const Place at;
   float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
 #pragma unroll
@@ -225,28 +205,34 @@ __global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a)
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
   const uint32_t m0 = (id / a.nt) * kTile, n0 = (id % a.nt) * kTile;
-  f32x4 acc[8][4];
-  gemm_tile<T>(a.w, a.x, m0, n0, 0, a.K, a.K, lds, acc);
   const Place at;
+  // what the epilogue needs of its tokens, in flight during the product
+  float c[4];
+  uint32_t hit[4];  // the target among the rows from at.row(0) on; kNone: no target
+  constexpr uint32_t kNone = 0x80000000u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = min(n0 + at.col(j), a.x.rows - 1u);
+    const int64_t t = a.target[n];
+    c[j] = a.lse[n] * kLog2e;
+    // at most 2^24 rows: the difference, also a negative one, is never kNone
+    hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
+  }
+  f32x4 acc[8][4];
+  gemm_tile<T, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
   if constexpr (ROW) tile_row(acc, a, m0, n0, a.rows + id);
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t n = n0 + at.col(j);
-    const int64_t t = n < a.x.rows ? a.target[n] : -1;
-    const bool live = has_target(t, a.vocab);
-    const float c = live ? a.lse[n] * kLog2e : 0.0f;
-    // the target's row among those of acc[0][j][0] on, or far off
-    const uint64_t hit = live ? (uint64_t)t - (a.v0 + m0 + at.row(0)) : ~0ull;
+    const bool live = hit[j] != kNone;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
-        p = (p - (hit == (uint64_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
+        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c[j]));
+        p = (p - (hit[j] == (uint32_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
         b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
-        acc[i][j][r] = __uint_as_float(b[r]);  // kept for the transposed store
       }
       *reinterpret_cast<uint2*>(st + at.col(j) * kStageRow + at.row(i)) =
           uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
@@ -257,48 +243,36 @@ __global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a)
 #pragma unroll 4
   for (uint32_t k = t >> 5; k < kTile; k += 16) {
     const uint32_t n = n0 + k, v = m0 + ch;
-    if (n < a.n_pad && v < a.v_pad)
+    if (n < a.x.rows && v < a.v_pad)
       *reinterpret_cast<u32x4*>(a.dz + (uint64_t)n * a.v_pad + v) =
-          *reinterpret_cast<const u32x4*>(st + k * kStageRow + ch);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        st[(at.row(i) + r) * kStageRow + at.col(j)] = (uint16_t)__float_as_uint(acc[i][j][r]);
-  __syncthreads();
-#pragma unroll 4
-  for (uint32_t k = t >> 5; k < kTile; k += 16) {
-    const uint32_t v = m0 + k, n = n0 + ch;
-    if (v < a.w.rows && n < a.n_pad)
-      *reinterpret_cast<u32x4*>(a.dzt + (uint64_t)v * a.n_pad + n) =
           *reinterpret_cast<const u32x4*>(st + k * kStageRow + ch);
   }
 }
 
 // ---- dx and dW --------------------------------------------------------------------
-struct DxArgs {
-  Operand wt, dz;      // [d][v_pad], [n_pad][v_pad]
-  uint32_t v_pad, chunk;
-  uint32_t N, d, nt, n_tiles, xcds;
+// Both products of a piece in one launch: dx's tiles first (they are the
+// longer ones), then dW's, so that the chip fills up once.
+struct ProductArgs {
+  Operand w, dz, x;    // [piece rows][d], [N][v_pad], [N][d] with the rows without a target zero
+  uint32_t N, d, rows, xcds;
+  uint32_t nt, md;     // token tiles, tiles of d
+  uint32_t n_dx, n_dw; // tiles
+  uint32_t chunk;      // k of a split of dx
   float* part;         // [splits][N][d]
   uint32_t first;      // 1: the first piece stores, later ones add
+  const float* grad;
+  uint16_t* dw;        // of the piece's first row
 };
 
 template <class T>
-__global__ void __launch_bounds__(kGemmBlock) dx_kernel(const DxArgs a) {
-  extern __shared__ __align__(16) unsigned char lds[];
-  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
-  const uint32_t n0 = (id % a.nt) * kTile, rest = id / a.nt, md = (a.d + kTile - 1) / kTile;
-  const uint32_t m0 = (rest % md) * kTile, split = rest / md;
-  const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.v_pad);
+__device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
+  const uint32_t n0 = (id % a.nt) * kTile, rest = id / a.nt;
+  const uint32_t m0 = (rest % a.md) * kTile, split = rest / a.md;
+  const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.rows);
   if (k0 >= k1 && !a.first) return;
   f32x4 acc[8][4];
   if (k0 < k1) {
-    gemm_tile<T>(a.wt, a.dz, m0, n0, k0, k1, a.v_pad, lds, acc);
+    gemm_tile<T, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -329,40 +303,13 @@ __global__ void __launch_bounds__(kGemmBlock) dx_kernel(const DxArgs a) {
   }
 }
 
-// dx = grad * the splits' sum, in split order; 0 for rows without a target.
 template <class T>
-__global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict__ part, uint32_t splits,
-                                                        uint32_t N, uint32_t d,
-                                                        const int64_t* __restrict__ target, uint64_t vocab,
-                                                        const float* __restrict__ grad,
-                                                        uint16_t* __restrict__ dx) {
-  const uint32_t n = blockIdx.x;
-  const bool live = has_target(target[n], vocab);
-  const float g = *grad * (1.0f / T::kDzScale);
-  for (uint32_t c = blockIdx.y * 1024u + threadIdx.x; c < d && c < (blockIdx.y + 1) * 1024u; c += 256) {
-    float s = 0.0f;
-    if (live)
-      for (uint32_t k = 0; k < splits; ++k) s += part[((uint64_t)k * N + n) * d + c];
-    dx[(uint64_t)n * d + c] = (uint16_t)T::bits(live ? s * g : 0.0f);
-  }
-}
-
-struct DwArgs {
-  Operand xt, dzt;     // [d][n_pad], [piece rows][n_pad]
-  uint32_t n_pad, d, md, n_tiles, xcds;
-  const float* grad;
-  uint16_t* dw;        // of the piece's first row
-};
-
-template <class T>
-__global__ void __launch_bounds__(kGemmBlock) dw_kernel(const DwArgs a) {
-  extern __shared__ __align__(16) unsigned char lds[];
-  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
+__device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
   const uint32_t m0 = (id % a.md) * kTile, n0 = (id / a.md) * kTile;
-  f32x4 acc[8][4];
-  gemm_tile<T>(a.xt, a.dzt, m0, n0, 0, a.n_pad, a.n_pad, lds, acc);
-  const Place at;
   const float g = *a.grad * (1.0f / T::kDzScale);
+  f32x4 acc[8][4];
+  gemm_tile<T, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
+  const Place at;
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -379,7 +326,7 @@ __global__ void __launch_bounds__(kGemmBlock) dw_kernel(const DwArgs a) {
 #pragma unroll 4
   for (uint32_t k = t >> 5; k < kTile; k += 16) {
     const uint32_t v = n0 + k, c = m0 + ch;
-    if (v >= a.dzt.rows || c >= a.d) continue;
+    if (v >= a.rows || c >= a.d) continue;
     uint16_t* p = a.dw + (uint64_t)v * a.d + c;
     const uint16_t* s = st + k * kStageRow + ch;
     if (c + 8u <= a.d) {
@@ -387,6 +334,31 @@ __global__ void __launch_bounds__(kGemmBlock) dw_kernel(const DwArgs a) {
     } else {
       for (uint32_t e = 0; c + e < a.d; ++e) p[e] = s[e];
     }
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kGemmBlock) products_kernel(const ProductArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  if (blockIdx.x < a.n_dx) dx_tile<T>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
+  else dw_tile<T>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
+}
+
+// dx = grad * the splits' sum, in split order; 0 for rows without a target.
+template <class T>
+__global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict__ part, uint32_t splits,
+                                                        uint32_t N, uint32_t d,
+                                                        const int64_t* __restrict__ target, uint64_t vocab,
+                                                        const float* __restrict__ grad,
+                                                        uint16_t* __restrict__ dx) {
+  const uint32_t n = blockIdx.x;
+  const bool live = has_target(target[n], vocab);
+  const float g = *grad * (1.0f / T::kDzScale);
+  for (uint32_t c = blockIdx.y * 1024u + threadIdx.x; c < d && c < (blockIdx.y + 1) * 1024u; c += 256) {
+    float s = 0.0f;
+    if (live)
+      for (uint32_t k = 0; k < splits; ++k) s += part[((uint64_t)k * N + n) * d + c];
+    dx[(uint64_t)n * d + c] = (uint16_t)T::bits(live ? s * g : 0.0f);
   }
 }
 
@@ -490,12 +462,12 @@ __global__ void __launch_bounds__(256) zero16_kernel(uint16_t* p, uint64_t n) {
 }
 
 // ---- host ----------------------------------------------------------------------------
-constexpr uint64_t kPieceBytes = 512ull << 20;  // of the gradient's workspace that grows with the piece
+constexpr uint64_t kPieceBytes = 256ull << 20;  // of the gradient's workspace that grows with the piece
 
 constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
-  uint32_t N, d, V, d_pad, n_pad;
+  uint32_t N, d, V, d_pad;
   bool copy;             // the operands need an aligned copy
   uint32_t piece;        // vocabulary rows of a piece
   uint32_t pieces;
@@ -528,19 +500,31 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.d = (uint32_t)h->d;
   p.V = (uint32_t)h->vocab;
   p.d_pad = (uint32_t)up(h->d, 8);
-  p.n_pad = (uint32_t)up(h->n, 64);
   p.copy = h->d % 8 || h->x_stride % 8 || h->w_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16 ||
            reinterpret_cast<uintptr_t>(h->w) % 16;
-  // A piece takes kPieceBytes of workspace, in steps of 4096 rows (16 tiles:
-  // with 16 token tiles a whole number of waves over 256 CUs).
-  uint64_t piece = up(p.V, 64);
-  const uint64_t col = (p.copy ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.d + 4ull * p.n_pad : 0);
-  if (col && col * piece > kPieceBytes)
-    piece = std::min<uint64_t>(piece, std::max<uint64_t>(kPieceBytes / col / 4096, 1) * 4096);
-  p.piece = (uint32_t)piece;
-  p.pieces = (uint32_t)((p.V + piece - 1) / piece);
-  const uint32_t dx_tiles = tiles(p.N) * tiles(p.d);
-  p.splits = std::max(1u, std::min(dx_tiles ? 256u / dx_tiles : 1u, tiles(piece)));
+  // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
+  // of that on, the one that needs the fewest rounds of 256 tiles.
+  const uint32_t nt = tiles(p.N), vt = tiles(p.V);
+  const uint64_t col = (p.copy ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.N : 0);
+  uint32_t most = vt;
+  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / kTile, 1);
+  uint32_t best = most;
+  if (most < vt) {
+    uint64_t least = ~0ull;
+    for (uint32_t k = most; k >= (most + 1) / 2; --k) {
+      const auto rounds_of = [&](uint64_t rows) { return (rows * nt + 255) / 256; };
+      const uint64_t rounds = (vt / k) * rounds_of(k) + rounds_of(vt % k);
+      if (rounds < least) {
+        least = rounds;
+        best = k;
+      }
+    }
+  }
+  const uint64_t piece = (uint64_t)best * kTile;
+  p.piece = (uint32_t)std::min<uint64_t>(piece, up(p.V, 8));
+  p.pieces = (vt + best - 1) / best;
+  const uint32_t dx_tiles = nt * tiles(p.d);
+  p.splits = std::max(1u, std::min(dx_tiles ? 256u / dx_tiles : 1u, best));
   p.n_tiles = 0;
   for (uint32_t k = 0; k < p.pieces; ++k)
     p.n_tiles += tiles(std::min<uint64_t>(piece, p.V - k * piece)) * tiles(p.N);
@@ -548,7 +532,7 @@ Head plan_head(const sdc_head* h, bool grad) {
 }
 
 struct Layout {
-  uint64_t part, rows, xc, wc, xt, wt, dz, dzt, dxp, end;
+  uint64_t part, rows, xc, wc, xm, dz, dxp, end;
 };
 
 Layout layout_head(const Head& p, bool grad) {
@@ -562,15 +546,13 @@ Layout layout_head(const Head& p, bool grad) {
   o.rows = take(32ull * p.n_tiles);
   o.xc = take(p.copy ? 2ull * p.N * p.d_pad : 0);
   o.wc = take(p.copy ? 2ull * p.piece * p.d_pad : 0);
-  o.part = o.xt = o.wt = o.dz = o.dzt = o.dxp = at;
+  o.part = o.xm = o.dz = o.dxp = at;
   if (grad) {
-    o.xt = take(2ull * p.d * p.n_pad);
-    o.wt = take(2ull * p.d * p.piece);
-    o.dz = take(2ull * p.n_pad * p.piece);
-    o.dzt = take(2ull * p.piece * p.n_pad);
+    o.xm = take(2ull * p.N * p.d_pad);
+    o.dz = take(2ull * p.N * p.piece);
     o.dxp = take(4ull * p.splits * p.N * p.d);
   } else {
-    o.part = take(8ull * p.N * tiles(p.V) + 8ull * p.N * p.pieces);
+    o.part = take(8ull * p.N * tiles(p.V));
   }
   o.end = std::max<uint64_t>(at, 256);
   return o;
@@ -588,19 +570,19 @@ int32_t piece_operands(const sdc_head* h, const Head& p, const Layout& o, unsign
   if (p.copy) {
     int32_t st;
     if (v0 == 0 &&
-        (st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, p.d_pad, 0,
-                                   reinterpret_cast<uint16_t*>(ws + o.xc), nullptr, nullptr, 0}, s)))
+        (st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, p.d_pad,
+                                   reinterpret_cast<uint16_t*>(ws + o.xc), nullptr, 0}, s)))
       return st;
-    if ((st = launch_pack(PackArgs{w, 2 * h->w_stride, rows, p.d, p.d_pad, 0,
-                                   reinterpret_cast<uint16_t*>(ws + o.wc), nullptr, nullptr, 0}, s)))
+    if ((st = launch_pack(PackArgs{w, 2 * h->w_stride, rows, p.d, p.d_pad,
+                                   reinterpret_cast<uint16_t*>(ws + o.wc), nullptr, 0}, s)))
       return st;
-    a->x = Operand{ws + o.xc, 2ull * p.d_pad, p.N};
-    a->w = Operand{ws + o.wc, 2ull * p.d_pad, rows};
+    a->x = Operand{ws + o.xc, 2ull * p.d_pad, p.N, p.d_pad};
+    a->w = Operand{ws + o.wc, 2ull * p.d_pad, rows, p.d_pad};
   } else {
-    a->x = Operand{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N};
-    a->w = Operand{w, 2 * h->w_stride, rows};
+    a->x = Operand{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d};
+    a->w = Operand{w, 2 * h->w_stride, rows, p.d};
   }
-  a->K = p.copy ? p.d_pad : p.d;
+  a->K = p.d;
   a->v0 = v0;
   a->nt = tiles(p.N);
   a->n_tiles = tiles(rows) * a->nt;
@@ -648,8 +630,7 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
     a.xcds = dev.xcds;
     a.part = reinterpret_cast<float2*>(ws + o.part);
     sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
-    a.n_vt = 0;
-    for (uint32_t k = 0; k < p.pieces; ++k) a.n_vt += tiles(std::min(p.piece, p.V - k * p.piece));
+    a.n_vt = tiles(p.V);
     for (uint32_t k = 0; k < p.pieces; ++k) {
       const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0);
       if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
@@ -713,50 +694,40 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     if ((st = launch_status())) return st;
     return d_row ? merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s) : SDC_OK;
   }
-  // x^T once, without the rows that have no target
-  st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, 0, p.n_pad, nullptr,
-                            reinterpret_cast<uint16_t*>(ws + o.xt), h->target, h->vocab}, s);
+  // x without what rows that have no target hold: dz is zero there, but 0 * NaN is not
+  st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, p.d_pad,
+                            reinterpret_cast<uint16_t*>(ws + o.xm), h->target, h->vocab}, s);
   if (st) return st;
   LogitArgs a = {};
   a.xcds = dev.xcds;
   a.target = h->target;
   a.lse = d_lse;
   a.dz = reinterpret_cast<uint16_t*>(ws + o.dz);
-  a.dzt = reinterpret_cast<uint16_t*>(ws + o.dzt);
-  a.n_pad = p.n_pad;
   sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
   float* dxp = reinterpret_cast<float*>(ws + o.dxp);
   for (uint32_t k = 0; k < p.pieces; ++k) {
-    const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0), v_pad = (uint32_t)up(n, 64);
+    const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0), v_pad = (uint32_t)up(n, 8);
     if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
-    st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->w) + 2ull * v0 * h->w_stride, 2 * h->w_stride, n,
-                              p.d, 0, v_pad, nullptr, reinterpret_cast<uint16_t*>(ws + o.wt), nullptr, 0}, s);
-    if (st) return st;
     a.v_pad = v_pad;
     a.rows = d_row ? rows : nullptr;
     rows += a.n_tiles;
-    DxArgs x;
-    x.wt = Operand{ws + o.wt, 2ull * v_pad, p.d};
-    x.dz = Operand{ws + o.dz, 2ull * v_pad, p.n_pad};
-    x.v_pad = v_pad;
-    x.chunk = (uint32_t)up((v_pad + p.splits - 1) / p.splits, kTileK);
+    ProductArgs x;
+    x.w = a.w;
+    x.dz = Operand{ws + o.dz, 2ull * v_pad, p.N, v_pad};
+    x.x = Operand{ws + o.xm, 2ull * p.d_pad, p.N, p.d_pad};
     x.N = p.N;
     x.d = p.d;
-    x.nt = tiles(p.N);
-    x.n_tiles = x.nt * tiles(p.d) * p.splits;
+    x.rows = n;
     x.xcds = dev.xcds;
+    x.nt = tiles(p.N);
+    x.md = tiles(p.d);
+    x.n_dx = x.nt * x.md * p.splits;
+    x.n_dw = x.md * tiles(n);
+    x.chunk = (uint32_t)up((n + p.splits - 1) / p.splits, kTileK);
     x.part = dxp;
     x.first = k == 0;
-    DwArgs w;
-    w.xt = Operand{ws + o.xt, 2ull * p.n_pad, p.d};
-    w.dzt = Operand{ws + o.dzt, 2ull * p.n_pad, n};
-    w.n_pad = p.n_pad;
-    w.d = p.d;
-    w.md = tiles(p.d);
-    w.n_tiles = w.md * tiles(n);
-    w.xcds = dev.xcds;
-    w.grad = d_grad;
-    w.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
+    x.grad = d_grad;
+    x.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
     st = for_type(h->dtype, [&](auto t) {
       typedef decltype(t) T;
       if (d_row)
@@ -764,9 +735,7 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
       else
         hipLaunchKernelGGL((logit_dz_kernel<T, false>), dim3(a.n_tiles), dim3(kGemmBlock), kStageLds, s, a);
       if (int32_t e = launch_status()) return e;
-      hipLaunchKernelGGL(dx_kernel<T>, dim3(x.n_tiles), dim3(kGemmBlock), kGemmLds, s, x);
-      if (int32_t e = launch_status()) return e;
-      hipLaunchKernelGGL(dw_kernel<T>, dim3(w.n_tiles), dim3(kGemmBlock), kStageLds, s, w);
+      hipLaunchKernelGGL(products_kernel<T>, dim3(x.n_dx + x.n_dw), dim3(kGemmBlock), kStageLds, s, x);
       return launch_status();
     });
     if (st) return st;
