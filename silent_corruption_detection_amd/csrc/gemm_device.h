@@ -2,23 +2,28 @@
 // gfx950: C[m][n] = sum_k A(m, k) B(n, k) for 16-bit operands whose rows are
 // contiguous either in k or, "k-major", in m (n), accumulated in fp32 by MFMA.
 //
-// A workgroup of 8 waves computes 256 x 256 of C; wave (wm, wn), wm = 0..1,
-// wn = 0..3, holds rows 128 wm .. and columns 64 wn .. of it as 8 x 4 tiles of
-// 16 x 16 (128 accumulator registers).  k advances 64 at a time through two
-// LDS buffers of 64 KiB: the next buffer is filled by direct global-to-LDS
-// loads (16 bytes a lane, no registers) while the current one is multiplied.
+// A workgroup computes a TILE x TILE tile of C, TILE 256 (8 waves) or, where
+// those would be too few to fill the chip, 128 (4 waves).  Wave (wm, wn),
+// wm = 0..1, wn = 0..TILE / 64 - 1, holds rows wm TILE / 2 .. and columns
+// 64 wn .. of it as TILE / 32 x 4 groups of 16 x 16 (for 256: 128 accumulator
+// registers).  k advances 64 at a time through two LDS buffers (64 KiB each
+// for 256): the next buffer is filled by direct global-to-LDS loads (16 bytes
+// a lane, no registers) while the current one is multiplied.  Four buffers of
+// 32 k instead measured 4 to 10 % slower where rows run along k (64-byte
+// pieces of rows) and equal where they do not.
 // Direct loads write LDS in lane order, so the permutations below, which keep
 // the lanes of one LDS read on different banks, are made in the addresses they
 // read from.
-//   rows along k: 256 rows of 128 bytes; the eight 16-byte chunks of a row are
+//   rows along k: TILE rows of 128 bytes; the eight 16-byte chunks of a row are
 //     permuted by its low three bits.  An operand register group is one
 //     16-byte read per lane.
-//   k-major: 64 rows of 512 bytes; the sixteen 32-byte granules (16 columns) of
-//     row k are permuted by f(k) = k & 3 | (k >> 3 & 3) << 2, which differs
-//     over the 16 rows that one transposing read takes.  A group is two
-//     transposing 8-byte reads (each gives a lane four k of its column), which
-//     is what spares transposed copies of the weights, the inputs and dz.
-// Measured alone on random data at 4096 x 50304 x 2048: 742 us (1140 TFLOP/s).
+//   k-major: 64 rows of 2 TILE bytes; the TILE / 16 granules of 32 bytes
+//     (16 columns) of row k are permuted by f(k) = k & 3 | (k >> 3 & 3) << 2,
+//     which differs over the 16 rows that one transposing read takes.  A group
+//     is two transposing 8-byte reads (each gives a lane four k of its column),
+//     which is what spares transposed copies of the weights, the inputs and dz.
+// Measured alone on random data, TILE 256: 4096 x 32768 x 2048 (rows along k)
+// 431 us (1275 TFLOP/s), 2048 x 32768 x 4096 (k-major) 455 us (1210).
 #pragma once
 
 #include "scan_device.h"
@@ -26,11 +31,10 @@
 namespace sdc {
 namespace {
 
-constexpr uint32_t kTile = 256;     // rows and columns of C per workgroup
-constexpr uint32_t kTileK = 64;     // k per LDS buffer
-constexpr uint32_t kGemmBlock = 512;
-constexpr uint32_t kBufBytes = 2 * kTile * kTileK * 2;  // A and B of one k step
-constexpr uint32_t kGemmLds = 2 * kBufBytes;
+constexpr uint32_t kTileK = 64;  // k per LDS buffer
+constexpr uint32_t gemm_block(uint32_t tile) { return 2 * tile; }              // threads
+constexpr uint32_t buf_bytes(uint32_t tile) { return 2 * tile * kTileK * 2; }  // A and B of one k step
+constexpr uint32_t gemm_lds(uint32_t tile) { return 2 * buf_bytes(tile); }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -76,11 +80,12 @@ struct Operand {
 
 // Where a thread's accumulators stand in the tile: element r of acc[i][j] is
 // C[row(i) + r][col(j)].
+template <uint32_t TILE>
 struct Place {
   uint32_t lane, wm, wn;
   __device__ __forceinline__ Place()
-      : lane(threadIdx.x & 63u), wm(threadIdx.x >> 8), wn((threadIdx.x >> 6) & 3u) {}
-  __device__ __forceinline__ uint32_t row(int i) const { return wm * 128u + i * 16u + (lane >> 4) * 4u; }
+      : lane(threadIdx.x & 63u), wm(threadIdx.x / TILE), wn((threadIdx.x >> 6) & (TILE / 64u - 1u)) {}
+  __device__ __forceinline__ uint32_t row(int i) const { return wm * (TILE / 2) + i * 16u + (lane >> 4) * 4u; }
   __device__ __forceinline__ uint32_t col(int j) const { return wn * 64u + j * 16u + (lane & 15u); }
 };
 
@@ -104,8 +109,11 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* src, uint32_t b
 
 // One operand's side of the tile: its loads into LDS, step after step, and its
 // reads.
-template <class T, bool KMAJOR>
+template <class T, uint32_t TILE, bool KMAJOR>
 struct Side {
+  static constexpr uint32_t kRow = 2 * TILE;         // bytes of a k-major row
+  static constexpr uint32_t kPass = 2 * TILE * 16;   // bytes that one load of every thread fills
+  static constexpr uint32_t kGranules = TILE / 16 - 1;
   const unsigned char* p[4];  // of the thread's loads of the next step
   uint64_t step;              // bytes from one step to the next
   uint32_t limit;             // k from here on reads as zero
@@ -119,16 +127,16 @@ struct Side {
     const uint32_t t = threadIdx.x, lane = t & 63u;
     if constexpr (KMAJOR) {
       limit = o.rows;
-      k_in = t >> 5;
+      k_in = t / (TILE / 8);
       step = o.stride * kTileK;
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t k = i * 16u + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
-        const uint32_t col = at0 + ((((t & 31u) >> 1) ^ f) * 16u) + (t & 1u) * 8u;
+        const uint32_t col = at0 + ((((t % (TILE / 8)) >> 1) ^ (f & kGranules)) * 16u) + (t & 1u) * 8u;
         p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)min(col, o.cols - 8u) * 2u;
       }
       const uint32_t g = lane >> 4, r = (lane >> 2) & 3u, f = r | g << 2;
-      off = (8u * g + r) * 512u + ((base ^ f) << 5) + (lane & 3u) * 8u;
+      off = (8u * g + r) * kRow + ((base ^ (f & kGranules)) << 5) + (lane & 3u) * 8u;
     } else {
       limit = o.cols;
       const uint32_t q = (t & 7u) ^ ((t >> 3) & 7u);
@@ -136,21 +144,21 @@ struct Side {
       step = kTileK * 2u;
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i)
-        p[i] = o.p + (uint64_t)min(at0 + i * 64u + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
+        p[i] = o.p + (uint64_t)min(at0 + i * (TILE / 4) + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
       off = (base + (lane & 15u)) * 128u + (((lane >> 4) ^ (lane & 7u)) << 4);
     }
   }
-  // Loads the 32 KiB of step k into LDS at byte `dst`; called step by step.
+  // Loads the operand's part of step k into LDS at byte `dst`; called step by step.
   __device__ __forceinline__ void fill(uint32_t k, uint32_t dst) {
     const uint32_t base = dst + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u) * 16u;
     if (k + kTileK <= limit) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * 8192u);
+      for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * kPass);
     } else {
       const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
 #pragma unroll
       for (uint32_t i = 0; i < 4; ++i)
-        load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * 8192u);
+        load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * kPass);
     }
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) p[i] += step;
@@ -158,13 +166,13 @@ struct Side {
   // Group i (16 rows of C's index) of k 32 s .. of the step in LDS at `src`.
   __device__ __forceinline__ typename T::frag read(const unsigned char* src, int i, uint32_t s) const {
     if constexpr (KMAJOR) {
-      const unsigned char* q = src + (off ^ ((uint32_t)i << 5)) + s * 16384u;
+      const unsigned char* q = src + (off ^ ((uint32_t)i << 5)) + s * (32u * kRow);
       union {
         s16x4 half[2];
         typename T::frag all;
       } u;
       u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)q);
-      u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + 2048));
+      u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + 4 * kRow));
       return u.all;
     } else {
       return *reinterpret_cast<const typename T::frag*>(src + (off ^ (s * 64u)) + i * 2048);
@@ -174,18 +182,21 @@ struct Side {
 
 // Sum over k in [k0, k1) (k0 a multiple of 64) of the tile at row m0 of A's
 // index and n0 of B's.  What the tile holds past either's last means nothing.
-template <class T, bool AK, bool BK>
+template <class T, uint32_t TILE, bool AK, bool BK>
 __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
-                                          uint32_t k0, uint32_t k1, unsigned char* lds, f32x4 (&acc)[8][4]) {
+                                          uint32_t k0, uint32_t k1, unsigned char* lds,
+                                          f32x4 (&acc)[TILE / 32][4]) {
+  constexpr int kI = TILE / 32;
+  constexpr uint32_t kBufBytes = buf_bytes(TILE);
   typedef typename T::frag frag;
-  const Place at;
-  Side<T, AK> sa;
-  Side<T, BK> sb;
-  sa.init(A, m0, AK ? at.wm * 8u : at.wm * 128u, k0);
+  const Place<TILE> at;
+  Side<T, TILE, AK> sa;
+  Side<T, TILE, BK> sb;
+  sa.init(A, m0, AK ? at.wm * (TILE / 32) : at.wm * (TILE / 2), k0);
   sb.init(B, n0, BK ? at.wn * 4u : at.wn * 64u, k0);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < kI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const auto fill = [&](uint32_t k, uint32_t buf) {
@@ -204,13 +215,13 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
     const unsigned char* lb = la + kBufBytes / 2;
 #pragma unroll
     for (uint32_t s = 0; s < 2; ++s) {
-      frag a[8], b[4];
+      frag a[kI], b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) b[j] = sb.read(lb, j, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = sa.read(la, i, s);
+      for (int i = 0; i < kI; ++i) a[i] = sa.read(la, i, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
     }

@@ -22,6 +22,7 @@
 // is summed over pieces and splits in fp32 in a fixed order.  Bound by the matrix cores: 2 N V d operations forward, 6 N V d
 // for the gradient.
 #include <algorithm>
+#include <type_traits>
 
 #include "fingerprint_device.h"
 #include "gemm_device.h"
@@ -30,9 +31,10 @@ namespace sdc {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr uint32_t kStageRow = kTile + 8;  // 16-bit elements of a staged row, padded off the banks
-constexpr uint32_t kStageLds = kTile * kStageRow * 2;
-static_assert(kStageLds >= kGemmLds && kStageLds <= 160u * 1024u, "the staging area holds the buffers");
+constexpr uint32_t stage_row(uint32_t tile) { return tile + 8; }  // 16-bit elements of a staged row, padded off the banks
+constexpr uint32_t stage_lds(uint32_t tile) { return tile * stage_row(tile) * 2; }
+constexpr uint32_t lds_bytes(uint32_t tile) { return std::max(gemm_lds(tile), stage_lds(tile)); }
+static_assert(lds_bytes(256) + 1024 <= 160u * 1024u, "one workgroup fits a CU");
 
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -57,34 +59,37 @@ struct PackArgs {
 };
 
 template <bool VEC>
-__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
-  const uint32_t per = a.c_pad / 8;
-  const uint64_t n = (uint64_t)a.R * per;
-  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) {
-    const uint32_t r = (uint32_t)(i / per), c = (uint32_t)(i % per) * 8u;
+__global__ void __launch_bounds__(kBlock) pack_kernel(const PackArgs a) {
+  const uint32_t r = wave_item_index(), l = threadIdx.x & 63u;
+  if (r >= a.R) return;
+  const bool live = !a.mask || has_target(a.mask[r], a.vocab);
+  const unsigned char* src = a.src + (uint64_t)r * a.stride;
+  uint16_t* dst = a.dst + (uint64_t)r * a.c_pad;
+#pragma unroll 4
+  for (uint32_t c = l * 8u; c < a.c_pad; c += 512u) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (!a.mask || has_target(a.mask[r], a.vocab)) {
-      const unsigned char* p = a.src + (uint64_t)r * a.stride + (uint64_t)c * 2u;
+    if (live) {
       if (VEC) {
-        v = *reinterpret_cast<const u32x4*>(p);
+        v = *reinterpret_cast<const u32x4*>(src + c * 2u);
+      } else if (c + 8u <= a.C) {
+        v = *reinterpret_cast<const u32x4_at2*>(src + c * 2u);
       } else {
         uint32_t e[8];
 #pragma unroll
         for (uint32_t k = 0; k < 8; ++k)
-          e[k] = c + k < a.C ? *reinterpret_cast<const uint16_t*>(p + 2u * k) : 0u;
+          e[k] = c + k < a.C ? *reinterpret_cast<const uint16_t*>(src + (c + k) * 2u) : 0u;
         v = u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
       }
     }
-    *reinterpret_cast<u32x4*>(a.dst + (uint64_t)r * a.c_pad + c) = v;
+    *reinterpret_cast<u32x4*>(dst + c) = v;
   }
 }
 
 int32_t launch_pack(const PackArgs& a, hipStream_t s) {
   const bool vec = a.C % 8 == 0 && a.stride % 16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
-  const uint64_t n = (uint64_t)a.R * (a.c_pad / 8);
-  const dim3 grid((uint32_t)std::min<uint64_t>((n + 255) / 256, 8192));
-  if (vec) hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(256), 0, s, a);
+  const dim3 grid((a.R + kWaves - 1) / kWaves);
+  if (vec) hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(kBlock), 0, s, a);
+  else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(kBlock), 0, s, a);
   return launch_status();
 }
 
@@ -109,9 +114,10 @@ struct LogitArgs {
 };
 
 // The tile's part of the fingerprint row of the fp32 logits [N][V].
-__device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitArgs& a, uint32_t m0,
+template <uint32_t TILE>
+__device__ __forceinline__ void tile_row(const f32x4 (&acc)[TILE / 32][4], const LogitArgs& a, uint32_t m0,
                                          uint32_t n0, sdc_row* out) {
-  const Place at;
+  const Place<TILE> at;
   Lane ln;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -119,7 +125,7 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitAr
     if (n >= a.x.rows) continue;
     uint64_t s = 0, ws = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < (int)TILE / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (m0 + at.row(i) + r >= a.w.rows) continue;
@@ -133,7 +139,8 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitAr
     ln.w += ws + ((uint64_t)n * a.vocab + a.v0 + m0 + at.row(0) + 1u) * s;
   }
   wave_reduce(ln);
-  __shared__ uint64_t waves[4][8];
+  constexpr int kW = TILE / 32;  // waves
+  __shared__ uint64_t waves[4][kW];
   const uint32_t wave = threadIdx.x >> 6;
   if (at.lane == 0) {
     waves[0][wave] = ln.s;
@@ -144,7 +151,7 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitAr
   __syncthreads();
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
+    for (int i = 1; i < kW; ++i) {
       ln.s += waves[0][i];
       ln.w += waves[1][i];
       ln.x ^= waves[2][i];
@@ -156,20 +163,20 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[8][4], const LogitAr
   }
 }
 
-template <class T, bool ROW>
-__global__ void __launch_bounds__(kGemmBlock) logit_lse_kernel(const LogitArgs a) {
+template <class T, uint32_t TILE, bool ROW>
+__global__ void __launch_bounds__(gemm_block(TILE)) logit_lse_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
-  const uint32_t m0 = vt * kTile, n0 = (id % a.nt) * kTile;
-  f32x4 acc[8][4];
-  gemm_tile<T, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
-  const Place at;
+  const uint32_t m0 = vt * TILE, n0 = (id % a.nt) * TILE;
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  const Place<TILE> at;
   float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < (int)TILE / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (m0 + at.row(i) + r < a.w.rows) m = __builtin_fmaxf(m, acc[i][j][r]);
@@ -178,34 +185,34 @@ __global__ void __launch_bounds__(kGemmBlock) logit_lse_kernel(const LogitArgs a
     const float c = (__builtin_isinf(m) ? 0.0f : m) * kLog2e;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < (int)TILE / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (m0 + at.row(i) + r < a.w.rows)
           s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (at.lane < 16) half[at.wm * kTile + at.col(j)] = float2{m, s};
+    if (at.lane < 16) half[at.wm * TILE + at.col(j)] = float2{m, s};
   }
   __syncthreads();
-  if (threadIdx.x < kTile && n0 + threadIdx.x < a.x.rows) {
-    const float2 p = half[threadIdx.x], q = half[kTile + threadIdx.x];
+  if (threadIdx.x < TILE && n0 + threadIdx.x < a.x.rows) {
+    const float2 p = half[threadIdx.x], q = half[TILE + threadIdx.x];
     const float M = __builtin_fmaxf(p.x, q.x);
     a.part[(uint64_t)(n0 + threadIdx.x) * a.n_vt + vt] =
         float2{M, p.y * rescale(p.x, M) + q.y * rescale(q.x, M)};
   }
-  if constexpr (ROW) tile_row(acc, a, m0, n0, a.rows + id);
+  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
 }
 
 // dz of the tile, in 16 bits (rounded to nearest: off by half a step of its
 // own size, which the products average out), 0 for rows without a target and
 // in the padding.
-template <class T, bool ROW>
-__global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a) {
+template <class T, uint32_t TILE, bool ROW>
+__global__ void __launch_bounds__(gemm_block(TILE)) logit_dz_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
-  const uint32_t m0 = (id / a.nt) * kTile, n0 = (id % a.nt) * kTile;
-  const Place at;
+  const uint32_t m0 = (id / a.nt) * TILE, n0 = (id % a.nt) * TILE;
+  const Place<TILE> at;
   // what the epilogue needs of its tokens, in flight during the product
   float c[4];
   uint32_t hit[4];  // the target among the rows from at.row(0) on; kNone: no target
@@ -218,15 +225,15 @@ __global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a)
     // at most 2^24 rows: the difference, also a negative one, is never kNone
     hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
   }
-  f32x4 acc[8][4];
-  gemm_tile<T, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
-  if constexpr (ROW) tile_row(acc, a, m0, n0, a.rows + id);
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const bool live = hit[j] != kNone;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < (int)TILE / 32; ++i) {
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -234,18 +241,18 @@ __global__ void __launch_bounds__(kGemmBlock) logit_dz_kernel(const LogitArgs a)
         p = (p - (hit[j] == (uint32_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
         b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
       }
-      *reinterpret_cast<uint2*>(st + at.col(j) * kStageRow + at.row(i)) =
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
           uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     }
   }
   __syncthreads();
-  const uint32_t t = threadIdx.x, ch = (t & 31u) * 8u;
+  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
 #pragma unroll 4
-  for (uint32_t k = t >> 5; k < kTile; k += 16) {
+  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
     const uint32_t n = n0 + k, v = m0 + ch;
     if (n < a.x.rows && v < a.v_pad)
       *reinterpret_cast<u32x4*>(a.dz + (uint64_t)n * a.v_pad + v) =
-          *reinterpret_cast<const u32x4*>(st + k * kStageRow + ch);
+          *reinterpret_cast<const u32x4*>(st + k * stage_row(TILE) + ch);
   }
 }
 
@@ -264,29 +271,29 @@ struct ProductArgs {
   uint16_t* dw;        // of the piece's first row
 };
 
-template <class T>
+template <class T, uint32_t TILE>
 __device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
-  const uint32_t n0 = (id % a.nt) * kTile, rest = id / a.nt;
-  const uint32_t m0 = (rest % a.md) * kTile, split = rest / a.md;
+  const uint32_t n0 = (id % a.nt) * TILE, rest = id / a.nt;
+  const uint32_t m0 = (rest % a.md) * TILE, split = rest / a.md;
   const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.rows);
   if (k0 >= k1 && !a.first) return;
-  f32x4 acc[8][4];
+  f32x4 acc[TILE / 32][4];
   if (k0 < k1) {
-    gemm_tile<T, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
+    gemm_tile<T, TILE, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < (int)TILE / 32; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const Place at;
+  const Place<TILE> at;
   float* out = a.part + (uint64_t)split * a.N * a.d;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t n = n0 + at.col(j);
     if (n >= a.N) continue;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < (int)TILE / 32; ++i) {
       const uint32_t m = m0 + at.row(i);
       float* p = out + (uint64_t)n * a.d + m;
       if (a.d % 4 == 0) {
@@ -303,32 +310,32 @@ __device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsig
   }
 }
 
-template <class T>
+template <class T, uint32_t TILE>
 __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
-  const uint32_t m0 = (id % a.md) * kTile, n0 = (id / a.md) * kTile;
+  const uint32_t m0 = (id % a.md) * TILE, n0 = (id / a.md) * TILE;
   const float g = *a.grad * (1.0f / T::kDzScale);
-  f32x4 acc[8][4];
-  gemm_tile<T, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
-  const Place at;
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
+  const Place<TILE> at;
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < (int)TILE / 32; ++i) {
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) b[r] = T::bits(acc[i][j][r] * g);
-      *reinterpret_cast<uint2*>(st + at.col(j) * kStageRow + at.row(i)) =
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
           uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     }
   __syncthreads();
-  const uint32_t t = threadIdx.x, ch = (t & 31u) * 8u;
+  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
 #pragma unroll 4
-  for (uint32_t k = t >> 5; k < kTile; k += 16) {
+  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
     const uint32_t v = n0 + k, c = m0 + ch;
     if (v >= a.rows || c >= a.d) continue;
     uint16_t* p = a.dw + (uint64_t)v * a.d + c;
-    const uint16_t* s = st + k * kStageRow + ch;
+    const uint16_t* s = st + k * stage_row(TILE) + ch;
     if (c + 8u <= a.d) {
       *reinterpret_cast<u32x4_at2*>(p) = *reinterpret_cast<const u32x4*>(s);
     } else {
@@ -337,11 +344,11 @@ __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsig
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kGemmBlock) products_kernel(const ProductArgs a) {
+template <class T, uint32_t TILE>
+__global__ void __launch_bounds__(gemm_block(TILE)) products_kernel(const ProductArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
-  if (blockIdx.x < a.n_dx) dx_tile<T>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
-  else dw_tile<T>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
+  if (blockIdx.x < a.n_dx) dx_tile<T, TILE>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
+  else dw_tile<T, TILE>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
 }
 
 // dx = grad * the splits' sum, in split order; 0 for rows without a target.
@@ -468,6 +475,8 @@ constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
   uint32_t N, d, V, d_pad;
+  uint32_t tile;         // 256 or 128
+  uint32_t nt, vt, md;   // tiles of the tokens, of the whole vocabulary, of d
   bool copy;             // the operands need an aligned copy
   uint32_t piece;        // vocabulary rows of a piece
   uint32_t pieces;
@@ -475,7 +484,7 @@ struct Head {
   uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
 };
 
-uint32_t tiles(uint64_t n) { return (uint32_t)((n + kTile - 1) / kTile); }
+uint32_t tiles(uint64_t n, uint32_t tile) { return (uint32_t)((n + tile - 1) / tile); }
 
 int32_t check_head(const sdc_head* h) {
   if (h == nullptr) return SDC_ERR_INVALID;
@@ -487,12 +496,17 @@ int32_t check_head(const sdc_head* h) {
       reinterpret_cast<uintptr_t>(h->target) % 8)
     return SDC_ERR_ALIGN;
   if (h->n >= 1ull << 24 || h->d >= 1ull << 20 || h->vocab >= 1ull << 24 || h->x_stride >= 1ull << 40 ||
-      h->w_stride >= 1ull << 40 || (uint64_t)tiles(h->n) * (tiles(h->vocab) + 4096) >= 1ull << 31)
+      h->w_stride >= 1ull << 40 || (uint64_t)tiles(h->n, 256) * (tiles(h->vocab, 256) + 4096) >= 1ull << 31)
     return SDC_ERR_RANGE;
   return SDC_OK;
 }
 
-// GRAD: the sizes of the gradient's pieces; else those of the forward pass,
+// 256 x 256 tiles where they fill the chip, else 128 x 128.
+uint32_t tile_of(uint64_t n, uint64_t vocab) {
+  return n > 128 && (uint64_t)tiles(n, 256) * tiles(vocab, 256) >= 192 ? 256u : 128u;
+}
+
+// grad: the sizes of the gradient's pieces; else those of the forward pass,
 // which needs pieces only for its copies.
 Head plan_head(const sdc_head* h, bool grad) {
   Head p;
@@ -502,12 +516,16 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.d_pad = (uint32_t)up(h->d, 8);
   p.copy = h->d % 8 || h->x_stride % 8 || h->w_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16 ||
            reinterpret_cast<uintptr_t>(h->w) % 16;
+  p.tile = tile_of(p.N, p.V);
+  p.nt = tiles(p.N, p.tile);
+  p.vt = tiles(p.V, p.tile);
+  p.md = tiles(p.d, p.tile);
   // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
   // of that on, the one that needs the fewest rounds of 256 tiles.
-  const uint32_t nt = tiles(p.N), vt = tiles(p.V);
+  const uint32_t nt = p.nt, vt = p.vt;
   const uint64_t col = (p.copy ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.N : 0);
   uint32_t most = vt;
-  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / kTile, 1);
+  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.tile, 1);
   uint32_t best = most;
   if (most < vt) {
     uint64_t least = ~0ull;
@@ -520,14 +538,11 @@ Head plan_head(const sdc_head* h, bool grad) {
       }
     }
   }
-  const uint64_t piece = (uint64_t)best * kTile;
+  const uint64_t piece = (uint64_t)best * p.tile;
   p.piece = (uint32_t)std::min<uint64_t>(piece, up(p.V, 8));
   p.pieces = (vt + best - 1) / best;
-  const uint32_t dx_tiles = nt * tiles(p.d);
-  p.splits = std::max(1u, std::min(dx_tiles ? 256u / dx_tiles : 1u, best));
-  p.n_tiles = 0;
-  for (uint32_t k = 0; k < p.pieces; ++k)
-    p.n_tiles += tiles(std::min<uint64_t>(piece, p.V - k * piece)) * tiles(p.N);
+  p.splits = std::max(1u, std::min(p.N ? 256u / (nt * p.md) : 1u, best));
+  p.n_tiles = nt * vt;
   return p;
 }
 
@@ -552,15 +567,19 @@ Layout layout_head(const Head& p, bool grad) {
     o.dz = take(2ull * p.N * p.piece);
     o.dxp = take(4ull * p.splits * p.N * p.d);
   } else {
-    o.part = take(8ull * p.N * tiles(p.V));
+    o.part = take(8ull * p.N * p.vt);
   }
   o.end = std::max<uint64_t>(at, 256);
   return o;
 }
 
+// f(type, tile) with both as compile-time constants
 template <class F>
-int32_t for_type(uint32_t dtype, F&& f) {
-  return dtype == SDC_BF16 ? f(Bf16()) : f(Fp16());
+int32_t for_type(uint32_t dtype, uint32_t tile, F&& f) {
+  const std::integral_constant<uint32_t, 256> big;
+  const std::integral_constant<uint32_t, 128> small;
+  if (dtype == SDC_BF16) return tile == 256 ? f(Bf16(), big) : f(Bf16(), small);
+  return tile == 256 ? f(Fp16(), big) : f(Fp16(), small);
 }
 
 // Operands of a piece, copied where they are not aligned.
@@ -584,8 +603,8 @@ int32_t piece_operands(const sdc_head* h, const Head& p, const Layout& o, unsign
   }
   a->K = p.d;
   a->v0 = v0;
-  a->nt = tiles(p.N);
-  a->n_tiles = tiles(rows) * a->nt;
+  a->nt = p.nt;
+  a->n_tiles = tiles(rows, p.tile) * a->nt;
   a->vocab = p.V;
   return SDC_OK;
 }
@@ -630,24 +649,24 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
     a.xcds = dev.xcds;
     a.part = reinterpret_cast<float2*>(ws + o.part);
     sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
-    a.n_vt = tiles(p.V);
+    a.n_vt = p.vt;
     for (uint32_t k = 0; k < p.pieces; ++k) {
       const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0);
       if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
       a.rows = d_row ? rows : nullptr;
-      st = for_type(h->dtype, [&](auto t) {
+      st = for_type(h->dtype, p.tile, [&](auto t, auto tile) {
         typedef decltype(t) T;
-        if (d_row)
-          hipLaunchKernelGGL((logit_lse_kernel<T, true>), dim3(a.n_tiles), dim3(kGemmBlock), kGemmLds, s, a);
-        else
-          hipLaunchKernelGGL((logit_lse_kernel<T, false>), dim3(a.n_tiles), dim3(kGemmBlock), kGemmLds, s, a);
+        constexpr uint32_t TILE = decltype(tile)::value;
+        const dim3 grid(a.n_tiles), block(gemm_block(TILE));
+        if (d_row) hipLaunchKernelGGL((logit_lse_kernel<T, TILE, true>), grid, block, gemm_lds(TILE), s, a);
+        else hipLaunchKernelGGL((logit_lse_kernel<T, TILE, false>), grid, block, gemm_lds(TILE), s, a);
         return launch_status();
       });
       if (st) return st;
       rows += a.n_tiles;
-      a.part += tiles(n);
+      a.part += tiles(n, p.tile);
     }
-    st = for_type(h->dtype, [&](auto t) {
+    st = for_type(h->dtype, p.tile, [&](auto t, auto) {
       typedef decltype(t) T;
       hipLaunchKernelGGL(lse_kernel<T>, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s,
                          reinterpret_cast<const float2*>(ws + o.part), a.n_vt, p.N, p.d,
@@ -719,28 +738,30 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     x.d = p.d;
     x.rows = n;
     x.xcds = dev.xcds;
-    x.nt = tiles(p.N);
-    x.md = tiles(p.d);
+    x.nt = p.nt;
+    x.md = p.md;
     x.n_dx = x.nt * x.md * p.splits;
-    x.n_dw = x.md * tiles(n);
+    x.n_dw = x.md * tiles(n, p.tile);
     x.chunk = (uint32_t)up((n + p.splits - 1) / p.splits, kTileK);
     x.part = dxp;
     x.first = k == 0;
     x.grad = d_grad;
     x.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
-    st = for_type(h->dtype, [&](auto t) {
+    st = for_type(h->dtype, p.tile, [&](auto t, auto tile) {
       typedef decltype(t) T;
+      constexpr uint32_t TILE = decltype(tile)::value;
+      const dim3 block(gemm_block(TILE));
       if (d_row)
-        hipLaunchKernelGGL((logit_dz_kernel<T, true>), dim3(a.n_tiles), dim3(kGemmBlock), kStageLds, s, a);
+        hipLaunchKernelGGL((logit_dz_kernel<T, TILE, true>), dim3(a.n_tiles), block, lds_bytes(TILE), s, a);
       else
-        hipLaunchKernelGGL((logit_dz_kernel<T, false>), dim3(a.n_tiles), dim3(kGemmBlock), kStageLds, s, a);
+        hipLaunchKernelGGL((logit_dz_kernel<T, TILE, false>), dim3(a.n_tiles), block, lds_bytes(TILE), s, a);
       if (int32_t e = launch_status()) return e;
-      hipLaunchKernelGGL(products_kernel<T>, dim3(x.n_dx + x.n_dw), dim3(kGemmBlock), kStageLds, s, x);
+      hipLaunchKernelGGL((products_kernel<T, TILE>), dim3(x.n_dx + x.n_dw), block, lds_bytes(TILE), s, x);
       return launch_status();
     });
     if (st) return st;
   }
-  st = for_type(h->dtype, [&](auto t) {
+  st = for_type(h->dtype, p.tile, [&](auto t, auto) {
     typedef decltype(t) T;
     hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 1023) / 1024), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
                        h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));
