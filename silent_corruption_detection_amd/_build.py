@@ -28,7 +28,8 @@ SANITIZE_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitiz
                   "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
                   "-Xarch_host", "-g"]
 SOURCES = ["scan.hip", "tensor.hip", "nonfinite.hip", "norm.hip", "compare.hip", "readsum.hip",
-           "noalloc.hip", "adamw.hip", "adamw32.hip", "adamw8.hip", "xent.hip", "plan.cpp", "device.cpp", "misc.cpp"]
+           "noalloc.hip", "adamw.hip", "adamw32.hip", "adamw8.hip", "xent.hip", "xent16.hip",
+           "xent_any.hip", "plan.cpp", "device.cpp", "misc.cpp"]
 ARCH = os.environ.get("SDC_OFFLOAD_ARCH", "gfx950")
 NOISE = "is not a recognized feature for this target"
 

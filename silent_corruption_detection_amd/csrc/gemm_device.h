@@ -71,7 +71,8 @@ struct Fp16 {
 };
 
 // An operand with `rows` rows (of C's index, or, k-major, of k), `stride` bytes
-// apart, each of `cols` elements; 16-byte aligned, cols a multiple of 8.
+// apart, each of `cols` elements: 16-byte aligned with cols a multiple of 8, or
+// (RowsAt kAny) at any even address with cols at least 8.
 struct Operand {
   const unsigned char* p;
   uint64_t stride;
@@ -107,9 +108,30 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* src, uint32_t b
       : "memory");
 }
 
+// How an operand's rows may lie: at 16-byte boundaries (kAt16), read straight
+// into LDS; or anywhere (kAny: rows of at least 8 elements at any even address,
+// of any length), read through registers, which direct loads to LDS cannot.
+enum RowsAt : int { kAt16, kAny };
+
+// Sixteen bytes at any even address.
+__device__ __forceinline__ u32x4 load16_any(const unsigned char* p) {
+  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(2)));
+  return *(const SDC_GLOBAL vec*)p;
+}
+
+// v moved down by n 16-bit elements (0..7), zeros above: the last chunk of a
+// row of a length not divisible by 8, read as the row's last 16 bytes.
+__device__ __forceinline__ u32x4 drop_elements(u32x4 v, uint32_t n) {
+  const uint64_t lo = lohi(v.x, v.y), hi = lohi(v.z, v.w);
+  const uint32_t bits = (n & 3u) * 16u;
+  const uint64_t a = n < 4u ? lo : hi, b = n < 4u ? hi : 0ull;
+  const uint64_t rl = bits ? (a >> bits) | (b << (64u - bits)) : a, rh = b >> bits;
+  return u32x4{(uint32_t)rl, (uint32_t)(rl >> 32), (uint32_t)rh, (uint32_t)(rh >> 32)};
+}
+
 // One operand's side of the tile: its loads into LDS, step after step, and its
 // reads.
-template <class T, uint32_t TILE, bool KMAJOR>
+template <class T, uint32_t TILE, bool KMAJOR, RowsAt AT>
 struct Side {
   static constexpr uint32_t kRow = 2 * TILE;         // bytes of a k-major row
   static constexpr uint32_t kPass = 2 * TILE * 16;   // bytes that one load of every thread fills
@@ -119,10 +141,12 @@ struct Side {
   uint32_t limit;             // k from here on reads as zero
   uint32_t k_in;              // k of the thread's first load within a step
   uint32_t off;               // of the lane's LDS reads
+  uint32_t drop[4];           // kAny, k-major: elements past the end of the rows that a load starts before
+  u32x4 held[4];              // kAny: the loads of the next step
 
   // at0: first row of C's index; base: LDS row (rows along k) or granule
   // (k-major) of the wave's first group.  Rows along k past the operand's last
-  // are read as the last, columns past a k-major one's last as its last eight.
+  // are read as the last, chunks past a k-major one's columns as its last eight.
   __device__ __forceinline__ void init(const Operand& o, uint32_t at0, uint32_t base, uint32_t k0) {
     const uint32_t t = threadIdx.x, lane = t & 63u;
     if constexpr (KMAJOR) {
@@ -133,7 +157,9 @@ struct Side {
       for (uint32_t i = 0; i < 4; ++i) {
         const uint32_t k = i * 16u + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
         const uint32_t col = at0 + ((((t % (TILE / 8)) >> 1) ^ (f & kGranules)) * 16u) + (t & 1u) * 8u;
-        p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)min(col, o.cols - 8u) * 2u;
+        const uint32_t from = min(col, o.cols - 8u);
+        p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)from * 2u;
+        drop[i] = min(col - from, 7u);
       }
       const uint32_t g = lane >> 4, r = (lane >> 2) & 3u, f = r | g << 2;
       off = (8u * g + r) * kRow + ((base ^ (f & kGranules)) << 5) + (lane & 3u) * 8u;
@@ -148,20 +174,53 @@ struct Side {
       off = (base + (lane & 15u)) * 128u + (((lane >> 4) ^ (lane & 7u)) << 4);
     }
   }
-  // Loads the operand's part of step k into LDS at byte `dst`; called step by step.
+  // Starts the loads of the operand's part of step k into LDS at byte `dst`;
+  // called step by step.
   __device__ __forceinline__ void fill(uint32_t k, uint32_t dst) {
-    const uint32_t base = dst + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u) * 16u;
-    if (k + kTileK <= limit) {
+    if constexpr (AT == kAt16) {
+      const uint32_t base = dst + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u) * 16u;
+      if (k + kTileK <= limit) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * kPass);
+        for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * kPass);
+      } else {
+        const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+          load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * kPass);
+      }
+    } else if (k + kTileK <= limit) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) held[i] = load16_any(p[i]);
+    } else if constexpr (KMAJOR) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        held[i] = u32x4{0u, 0u, 0u, 0u};
+        if (k + k_in + i * 16u < limit) held[i] = load16_any(p[i]);
+      }
     } else {
-      const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+      // chunks that end past the row start at its last 16 bytes; those past it are zero
+      const uint32_t at = k + k_in, back = at + 8u > limit ? min(at + 8u - limit, 8u) : 0u;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-        load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * kPass);
+      for (uint32_t i = 0; i < 4; ++i) {
+        held[i] = u32x4{0u, 0u, 0u, 0u};
+        if (at < limit) held[i] = drop_elements(load16_any(p[i] - back * 2u), back & 7u);
+      }
     }
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) p[i] += step;
+  }
+  // kAny: writes what fill has loaded to LDS at `dst`.
+  __device__ __forceinline__ void settle(unsigned char* dst) const {
+    if constexpr (AT == kAny) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        u32x4 v = held[i];
+        if constexpr (KMAJOR) {
+          if (__any(drop[i] != 0u)) v = drop_elements(v, drop[i]);
+        }
+        *reinterpret_cast<u32x4*>(dst + i * kPass + threadIdx.x * 16u) = v;
+      }
+    }
   }
   // Group i (16 rows of C's index) of k 32 s .. of the step in LDS at `src`.
   __device__ __forceinline__ typename T::frag read(const unsigned char* src, int i, uint32_t s) const {
@@ -182,7 +241,8 @@ struct Side {
 
 // Sum over k in [k0, k1) (k0 a multiple of 64) of the tile at row m0 of A's
 // index and n0 of B's.  What the tile holds past either's last means nothing.
-template <class T, uint32_t TILE, bool AK, bool BK>
+// AAT: how A's rows lie; B's lie at 16-byte boundaries.
+template <class T, uint32_t TILE, RowsAt AAT, bool AK, bool BK>
 __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
                                           uint32_t k0, uint32_t k1, unsigned char* lds,
                                           f32x4 (&acc)[TILE / 32][4]) {
@@ -190,8 +250,8 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
   constexpr uint32_t kBufBytes = buf_bytes(TILE);
   typedef typename T::frag frag;
   const Place<TILE> at;
-  Side<T, TILE, AK> sa;
-  Side<T, TILE, BK> sb;
+  Side<T, TILE, AK, AAT> sa;
+  Side<T, TILE, BK, kAt16> sb;
   sa.init(A, m0, AK ? at.wm * (TILE / 32) : at.wm * (TILE / 2), k0);
   sb.init(B, n0, BK ? at.wn * 4u : at.wn * 64u, k0);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
@@ -204,9 +264,10 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
     sb.fill(k, lds0 + buf * kBufBytes + kBufBytes / 2);
   };
   fill(k0, 0);
+  sa.settle(lds);
   uint32_t buf = 0;
   for (uint32_t k = k0; k < k1; k += kTileK, buf ^= 1u) {
-    // own loads have landed, own reads of the other buffer are done
+    // own loads have landed, own reads and writes of the other buffer are done
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
     asm volatile("" ::: "memory");
@@ -225,6 +286,7 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
     }
+    if (k + kTileK < k1) sa.settle(lds + (buf ^ 1u) * kBufBytes);
   }
   __syncthreads();  // the buffers may be reused
 }

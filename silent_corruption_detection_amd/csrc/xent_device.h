@@ -1,0 +1,337 @@
+// xent_device.h -- the tiled kernels of the cross-entropy head (csrc/xent.hip
+// says what they compute), instantiated for weights whose rows lie at 16-byte
+// boundaries (csrc/xent16.hip) and for any others (csrc/xent_any.hip).
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fingerprint_device.h"
+#include "gemm_device.h"
+
+namespace sdc {
+
+struct LogitArgs {
+  Operand w, x;            // rows of the vocabulary (from v0 on), rows of tokens
+  uint32_t K;              // elements of a row
+  uint32_t v0;             // vocabulary index of w's first row
+  uint32_t nt;             // token tiles
+  uint32_t n_tiles, xcds;
+  uint64_t vocab;
+  // forward: [token][tile] maxima and sums
+  float2* part;
+  uint32_t n_vt;
+  // gradient
+  const int64_t* target;
+  const float* lse;
+  uint16_t* dz;            // [x.rows][v_pad]
+  uint32_t v_pad;
+  // fingerprint of the logits: one partial row per tile, or null
+  sdc_row* rows;
+};
+
+// Both products of a piece in one launch: dx's tiles first (they are the
+// longer ones), then dW's, so that the chip fills up once.
+struct ProductArgs {
+  Operand w, dz, x;    // [piece rows][d], [N][v_pad], [N][d] with the rows without a target zero
+  uint32_t N, d, rows, xcds;
+  uint32_t nt, md;     // token tiles, tiles of d
+  uint32_t n_dx, n_dw; // tiles
+  uint32_t chunk;      // k of a split of dx
+  float* part;         // [splits][N][d]
+  uint32_t first;      // 1: the first piece stores, later ones add
+  const float* grad;
+  uint16_t* dw;        // of the piece's first row
+};
+
+// Launches over the tiles of one piece (tile: 256 or 128; at: how w's rows lie).
+struct HeadLaunch {
+  uint32_t dtype, tile;
+};
+int32_t launch_logit_lse16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_logit_lse_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_gradient16(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s);
+int32_t launch_gradient_any(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s);
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+constexpr uint32_t stage_row(uint32_t tile) { return tile + 8; }  // 16-bit elements of a staged row, padded off the banks
+constexpr uint32_t stage_lds(uint32_t tile) { return tile * stage_row(tile) * 2; }
+constexpr uint32_t lds_bytes(uint32_t tile) { return std::max(gemm_lds(tile), stage_lds(tile)); }
+static_assert(lds_bytes(256) + 1024 <= 160u * 1024u, "one workgroup fits a CU");
+
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+
+__device__ __forceinline__ bool has_target(int64_t t, uint64_t vocab) { return (uint64_t)t < vocab; }
+
+// exp(m - M) of a running maximum m <= M, also where both are the same infinity
+__device__ __forceinline__ float rescale(float m, float M) {
+  return m == M ? 1.0f : __builtin_amdgcn_exp2f((m - M) * kLog2e);
+}
+
+// ---- logit tiles ------------------------------------------------------------------
+
+// The tile's part of the fingerprint row of the fp32 logits [N][V].
+template <uint32_t TILE>
+__device__ __forceinline__ void tile_row(const f32x4 (&acc)[TILE / 32][4], const LogitArgs& a, uint32_t m0,
+                                         uint32_t n0, sdc_row* out) {
+  const Place<TILE> at;
+  Lane ln;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = n0 + at.col(j);
+    if (n >= a.x.rows) continue;
+    uint64_t s = 0, ws = 0;
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (m0 + at.row(i) + r >= a.w.rows) continue;
+        const uint32_t x = __float_as_uint(acc[i][j][r]);
+        s += x;
+        ws += (uint64_t)(i * 16 + r) * x;
+        ln.x ^= x;
+        ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+      }
+    ln.s += s;
+    ln.w += ws + ((uint64_t)n * a.vocab + a.v0 + m0 + at.row(0) + 1u) * s;
+  }
+  wave_reduce(ln);
+  constexpr int kW = TILE / 32;  // waves
+  __shared__ uint64_t waves[4][kW];
+  const uint32_t wave = threadIdx.x >> 6;
+  if (at.lane == 0) {
+    waves[0][wave] = ln.s;
+    waves[1][wave] = ln.w;
+    waves[2][wave] = ln.x;
+    waves[3][wave] = ln.nf;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < kW; ++i) {
+      ln.s += waves[0][i];
+      ln.w += waves[1][i];
+      ln.x ^= waves[2][i];
+      ln.nf += waves[3][i];
+    }
+    ulonglong2* d = reinterpret_cast<ulonglong2*>(out);
+    d[0] = ulonglong2{ln.s, ln.w};
+    d[1] = ulonglong2{ln.x, ln.nf};
+  }
+}
+
+template <class T, uint32_t TILE, RowsAt AT, bool ROW>
+__global__ void __launch_bounds__(gemm_block(TILE)) logit_lse_kernel(const LogitArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
+  const uint32_t m0 = vt * TILE, n0 = (id % a.nt) * TILE;
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  const Place<TILE> at;
+  float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (m0 + at.row(i) + r < a.w.rows) m = __builtin_fmaxf(m, acc[i][j][r]);
+    m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+    m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+    const float c = (__builtin_isinf(m) ? 0.0f : m) * kLog2e;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (m0 + at.row(i) + r < a.w.rows)
+          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (at.lane < 16) half[at.wm * TILE + at.col(j)] = float2{m, s};
+  }
+  __syncthreads();
+  if (threadIdx.x < TILE && n0 + threadIdx.x < a.x.rows) {
+    const float2 p = half[threadIdx.x], q = half[TILE + threadIdx.x];
+    const float M = __builtin_fmaxf(p.x, q.x);
+    a.part[(uint64_t)(n0 + threadIdx.x) * a.n_vt + vt] =
+        float2{M, p.y * rescale(p.x, M) + q.y * rescale(q.x, M)};
+  }
+  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
+}
+
+// dz of the tile, in 16 bits (rounded to nearest: off by half a step of its
+// own size, which the products average out), 0 for rows without a target and
+// in the padding.
+template <class T, uint32_t TILE, RowsAt AT, bool ROW>
+__global__ void __launch_bounds__(gemm_block(TILE)) logit_dz_kernel(const LogitArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
+  const uint32_t m0 = (id / a.nt) * TILE, n0 = (id % a.nt) * TILE;
+  const Place<TILE> at;
+  // what the epilogue needs of its tokens, in flight during the product
+  float c[4];
+  uint32_t hit[4];  // the target among the rows from at.row(0) on; kNone: no target
+  constexpr uint32_t kNone = 0x80000000u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = min(n0 + at.col(j), a.x.rows - 1u);
+    const int64_t t = a.target[n];
+    c[j] = a.lse[n] * kLog2e;
+    // at most 2^24 rows: the difference, also a negative one, is never kNone
+    hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
+  }
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
+  uint16_t* st = reinterpret_cast<uint16_t*>(lds);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool live = hit[j] != kNone;
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c[j]));
+        p = (p - (hit[j] == (uint32_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
+        b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
+      }
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
+          uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+    }
+  }
+  __syncthreads();
+  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
+#pragma unroll 4
+  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
+    const uint32_t n = n0 + k, v = m0 + ch;
+    if (n < a.x.rows && v < a.v_pad)
+      *reinterpret_cast<u32x4*>(a.dz + (uint64_t)n * a.v_pad + v) =
+          *reinterpret_cast<const u32x4*>(st + k * stage_row(TILE) + ch);
+  }
+}
+
+// ---- dx and dW --------------------------------------------------------------------
+
+template <class T, uint32_t TILE, RowsAt AT>
+__device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
+  const uint32_t n0 = (id % a.nt) * TILE, rest = id / a.nt;
+  const uint32_t m0 = (rest % a.md) * TILE, split = rest / a.md;
+  const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.rows);
+  if (k0 >= k1 && !a.first) return;
+  f32x4 acc[TILE / 32][4];
+  if (k0 < k1) {
+    gemm_tile<T, TILE, AT, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const Place<TILE> at;
+  float* out = a.part + (uint64_t)split * a.N * a.d;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t n = n0 + at.col(j);
+    if (n >= a.N) continue;
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i) {
+      const uint32_t m = m0 + at.row(i);
+      float* p = out + (uint64_t)n * a.d + m;
+      if (a.d % 4 == 0) {
+        if (m < a.d) {
+          f32x4* q = reinterpret_cast<f32x4*>(p);
+          *q = a.first ? acc[i][j] : *q + acc[i][j];
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (m + r < a.d) p[r] = a.first ? acc[i][j][r] : p[r] + acc[i][j][r];
+      }
+    }
+  }
+}
+
+template <class T, uint32_t TILE>
+__device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
+  const uint32_t m0 = (id % a.md) * TILE, n0 = (id / a.md) * TILE;
+  const float g = *a.grad * (1.0f / T::kDzScale);
+  f32x4 acc[TILE / 32][4];
+  gemm_tile<T, TILE, kAt16, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
+  const Place<TILE> at;
+  uint16_t* st = reinterpret_cast<uint16_t*>(lds);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < (int)TILE / 32; ++i) {
+      uint32_t b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = T::bits(acc[i][j][r] * g);
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
+          uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
+    }
+  __syncthreads();
+  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
+#pragma unroll 4
+  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
+    const uint32_t v = n0 + k, c = m0 + ch;
+    if (v >= a.rows || c >= a.d) continue;
+    uint16_t* p = a.dw + (uint64_t)v * a.d + c;
+    const uint16_t* s = st + k * stage_row(TILE) + ch;
+    if (c + 8u <= a.d) {
+      *reinterpret_cast<u32x4_at2*>(p) = *reinterpret_cast<const u32x4*>(s);
+    } else {
+      for (uint32_t e = 0; c + e < a.d; ++e) p[e] = s[e];
+    }
+  }
+}
+
+template <class T, uint32_t TILE, RowsAt AT>
+__global__ void __launch_bounds__(gemm_block(TILE)) products_kernel(const ProductArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  if (blockIdx.x < a.n_dx) dx_tile<T, TILE, AT>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
+  else dw_tile<T, TILE>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
+}
+
+
+// f(type, tile) with both as compile-time constants
+template <class F>
+int32_t for_type(uint32_t dtype, uint32_t tile, F&& f) {
+  const std::integral_constant<uint32_t, 256> big;
+  const std::integral_constant<uint32_t, 128> small;
+  if (dtype == SDC_BF16) return tile == 256 ? f(Bf16(), big) : f(Bf16(), small);
+  return tile == 256 ? f(Fp16(), big) : f(Fp16(), small);
+}
+
+template <RowsAt AT>
+int32_t launch_logit_lse(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
+  return for_type(h.dtype, h.tile, [&](auto t, auto tile) {
+    typedef decltype(t) T;
+    constexpr uint32_t TILE = decltype(tile)::value;
+    const dim3 grid(a.n_tiles), block(gemm_block(TILE));
+    if (a.rows) hipLaunchKernelGGL((logit_lse_kernel<T, TILE, AT, true>), grid, block, gemm_lds(TILE), s, a);
+    else hipLaunchKernelGGL((logit_lse_kernel<T, TILE, AT, false>), grid, block, gemm_lds(TILE), s, a);
+    return launch_status();
+  });
+}
+
+template <RowsAt AT>
+int32_t launch_gradient(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s) {
+  return for_type(h.dtype, h.tile, [&](auto t, auto tile) {
+    typedef decltype(t) T;
+    constexpr uint32_t TILE = decltype(tile)::value;
+    const dim3 grid(a.n_tiles), block(gemm_block(TILE));
+    if (a.rows) hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, true>), grid, block, lds_bytes(TILE), s, a);
+    else hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, false>), grid, block, lds_bytes(TILE), s, a);
+    if (int32_t e = launch_status()) return e;
+    hipLaunchKernelGGL((products_kernel<T, TILE, AT>), dim3(x.n_dx + x.n_dw), block, lds_bytes(TILE), s, x);
+    return launch_status();
+  });
+}
+
+}  // namespace
+}  // namespace sdc
