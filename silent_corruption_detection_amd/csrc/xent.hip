@@ -96,20 +96,54 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict_
 }
 
 // ---- row results -------------------------------------------------------------------
-// One wave per token: merges its tiles' maxima and sums, and the target's
-// logit as a plain dot product (fp32, a fixed order).
+// What the row kernels need of a head.
+struct RowArgs {
+  const float2* part;  // [N][n_vt]
+  uint32_t n_vt, N, d;
+  const unsigned char *x, *w;
+  uint64_t x_stride, w_stride;  // bytes
+  const int64_t* target;
+  uint64_t vocab;
+  float *loss, *lse;
+  float* total;
+  uint64_t* count;
+};
+
+// Token n by one wave: merges its tiles' maxima and sums, and takes the
+// target's logit as a plain dot product (fp32, a fixed order).  Lane 0 stores;
+// every lane returns the loss.
 template <class T>
-__global__ void __launch_bounds__(kBlock) lse_kernel(const float2* __restrict__ part, uint32_t n_vt,
-                                                     uint32_t N, uint32_t d, const unsigned char* x,
-                                                     uint64_t x_stride, const unsigned char* w,
-                                                     uint64_t w_stride, const int64_t* __restrict__ target,
-                                                     uint64_t vocab, float* __restrict__ loss,
-                                                     float* __restrict__ lse) {
-  const uint32_t n = wave_item_index(), l = threadIdx.x & 63u;
-  if (n >= N) return;
+__device__ __forceinline__ float token_loss(const RowArgs& a, uint32_t n) {
+  const uint32_t l = threadIdx.x & 63u;
+  const int64_t t = a.target[n];
+  const bool live = has_target(t, a.vocab);
+  float dot = 0.0f;
+  if (live) {
+    const unsigned char* p = a.x + (uint64_t)n * a.x_stride;
+    const unsigned char* q = a.w + (uint64_t)t * a.w_stride;
+    const auto add = [&](uint32_t u, uint32_t v) {
+      dot = __builtin_fmaf(T::value(u & 0xFFFFu), T::value(v & 0xFFFFu), dot);
+      dot = __builtin_fmaf(T::value(u >> 16), T::value(v >> 16), dot);
+    };
+    uint32_t c = l * 8u;
+#pragma unroll 4
+    for (; c + 8u <= a.d; c += 512u) {
+      const u32x4 u = load16_any(p + c * 2u), v = load16_any(q + c * 2u);
+      add(u.x, v.x);
+      add(u.y, v.y);
+      add(u.z, v.z);
+      add(u.w, v.w);
+    }
+    for (uint32_t e = 0; e < 7u; ++e)
+      if (c + e < a.d)
+        dot = __builtin_fmaf(T::value(*reinterpret_cast<const uint16_t*>(p + (c + e) * 2u)),
+                             T::value(*reinterpret_cast<const uint16_t*>(q + (c + e) * 2u)), dot);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
+  }
   float m = -__builtin_inff(), s = 0.0f;
-  for (uint32_t k = l; k < n_vt; k += 64) {
-    const float2 p = part[(uint64_t)n * n_vt + k];
+  for (uint32_t k = l; k < a.n_vt; k += 64) {
+    const float2 p = a.part[(uint64_t)n * a.n_vt + k];
     const float M = __builtin_fmaxf(m, p.x);
     s = s * rescale(m, M) + p.y * rescale(p.x, M);
     m = M;
@@ -120,33 +154,28 @@ __global__ void __launch_bounds__(kBlock) lse_kernel(const float2* __restrict__ 
     s = s * rescale(m, M) + ps * rescale(pm, M);
     m = M;
   }
-  const float r = m + kLn2 * __builtin_amdgcn_logf(s);
-  const int64_t t = target[n];
-  float dot = 0.0f;
-  if (has_target(t, vocab)) {
-    const uint16_t* a = reinterpret_cast<const uint16_t*>(x + (uint64_t)n * x_stride);
-    const uint16_t* b = reinterpret_cast<const uint16_t*>(w + (uint64_t)t * w_stride);
-    for (uint32_t k = l; k < d; k += 64) dot = __builtin_fmaf(T::value(a[k]), T::value(b[k]), dot);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
-  }
+  const float r = m + kLn2 * __builtin_amdgcn_logf(s), loss = live ? r - dot : 0.0f;
   if (l == 0) {
-    lse[n] = r;
-    loss[n] = has_target(t, vocab) ? r - dot : 0.0f;
+    a.lse[n] = r;
+    a.loss[n] = loss;
   }
+  return loss;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kBlock) lse_kernel(const RowArgs a) {
+  const uint32_t n = wave_item_index();
+  if (n < a.N) token_loss<T>(a, n);
 }
 
 // total = sum of the losses (in double, thread t adding t, t + 1024, ..., then
 // a fixed tree; rounded once to fp32), count = rows with a target.
-__global__ void __launch_bounds__(1024) loss_total_kernel(const float* __restrict__ loss,
-                                                          const int64_t* __restrict__ target, uint32_t N,
-                                                          uint64_t vocab, float* __restrict__ total,
-                                                          uint64_t* __restrict__ count) {
+__device__ __forceinline__ void store_total(const RowArgs& a, const float* loss) {
   double s = 0.0;
   uint32_t c = 0;
-  for (uint32_t k = threadIdx.x; k < N; k += 1024) {
+  for (uint32_t k = threadIdx.x; k < a.N; k += 1024) {
     s += loss[k];
-    c += has_target(target[k], vocab);
+    c += has_target(a.target[k], a.vocab);
   }
   __shared__ double sw[16];
   __shared__ uint32_t cw[16];
@@ -165,8 +194,24 @@ __global__ void __launch_bounds__(1024) loss_total_kernel(const float* __restric
     s += sw[i];
     c += cw[i];
   }
-  *total = (float)s;
-  if (count) *count = c;
+  *a.total = (float)s;
+  if (a.count) *a.count = c;
+}
+
+__global__ void __launch_bounds__(1024) loss_total_kernel(const RowArgs a) { store_total(a, a.loss); }
+
+// Few tokens: their losses and the total in one launch of one workgroup.
+constexpr uint32_t kFewTokens = 32;
+
+template <class T>
+__global__ void __launch_bounds__(1024) few_tokens_kernel(const RowArgs a) {
+  __shared__ float losses[kFewTokens];
+  for (uint32_t n = threadIdx.x >> 6; n < a.N; n += 16) {
+    const float loss = token_loss<T>(a, n);
+    if ((threadIdx.x & 63u) == 0) losses[n] = loss;
+  }
+  __syncthreads();
+  store_total(a, losses);
 }
 
 // The logits' row from its tiles' rows; with ref, a difference under col_mask
@@ -201,8 +246,9 @@ constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
   uint32_t N, d, V, d_pad;
-  uint32_t tile;         // 256 or 128
-  uint32_t nt, vt, md;   // tiles of the tokens, of the whole vocabulary, of d
+  uint32_t tile;         // 256 or 128, of the logits' product
+  uint32_t nt, vt;       // tiles of the tokens, of the whole vocabulary
+  uint32_t ptile;        // 256 or 128, of the gradient's products
   bool copy_x, copy_w;   // the operand needs an aligned copy
   bool any;              // w's rows are read where they lie, off 16-byte boundaries
   uint32_t piece;        // vocabulary rows of a piece
@@ -228,9 +274,39 @@ int32_t check_head(const sdc_head* h) {
   return SDC_OK;
 }
 
-// 256 x 256 tiles where they fill the chip, else 128 x 128.
-uint32_t tile_of(uint64_t n, uint64_t vocab) {
-  return n > 128 && (uint64_t)tiles(n, 256) * tiles(vocab, 256) >= 192 ? 256u : 128u;
+// The tile of the logits' product, from the rounds that 256 CUs take: a 128 x
+// 128 tile has a quarter of the work at 1.15 times the cost (twice the operand
+// bytes per operation).  The larger tile wins where it fills whole rounds, the
+// smaller where it would leave CUs idle or tiles half empty.  Measured (us, 128
+// / 256): 100 x 2048 x 50304 53 / 79, 300 x 1000 x 16000 33 / 43, 2000 x 512 x
+// 8000 30 / 28, 800 x 2048 x 50304 188 / 232, 1500 x 4096 x 30000 370 / 332.
+uint32_t logit_tile(uint64_t n, uint64_t vocab) {
+  const auto rounds = [&](uint32_t t) { return ((uint64_t)tiles(n, t) * tiles(vocab, t) + 255) / 256; };
+  return (double)rounds(128) * (1.15 / 4) < (double)rounds(256) ? 128u : 256u;
+}
+
+// Parts that dx's sum over `rows` vocabulary rows is split into: 256 tiles.
+uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
+  const uint32_t per = tiles(n, tile) * tiles(d, tile);
+  return std::max(1u, std::min(256u / std::max(per, 1u), tiles(rows, 256)));
+}
+
+// The tile of the gradient's two products over `rows` vocabulary rows: the
+// time of all tiles, in k steps and the steps' worth of an epilogue (6 of a
+// 256 x 256 tile, 3 of the smaller), over the workgroups that run at a time (one of
+// 256, or two of 128 a CU, whose steps take 0.575 of the time), or that of the
+// longest tile.  Measured (the whole gradient in us, 128 / 256): 4096 x 256 x
+// 12800 126 / 220, 600 x 1024 x 20000 109 / 137, 800 x 2048 x 50304 615 / 638,
+// 1500 x 4096 x 30000 1275 / 1085.
+uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
+  const auto steps = [&](uint32_t t) {
+    const double k_dw = (double)tiles(n, kTileK), k_dx = (double)tiles(rows, kTileK);
+    const double n_dw = (double)tiles(d, t) * tiles(rows, t), n_dx = (double)tiles(n, t) * tiles(d, t);
+    const uint32_t splits = dx_splits(n, d, rows, t);
+    const double all = n_dw * k_dw + n_dx * k_dx + (n_dw + n_dx * splits) * (t == 256 ? 6 : 3);
+    return std::max(all / (t == 256 ? 256 : 512), std::max(k_dw, k_dx / splits));
+  };
+  return 0.575 * steps(128) < steps(256) ? 128u : 256u;
 }
 
 // grad: the sizes of the gradient's pieces; else those of the forward pass,
@@ -246,10 +322,9 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.any = h->d % 8 || h->w_stride % 8 || reinterpret_cast<uintptr_t>(h->w) % 16;
   p.copy_w = p.any && h->d < 8;
   p.any = p.any && !p.copy_w;
-  p.tile = tile_of(p.N, p.V);
+  p.tile = logit_tile(p.N, p.V);
   p.nt = tiles(p.N, p.tile);
   p.vt = tiles(p.V, p.tile);
-  p.md = tiles(p.d, p.tile);
   // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
   // of that on, the one that needs the fewest rounds of 256 tiles.
   const uint32_t nt = p.nt, vt = p.vt;
@@ -271,7 +346,8 @@ Head plan_head(const sdc_head* h, bool grad) {
   const uint64_t piece = (uint64_t)best * p.tile;
   p.piece = (uint32_t)std::min<uint64_t>(piece, up(p.V, 8));
   p.pieces = (vt + best - 1) / best;
-  p.splits = std::max(1u, std::min(p.N ? 256u / (nt * p.md) : 1u, best));
+  p.ptile = product_tile(p.N, p.d, p.piece);
+  p.splits = dx_splits(p.N, p.d, p.piece, p.ptile);
   p.n_tiles = nt * vt;
   return p;
 }
@@ -375,25 +451,27 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
       const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0);
       if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
       a.rows = d_row ? rows : nullptr;
-      const HeadLaunch l = {h->dtype, p.tile};
+      const HeadLaunch l = {h->dtype, p.tile, p.ptile};
       if ((st = p.any ? launch_logit_lse_any(l, a, s) : launch_logit_lse16(l, a, s))) return st;
       rows += a.n_tiles;
       a.part += tiles(n, p.tile);
     }
-    st = for_type(h->dtype, p.tile, [&](auto t, auto) {
-      typedef decltype(t) T;
-      hipLaunchKernelGGL(lse_kernel<T>, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s,
-                         reinterpret_cast<const float2*>(ws + o.part), a.n_vt, p.N, p.d,
-                         static_cast<const unsigned char*>(h->x), 2 * h->x_stride,
-                         static_cast<const unsigned char*>(h->w), 2 * h->w_stride, h->target, h->vocab, d_loss,
-                         d_lse);
-      return launch_status();
-    });
-    if (st) return st;
   }
-  hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, s, d_loss, h->target, p.N, h->vocab, d_total,
-                     d_count);
-  if ((st = launch_status())) return st;
+  const RowArgs r = {reinterpret_cast<const float2*>(ws + o.part), p.vt, p.N, p.d,
+                     static_cast<const unsigned char*>(h->x), static_cast<const unsigned char*>(h->w),
+                     2 * h->x_stride, 2 * h->w_stride, h->target, h->vocab, d_loss, d_lse, d_total, d_count};
+  st = for_type(h->dtype, p.tile, [&](auto t, auto) {
+    typedef decltype(t) T;
+    if (p.N <= kFewTokens) {
+      hipLaunchKernelGGL(few_tokens_kernel<T>, dim3(1), dim3(1024), 0, s, r);
+      return launch_status();
+    }
+    hipLaunchKernelGGL(lse_kernel<T>, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s, r);
+    if (int32_t e = launch_status()) return e;
+    hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, s, r);
+    return launch_status();
+  });
+  if (st) return st;
   if (d_row) return merge_logit_row(o, p, ws, nullptr, 0, d_row, nullptr, s);
   return SDC_OK;
 }
@@ -452,16 +530,16 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     x.d = p.d;
     x.rows = n;
     x.xcds = dev.xcds;
-    x.nt = p.nt;
-    x.md = p.md;
+    x.nt = tiles(p.N, p.ptile);
+    x.md = tiles(p.d, p.ptile);
     x.n_dx = x.nt * x.md * p.splits;
-    x.n_dw = x.md * tiles(n, p.tile);
+    x.n_dw = x.md * tiles(n, p.ptile);
     x.chunk = (uint32_t)up((n + p.splits - 1) / p.splits, kTileK);
     x.part = dxp;
     x.first = k == 0;
     x.grad = d_grad;
     x.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
-    const HeadLaunch l = {h->dtype, p.tile};
+    const HeadLaunch l = {h->dtype, p.tile, p.ptile};
     if ((st = p.any ? launch_gradient_any(l, a, x, s) : launch_gradient16(l, a, x, s))) return st;
   }
   st = for_type(h->dtype, p.tile, [&](auto t, auto) {

@@ -44,9 +44,10 @@ struct ProductArgs {
   uint16_t* dw;        // of the piece's first row
 };
 
-// Launches over the tiles of one piece (tile: 256 or 128; at: how w's rows lie).
+// Launches over the tiles of one piece; tile, ptile: 256 or 128, of the logits'
+// product and of the gradient's.
 struct HeadLaunch {
-  uint32_t dtype, tile;
+  uint32_t dtype, tile, ptile;
 };
 int32_t launch_logit_lse16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
 int32_t launch_logit_lse_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
@@ -321,14 +322,20 @@ int32_t launch_logit_lse(const HeadLaunch& h, const LogitArgs& a, hipStream_t s)
 
 template <RowsAt AT>
 int32_t launch_gradient(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s) {
-  return for_type(h.dtype, h.tile, [&](auto t, auto tile) {
+  const int32_t st = for_type(h.dtype, h.tile, [&](auto t, auto tile) {
     typedef decltype(t) T;
     constexpr uint32_t TILE = decltype(tile)::value;
     const dim3 grid(a.n_tiles), block(gemm_block(TILE));
     if (a.rows) hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, true>), grid, block, lds_bytes(TILE), s, a);
     else hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, false>), grid, block, lds_bytes(TILE), s, a);
-    if (int32_t e = launch_status()) return e;
-    hipLaunchKernelGGL((products_kernel<T, TILE, AT>), dim3(x.n_dx + x.n_dw), block, lds_bytes(TILE), s, x);
+    return launch_status();
+  });
+  if (st) return st;
+  return for_type(h.dtype, h.ptile, [&](auto t, auto tile) {
+    typedef decltype(t) T;
+    constexpr uint32_t TILE = decltype(tile)::value;
+    hipLaunchKernelGGL((products_kernel<T, TILE, AT>), dim3(x.n_dx + x.n_dw), dim3(gemm_block(TILE)),
+                       lds_bytes(TILE), s, x);
     return launch_status();
   });
 }
