@@ -1,6 +1,7 @@
 /*
  * sdc.h -- C ABI of libsdc.so, the MI355X (gfx950) integrity scan for
- * silent-data-corruption checks in data-parallel training.
+ * silent-data-corruption checks in data-parallel training, with the loss of a
+ * linear head and the optimizer step between which the checks stand.
  *
  * What the library computes comes from these pages:
  *   [BLOG] AWS Machine Learning Blog, "Detecting and recovering from silent
@@ -32,9 +33,11 @@
  *     their device outputs are valid once the stream reaches that point.
  *   - The fingerprints are arithmetic on unsigned 64-bit integers modulo 2^64
  *     over raw bit patterns (floating-point data are never converted), so
- *     every row is exact and independent of launch shape and scheduling.  The
- *     one floating-point result, sdc_sqnorm's squared norms, is summed in an
- *     order fixed by the plan.
+ *     every row is exact and independent of launch shape and scheduling.
+ *     Floating-point results (squared norms, the optimizer step, the loss of a
+ *     linear head and its gradient) are summed in an order fixed by the plan or
+ *     the sizes, never by scheduling: a call repeated on the same inputs gives
+ *     the same bits.
  *   - Functions are thread-safe.  Two scans that write the same output rows
  *     must not run concurrently.
  *   - Launch shapes: scans of large items (list scans whose items average at
@@ -572,7 +575,7 @@ int32_t sdc_cross_entropy(const sdc_head* h_head, void* d_ws, uint64_t ws_bytes,
  * onehot) * *d_grad, zero in rows without a target,
  *   d_dx = dz w  (n x d, contiguous)      d_dw = dz^T x  (vocab x d, contiguous)
  * both of the head's dtype, summed in fp32 from dz rounded to that type's
- * precision.  d_lse: the forward pass'.  d_row: as there, of the recomputed
+ * precision; one of the two may be NULL and is then not computed.  d_lse: the forward pass'.  d_row: as there, of the recomputed
  * logits; with d_ref (the forward pass' row) a difference under col_mask adds 1
  * to *d_mismatch (required then; the caller clears it).
  * ASYNCHRONOUS on stream.  Errors as sdc_cross_entropy. */

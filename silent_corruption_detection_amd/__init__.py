@@ -1,5 +1,6 @@
 """Python binding of libsdc.so -- the MI355X integrity scan for silent data
-corruption checks (see include/sdc.h for the C ABI and the semantics).
+corruption checks, the loss of a linear head and the optimizer step (see
+include/sdc.h for the C ABI and the semantics).
 
 Argument marshalling only: every computation runs in the library's HIP
 kernels.  PyTorch provides device memory and streams.  Importing this module
@@ -735,20 +736,37 @@ class AdamwPlan:
         return self.info.total_elems
 
 
-def _adamw_column(table, col, tensors, n, name, check):
-    """Fills pointer column `col` from a list of n tensors (None allowed)."""
+def _adamw_column(table, name, tensors, numels, dtypes, dev):
+    """Fills the pointer column `name` from a list of tensors (None allowed: a
+    null pointer) after checking each; returns (those that are not None, their
+    indices).  numels, dtypes: what each must have (dtypes: sets).  Column-wise,
+    as a Python step per tensor and check costs too much for long lists."""
+    n = len(numels)
     if tensors is None:
-        return []
+        return [], []
     if len(tensors) != n:
         raise ValueError(f"{name} has {len(tensors)} entries for {n} params")
-    for k, t in enumerate(tensors):
-        if t is None:
-            continue
-        check(k, t)
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{k}] is not contiguous (a plan reads and writes it in place)")
-        table[col][k] = t.data_ptr() if t.numel() else 0
-    return [t for t in tensors if t is not None]
+    idx = [k for k, t in enumerate(tensors) if t is not None]
+    ts = [tensors[k] for k in idx] if len(idx) != n else list(tensors)
+
+    def refuse(bad, error, text):
+        for k, t, b in zip(idx, ts, bad):
+            if b:
+                raise error(f"{name}[{k}] {text(k, t)}")
+
+    devs = list(map(torch.Tensor.get_device, ts))
+    refuse([d < 0 for d in devs], ValueError, lambda k, t: "is not on a GPU")
+    if dev is not None:
+        refuse([d != dev.index for d in devs], ValueError, lambda k, t: f"must be on {dev}, not {t.device}")
+    refuse([t.dtype not in dtypes[k] for k, t in zip(idx, ts)], TypeError,
+           lambda k, t: f"has the unsupported dtype {t.dtype}")
+    got = list(map(torch.Tensor.numel, ts))
+    refuse([m != numels[k] for k, m in zip(idx, got)], ValueError,
+           lambda k, t: f"has {t.numel()} elements, needs {numels[k]}")
+    refuse([not c for c in map(torch.Tensor.is_contiguous, ts)], ValueError,
+           lambda k, t: "is not contiguous (a plan reads and writes it in place)")
+    table[name][idx] = [p if m else 0 for p, m in zip(map(torch.Tensor.data_ptr, ts), got)]
+    return ts, idx
 
 
 def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None,
@@ -768,44 +786,24 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     if not n:
         raise ValueError("the list is empty")
     table = np.zeros(n, dtype=_ADAMW_DESC)
-    dev = None
-    for k, p in enumerate(params):
-        if p.get_device() < 0:
-            raise ValueError(f"params[{k}] is not on a GPU")
-        if dev is None:
-            dev = _cuda_device(p.get_device())
-        if _TORCH_DTYPE.get(p.dtype) not in (F32, BF16, F16):
-            raise TypeError(f"params[{k}]: unsupported dtype {p.dtype}")
-        if exp_avg[k].dtype not in _ADAMW_STATE if k < len(exp_avg) and exp_avg[k] is not None else True:
-            raise TypeError(f"exp_avg[{k}] must be float32 or float8_e4m3fn")
-        table["numel"][k] = p.numel()
-        table["param_dtype"][k] = _TORCH_DTYPE[p.dtype]
-        table["grad_dtype"][k] = _TORCH_DTYPE[p.dtype]
-        table["state_dtype"][k] = _ADAMW_STATE[exp_avg[k].dtype]
-
-    def same(name, dtypes, numel=lambda k: params[k].numel()):
-        def check(k, t):
-            if not _on_device(t, dev):
-                raise ValueError(f"{name}[{k}] must be on {dev}, not {t.device}")
-            if t.dtype not in dtypes(k):
-                raise TypeError(f"{name}[{k}]: unsupported dtype {t.dtype}")
-            if t.numel() != numel(k):
-                raise ValueError(f"{name}[{k}] has {t.numel()} elements, needs {numel(k)}")
-        return check
-
-    floats = (torch.float32, torch.bfloat16, torch.float16)
-    blocks = same("a scale", lambda k: (torch.uint8,), lambda k: -(-params[k].numel() // _STATE_BLOCK))
-    keep = _adamw_column(table, "param", params, n, "params", same("params", lambda k: floats))
-    keep += _adamw_column(table, "grad", grads, n, "grads", same("grads", lambda k: floats))
-    keep += _adamw_column(table, "exp_avg", exp_avg, n, "exp_avg", same("exp_avg", lambda k: (exp_avg[k].dtype,)))
-    keep += _adamw_column(table, "exp_avg_sq", exp_avg_sq, n, "exp_avg_sq",
-                          same("exp_avg_sq", lambda k: (exp_avg[k].dtype,)))
-    keep += _adamw_column(table, "master", master, n, "master", same("master", lambda k: (torch.float32,)))
-    keep += _adamw_column(table, "exp_avg_scale", exp_avg_scale, n, "exp_avg_scale", blocks)
-    keep += _adamw_column(table, "exp_avg_sq_scale", exp_avg_sq_scale, n, "exp_avg_sq_scale", blocks)
-    for k, g in enumerate(grads):
-        if g is not None:
-            table["grad_dtype"][k] = _TORCH_DTYPE[g.dtype]
+    numels = [p.numel() for p in params]
+    floats = [{torch.float32, torch.bfloat16, torch.float16}] * n
+    dev = _cuda_device(params[0].get_device()) if params[0].get_device() >= 0 else None
+    keep, _ = _adamw_column(table, "param", params, numels, floats, dev)
+    ms, idx = _adamw_column(table, "exp_avg", exp_avg, numels, [_ADAMW_STATE] * n, dev)
+    if len(ms) != n:
+        raise ValueError("every param needs an exp_avg")
+    vs, _ = _adamw_column(table, "exp_avg_sq", exp_avg_sq, numels, [{t.dtype} for t in ms], dev)
+    gs, at = _adamw_column(table, "grad", grads, numels, floats, dev)
+    keep += ms + vs + gs
+    keep += _adamw_column(table, "master", master, numels, [{torch.float32}] * n, dev)[0]
+    blocks = [-(-m // _STATE_BLOCK) for m in numels]
+    for name, scales in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
+        keep += _adamw_column(table, name, scales, blocks, [{torch.uint8}] * n, dev)[0]
+    table["numel"] = numels
+    table["param_dtype"] = table["grad_dtype"] = [_TORCH_DTYPE[p.dtype] for p in params]
+    table["grad_dtype"][at] = [_TORCH_DTYPE[g.dtype] for g in gs]
+    table["state_dtype"] = [_ADAMW_STATE[t.dtype] for t in ms]
     if group is not None:
         if len(group) != n or min(group) < 0:
             raise ValueError(f"group needs {n} indices, none negative")
@@ -950,27 +948,30 @@ def sdc_cross_entropy(x, w, target, count=None, row=None, ws=None, stream=None):
 
 
 def sdc_cross_entropy_grad(x, w, target, lse, grad, dx=None, dw=None, row=None, ref=None, mismatch=None,
-                           col_mask=COL_ALL, ws=None, stream=None):
+                           col_mask=COL_ALL, ws=None, stream=None, need_dx=True, need_dw=True):
     """(dx, dw): the gradient of the total loss times `grad` (an fp32 [1]
     tensor), from the logits computed again (asynchronous; see include/sdc.h).
 
     lse: the forward pass'.  dx, dw: contiguous outputs of x's and w's shape and
-    dtype (allocated by default).  row: receives the recomputed logits'
-    fingerprint row.  ref, mismatch: the forward pass' row and an int32 [1]
-    counter that a difference under col_mask adds 1 to."""
+    dtype (allocated by default; None for one that need_dx / need_dw leaves
+    out).  row: receives the recomputed logits' fingerprint row.  ref, mismatch:
+    the forward pass' row and an int32 [1] counter that a difference under
+    col_mask adds 1 to."""
     h, dev, keep = _head(x, w, target)
     n, d, vocab = x.shape[0], x.shape[1], w.shape[0]
     _arg(lse, "lse", torch.float32, n, dev)
     _arg(grad, "grad", torch.float32, 1, dev)
     made = [t for t in keep if t is not x and t is not w]
-    if dx is None:
-        dx = torch.empty((n, d), dtype=x.dtype, device=dev)
-        made.append(dx)
-    _arg(dx, "dx", x.dtype, n * d, dev)
-    if dw is None:
-        dw = torch.empty((vocab, d), dtype=x.dtype, device=dev)
-        made.append(dw)
-    _arg(dw, "dw", x.dtype, vocab * d, dev)
+
+    def output(t, name, shape, needed):
+        if not needed:
+            return None
+        if t is None:
+            t = torch.empty(shape, dtype=x.dtype, device=dev)
+            made.append(t)
+        return _arg(t, name, x.dtype, shape[0] * shape[1], dev)
+
+    dx, dw = output(dx, "dx", (n, d), need_dx), output(dw, "dw", (vocab, d), need_dw)
     if ref is not None and row is None:
         row = torch.empty((1, 4), dtype=torch.int64, device=dev)
         made.append(row)
@@ -982,8 +983,8 @@ def sdc_cross_entropy_grad(x, w, target, lse, grad, dx=None, dw=None, row=None, 
         made.append(ws)
     with _device_guard(dev):
         s = _scan_stream(stream, dev, made)
-        _check(_lib.sdc_cross_entropy_grad(ctypes.byref(h), lse.data_ptr(), grad.data_ptr(), ws.data_ptr(),
-                                           ws.numel(), dx.data_ptr(), dw.data_ptr(), ref_p, col_mask,
-                                           None if row is None else row.data_ptr(), mis_p, s),
-               "sdc_cross_entropy_grad")
+        _check(_lib.sdc_cross_entropy_grad(
+            ctypes.byref(h), lse.data_ptr(), grad.data_ptr(), ws.data_ptr(), ws.numel(),
+            None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), ref_p, col_mask,
+            None if row is None else row.data_ptr(), mis_p, s), "sdc_cross_entropy_grad")
     return dx, dw

@@ -482,8 +482,8 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
                                           sdc_stream_t stream) {
   int32_t st = check_head(h);
   if (st) return st;
-  if (d_grad == nullptr || d_ws == nullptr || d_dw == nullptr ||
-      (h->n > 0 && (d_lse == nullptr || d_dx == nullptr)))
+  if (d_grad == nullptr || d_ws == nullptr || (d_dx == nullptr && d_dw == nullptr) ||
+      (h->n > 0 && d_lse == nullptr))
     return SDC_ERR_INVALID;
   if (d_ref != nullptr && (d_row == nullptr || d_mismatch == nullptr || col_mask == 0 || (col_mask & ~15u)))
     return SDC_ERR_INVALID;
@@ -500,15 +500,17 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
   hipStream_t s = as_stream(stream);
   unsigned char* ws = static_cast<unsigned char*>(d_ws);
   if (p.N == 0) {
-    hipLaunchKernelGGL(zero16_kernel, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(d_dw),
-                       (uint64_t)p.V * p.d);
+    if (d_dw)
+      hipLaunchKernelGGL(zero16_kernel, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(d_dw),
+                         (uint64_t)p.V * p.d);
     if ((st = launch_status())) return st;
     return d_row ? merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s) : SDC_OK;
   }
   // x without what rows that have no target hold: dz is zero there, but 0 * NaN is not
-  st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d, p.d_pad,
-                            reinterpret_cast<uint16_t*>(ws + o.xm), h->target, h->vocab}, s);
-  if (st) return st;
+  if (d_dw && (st = launch_pack(PackArgs{static_cast<const unsigned char*>(h->x), 2 * h->x_stride, p.N, p.d,
+                                         p.d_pad, reinterpret_cast<uint16_t*>(ws + o.xm), h->target, h->vocab},
+                                s)))
+    return st;
   LogitArgs a = {};
   a.xcds = dev.xcds;
   a.target = h->target;
@@ -532,23 +534,25 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     x.xcds = dev.xcds;
     x.nt = tiles(p.N, p.ptile);
     x.md = tiles(p.d, p.ptile);
-    x.n_dx = x.nt * x.md * p.splits;
-    x.n_dw = x.md * tiles(n, p.ptile);
+    x.n_dx = d_dx ? x.nt * x.md * p.splits : 0;
+    x.n_dw = d_dw ? x.md * tiles(n, p.ptile) : 0;
     x.chunk = (uint32_t)up((n + p.splits - 1) / p.splits, kTileK);
     x.part = dxp;
     x.first = k == 0;
     x.grad = d_grad;
-    x.dw = static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d;
+    x.dw = d_dw ? static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d : nullptr;
     const HeadLaunch l = {h->dtype, p.tile, p.ptile};
     if ((st = p.any ? launch_gradient_any(l, a, x, s) : launch_gradient16(l, a, x, s))) return st;
   }
-  st = for_type(h->dtype, p.tile, [&](auto t, auto) {
-    typedef decltype(t) T;
-    hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 1023) / 1024), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
-                       h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));
-    return launch_status();
-  });
-  if (st) return st;
+  if (d_dx) {
+    st = for_type(h->dtype, p.tile, [&](auto t, auto) {
+      typedef decltype(t) T;
+      hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 1023) / 1024), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
+                         h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));
+      return launch_status();
+    });
+    if (st) return st;
+  }
   if (d_row) return merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s);
   return SDC_OK;
 }

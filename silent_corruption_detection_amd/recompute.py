@@ -23,11 +23,18 @@ make the non-reentrant `checkpoint` calls of the forward pass inside
 the recomputation as soon as the saved tensors are rebuilt, before the
 segment's output exists; the setting is read when `checkpoint` is called).
 A segment that was not recomputed is reported in `result()["not_recomputed"]`.
+
+`RecomputeAudit.cross_entropy(k, x, w, target)` is the last segment of a model
+with a large vocabulary: the loss of a linear head whose logits are computed in
+the forward pass, never kept, and computed again in the backward pass.  Both
+passes fingerprint them where they are computed; a difference is counted and
+reported like any other segment's.
 """
 import torch
 
 from . import (COL_ALL, _current_stream_handle, rows_numpy, sdc_fingerprint_diff, sdc_fingerprint_tensor,
                sdc_tensor_ws_bytes)
+from .loss import linear_cross_entropy
 
 
 class RecomputeAudit:
@@ -108,6 +115,27 @@ class RecomputeAudit:
                                        mismatch=self._mismatch_at[k], col_mask=self.col_mask,
                                        ws=self._workspace(t))
         self.calls[k] = c + 1
+
+    def cross_entropy(self, k, x, w, target, reduction="mean"):
+        """The loss of a linear head as segment k (see
+        loss.linear_cross_entropy): the fingerprint row of its logits is stored,
+        and compared when the backward pass computes them again."""
+        if not 0 <= k < self.n:
+            raise IndexError(f"segment {k} out of range 0..{self.n - 1}")
+        if self.calls[k]:
+            raise RuntimeError(f"segment {k} ran before in this step (call begin_step())")
+        r = k * self.outputs
+
+        def checked():
+            if self.calls[k] != 1:
+                raise RuntimeError(f"segment {k}'s backward pass ran again in one step (call begin_step())")
+            self.calls[k] = 2
+            return dict(row=self._recomputed_rows[r], ref=self._original_rows[r], mismatch=self._mismatch_at[k],
+                        col_mask=self.col_mask)
+
+        loss = linear_cross_entropy(x, w, target, reduction, row=self._original_rows[r], checked=checked)
+        self.calls[k] = 1
+        return loss
 
     def result(self):
         """After backward (synchronises): segments whose recomputation differed

@@ -70,8 +70,9 @@ def test_refused_calls():
         assert f(**{k: None}) == INVALID, k
     assert f(nbytes=16) == WORKSPACE
     assert f(ws=0x10008) == ALIGN and f(row=0x8008) == ALIGN
-    for k in ("lse", "grad", "ws", "dx", "dw"):
+    for k in ("lse", "grad", "ws"):
         assert g(**{k: None}) == INVALID, k
+    assert g(dx=None, dw=None) == INVALID
     assert g(nbytes=1000) == WORKSPACE
     for k, v in (("ws", 0x10008), ("lse", 0x4002), ("grad", 0x5001), ("dx", 0x6001), ("dw", 0x7001),
                  ("row", 0x8008)):
