@@ -29,7 +29,7 @@ SANITIZE_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitiz
                   "-Xarch_host", "-g"]
 SOURCES = ["scan.hip", "tensor.hip", "nonfinite.hip", "norm.hip", "compare.hip", "readsum.hip",
            "noalloc.hip", "adamw.hip", "adamw32.hip", "adamw8.hip", "xent.hip", "xent16.hip",
-           "xent_any.hip", "plan.cpp", "device.cpp", "misc.cpp"]
+           "xent_any.hip", "xent_few.hip", "plan.cpp", "device.cpp", "misc.cpp"]
 ARCH = os.environ.get("SDC_OFFLOAD_ARCH", "gfx950")
 NOISE = "is not a recognized feature for this target"
 

@@ -2,27 +2,27 @@
 // gfx950: C[m][n] = sum_k A(m, k) B(n, k) for 16-bit operands whose rows are
 // contiguous either in k or, "k-major", in m (n), accumulated in fp32 by MFMA.
 //
-// A workgroup computes a TILE x TILE tile of C, TILE 256 (8 waves) or, where
-// those would be too few to fill the chip, 128 (4 waves).  Wave (wm, wn),
-// wm = 0..1, wn = 0..TILE / 64 - 1, holds rows wm TILE / 2 .. and columns
-// 64 wn .. of it as TILE / 32 x 4 groups of 16 x 16 (for 256: 128 accumulator
-// registers).  k advances 64 at a time through two LDS buffers (64 KiB each
-// for 256): the next buffer is filled by direct global-to-LDS loads (16 bytes
-// a lane, no registers) while the current one is multiplied.  Four buffers of
-// 32 k instead measured 4 to 10 % slower where rows run along k (64-byte
-// pieces of rows) and equal where they do not.
+// A workgroup computes an M x N tile of C (a Shape): 256 x 256 by 8 waves, 128 x
+// 128 by 4 where the larger tiles would be too few to fill the chip, and 128 x
+// 32 by 4 for few rows of B.  Wave (wm, wn) holds M / WM rows and N / WN columns
+// of it as I x J groups of 16 x 16 (for 256 x 256: 128 accumulator registers).
+// k advances 64 at a time through two LDS buffers (64 KiB each for 256 x 256):
+// the next buffer is filled by direct global-to-LDS loads (16 bytes a lane, no
+// registers) while the current one is multiplied.  Four buffers of 32 k instead
+// measured 4 to 10 % slower where rows run along k (64-byte pieces of rows) and
+// equal where they do not.
 // Direct loads write LDS in lane order, so the permutations below, which keep
 // the lanes of one LDS read on different banks, are made in the addresses they
 // read from.
-//   rows along k: TILE rows of 128 bytes; the eight 16-byte chunks of a row are
+//   rows along k: rows of 128 bytes; the eight 16-byte chunks of a row are
 //     permuted by its low three bits.  An operand register group is one
 //     16-byte read per lane.
-//   k-major: 64 rows of 2 TILE bytes; the TILE / 16 granules of 32 bytes
-//     (16 columns) of row k are permuted by f(k) = k & 3 | (k >> 3 & 3) << 2,
-//     which differs over the 16 rows that one transposing read takes.  A group
-//     is two transposing 8-byte reads (each gives a lane four k of its column),
-//     which is what spares transposed copies of the weights, the inputs and dz.
-// Measured alone on random data, TILE 256: 4096 x 32768 x 2048 (rows along k)
+//   k-major: 64 rows of 2 M (2 N) bytes; their granules of 32 bytes (16 columns)
+//     in row k are permuted by f(k) = k & 3 | (k >> 3 & 3) << 2, which differs
+//     over the 16 rows that one transposing read takes.  A group is two
+//     transposing 8-byte reads (each gives a lane four k of its column), which
+//     is what spares transposed copies of the weights, the inputs and dz.
+// Measured alone on random data, 256 x 256: 4096 x 32768 x 2048 (rows along k)
 // 431 us (1275 TFLOP/s), 2048 x 32768 x 4096 (k-major) 455 us (1210).
 #pragma once
 
@@ -32,9 +32,18 @@ namespace sdc {
 namespace {
 
 constexpr uint32_t kTileK = 64;  // k per LDS buffer
-constexpr uint32_t gemm_block(uint32_t tile) { return 2 * tile; }              // threads
-constexpr uint32_t buf_bytes(uint32_t tile) { return 2 * tile * kTileK * 2; }  // A and B of one k step
-constexpr uint32_t gemm_lds(uint32_t tile) { return 2 * buf_bytes(tile); }
+
+template <uint32_t M_, uint32_t N_, uint32_t WM_, uint32_t WN_>
+struct Shape {
+  static constexpr uint32_t M = M_, N = N_, WM = WM_, WN = WN_;
+  static constexpr uint32_t kThreads = 64 * WM * WN;
+  static constexpr int I = M / WM / 16, J = N / WN / 16;
+  static constexpr uint32_t kA = M * kTileK * 2, kBuf = (M + N) * kTileK * 2;  // bytes of A, of both, of one k step
+  static constexpr uint32_t kLds = 2 * kBuf;
+};
+typedef Shape<256, 256, 2, 4> BigTile;
+typedef Shape<128, 128, 2, 2> SmallTile;
+typedef Shape<128, 32, 4, 1> FewTile;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -81,13 +90,13 @@ struct Operand {
 
 // Where a thread's accumulators stand in the tile: element r of acc[i][j] is
 // C[row(i) + r][col(j)].
-template <uint32_t TILE>
+template <class S>
 struct Place {
   uint32_t lane, wm, wn;
   __device__ __forceinline__ Place()
-      : lane(threadIdx.x & 63u), wm(threadIdx.x / TILE), wn((threadIdx.x >> 6) & (TILE / 64u - 1u)) {}
-  __device__ __forceinline__ uint32_t row(int i) const { return wm * (TILE / 2) + i * 16u + (lane >> 4) * 4u; }
-  __device__ __forceinline__ uint32_t col(int j) const { return wn * 64u + j * 16u + (lane & 15u); }
+      : lane(threadIdx.x & 63u), wm((threadIdx.x >> 6) / S::WN), wn((threadIdx.x >> 6) % S::WN) {}
+  __device__ __forceinline__ uint32_t row(int i) const { return wm * (S::M / S::WM) + i * 16u + (lane >> 4) * 4u; }
+  __device__ __forceinline__ uint32_t col(int j) const { return wn * (S::N / S::WN) + j * 16u + (lane & 15u); }
 };
 
 #define SDC_LDS __attribute__((address_space(3)))
@@ -108,10 +117,12 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* src, uint32_t b
       : "memory");
 }
 
-// How an operand's rows may lie: at 16-byte boundaries (kAt16), read straight
-// into LDS; or anywhere (kAny: rows of at least 8 elements at any even address,
-// of any length), read through registers, which direct loads to LDS cannot.
-enum RowsAt : int { kAt16, kAny };
+// How A's rows may lie: at 16-byte boundaries (kAt16), read straight into LDS;
+// or anywhere (kAny: rows of at least 8 elements at any even address, of any
+// length), read through registers, which direct loads to LDS cannot.  kDeep:
+// anywhere, and both operands through registers three steps ahead (see
+// gemm_tile_deep).
+enum RowsAt : int { kAt16, kAny, kDeep };
 
 // Sixteen bytes at any even address.
 __device__ __forceinline__ u32x4 load16_any(const unsigned char* p) {
@@ -131,18 +142,19 @@ __device__ __forceinline__ u32x4 drop_elements(u32x4 v, uint32_t n) {
 
 // One operand's side of the tile: its loads into LDS, step after step, and its
 // reads.
-template <class T, uint32_t TILE, bool KMAJOR, RowsAt AT>
+template <class T, uint32_t ROWS, uint32_t THREADS, bool KMAJOR, RowsAt AT>
 struct Side {
-  static constexpr uint32_t kRow = 2 * TILE;         // bytes of a k-major row
-  static constexpr uint32_t kPass = 2 * TILE * 16;   // bytes that one load of every thread fills
-  static constexpr uint32_t kGranules = TILE / 16 - 1;
-  const unsigned char* p[4];  // of the thread's loads of the next step
-  uint64_t step;              // bytes from one step to the next
-  uint32_t limit;             // k from here on reads as zero
-  uint32_t k_in;              // k of the thread's first load within a step
-  uint32_t off;               // of the lane's LDS reads
-  uint32_t drop[4];           // kAny, k-major: elements past the end of the rows that a load starts before
-  u32x4 held[4];              // kAny: the loads of the next step
+  static constexpr uint32_t kLoads = ROWS * 8 / THREADS;  // 16-byte loads of a thread per step
+  static constexpr uint32_t kRow = 2 * ROWS;              // bytes of a k-major row
+  static constexpr uint32_t kPass = THREADS * 16;         // bytes that one load of every thread fills
+  static constexpr uint32_t kGranules = ROWS / 16 - 1;
+  static_assert(kLoads * THREADS == ROWS * 8 && (!KMAJOR || THREADS == 2 * ROWS), "the loads cover a step");
+  const unsigned char* p[kLoads];  // of the thread's loads of the next step
+  uint64_t step;                   // bytes from one step to the next
+  uint32_t limit;                  // k from here on reads as zero
+  uint32_t k_in;                   // k of the thread's first load within a step
+  uint32_t off;                    // of the lane's LDS reads
+  uint32_t drop[kLoads];           // kAny, k-major: elements past the end of the rows that a load starts before
 
   // at0: first row of C's index; base: LDS row (rows along k) or granule
   // (k-major) of the wave's first group.  Rows along k past the operand's last
@@ -151,12 +163,12 @@ struct Side {
     const uint32_t t = threadIdx.x, lane = t & 63u;
     if constexpr (KMAJOR) {
       limit = o.rows;
-      k_in = t / (TILE / 8);
+      k_in = t / (ROWS / 8);
       step = o.stride * kTileK;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+      for (uint32_t i = 0; i < kLoads; ++i) {
         const uint32_t k = i * 16u + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
-        const uint32_t col = at0 + ((((t % (TILE / 8)) >> 1) ^ (f & kGranules)) * 16u) + (t & 1u) * 8u;
+        const uint32_t col = at0 + ((((t % (ROWS / 8)) >> 1) ^ (f & kGranules)) * 16u) + (t & 1u) * 8u;
         const uint32_t from = min(col, o.cols - 8u);
         p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)from * 2u;
         drop[i] = min(col - from, 7u);
@@ -169,54 +181,59 @@ struct Side {
       k_in = q * 8u;
       step = kTileK * 2u;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i)
-        p[i] = o.p + (uint64_t)min(at0 + i * (TILE / 4) + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
+      for (uint32_t i = 0; i < kLoads; ++i)
+        p[i] = o.p + (uint64_t)min(at0 + i * (THREADS / 8) + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
       off = (base + (lane & 15u)) * 128u + (((lane >> 4) ^ (lane & 7u)) << 4);
     }
   }
-  // Starts the loads of the operand's part of step k into LDS at byte `dst`;
-  // called step by step.
-  __device__ __forceinline__ void fill(uint32_t k, uint32_t dst) {
+  // Starts the loads of the operand's part of step k, into LDS at byte `dst`
+  // (kAt16) or into held, which settle writes to LDS; called step by step.
+  __device__ __forceinline__ void fill(uint32_t k, uint32_t dst, u32x4 (&held)[kLoads]) {
     if constexpr (AT == kAt16) {
       const uint32_t base = dst + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63u) * 16u;
       if (k + kTileK <= limit) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) load_to_lds(p[i], base + i * kPass);
+        for (uint32_t i = 0; i < kLoads; ++i) load_to_lds(p[i], base + i * kPass);
       } else {
         const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
+        for (uint32_t i = 0; i < kLoads; ++i)
           load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * kPass);
       }
-    } else if (k + kTileK <= limit) {
+    } else if (AT == kAny && k + kTileK <= limit) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) held[i] = load16_any(p[i]);
-    } else if constexpr (KMAJOR) {
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        held[i] = u32x4{0u, 0u, 0u, 0u};
-        if (k + k_in + i * 16u < limit) held[i] = load16_any(p[i]);
-      }
+      for (uint32_t i = 0; i < kLoads; ++i) held[i] = load16_any(p[i]);
     } else {
-      // chunks that end past the row start at its last 16 bytes; those past it are zero
-      const uint32_t at = k + k_in, back = at + 8u > limit ? min(at + 8u - limit, 8u) : 0u;
+      // Chunks past the end come from the zero vector; one that ends past its
+      // row starts at the row's last 16 bytes.  kDeep takes this path at every
+      // step and shifts them in settle: with no branch around the loads and no
+      // use of them here, the waits count exactly the younger ones.
+      const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+      const uint32_t back = past_end(k);
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        held[i] = u32x4{0u, 0u, 0u, 0u};
-        if (at < limit) held[i] = drop_elements(load16_any(p[i] - back * 2u), back & 7u);
+      for (uint32_t i = 0; i < kLoads; ++i) {
+        const bool in = k + k_in + (KMAJOR ? i * 16u : 0u) < limit;
+        held[i] = load16_any(in ? p[i] - back * 2u : zero);
+        if (AT == kAny && !KMAJOR) held[i] = drop_elements(held[i], back);
       }
     }
 #pragma unroll
-    for (uint32_t i = 0; i < 4; ++i) p[i] += step;
+    for (uint32_t i = 0; i < kLoads; ++i) p[i] += step;
   }
-  // kAny: writes what fill has loaded to LDS at `dst`.
-  __device__ __forceinline__ void settle(unsigned char* dst) const {
-    if constexpr (AT == kAny) {
+  // Rows along k: elements past the row's end in the thread's chunk of step k
+  // (below 8 for a chunk that has any of the row's).
+  __device__ __forceinline__ uint32_t past_end(uint32_t k) const {
+    const uint32_t at = k + k_in;
+    return !KMAJOR && at < limit && at + 8u > limit ? at + 8u - limit : 0u;
+  }
+  __device__ __forceinline__ void settle(uint32_t k, const u32x4 (&held)[kLoads], unsigned char* dst) const {
+    if constexpr (AT != kAt16) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+      for (uint32_t i = 0; i < kLoads; ++i) {
         u32x4 v = held[i];
-        if constexpr (KMAJOR) {
-          if (__any(drop[i] != 0u)) v = drop_elements(v, drop[i]);
+        if constexpr (KMAJOR || AT == kDeep) {
+          const uint32_t n = KMAJOR ? drop[i] : past_end(k);
+          if (__any(n != 0u)) v = drop_elements(v, n);
         }
         *reinterpret_cast<u32x4*>(dst + i * kPass + threadIdx.x * 16u) = v;
       }
@@ -239,56 +256,116 @@ struct Side {
   }
 };
 
+// The products of a step from LDS at la and lb.
+template <class T, class S, class SA, class SB>
+__device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsigned char* la,
+                                          const unsigned char* lb, f32x4 (&acc)[S::I][S::J]) {
+#pragma unroll
+  for (uint32_t s = 0; s < 2; ++s) {
+    typename T::frag a[S::I], b[S::J];
+#pragma unroll
+    for (int j = 0; j < S::J; ++j) b[j] = sb.read(lb, j, s);
+#pragma unroll
+    for (int i = 0; i < S::I; ++i) a[i] = sa.read(la, i, s);
+#pragma unroll
+    for (int i = 0; i < S::I; ++i)
+#pragma unroll
+      for (int j = 0; j < S::J; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
+  }
+}
+
+// gemm_tile for few rows of B, where a step lasts as long as the loads it waits
+// for: three steps of both operands are in flight, in registers, of which there
+// are plenty.  Same operations in the same order, so the same bits.  k1 is where
+// the operands end.
+template <class T, class S>
+__device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
+                                               uint32_t k0, uint32_t k1, unsigned char* lds,
+                                               f32x4 (&acc)[S::I][S::J]) {
+  const Place<S> at;
+  Side<T, S::M, S::kThreads, false, kDeep> sa;
+  Side<T, S::N, S::kThreads, false, kDeep> sb;
+  sa.init(A, m0, at.wm * (S::M / S::WM), k0);
+  sb.init(B, n0, at.wn * (S::N / S::WN), k0);
+#pragma unroll
+  for (int i = 0; i < S::I; ++i)
+#pragma unroll
+    for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 ha[3][sa.kLoads], hb[3][sb.kLoads];  // step k of every three in set k % 3
+#pragma unroll
+  for (uint32_t i = 0; i < 3; ++i) {
+    sa.fill(k0 + i * kTileK, 0, ha[i]);
+    sb.fill(k0 + i * kTileK, 0, hb[i]);
+  }
+  sa.settle(k0, ha[0], lds);
+  sb.settle(k0, hb[0], lds + S::kA);
+  uint32_t buf = 0;
+  const auto step = [&](uint32_t k, auto set) {
+    constexpr int C = decltype(set)::value, N = (C + 1) % 3;
+    // own writes of this buffer and reads of the other are done (a barrier that
+    // also waited for the loads in flight would undo them)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
+    asm volatile("" ::: "memory");
+    sa.fill(k + 3 * kTileK, 0, ha[C]);
+    sb.fill(k + 3 * kTileK, 0, hb[C]);
+    __builtin_amdgcn_sched_barrier(0);  // the loads go first
+    gemm_step<T, S>(sa, sb, lds + buf * S::kBuf, lds + buf * S::kBuf + S::kA, acc);
+    buf ^= 1u;
+    sa.settle(k + kTileK, ha[N], lds + buf * S::kBuf);
+    sb.settle(k + kTileK, hb[N], lds + buf * S::kBuf + S::kA);
+  };
+  // Steps past the last, up to a multiple of three, multiply zeros: no sum that
+  // starts at +0 changes by them.
+  for (uint32_t k = k0; k < k1; k += 3 * kTileK) {
+    step(k, std::integral_constant<int, 0>());
+    step(k + kTileK, std::integral_constant<int, 1>());
+    step(k + 2 * kTileK, std::integral_constant<int, 2>());
+  }
+  __syncthreads();  // the buffers may be reused
+}
+
 // Sum over k in [k0, k1) (k0 a multiple of 64) of the tile at row m0 of A's
 // index and n0 of B's.  What the tile holds past either's last means nothing.
 // AAT: how A's rows lie; B's lie at 16-byte boundaries.
-template <class T, uint32_t TILE, RowsAt AAT, bool AK, bool BK>
+template <class T, class S, RowsAt AAT, bool AK, bool BK>
 __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
                                           uint32_t k0, uint32_t k1, unsigned char* lds,
-                                          f32x4 (&acc)[TILE / 32][4]) {
-  constexpr int kI = TILE / 32;
-  constexpr uint32_t kBufBytes = buf_bytes(TILE);
-  typedef typename T::frag frag;
-  const Place<TILE> at;
-  Side<T, TILE, AK, AAT> sa;
-  Side<T, TILE, BK, kAt16> sb;
-  sa.init(A, m0, AK ? at.wm * (TILE / 32) : at.wm * (TILE / 2), k0);
-  sb.init(B, n0, BK ? at.wn * 4u : at.wn * 64u, k0);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+                                          f32x4 (&acc)[S::I][S::J]) {
+  if constexpr (AAT == kDeep) {
+    static_assert(!AK && !BK, "rows along k");
+    gemm_tile_deep<T, S>(A, B, m0, n0, k0, k1, lds, acc);
+  } else {
+    const Place<S> at;
+    Side<T, S::M, S::kThreads, AK, AAT> sa;
+    Side<T, S::N, S::kThreads, BK, kAt16> sb;
+    sa.init(A, m0, at.wm * (S::M / S::WM) / (AK ? 16u : 1u), k0);
+    sb.init(B, n0, at.wn * (S::N / S::WN) / (BK ? 16u : 1u), k0);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
 #pragma unroll
-  for (int i = 0; i < kI; ++i)
+    for (int i = 0; i < S::I; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const auto fill = [&](uint32_t k, uint32_t buf) {
-    sa.fill(k, lds0 + buf * kBufBytes);
-    sb.fill(k, lds0 + buf * kBufBytes + kBufBytes / 2);
-  };
-  fill(k0, 0);
-  sa.settle(lds);
-  uint32_t buf = 0;
-  for (uint32_t k = k0; k < k1; k += kTileK, buf ^= 1u) {
-    // own loads have landed, own reads and writes of the other buffer are done
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
-    asm volatile("" ::: "memory");
-    if (k + kTileK < k1) fill(k + kTileK, buf ^ 1u);
-    const unsigned char* la = lds + buf * kBufBytes;
-    const unsigned char* lb = la + kBufBytes / 2;
-#pragma unroll
-    for (uint32_t s = 0; s < 2; ++s) {
-      frag a[kI], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = sb.read(lb, j, s);
-#pragma unroll
-      for (int i = 0; i < kI; ++i) a[i] = sa.read(la, i, s);
-#pragma unroll
-      for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
+      for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 ha[sa.kLoads], hb[sb.kLoads];  // ha: kAny, A's loads of the next step; hb is not used
+    const auto fill = [&](uint32_t k, uint32_t buf) {
+      sa.fill(k, lds0 + buf * S::kBuf, ha);
+      sb.fill(k, lds0 + buf * S::kBuf + S::kA, hb);
+    };
+    fill(k0, 0);
+    sa.settle(k0, ha, lds);
+    uint32_t buf = 0;
+    for (uint32_t k = k0; k < k1; k += kTileK, buf ^= 1u) {
+      // own loads have landed, own reads and writes of the other buffer are done
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
+      asm volatile("" ::: "memory");
+      if (k + kTileK < k1) fill(k + kTileK, buf ^ 1u);
+      const unsigned char* la = lds + buf * S::kBuf;
+      gemm_step<T, S>(sa, sb, la, la + S::kA, acc);
+      if (k + kTileK < k1) sa.settle(k + kTileK, ha, lds + (buf ^ 1u) * S::kBuf);
     }
-    if (k + kTileK < k1) sa.settle(lds + (buf ^ 1u) * kBufBytes);
+    __syncthreads();  // the buffers may be reused
   }
-  __syncthreads();  // the buffers may be reused
 }
 
 // Tile of workgroup b of the nm x nn tiles of C: each XCD (workgroups go to

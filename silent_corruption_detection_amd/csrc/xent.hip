@@ -19,8 +19,10 @@
 // into each lane: a token's maximum and sum need two shuffles.
 // Gradient: the vocabulary in pieces; per piece the logit tiles again, whose
 // epilogue writes dz (16-bit), then the two products of dz in one launch.  dx
-// is summed over pieces and splits in fp32 in a fixed order.  Bound by the matrix cores: 2 N V d operations forward, 6 N V d
-// for the gradient.
+// is summed over pieces and splits in fp32 in a fixed order.  Bound by the
+// matrix cores (2 N V d operations forward, 6 N V d for the gradient), for up to
+// about 200 tokens by reading W (and, for the gradient, reading it again and
+// writing dW).
 #include <algorithm>
 
 #include "xent_device.h"
@@ -41,6 +43,8 @@ struct PackArgs {
   uint64_t vocab;
 };
 
+constexpr uint32_t kPackCols = 2048;  // of one wave: four loads of 16 bytes in flight
+
 template <bool VEC>
 __global__ void __launch_bounds__(kBlock) pack_kernel(const PackArgs a) {
   const uint32_t r = wave_item_index(), l = threadIdx.x & 63u;
@@ -48,8 +52,9 @@ __global__ void __launch_bounds__(kBlock) pack_kernel(const PackArgs a) {
   const bool live = !a.mask || has_target(a.mask[r], a.vocab);
   const unsigned char* src = a.src + (uint64_t)r * a.stride;
   uint16_t* dst = a.dst + (uint64_t)r * a.c_pad;
+  const uint32_t end = min(a.c_pad, (blockIdx.y + 1u) * kPackCols);
 #pragma unroll 4
-  for (uint32_t c = l * 8u; c < a.c_pad; c += 512u) {
+  for (uint32_t c = blockIdx.y * kPackCols + l * 8u; c < end; c += 512u) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if (live) {
       if (VEC) {
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(kBlock) pack_kernel(const PackArgs a) {
 
 int32_t launch_pack(const PackArgs& a, hipStream_t s) {
   const bool vec = a.C % 8 == 0 && a.stride % 16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
-  const dim3 grid((a.R + kWaves - 1) / kWaves);
+  const dim3 grid((a.R + kWaves - 1) / kWaves, (a.c_pad + kPackCols - 1) / kPackCols);
   if (vec) hipLaunchKernelGGL(pack_kernel<true>, grid, dim3(kBlock), 0, s, a);
   else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(kBlock), 0, s, a);
   return launch_status();
@@ -78,6 +83,8 @@ int32_t launch_pack(const PackArgs& a, hipStream_t s) {
 
 // ---- dx's sum ---------------------------------------------------------------------
 // dx = grad * the splits' sum, in split order; 0 for rows without a target.
+// Bound by latency, so the loads of 16 splits are in flight at a time: 256
+// splits of 5 x 163 took 32 us one by one and take 5.6.
 template <class T>
 __global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict__ part, uint32_t splits,
                                                         uint32_t N, uint32_t d,
@@ -87,12 +94,23 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict_
   const uint32_t n = blockIdx.x;
   const bool live = has_target(target[n], vocab);
   const float g = *grad * (1.0f / T::kDzScale);
-  for (uint32_t c = blockIdx.y * 1024u + threadIdx.x; c < d && c < (blockIdx.y + 1) * 1024u; c += 256) {
-    float s = 0.0f;
-    if (live)
-      for (uint32_t k = 0; k < splits; ++k) s += part[((uint64_t)k * N + n) * d + c];
-    dx[(uint64_t)n * d + c] = (uint16_t)T::bits(live ? s * g : 0.0f);
+  const uint32_t c = blockIdx.y * 256u + threadIdx.x;
+  if (c >= d) return;
+  float s = 0.0f;
+  if (live) {
+    const float* p = part + (uint64_t)n * d + c;
+    const uint64_t step = (uint64_t)N * d;
+    uint32_t k = 0;
+    for (; k + 16 <= splits; k += 16) {
+      float v[16];
+#pragma unroll
+      for (uint32_t i = 0; i < 16; ++i) v[i] = p[(k + i) * step];
+#pragma unroll
+      for (uint32_t i = 0; i < 16; ++i) s += v[i];
+    }
+    for (; k < splits; ++k) s += p[k * step];
   }
+  dx[(uint64_t)n * d + c] = (uint16_t)T::bits(live ? s * g : 0.0f);
 }
 
 // ---- row results -------------------------------------------------------------------
@@ -246,7 +264,8 @@ constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
   uint32_t N, d, V, d_pad;
-  uint32_t tile;         // 256 or 128, of the logits' product
+  uint32_t tile;         // 256, 128 or kFew, of the logits' product
+  uint32_t vtile;        // vocabulary rows of that tile
   uint32_t nt, vt;       // tiles of the tokens, of the whole vocabulary
   uint32_t ptile;        // 256 or 128, of the gradient's products
   bool copy_x, copy_w;   // the operand needs an aligned copy
@@ -256,6 +275,9 @@ struct Head {
   uint32_t splits;       // of dx's sum over a piece
   uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
 };
+
+// The tile of FewTile (128 x 32).
+constexpr uint32_t kFew = FewTile::N;
 
 uint32_t tiles(uint64_t n, uint32_t tile) { return (uint32_t)((n + tile - 1) / tile); }
 
@@ -280,8 +302,12 @@ int32_t check_head(const sdc_head* h) {
 // smaller where it would leave CUs idle or tiles half empty.  Measured (us, 128
 // / 256): 100 x 2048 x 50304 53 / 79, 300 x 1000 x 16000 33 / 43, 2000 x 512 x
 // 8000 30 / 28, 800 x 2048 x 50304 188 / 232, 1500 x 4096 x 30000 370 / 332.
+// Up to 32 tokens fit one 128 x 32 tile, whose few accumulators leave the
+// registers to keep three steps of loads in flight.  Measured against 128 x 128 (us): 5 x
+// 8190 x 128255 396 / 486, 32 x 1001 x 20001 25 / 37, 32 x 2048 x 50304 49 / 48.
 uint32_t logit_tile(uint64_t n, uint64_t vocab) {
   const auto rounds = [&](uint32_t t) { return ((uint64_t)tiles(n, t) * tiles(vocab, t) + 255) / 256; };
+  if (n <= kFew) return kFew;
   return (double)rounds(128) * (1.15 / 4) < (double)rounds(256) ? 128u : 256u;
 }
 
@@ -317,20 +343,22 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.d = (uint32_t)h->d;
   p.V = (uint32_t)h->vocab;
   p.d_pad = (uint32_t)up(h->d, 8);
-  p.copy_x = h->d % 8 || h->x_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16;
   // w is copied only where its rows are shorter than a load
   p.any = h->d % 8 || h->w_stride % 8 || reinterpret_cast<uintptr_t>(h->w) % 16;
   p.copy_w = p.any && h->d < 8;
   p.any = p.any && !p.copy_w;
   p.tile = logit_tile(p.N, p.V);
+  p.vtile = p.tile == kFew ? (uint32_t)FewTile::M : p.tile;
+  p.copy_x = (h->d % 8 || h->x_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16) &&
+             (p.tile != kFew || h->d < 8);  // few rows are read where they lie
   p.nt = tiles(p.N, p.tile);
-  p.vt = tiles(p.V, p.tile);
+  p.vt = tiles(p.V, p.vtile);
   // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
   // of that on, the one that needs the fewest rounds of 256 tiles.
   const uint32_t nt = p.nt, vt = p.vt;
   const uint64_t col = (p.copy_w ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.N : 0);
   uint32_t most = vt;
-  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.tile, 1);
+  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.vtile, 1);
   uint32_t best = most;
   if (most < vt) {
     uint64_t least = ~0ull;
@@ -343,7 +371,7 @@ Head plan_head(const sdc_head* h, bool grad) {
       }
     }
   }
-  const uint64_t piece = (uint64_t)best * p.tile;
+  const uint64_t piece = (uint64_t)best * p.vtile;
   p.piece = (uint32_t)std::min<uint64_t>(piece, up(p.V, 8));
   p.pieces = (vt + best - 1) / best;
   p.ptile = product_tile(p.N, p.d, p.piece);
@@ -401,7 +429,7 @@ int32_t piece_operands(const sdc_head* h, const Head& p, const Layout& o, unsign
   a->K = p.d;
   a->v0 = v0;
   a->nt = p.nt;
-  a->n_tiles = tiles(rows, p.tile) * a->nt;
+  a->n_tiles = tiles(rows, p.vtile) * a->nt;
   a->vocab = p.V;
   return SDC_OK;
 }
@@ -452,15 +480,18 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
       if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
       a.rows = d_row ? rows : nullptr;
       const HeadLaunch l = {h->dtype, p.tile, p.ptile};
-      if ((st = p.any ? launch_logit_lse_any(l, a, s) : launch_logit_lse16(l, a, s))) return st;
+      if ((st = p.tile == kFew ? launch_logit_lse_few(l, a, s)
+                : p.any        ? launch_logit_lse_any(l, a, s)
+                               : launch_logit_lse16(l, a, s)))
+        return st;
       rows += a.n_tiles;
-      a.part += tiles(n, p.tile);
+      a.part += tiles(n, p.vtile);
     }
   }
   const RowArgs r = {reinterpret_cast<const float2*>(ws + o.part), p.vt, p.N, p.d,
                      static_cast<const unsigned char*>(h->x), static_cast<const unsigned char*>(h->w),
                      2 * h->x_stride, 2 * h->w_stride, h->target, h->vocab, d_loss, d_lse, d_total, d_count};
-  st = for_type(h->dtype, p.tile, [&](auto t, auto) {
+  st = for_type<kAt16>(h->dtype, 128, [&](auto t, auto) {
     typedef decltype(t) T;
     if (p.N <= kFewTokens) {
       hipLaunchKernelGGL(few_tokens_kernel<T>, dim3(1), dim3(1024), 0, s, r);
@@ -542,12 +573,16 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     x.grad = d_grad;
     x.dw = d_dw ? static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d : nullptr;
     const HeadLaunch l = {h->dtype, p.tile, p.ptile};
-    if ((st = p.any ? launch_gradient_any(l, a, x, s) : launch_gradient16(l, a, x, s))) return st;
+    if ((st = p.tile == kFew ? launch_logit_dz_few(l, a, s)
+              : p.any        ? launch_logit_dz_any(l, a, s)
+                             : launch_logit_dz16(l, a, s)))
+      return st;
+    if ((st = p.any ? launch_products_any(l, x, s) : launch_products16(l, x, s))) return st;
   }
   if (d_dx) {
-    st = for_type(h->dtype, p.tile, [&](auto t, auto) {
+    st = for_type<kAt16>(h->dtype, 128, [&](auto t, auto) {
       typedef decltype(t) T;
-      hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 1023) / 1024), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
+      hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 255) / 256), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
                          h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));
       return launch_status();
     });

@@ -6,7 +6,10 @@ namespace sdc {
 int32_t launch_logit_lse16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
   return launch_logit_lse<kAt16>(h, a, s);
 }
-int32_t launch_gradient16(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s) {
-  return launch_gradient<kAt16>(h, a, x, s);
+int32_t launch_logit_dz16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
+  return launch_logit_dz<kAt16>(h, a, s);
+}
+int32_t launch_products16(const HeadLaunch& h, const ProductArgs& x, hipStream_t s) {
+  return launch_products<kAt16>(h, x, s);
 }
 }  // namespace sdc

@@ -6,7 +6,10 @@ namespace sdc {
 int32_t launch_logit_lse_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
   return launch_logit_lse<kAny>(h, a, s);
 }
-int32_t launch_gradient_any(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s) {
-  return launch_gradient<kAny>(h, a, x, s);
+int32_t launch_logit_dz_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
+  return launch_logit_dz<kAny>(h, a, s);
+}
+int32_t launch_products_any(const HeadLaunch& h, const ProductArgs& x, hipStream_t s) {
+  return launch_products<kAny>(h, x, s);
 }
 }  // namespace sdc

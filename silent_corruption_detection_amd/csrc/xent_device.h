@@ -1,6 +1,7 @@
 // xent_device.h -- the tiled kernels of the cross-entropy head (csrc/xent.hip
 // says what they compute), instantiated for weights whose rows lie at 16-byte
-// boundaries (csrc/xent16.hip) and for any others (csrc/xent_any.hip).
+// boundaries (csrc/xent16.hip), for any others (csrc/xent_any.hip) and for
+// few rows of x (csrc/xent_few.hip).
 #pragma once
 
 #include <algorithm>
@@ -44,23 +45,29 @@ struct ProductArgs {
   uint16_t* dw;        // of the piece's first row
 };
 
-// Launches over the tiles of one piece; tile, ptile: 256 or 128, of the logits'
-// product and of the gradient's.
+// Launches over the tiles of one piece; tile: 256, 128, or 32 (128 x 32) of the
+// logits' product, ptile: 256 or 128, of the gradient's.
 struct HeadLaunch {
   uint32_t dtype, tile, ptile;
 };
 int32_t launch_logit_lse16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
 int32_t launch_logit_lse_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
-int32_t launch_gradient16(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s);
-int32_t launch_gradient_any(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s);
+int32_t launch_logit_lse_few(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_logit_dz16(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_logit_dz_any(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_logit_dz_few(const HeadLaunch& h, const LogitArgs& a, hipStream_t s);
+int32_t launch_products16(const HeadLaunch& h, const ProductArgs& x, hipStream_t s);
+int32_t launch_products_any(const HeadLaunch& h, const ProductArgs& x, hipStream_t s);
 
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr uint32_t stage_row(uint32_t tile) { return tile + 8; }  // 16-bit elements of a staged row, padded off the banks
-constexpr uint32_t stage_lds(uint32_t tile) { return tile * stage_row(tile) * 2; }
-constexpr uint32_t lds_bytes(uint32_t tile) { return std::max(gemm_lds(tile), stage_lds(tile)); }
-static_assert(lds_bytes(256) + 1024 <= 160u * 1024u, "one workgroup fits a CU");
+// 16-bit elements of a staged row of M, padded off the banks
+template <class S>
+constexpr uint32_t stage_row() { return S::M + 8; }
+template <class S>
+constexpr uint32_t lds_bytes() { return std::max(S::kLds, S::N * stage_row<S>() * 2); }
+static_assert(lds_bytes<BigTile>() + 1024 <= 160u * 1024u, "one workgroup fits a CU");
 
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -74,18 +81,18 @@ __device__ __forceinline__ float rescale(float m, float M) {
 // ---- logit tiles ------------------------------------------------------------------
 
 // The tile's part of the fingerprint row of the fp32 logits [N][V].
-template <uint32_t TILE>
-__device__ __forceinline__ void tile_row(const f32x4 (&acc)[TILE / 32][4], const LogitArgs& a, uint32_t m0,
+template <class S>
+__device__ __forceinline__ void tile_row(const f32x4 (&acc)[S::I][S::J], const LogitArgs& a, uint32_t m0,
                                          uint32_t n0, sdc_row* out) {
-  const Place<TILE> at;
+  const Place<S> at;
   Lane ln;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < S::J; ++j) {
     const uint32_t n = n0 + at.col(j);
     if (n >= a.x.rows) continue;
     uint64_t s = 0, ws = 0;
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i)
+    for (int i = 0; i < S::I; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if (m0 + at.row(i) + r >= a.w.rows) continue;
@@ -99,7 +106,7 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[TILE / 32][4], const
     ln.w += ws + ((uint64_t)n * a.vocab + a.v0 + m0 + at.row(0) + 1u) * s;
   }
   wave_reduce(ln);
-  constexpr int kW = TILE / 32;  // waves
+  constexpr int kW = S::kThreads / 64;
   __shared__ uint64_t waves[4][kW];
   const uint32_t wave = threadIdx.x >> 6;
   if (at.lane == 0) {
@@ -123,20 +130,20 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[TILE / 32][4], const
   }
 }
 
-template <class T, uint32_t TILE, RowsAt AT, bool ROW>
-__global__ void __launch_bounds__(gemm_block(TILE)) logit_lse_kernel(const LogitArgs a) {
+template <class T, class S, RowsAt AT, bool ROW>
+__global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
-  const uint32_t m0 = vt * TILE, n0 = (id % a.nt) * TILE;
-  f32x4 acc[TILE / 32][4];
-  gemm_tile<T, TILE, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
-  const Place<TILE> at;
+  const uint32_t m0 = vt * S::M, n0 = (id % a.nt) * S::N;
+  f32x4 acc[S::I][S::J];
+  gemm_tile<T, S, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  const Place<S> at;
   float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < S::J; ++j) {
     float m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i)
+    for (int i = 0; i < S::I; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (m0 + at.row(i) + r < a.w.rows) m = __builtin_fmaxf(m, acc[i][j][r]);
@@ -145,55 +152,59 @@ __global__ void __launch_bounds__(gemm_block(TILE)) logit_lse_kernel(const Logit
     const float c = (__builtin_isinf(m) ? 0.0f : m) * kLog2e;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i)
+    for (int i = 0; i < S::I; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (m0 + at.row(i) + r < a.w.rows)
           s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (at.lane < 16) half[at.wm * TILE + at.col(j)] = float2{m, s};
+    if (at.lane < 16) half[at.wm * S::N + at.col(j)] = float2{m, s};
   }
   __syncthreads();
-  if (threadIdx.x < TILE && n0 + threadIdx.x < a.x.rows) {
-    const float2 p = half[threadIdx.x], q = half[TILE + threadIdx.x];
-    const float M = __builtin_fmaxf(p.x, q.x);
-    a.part[(uint64_t)(n0 + threadIdx.x) * a.n_vt + vt] =
-        float2{M, p.y * rescale(p.x, M) + q.y * rescale(q.x, M)};
+  if (threadIdx.x < S::N && n0 + threadIdx.x < a.x.rows) {
+    float2 p = half[threadIdx.x];
+#pragma unroll
+    for (uint32_t k = 1; k < S::WM; ++k) {
+      const float2 q = half[k * S::N + threadIdx.x];
+      const float M = __builtin_fmaxf(p.x, q.x);
+      p = float2{M, p.y * rescale(p.x, M) + q.y * rescale(q.x, M)};
+    }
+    a.part[(uint64_t)(n0 + threadIdx.x) * a.n_vt + vt] = p;
   }
-  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
+  if constexpr (ROW) tile_row<S>(acc, a, m0, n0, a.rows + id);
 }
 
 // dz of the tile, in 16 bits (rounded to nearest: off by half a step of its
 // own size, which the products average out), 0 for rows without a target and
 // in the padding.
-template <class T, uint32_t TILE, RowsAt AT, bool ROW>
-__global__ void __launch_bounds__(gemm_block(TILE)) logit_dz_kernel(const LogitArgs a) {
+template <class T, class S, RowsAt AT, bool ROW>
+__global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds);
-  const uint32_t m0 = (id / a.nt) * TILE, n0 = (id % a.nt) * TILE;
-  const Place<TILE> at;
+  const uint32_t m0 = (id / a.nt) * S::M, n0 = (id % a.nt) * S::N;
+  const Place<S> at;
   // what the epilogue needs of its tokens, in flight during the product
-  float c[4];
-  uint32_t hit[4];  // the target among the rows from at.row(0) on; kNone: no target
+  float c[S::J];
+  uint32_t hit[S::J];  // the target among the rows from at.row(0) on; kNone: no target
   constexpr uint32_t kNone = 0x80000000u;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < S::J; ++j) {
     const uint32_t n = min(n0 + at.col(j), a.x.rows - 1u);
     const int64_t t = a.target[n];
     c[j] = a.lse[n] * kLog2e;
     // at most 2^24 rows: the difference, also a negative one, is never kNone
     hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
   }
-  f32x4 acc[TILE / 32][4];
-  gemm_tile<T, TILE, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
-  if constexpr (ROW) tile_row<TILE>(acc, a, m0, n0, a.rows + id);
+  f32x4 acc[S::I][S::J];
+  gemm_tile<T, S, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
+  if constexpr (ROW) tile_row<S>(acc, a, m0, n0, a.rows + id);
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < S::J; ++j) {
     const bool live = hit[j] != kNone;
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i) {
+    for (int i = 0; i < S::I; ++i) {
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -201,46 +212,46 @@ __global__ void __launch_bounds__(gemm_block(TILE)) logit_dz_kernel(const LogitA
         p = (p - (hit[j] == (uint32_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
         b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
       }
-      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row<S>() + at.row(i)) =
           uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     }
   }
   __syncthreads();
-  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
+  const uint32_t t = threadIdx.x, ch = t % (S::M / 8) * 8u;
 #pragma unroll 4
-  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
+  for (uint32_t k = t / (S::M / 8); k < S::N; k += S::kThreads / (S::M / 8)) {
     const uint32_t n = n0 + k, v = m0 + ch;
     if (n < a.x.rows && v < a.v_pad)
       *reinterpret_cast<u32x4*>(a.dz + (uint64_t)n * a.v_pad + v) =
-          *reinterpret_cast<const u32x4*>(st + k * stage_row(TILE) + ch);
+          *reinterpret_cast<const u32x4*>(st + k * stage_row<S>() + ch);
   }
 }
 
 // ---- dx and dW --------------------------------------------------------------------
 
-template <class T, uint32_t TILE, RowsAt AT>
+template <class T, class S, RowsAt AT>
 __device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
-  const uint32_t n0 = (id % a.nt) * TILE, rest = id / a.nt;
-  const uint32_t m0 = (rest % a.md) * TILE, split = rest / a.md;
+  const uint32_t n0 = (id % a.nt) * S::N, rest = id / a.nt;
+  const uint32_t m0 = (rest % a.md) * S::M, split = rest / a.md;
   const uint32_t k0 = split * a.chunk, k1 = min(k0 + a.chunk, a.rows);
   if (k0 >= k1 && !a.first) return;
-  f32x4 acc[TILE / 32][4];
+  f32x4 acc[S::I][S::J];
   if (k0 < k1) {
-    gemm_tile<T, TILE, AT, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
+    gemm_tile<T, S, AT, true, false>(a.w, a.dz, m0, n0, k0, k1, lds, acc);
   } else {
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i)
+    for (int i = 0; i < S::I; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const Place<TILE> at;
+  const Place<S> at;
   float* out = a.part + (uint64_t)split * a.N * a.d;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < S::J; ++j) {
     const uint32_t n = n0 + at.col(j);
     if (n >= a.N) continue;
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i) {
+    for (int i = 0; i < S::I; ++i) {
       const uint32_t m = m0 + at.row(i);
       float* p = out + (uint64_t)n * a.d + m;
       if (a.d % 4 == 0) {
@@ -257,32 +268,32 @@ __device__ __forceinline__ void dx_tile(const ProductArgs& a, uint32_t id, unsig
   }
 }
 
-template <class T, uint32_t TILE>
+template <class T, class S>
 __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsigned char* lds) {
-  const uint32_t m0 = (id % a.md) * TILE, n0 = (id / a.md) * TILE;
+  const uint32_t m0 = (id % a.md) * S::M, n0 = (id / a.md) * S::N;
   const float g = *a.grad * (1.0f / T::kDzScale);
-  f32x4 acc[TILE / 32][4];
-  gemm_tile<T, TILE, kAt16, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
-  const Place<TILE> at;
+  f32x4 acc[S::I][S::J];
+  gemm_tile<T, S, kAt16, true, true>(a.x, a.dz, m0, n0, 0, a.N, lds, acc);
+  const Place<S> at;
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < S::J; ++j)
 #pragma unroll
-    for (int i = 0; i < (int)TILE / 32; ++i) {
+    for (int i = 0; i < S::I; ++i) {
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) b[r] = T::bits(acc[i][j][r] * g);
-      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row(TILE) + at.row(i)) =
+      *reinterpret_cast<uint2*>(st + at.col(j) * stage_row<S>() + at.row(i)) =
           uint2{b[0] | b[1] << 16, b[2] | b[3] << 16};
     }
   __syncthreads();
-  const uint32_t t = threadIdx.x, ch = t % (TILE / 8) * 8u;
+  const uint32_t t = threadIdx.x, ch = t % (S::M / 8) * 8u;
 #pragma unroll 4
-  for (uint32_t k = t / (TILE / 8); k < TILE; k += 16) {
+  for (uint32_t k = t / (S::M / 8); k < S::N; k += S::kThreads / (S::M / 8)) {
     const uint32_t v = n0 + k, c = m0 + ch;
     if (v >= a.rows || c >= a.d) continue;
     uint16_t* p = a.dw + (uint64_t)v * a.d + c;
-    const uint16_t* s = st + k * stage_row(TILE) + ch;
+    const uint16_t* s = st + k * stage_row<S>() + ch;
     if (c + 8u <= a.d) {
       *reinterpret_cast<u32x4_at2*>(p) = *reinterpret_cast<const u32x4*>(s);
     } else {
@@ -291,51 +302,55 @@ __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsig
   }
 }
 
-template <class T, uint32_t TILE, RowsAt AT>
-__global__ void __launch_bounds__(gemm_block(TILE)) products_kernel(const ProductArgs a) {
+template <class T, class S, RowsAt AT>
+__global__ void __launch_bounds__(S::kThreads) products_kernel(const ProductArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
-  if (blockIdx.x < a.n_dx) dx_tile<T, TILE, AT>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
-  else dw_tile<T, TILE>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
+  if (blockIdx.x < a.n_dx) dx_tile<T, S, AT>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
+  else dw_tile<T, S>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
 }
 
-
-// f(type, tile) with both as compile-time constants
-template <class F>
+// f(type, shape) with both as types; tile: 256, 128, or 32 for FewTile, which is
+// the only one of kDeep and of no other.
+template <RowsAt AT, class F>
 int32_t for_type(uint32_t dtype, uint32_t tile, F&& f) {
-  const std::integral_constant<uint32_t, 256> big;
-  const std::integral_constant<uint32_t, 128> small;
-  if (dtype == SDC_BF16) return tile == 256 ? f(Bf16(), big) : f(Bf16(), small);
-  return tile == 256 ? f(Fp16(), big) : f(Fp16(), small);
+  if constexpr (AT == kDeep) {
+    return dtype == SDC_BF16 ? f(Bf16(), FewTile()) : f(Fp16(), FewTile());
+  } else {
+    if (dtype == SDC_BF16) return tile == 256 ? f(Bf16(), BigTile()) : f(Bf16(), SmallTile());
+    return tile == 256 ? f(Fp16(), BigTile()) : f(Fp16(), SmallTile());
+  }
 }
 
 template <RowsAt AT>
 int32_t launch_logit_lse(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
-  return for_type(h.dtype, h.tile, [&](auto t, auto tile) {
+  return for_type<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
     typedef decltype(t) T;
-    constexpr uint32_t TILE = decltype(tile)::value;
-    const dim3 grid(a.n_tiles), block(gemm_block(TILE));
-    if (a.rows) hipLaunchKernelGGL((logit_lse_kernel<T, TILE, AT, true>), grid, block, gemm_lds(TILE), s, a);
-    else hipLaunchKernelGGL((logit_lse_kernel<T, TILE, AT, false>), grid, block, gemm_lds(TILE), s, a);
+    typedef decltype(shape) S;
+    const dim3 grid(a.n_tiles), block(S::kThreads);
+    if (a.rows) hipLaunchKernelGGL((logit_lse_kernel<T, S, AT, true>), grid, block, S::kLds, s, a);
+    else hipLaunchKernelGGL((logit_lse_kernel<T, S, AT, false>), grid, block, S::kLds, s, a);
     return launch_status();
   });
 }
 
 template <RowsAt AT>
-int32_t launch_gradient(const HeadLaunch& h, const LogitArgs& a, const ProductArgs& x, hipStream_t s) {
-  const int32_t st = for_type(h.dtype, h.tile, [&](auto t, auto tile) {
+int32_t launch_logit_dz(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
+  return for_type<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
     typedef decltype(t) T;
-    constexpr uint32_t TILE = decltype(tile)::value;
-    const dim3 grid(a.n_tiles), block(gemm_block(TILE));
-    if (a.rows) hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, true>), grid, block, lds_bytes(TILE), s, a);
-    else hipLaunchKernelGGL((logit_dz_kernel<T, TILE, AT, false>), grid, block, lds_bytes(TILE), s, a);
+    typedef decltype(shape) S;
+    const dim3 grid(a.n_tiles), block(S::kThreads);
+    if (a.rows) hipLaunchKernelGGL((logit_dz_kernel<T, S, AT, true>), grid, block, lds_bytes<S>(), s, a);
+    else hipLaunchKernelGGL((logit_dz_kernel<T, S, AT, false>), grid, block, lds_bytes<S>(), s, a);
     return launch_status();
   });
-  if (st) return st;
-  return for_type(h.dtype, h.ptile, [&](auto t, auto tile) {
+}
+
+template <RowsAt AT>
+int32_t launch_products(const HeadLaunch& h, const ProductArgs& x, hipStream_t s) {
+  return for_type<AT>(h.dtype, h.ptile, [&](auto t, auto shape) {
     typedef decltype(t) T;
-    constexpr uint32_t TILE = decltype(tile)::value;
-    hipLaunchKernelGGL((products_kernel<T, TILE, AT>), dim3(x.n_dx + x.n_dw), dim3(gemm_block(TILE)),
-                       lds_bytes(TILE), s, x);
+    typedef decltype(shape) S;
+    hipLaunchKernelGGL((products_kernel<T, S, AT>), dim3(x.n_dx + x.n_dw), dim3(S::kThreads), lds_bytes<S>(), s, x);
     return launch_status();
   });
 }

@@ -231,6 +231,33 @@ def test_rows_do_not_change_the_results_and_runs_repeat():
     assert mis.item() == 0 and torch.equal(rows[0], rows[1])
 
 
+@pytest.mark.parametrize("n", [1, 31, 32, 33])
+@pytest.mark.parametrize("d", [7, 8, 9, 64, 130, 193, 320])
+def test_few_tokens_wherever_their_rows_lie(n, d):
+    """Around the smallest tile's 32 tokens, with one to six steps of k: rows of
+    x and w at odd element offsets give the bits of aligned ones, and the logits'
+    row too, in both passes."""
+    say(f"case few n={n} d={d}")
+    x0, w0, t = make(n, d, 301, BF, seed=n * d, ignored=0.2 if n > 1 else 0.0)
+    want = check(x0, w0, t)
+    rows = []
+    for pad, off in ((0, 0), (3, 1), (1, 6)):
+        bx = torch.full((n * (d + pad) + off + 8,), float("inf"), dtype=BF, device=DEV)
+        bw = torch.full((301 * (d + pad) + off + 8,), float("inf"), dtype=BF, device=DEV)
+        x = bx[off:off + n * (d + pad)].view(n, d + pad)[:, :d].copy_(x0)
+        w = bw[off:off + 301 * (d + pad)].view(301, d + pad)[:, :d].copy_(w0)
+        row, again = (torch.zeros(1, 4, dtype=torch.int64, device=DEV) for _ in range(2))
+        mismatch = torch.zeros(1, dtype=torch.int32, device=DEV)
+        loss, lse, total = sdc.sdc_cross_entropy(x, w, t, row=row)
+        dx, dw = sdc.sdc_cross_entropy_grad(x, w, t, lse, torch.tensor([0.25], device=DEV), row=again, ref=row,
+                                            mismatch=mismatch)
+        assert mismatch.item() == 0 and torch.equal(row, again)
+        rows.append(row)
+        for got, ref, what in zip((loss, lse, total, dx, dw), want, ("loss", "lse", "total", "dx", "dw")):
+            assert torch.equal(got, ref), (what, pad, off)
+    assert torch.equal(rows[0], rows[1]) and torch.equal(rows[0], rows[2])
+
+
 def test_gradient_against_differences():
     """Central differences of the 64-bit loss at 16-bit x and w: their error is
     the second-order remainder, e^2 / 6 times a third derivative below 1."""
