@@ -491,7 +491,7 @@ int32_t sdc_adamw_plan_bytes(const sdc_adamw_tensor* h_tensors, uint64_t n, uint
  * step's scratch: steps of one plan must not overlap in time.  SYNCHRONOUS.
  * Errors: SDC_ERR_INVALID (NULL, a group out of range, a master of an fp32
  * param, scale bytes that do not go with the state type), SDC_ERR_DTYPE,
- * SDC_ERR_ALIGN (a pointer not aligned to its element), SDC_ERR_RANGE (2^31
+ * SDC_ERR_ALIGN (a pointer not aligned to its element), SDC_ERR_RANGE (2^25
  * tensors, 2^48 elements), SDC_ERR_WORKSPACE, SDC_ERR_HIP. */
 int32_t sdc_adamw_plan_build(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
                              void* d_plan, uint64_t plan_bytes, sdc_adamw_info* h_info,
@@ -551,10 +551,11 @@ typedef struct {
 /* Device workspace bytes of sdc_cross_entropy (h_bytes) and
  * sdc_cross_entropy_grad (h_grad_bytes); either may be NULL.  The gradient's
  * holds dz of one piece of the vocabulary (up to 256 MiB, or 256 rows' worth
- * where that is more), a copy of x and fp32 sums of dx.  Host only.  Errors: SDC_ERR_INVALID
+ * where that is more), a copy of x and fp32 sums of dx; the loss' 8 bytes for
+ * each row of x and 128 or 256 rows of w.  Host only.  Errors: SDC_ERR_INVALID
  * (NULL x, w or target, d or vocab 0, a stride below d, flags), SDC_ERR_DTYPE,
  * SDC_ERR_ALIGN (an element, or target, not aligned), SDC_ERR_RANGE (2^24
- * rows of x or w, d 2^20, a stride of 2^40). */
+ * rows of x or w, about 2^47 logits, d 2^20, a stride of 2^40). */
 int32_t sdc_cross_entropy_ws_bytes(const sdc_head* h_head, uint64_t* h_bytes, uint64_t* h_grad_bytes);
 
 /* z = x w^T in fp32; per row n
@@ -575,9 +576,10 @@ int32_t sdc_cross_entropy(const sdc_head* h_head, void* d_ws, uint64_t ws_bytes,
  * onehot) * *d_grad, zero in rows without a target,
  *   d_dx = dz w  (n x d, contiguous)      d_dw = dz^T x  (vocab x d, contiguous)
  * both of the head's dtype, summed in fp32 from dz rounded to that type's
- * precision; one of the two may be NULL and is then not computed.  d_lse: the forward pass'.  d_row: as there, of the recomputed
- * logits; with d_ref (the forward pass' row) a difference under col_mask adds 1
- * to *d_mismatch (required then; the caller clears it).
+ * precision; one of the two may be NULL and is then not computed.  d_lse: the
+ * forward pass'.  d_row: as there, of the recomputed logits; with d_ref (the
+ * forward pass' row) a difference under col_mask adds 1 to *d_mismatch
+ * (required then; the caller clears it).
  * ASYNCHRONOUS on stream.  Errors as sdc_cross_entropy. */
 int32_t sdc_cross_entropy_grad(const sdc_head* h_head, const float* d_lse, const float* d_grad,
                                void* d_ws, uint64_t ws_bytes, void* d_dx, void* d_dw,

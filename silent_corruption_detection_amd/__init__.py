@@ -781,7 +781,8 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     None where the state is fp32).  master: fp32 weights behind 16-bit params
     (None: the param itself is updated).  group: parameter group of each
     tensor.  The plan keeps the tensors' addresses: gradients have to stay
-    where they are (zero them in place)."""
+    where they are (zero them in place).  No tensor that the step writes may be
+    listed twice or overlap another."""
     n = len(params)
     if not n:
         raise ValueError("the list is empty")
@@ -800,6 +801,11 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     blocks = [-(-m // _STATE_BLOCK) for m in numels]
     for name, scales in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
         keep += _adamw_column(table, name, scales, blocks, [{torch.uint8}] * n, dev)[0]
+    written = np.concatenate([table[c] for c in ("param", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
+                                                 "exp_avg_sq_scale")])
+    written = np.sort(written[written != 0])
+    if (written[1:] == written[:-1]).any():
+        raise ValueError("a tensor that the step writes is listed twice (shared weights: list them once)")
     table["numel"] = numels
     table["param_dtype"] = table["grad_dtype"] = [_TORCH_DTYPE[p.dtype] for p in params]
     table["grad_dtype"][at] = [_TORCH_DTYPE[g.dtype] for g in gs]
@@ -831,7 +837,8 @@ def sdc_adamw_control(device="cuda", step=0, seed=0):
 def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0, grad_scale=1.0,
                    rows=None, stream=None):
     """One AdamW step over the plan's list, in place (asynchronous; see
-    sdc_adamw_step in include/sdc.h).
+    sdc_adamw_step in include/sdc.h).  The weights are written behind autograd's
+    back: run the backward passes that need the old ones before.
 
     groups: float64 [n_groups, 5] device tensor of (lr, beta1, beta2, eps,
     weight_decay), which may change between steps.  control: the block of

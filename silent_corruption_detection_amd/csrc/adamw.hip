@@ -63,6 +63,10 @@ __global__ void __launch_bounds__(kBlock) adamw_merge_kernel(const PlanSplit* __
   if (l == 0) store_row(rows + sp.row, ln, ln.w);
 }
 
+// A grid has fewer than 2^32 threads: a launch takes at most this many items of
+// each kind, and the merge one wave for each tensor.
+constexpr uint64_t kLaunchItems = 1ull << 23, kMaxTensors = 1ull << 25;
+
 struct Layout {
   uint64_t n_items = 0, n_split = 0, n_slots = 0, total_elems = 0;
   uint64_t n_block[kAdamwClasses] = {}, n_wave[kAdamwClasses] = {};
@@ -111,7 +115,7 @@ bool of_wave(const sdc_adamw_tensor& t) { return t.numel + shift_of(t) <= kAdamw
 
 int32_t layout_adamw(const sdc_adamw_tensor* t, uint64_t n, uint32_t n_groups, Layout* L) {
   if ((n > 0 && t == nullptr) || n_groups == 0 || n_groups > 65536) return SDC_ERR_INVALID;
-  if (n >= 1ull << 31) return SDC_ERR_RANGE;
+  if (n >= kMaxTensors) return SDC_ERR_RANGE;
   for (uint64_t k = 0; k < n; ++k) {
     if (int32_t st = check_tensor(t[k], n_groups)) return st;
     L->total_elems += t[k].numel;
@@ -178,7 +182,7 @@ void fill_info(const Layout& L, uint64_t n, uint32_t n_groups, sdc_adamw_info* h
 
 bool adamw_info_ok(const sdc_adamw_info* h) {
   if (h->magic != kAdamwMagic || h->n_items > kMaxGrid || h->n_split > h->n_tensors ||
-      h->n_tensors >= 1ull << 31 || h->n_groups == 0 || h->n_groups > 65536 || h->n_slots > h->n_items)
+      h->n_tensors >= kMaxTensors || h->n_groups == 0 || h->n_groups > 65536 || h->n_slots > h->n_items)
     return false;
   uint64_t items = 0;
   for (uint32_t c = 0; c < kAdamwClasses; ++c) {
@@ -254,12 +258,15 @@ extern "C" int32_t sdc_adamw_step(void* d_plan, const sdc_adamw_info* h_info,
               reinterpret_cast<const AdamwItem*>(base + o.items), 0, 0,
               reinterpret_cast<sdc_row*>(base + o.partials), d_rows};
   for (uint32_t c = 0; c < kAdamwClasses; ++c) {
-    a.n_block = (uint32_t)h_info->n_block[c];
-    a.n_wave = (uint32_t)h_info->n_wave[c];
-    if (a.n_block + a.n_wave == 0) continue;
-    st = (c & 1) ? launch_adamw8(c, a, s) : launch_adamw32(c, a, s);
-    if (st) return st;
-    a.items += a.n_block + a.n_wave;
+    for (uint64_t block = h_info->n_block[c], wave = h_info->n_wave[c]; block + wave > 0;) {
+      a.n_block = (uint32_t)std::min(block, kLaunchItems);
+      a.n_wave = block > kLaunchItems ? 0u : (uint32_t)std::min(wave, kLaunchItems);
+      st = (c & 1) ? launch_adamw8(c, a, s) : launch_adamw32(c, a, s);
+      if (st) return st;
+      a.items += a.n_block + a.n_wave;
+      block -= a.n_block;
+      wave -= a.n_wave;
+    }
   }
   if (d_rows && h_info->n_split) {
     hipLaunchKernelGGL(adamw_merge_kernel, dim3((uint32_t)((h_info->n_split + kWaves - 1) / kWaves)),

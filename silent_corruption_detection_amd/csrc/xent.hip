@@ -335,8 +335,11 @@ uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
   return 0.575 * steps(128) < steps(256) ? 128u : 256u;
 }
 
+// Tiles of one launch: a grid has fewer than 2^32 threads.
+constexpr uint32_t kLaunchTiles = 1u << 22;
+
 // grad: the sizes of the gradient's pieces; else those of the forward pass,
-// which needs pieces only for a copy of w.
+// which needs pieces only for a copy of w or for more than kLaunchTiles tiles.
 Head plan_head(const sdc_head* h, bool grad) {
   Head p;
   p.N = (uint32_t)h->n;
@@ -359,6 +362,7 @@ Head plan_head(const sdc_head* h, bool grad) {
   const uint64_t col = (p.copy_w ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.N : 0);
   uint32_t most = vt;
   if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.vtile, 1);
+  most = std::min(most, std::max(kLaunchTiles / std::max(nt, 1u), 1u));
   uint32_t best = most;
   if (most < vt) {
     uint64_t least = ~0ull;
@@ -461,7 +465,10 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
   if (st) return st;
   if (d_total == nullptr || d_ws == nullptr || (h->n > 0 && (d_loss == nullptr || d_lse == nullptr)))
     return SDC_ERR_INVALID;
-  if (reinterpret_cast<uintptr_t>(d_ws) % 16 || reinterpret_cast<uintptr_t>(d_row) % 16) return SDC_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(d_ws) % 16 || reinterpret_cast<uintptr_t>(d_row) % 16 ||
+      reinterpret_cast<uintptr_t>(d_loss) % 4 || reinterpret_cast<uintptr_t>(d_lse) % 4 ||
+      reinterpret_cast<uintptr_t>(d_total) % 4 || reinterpret_cast<uintptr_t>(d_count) % 8)
+    return SDC_ERR_ALIGN;
   const Head p = plan_head(h, false);
   const Layout o = layout_head(p, false);
   if (ws_bytes < o.end) return SDC_ERR_WORKSPACE;
@@ -521,7 +528,7 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
   if (reinterpret_cast<uintptr_t>(d_ws) % 16 || reinterpret_cast<uintptr_t>(d_row) % 16 ||
       reinterpret_cast<uintptr_t>(d_ref) % 16 || reinterpret_cast<uintptr_t>(d_dx) % 2 ||
       reinterpret_cast<uintptr_t>(d_dw) % 2 || reinterpret_cast<uintptr_t>(d_lse) % 4 ||
-      reinterpret_cast<uintptr_t>(d_grad) % 4)
+      reinterpret_cast<uintptr_t>(d_grad) % 4 || reinterpret_cast<uintptr_t>(d_mismatch) % 4)
     return SDC_ERR_ALIGN;
   const Head p = plan_head(h, true);
   const Layout o = layout_head(p, true);

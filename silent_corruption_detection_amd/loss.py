@@ -52,7 +52,11 @@ def linear_cross_entropy(x, w, target, reduction="mean", row=None, checked=None)
 
     row: an int64 [1, 4] device tensor that receives the logits' fingerprint row.
     checked: called when the backward pass starts; returns sdc_cross_entropy_grad's
-    arguments of the comparison (row, ref, mismatch, col_mask)."""
+    arguments of the comparison (row, ref, mismatch, col_mask).
+
+    Captured into a HIP graph, forward and backward pass belong into the same
+    capture, with no loss of the same leaves from before it still alive (autograd
+    would wait for that one's stream inside the capture)."""
     if reduction not in ("mean", "sum"):
         raise ValueError(f"reduction must be 'mean' or 'sum', not {reduction!r}")
     if x.dim() < 1 or target.shape != x.shape[:-1]:

@@ -70,6 +70,7 @@ def test_refused_lists():
     assert nbytes([tensor()], n_groups=0)[0] == INVALID
     assert nbytes([tensor()], n_groups=65537)[0] == INVALID
     assert nbytes([tensor(numel=(1 << 48) - 1)] * 2)[0] == RANGE
+    assert nbytes([tensor()], n=1 << 25)[0] == RANGE     # before any entry is read
     lib = ctypes.CDLL(sdc.LIB_PATH)
     assert lib.sdc_adamw_plan_bytes(None, ctypes.c_uint64(1), 1, ctypes.byref(ctypes.c_uint64())) == INVALID
     assert lib.sdc_adamw_plan_bytes(None, ctypes.c_uint64(0), 1, None) == INVALID

@@ -60,8 +60,8 @@ def test_refused_calls():
     h = head()
     hp, big = ctypes.addressof(h), 1 << 40
 
-    def f(ws=0x10000, nbytes=big, loss=0x4000, lse=0x5000, total=0x6000, row=None):
-        return fwd(hp, ws, nbytes, loss, lse, total, None, row, None)
+    def f(ws=0x10000, nbytes=big, loss=0x4000, lse=0x5000, total=0x6000, count=None, row=None):
+        return fwd(hp, ws, nbytes, loss, lse, total, count, row, None)
 
     def g(lse=0x4000, grad=0x5000, ws=0x10000, nbytes=big, dx=0x6000, dw=0x7000, ref=None, mask=15, row=None, mis=None):
         return bwd(hp, lse, grad, ws, nbytes, dx, dw, ref, mask, row, mis, None)
@@ -69,7 +69,9 @@ def test_refused_calls():
     for k in ("ws", "loss", "lse", "total"):
         assert f(**{k: None}) == INVALID, k
     assert f(nbytes=16) == WORKSPACE
-    assert f(ws=0x10008) == ALIGN and f(row=0x8008) == ALIGN
+    for k, v in (("ws", 0x10008), ("row", 0x8008), ("loss", 0x4002), ("lse", 0x5002), ("total", 0x6001),
+                 ("count", 0x8004)):
+        assert f(**{k: v}) == ALIGN, k
     for k in ("lse", "grad", "ws"):
         assert g(**{k: None}) == INVALID, k
     assert g(dx=None, dw=None) == INVALID
@@ -82,6 +84,7 @@ def test_refused_calls():
     assert g(ref=0x9000, row=0x8000, mis=0x100, mask=0) == INVALID
     assert g(ref=0x9000, row=0x8000, mis=0x100, mask=16) == INVALID
     assert g(ref=0x9008, row=0x8000, mis=0x100) == ALIGN
+    assert g(ref=0x9000, row=0x8000, mis=0x102) == ALIGN
     for bad, status in BAD:
         h2 = head(**bad)
         assert fwd(ctypes.addressof(h2), 0x10000, big, 0x4000, 0x5000, 0x6000, None, None, None) == status

@@ -12,6 +12,8 @@ Tolerances, with u = 2^-24 the largest relative rounding of fp32:
   that the element's random bits choose, except where the choice hangs on less
   than the errors above.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -405,6 +407,43 @@ def test_mixed_list_in_one_plan():
     assert_rows_equal(sdc.rows_numpy(rows), oracle_rows(p))
 
 
+def test_more_tensors_than_one_launch_takes():
+    """2^23 + 70 tensors of one weight each, through the C entry points: their
+    items need two launches, as a grid has fewer than 2^32 threads."""
+    n = (1 << 23) + 70
+    say(f"case adamw of {n} tensors")
+    g = gen(19)
+    p, gr, m, v = (torch.empty(n, device=DEV).normal_(generator=g) for _ in range(4))
+    v.abs_()
+    p0 = p.double()
+    want_m = 0.9 * m.double() + (1 - 0.9) * gr.double()
+    want_v = 0.99 * v.double() + (1 - 0.99) * gr.double() ** 2
+    den = want_v.sqrt() / (1 - 0.99) ** 0.5 + 1e-8
+    update = 1e-2 / (1 - 0.9) * want_m / den
+    tol_m = 5 * U * (0.9 * m.double().abs() + 0.1 * gr.double().abs())
+    table = np.zeros(n, dtype=sdc._ADAMW_DESC)
+    for name, t in (("param", p), ("grad", gr), ("exp_avg", m), ("exp_avg_sq", v)):
+        table[name] = np.arange(n, dtype=np.uint64) * 4 + t.data_ptr()
+    table["numel"] = 1
+    table["param_dtype"] = table["grad_dtype"] = table["state_dtype"] = sdc.F32
+    h, nbytes, info = ctypes.c_void_p(table.ctypes.data), ctypes.c_uint64(0), sdc._AdamwInfo()
+    assert sdc._lib.sdc_adamw_plan_bytes(h, n, 1, ctypes.byref(nbytes)) == 0
+    buf = torch.empty(nbytes.value, dtype=torch.uint8, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    assert sdc._lib.sdc_adamw_plan_build(h, n, 1, buf.data_ptr(), buf.numel(), ctypes.byref(info), s) == 0
+    assert sum(info.n_wave) == n
+    groups = torch.tensor([[1e-2, 0.9, 0.99, 1e-8, 0.0]], dtype=torch.float64, device=DEV)
+    rows = torch.zeros((n, 4), dtype=torch.int64, device=DEV)
+    sdc.sdc_adamw_step(sdc.AdamwPlan(buf, info, [], torch.device(DEV, 0)), groups, sdc.sdc_adamw_control(DEV), rows=rows)
+    assert ((m.double() - want_m).abs() <= tol_m).all()
+    assert ((v.double() - want_v).abs() <= 8 * U * want_v).all()
+    tol_p = 4 * U * p0.abs() + 16 * U * update.abs() + 1e-2 / (1 - 0.9) * tol_m / den
+    assert ((p.double() - (p0 - update)).abs() <= tol_p).all()
+    bits = p.view(torch.int32).long() & 0xFFFFFFFF
+    assert torch.equal(rows[:, 0], bits) and torch.equal(rows[:, 1], bits) and torch.equal(rows[:, 2], bits)
+    assert not rows[:, 3].any()
+
+
 def test_binding_refuses():
     lst = List([100], "bf16", "bf16", False, 32, seed=18)
     P, G, M, V = [lst.p], [lst.g], [lst.m], [lst.v]
@@ -421,6 +460,11 @@ def test_binding_refuses():
         build(P, [lst.g.cpu()], M, V)
     with pytest.raises(ValueError):
         build(P, [], M, V)
+    for twice in ((P * 2, G * 2, M + [M[0].clone()], V + [V[0].clone()]),
+                  (P, G, M, M),
+                  (P + [P[0].clone()], G * 2, M * 2, V + [V[0].clone()])):
+        with pytest.raises(ValueError, match="listed twice"):
+            build(*twice)
     with pytest.raises(ValueError):
         build([torch.zeros(10, 20, device=DEV).bfloat16().t()[:, :10]], G, M, V)
     with pytest.raises(sdc.SdcError):

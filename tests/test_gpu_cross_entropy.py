@@ -258,6 +258,34 @@ def test_few_tokens_wherever_their_rows_lie(n, d):
     assert torch.equal(rows[0], rows[1]) and torch.equal(rows[0], rows[2])
 
 
+def test_more_tiles_than_one_launch_takes():
+    """2^21 tokens over 2^18 + 300 words (8.4 million tiles: a grid has fewer than
+    2^32 threads), the word that a token's logit stands out at in the first, a
+    middle and the last rows of the vocabulary."""
+    n, v = 1 << 21, (1 << 18) + 300
+    say(f"case xent n={n} v={v}")
+    words = (3, v // 2, v - 1)
+    x = torch.zeros(n, 8, dtype=BF, device=DEV)
+    w = torch.zeros(v, 8, dtype=BF, device=DEV)
+    kind = torch.arange(n, device=DEV) % 3
+    x[torch.arange(n, device=DEV), kind] = 8.0
+    for j, at in enumerate(words):
+        w[at, j] = 1.0
+    t = torch.tensor(words, device=DEV)[kind]
+    row = torch.empty((1, 4), dtype=torch.int64, device=DEV)
+    loss, lse, total = sdc.sdc_cross_entropy(x, w, t, row=row)
+    want = np.log(v - 1 + np.exp(8.0))
+    # exact logits; the sum and the logarithm as in the note at the top
+    tol = U * (6 * 8 + 80 + 2 * want)
+    assert (lse.double() - want).abs().max().item() <= tol
+    assert (loss.double() - (want - 8)).abs().max().item() <= tol + 2 * U * 16
+    assert abs(total.item() - n * (want - 8)) <= n * (tol + 2 * U * 16) + U * n * want
+    bits = 0x41000000                                            # of 8.0f
+    at = np.arange(n, dtype=np.uint64) * np.uint64(v) + np.array(words, dtype=np.uint64)[np.arange(n) % 3] + np.uint64(1)
+    got = sdc.rows_numpy(row)[0].tolist()
+    assert got == [n * bits, int(at.sum(dtype=np.uint64)) * bits % 2 ** 64, 0, 0]
+
+
 def test_gradient_against_differences():
     """Central differences of the 64-bit loss at 16-bit x and w: their error is
     the second-order remainder, e^2 / 6 times a third derivative below 1."""
