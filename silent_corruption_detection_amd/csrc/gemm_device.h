@@ -3,8 +3,8 @@
 // contiguous either in k or, "k-major", in m (n), accumulated in fp32 by MFMA.
 //
 // A workgroup computes an M x N tile of C (a Shape): 256 x 256 by 8 waves, 128 x
-// 128 by 4 where the larger tiles would be too few to fill the chip, and 128 x
-// 32 by 4 for few rows of B.  Wave (wm, wn) holds M / WM rows and N / WN columns
+// 128 or 64 x 64 by 4 where the larger tiles would be too few to fill the chip,
+// and 128 x 32 or 64 x 32 by 4 for few rows of B.  Wave (wm, wn) holds M / WM rows and N / WN columns
 // of it as I x J groups of 16 x 16 (for 256 x 256: 128 accumulator registers).
 // k advances 64 at a time through two LDS buffers (64 KiB each for 256 x 256):
 // the next buffer is filled by direct global-to-LDS loads (16 bytes a lane, no
@@ -33,9 +33,10 @@ namespace {
 
 constexpr uint32_t kTileK = 64;  // k per LDS buffer
 
-template <uint32_t M_, uint32_t N_, uint32_t WM_, uint32_t WN_>
+template <uint32_t M_, uint32_t N_, uint32_t WM_, uint32_t WN_, uint32_t DEEP = 0>
 struct Shape {
   static constexpr uint32_t M = M_, N = N_, WM = WM_, WN = WN_;
+  static constexpr uint32_t kDeep = DEEP;  // steps in flight of gemm_tile_deep
   static constexpr uint32_t kThreads = 64 * WM * WN;
   static constexpr int I = M / WM / 16, J = N / WN / 16;
   static constexpr uint32_t kA = M * kTileK * 2, kBuf = (M + N) * kTileK * 2;  // bytes of A, of both, of one k step
@@ -43,7 +44,9 @@ struct Shape {
 };
 typedef Shape<256, 256, 2, 4> BigTile;
 typedef Shape<128, 128, 2, 2> SmallTile;
-typedef Shape<128, 32, 4, 1> FewTile;
+typedef Shape<64, 64, 2, 2> TinyTile;
+typedef Shape<128, 32, 4, 1, 3> FewTile;
+typedef Shape<64, 32, 4, 1, 4> FewTinyTile;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -120,7 +123,7 @@ __device__ __forceinline__ void load_to_lds(const unsigned char* src, uint32_t b
 // How A's rows may lie: at 16-byte boundaries (kAt16), read straight into LDS;
 // or anywhere (kAny: rows of at least 8 elements at any even address, of any
 // length), read through registers, which direct loads to LDS cannot.  kDeep:
-// anywhere, and both operands through registers three steps ahead (see
+// anywhere, and both operands through registers, several steps ahead (see
 // gemm_tile_deep).
 enum RowsAt : int { kAt16, kAny, kDeep };
 
@@ -291,36 +294,34 @@ __device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& 
   for (int i = 0; i < S::I; ++i)
 #pragma unroll
     for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4 ha[3][sa.kLoads], hb[3][sb.kLoads];  // step k of every three in set k % 3
+  u32x4 ha[S::kDeep][sa.kLoads], hb[S::kDeep][sb.kLoads];  // step k of every kDeep in set k % kDeep
 #pragma unroll
-  for (uint32_t i = 0; i < 3; ++i) {
+  for (uint32_t i = 0; i < S::kDeep; ++i) {
     sa.fill(k0 + i * kTileK, 0, ha[i]);
     sb.fill(k0 + i * kTileK, 0, hb[i]);
   }
   sa.settle(k0, ha[0], lds);
   sb.settle(k0, hb[0], lds + S::kA);
   uint32_t buf = 0;
-  const auto step = [&](uint32_t k, auto set) {
-    constexpr int C = decltype(set)::value, N = (C + 1) % 3;
-    // own writes of this buffer and reads of the other are done (a barrier that
-    // also waited for the loads in flight would undo them)
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
-    asm volatile("" ::: "memory");
-    sa.fill(k + 3 * kTileK, 0, ha[C]);
-    sb.fill(k + 3 * kTileK, 0, hb[C]);
-    __builtin_amdgcn_sched_barrier(0);  // the loads go first
-    gemm_step<T, S>(sa, sb, lds + buf * S::kBuf, lds + buf * S::kBuf + S::kA, acc);
-    buf ^= 1u;
-    sa.settle(k + kTileK, ha[N], lds + buf * S::kBuf);
-    sb.settle(k + kTileK, hb[N], lds + buf * S::kBuf + S::kA);
-  };
-  // Steps past the last, up to a multiple of three, multiply zeros: no sum that
+  // Steps past the last, up to a multiple of kDeep, multiply zeros: no sum that
   // starts at +0 changes by them.
-  for (uint32_t k = k0; k < k1; k += 3 * kTileK) {
-    step(k, std::integral_constant<int, 0>());
-    step(k + kTileK, std::integral_constant<int, 1>());
-    step(k + 2 * kTileK, std::integral_constant<int, 2>());
+  for (uint32_t k = k0; k < k1; k += S::kDeep * kTileK) {
+#pragma unroll
+    for (uint32_t i = 0; i < S::kDeep; ++i) {
+      const uint32_t next = (i + 1) % S::kDeep, at_k = k + i * kTileK;
+      // own writes of this buffer and reads of the other are done (a barrier that
+      // also waited for the loads in flight would undo them)
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
+      asm volatile("" ::: "memory");
+      sa.fill(at_k + S::kDeep * kTileK, 0, ha[i]);
+      sb.fill(at_k + S::kDeep * kTileK, 0, hb[i]);
+      __builtin_amdgcn_sched_barrier(0);  // the loads go first
+      gemm_step<T, S>(sa, sb, lds + buf * S::kBuf, lds + buf * S::kBuf + S::kA, acc);
+      buf ^= 1u;
+      sa.settle(at_k + kTileK, ha[next], lds + buf * S::kBuf);
+      sb.settle(at_k + kTileK, hb[next], lds + buf * S::kBuf + S::kA);
+    }
   }
   __syncthreads();  // the buffers may be reused
 }

@@ -264,8 +264,7 @@ constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
   uint32_t N, d, V, d_pad;
-  uint32_t tile;         // 256, 128 or kFew, of the logits' product
-  uint32_t vtile;        // vocabulary rows of that tile
+  uint32_t tile, vtile;  // tokens (256, 128, 64 or kFew) and vocabulary rows of the logits' tiles
   uint32_t nt, vt;       // tiles of the tokens, of the whole vocabulary
   uint32_t ptile;        // 256 or 128, of the gradient's products
   bool copy_x, copy_w;   // the operand needs an aligned copy
@@ -276,7 +275,7 @@ struct Head {
   uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
 };
 
-// The tile of FewTile (128 x 32).
+// Tokens of the tiles for few of them.
 constexpr uint32_t kFew = FewTile::N;
 
 uint32_t tiles(uint64_t n, uint32_t tile) { return (uint32_t)((n + tile - 1) / tile); }
@@ -296,20 +295,33 @@ int32_t check_head(const sdc_head* h) {
   return SDC_OK;
 }
 
-// The tile of the logits' product, from the rounds that 256 CUs take: a 128 x
-// 128 tile has a quarter of the work at 1.15 times the cost (twice the operand
-// bytes per operation).  The larger tile wins where it fills whole rounds, the
-// smaller where it would leave CUs idle or tiles half empty.  Measured (us, 128
-// / 256): 100 x 2048 x 50304 53 / 79, 300 x 1000 x 16000 33 / 43, 2000 x 512 x
-// 8000 30 / 28, 800 x 2048 x 50304 188 / 232, 1500 x 4096 x 30000 370 / 332.
-// Up to 32 tokens fit one 128 x 32 tile, whose few accumulators leave the
-// registers to keep three steps of loads in flight.  Measured against 128 x 128 (us): 5 x
+// The tile of the logits' product, from the rounds that 256 CUs take: a tile has
+// the work of its share of a 256 x 256 one at 1.15 times the cost for 128 x 128
+// (twice the operand bytes per operation) and 2 for 64 x 64.  Larger tiles win
+// where they fill whole rounds, smaller ones where they would leave CUs idle (a
+// CU takes about 27 GB/s from beyond its L2 whatever is in flight) or tiles half
+// empty.  Measured (loss, us, 128 / 256): 100 x 2048 x 50304 53 / 79, 300 x 1000
+// x 16000 33 / 43, 2000 x 512 x 8000 30 / 28, 800 x 2048 x 50304 188 / 232, 1500
+// x 4096 x 30000 370 / 332; (64 / 128): 755 x 5296 x 688 54 / 79, 100 x 2048 x
+// 8000 28 / 33, 64 x 8192 x 32000 142 / 154, 500 x 2048 x 10000 49 / 39, 64 x
+// 2048 x 50304 48 / 44.
+// Up to 32 tokens fit a tile of 32, whose few accumulators leave the registers
+// to keep several steps of loads in flight.  Measured against 128 x 128 (us): 5 x
 // 8190 x 128255 396 / 486, 32 x 1001 x 20001 25 / 37, 32 x 2048 x 50304 49 / 48.
 uint32_t logit_tile(uint64_t n, uint64_t vocab) {
-  const auto rounds = [&](uint32_t t) { return ((uint64_t)tiles(n, t) * tiles(vocab, t) + 255) / 256; };
   if (n <= kFew) return kFew;
-  return (double)rounds(128) * (1.15 / 4) < (double)rounds(256) ? 128u : 256u;
+  const auto cost = [&](uint32_t t, double each) {
+    return (double)(((uint64_t)tiles(n, t) * tiles(vocab, t) + 255) / 256) * each;
+  };
+  const double c256 = cost(256, 1.0), c128 = cost(128, 1.15 / 4), c64 = cost(64, 2.0 / 16);
+  if (c64 < c128 && c64 < c256) return 64;
+  return c128 < c256 ? 128 : 256;
 }
+
+// Vocabulary rows of a tile of 32 tokens: 128, or 64 where those would leave CUs
+// idle.  Measured (loss, us, 64 / 128): 4 x 3312 x 8340 30 / 39, 10 x 4096 x
+// 24000 42 / 48, 10 x 4096 x 32768 53 / 51, 19 x 836 x 49450 37 / 32.
+uint32_t few_rows(uint64_t vocab) { return tiles(vocab, FewTile::M) < 256 ? FewTinyTile::M : FewTile::M; }
 
 // Parts that dx's sum over `rows` vocabulary rows is split into: 256 tiles.
 uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
@@ -351,7 +363,7 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.copy_w = p.any && h->d < 8;
   p.any = p.any && !p.copy_w;
   p.tile = logit_tile(p.N, p.V);
-  p.vtile = p.tile == kFew ? (uint32_t)FewTile::M : p.tile;
+  p.vtile = p.tile == kFew ? few_rows(p.V) : p.tile;
   p.copy_x = (h->d % 8 || h->x_stride % 8 || reinterpret_cast<uintptr_t>(h->x) % 16) &&
              (p.tile != kFew || h->d < 8);  // few rows are read where they lie
   p.nt = tiles(p.N, p.tile);
@@ -486,7 +498,7 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
       const uint32_t v0 = k * p.piece, n = std::min(p.piece, p.V - v0);
       if ((st = piece_operands(h, p, o, ws, v0, n, &a, s))) return st;
       a.rows = d_row ? rows : nullptr;
-      const HeadLaunch l = {h->dtype, p.tile, p.ptile};
+      const HeadLaunch l = {h->dtype, p.vtile, p.ptile};
       if ((st = p.tile == kFew ? launch_logit_lse_few(l, a, s)
                 : p.any        ? launch_logit_lse_any(l, a, s)
                                : launch_logit_lse16(l, a, s)))
@@ -498,7 +510,7 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
   const RowArgs r = {reinterpret_cast<const float2*>(ws + o.part), p.vt, p.N, p.d,
                      static_cast<const unsigned char*>(h->x), static_cast<const unsigned char*>(h->w),
                      2 * h->x_stride, 2 * h->w_stride, h->target, h->vocab, d_loss, d_lse, d_total, d_count};
-  st = for_type<kAt16>(h->dtype, 128, [&](auto t, auto) {
+  st = for_dtype(h->dtype, [&](auto t) {
     typedef decltype(t) T;
     if (p.N <= kFewTokens) {
       hipLaunchKernelGGL(few_tokens_kernel<T>, dim3(1), dim3(1024), 0, s, r);
@@ -579,7 +591,7 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     x.first = k == 0;
     x.grad = d_grad;
     x.dw = d_dw ? static_cast<uint16_t*>(d_dw) + (uint64_t)v0 * p.d : nullptr;
-    const HeadLaunch l = {h->dtype, p.tile, p.ptile};
+    const HeadLaunch l = {h->dtype, p.vtile, p.ptile};
     if ((st = p.tile == kFew ? launch_logit_dz_few(l, a, s)
               : p.any        ? launch_logit_dz_any(l, a, s)
                              : launch_logit_dz16(l, a, s)))
@@ -587,7 +599,7 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
     if ((st = p.any ? launch_products_any(l, x, s) : launch_products16(l, x, s))) return st;
   }
   if (d_dx) {
-    st = for_type<kAt16>(h->dtype, 128, [&](auto t, auto) {
+    st = for_dtype(h->dtype, [&](auto t) {
       typedef decltype(t) T;
       hipLaunchKernelGGL(dx_finish_kernel<T>, dim3(p.N, (p.d + 255) / 256), dim3(256), 0, s, dxp, p.splits, p.N, p.d,
                          h->target, h->vocab, d_grad, static_cast<uint16_t*>(d_dx));

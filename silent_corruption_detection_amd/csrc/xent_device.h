@@ -45,8 +45,8 @@ struct ProductArgs {
   uint16_t* dw;        // of the piece's first row
 };
 
-// Launches over the tiles of one piece; tile: 256, 128, or 32 (128 x 32) of the
-// logits' product, ptile: 256 or 128, of the gradient's.
+// Launches over the tiles of one piece; tile: the rows of W of the logits'
+// product's (256, 128 or 64), ptile: 256 or 128, of the gradient's.
 struct HeadLaunch {
   uint32_t dtype, tile, ptile;
 };
@@ -309,21 +309,25 @@ __global__ void __launch_bounds__(S::kThreads) products_kernel(const ProductArgs
   else dw_tile<T, S>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
 }
 
-// f(type, shape) with both as types; tile: 256, 128, or 32 for FewTile, which is
-// the only one of kDeep and of no other.
+// f(type)
+template <class F>
+int32_t for_dtype(uint32_t dtype, F&& f) {
+  return dtype == SDC_BF16 ? f(Bf16()) : f(Fp16());
+}
+
+// f(type, shape) of the logits' product; tile: rows of the shape.  kDeep has the
+// shapes for few tokens, the others the square ones.
 template <RowsAt AT, class F>
-int32_t for_type(uint32_t dtype, uint32_t tile, F&& f) {
-  if constexpr (AT == kDeep) {
-    return dtype == SDC_BF16 ? f(Bf16(), FewTile()) : f(Fp16(), FewTile());
-  } else {
-    if (dtype == SDC_BF16) return tile == 256 ? f(Bf16(), BigTile()) : f(Bf16(), SmallTile());
-    return tile == 256 ? f(Fp16(), BigTile()) : f(Fp16(), SmallTile());
-  }
+int32_t for_logits(uint32_t dtype, uint32_t tile, F&& f) {
+  return for_dtype(dtype, [&](auto t) {
+    if constexpr (AT == kDeep) return tile == 128 ? f(t, FewTile()) : f(t, FewTinyTile());
+    else return tile == 256 ? f(t, BigTile()) : tile == 128 ? f(t, SmallTile()) : f(t, TinyTile());
+  });
 }
 
 template <RowsAt AT>
 int32_t launch_logit_lse(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
-  return for_type<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
+  return for_logits<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
     typedef decltype(t) T;
     typedef decltype(shape) S;
     const dim3 grid(a.n_tiles), block(S::kThreads);
@@ -335,7 +339,7 @@ int32_t launch_logit_lse(const HeadLaunch& h, const LogitArgs& a, hipStream_t s)
 
 template <RowsAt AT>
 int32_t launch_logit_dz(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) {
-  return for_type<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
+  return for_logits<AT>(h.dtype, h.tile, [&](auto t, auto shape) {
     typedef decltype(t) T;
     typedef decltype(shape) S;
     const dim3 grid(a.n_tiles), block(S::kThreads);
@@ -347,11 +351,14 @@ int32_t launch_logit_dz(const HeadLaunch& h, const LogitArgs& a, hipStream_t s) 
 
 template <RowsAt AT>
 int32_t launch_products(const HeadLaunch& h, const ProductArgs& x, hipStream_t s) {
-  return for_type<AT>(h.dtype, h.ptile, [&](auto t, auto shape) {
-    typedef decltype(t) T;
-    typedef decltype(shape) S;
-    hipLaunchKernelGGL((products_kernel<T, S, AT>), dim3(x.n_dx + x.n_dw), dim3(S::kThreads), lds_bytes<S>(), s, x);
-    return launch_status();
+  return for_dtype(h.dtype, [&](auto t) {
+    const auto launch = [&](auto shape) {
+      typedef decltype(t) T;
+      typedef decltype(shape) S;
+      hipLaunchKernelGGL((products_kernel<T, S, AT>), dim3(x.n_dx + x.n_dw), dim3(S::kThreads), lds_bytes<S>(), s, x);
+      return launch_status();
+    };
+    return h.ptile == 256 ? launch(BigTile()) : launch(SmallTile());
   });
 }
 

@@ -97,7 +97,7 @@ def check(x, w, t, g=0.25, ex=None):
 @pytest.mark.parametrize("n, d, v", [
     (1, 1, 1), (1, 8, 2), (2, 7, 3), (1, 64, 300), (3, 65, 255), (17, 63, 256), (16, 128, 257), (64, 72, 511),
     (65, 200, 1000), (255, 256, 129), (256, 64, 512), (257, 320, 513), (300, 1000, 777), (33, 33, 4097),
-    (1037, 264, 1501), (5, 2048, 1003), (400, 200, 25011), (400, 203, 25011), (300, 1027, 30001), (129, 9, 24500)])
+    (1037, 264, 1501), (5, 2048, 1003), (100, 328, 30000), (400, 200, 25011), (400, 203, 25011), (300, 1027, 30001), (129, 9, 24500)])
 def test_sizes(n, d, v, dtype):
     say(f"case xent n={n} d={d} v={v} {dtype}")
     check(*make(n, d, v, dtype, seed=n + d + v, ignored=0.3 if n > 2 else 0.0))
@@ -194,7 +194,8 @@ def test_split_sum_of_dx():
 def test_logit_rows_are_those_of_the_logits():
     """Small whole numbers make every logit exact, so the row is the scan's row
     of the logits in memory; the gradient's recomputed logits have it too."""
-    for n, d, v, dtype in ((1, 8, 3, BF), (300, 64, 700, BF), (257, 200, 511, FP), (9, 33, 1025, BF)):
+    for n, d, v, dtype in ((1, 8, 3, BF), (300, 64, 700, BF), (257, 200, 511, FP), (9, 33, 1025, BF),
+                           (100, 72, 30000, FP), (400, 64, 25011, BF), (9, 65, 33000, FP)):
         g = gen(n)
         x = torch.randint(-4, 5, (n, d), device=DEV, generator=g).to(dtype)
         w = torch.randint(-4, 5, (v, d), device=DEV, generator=g).to(dtype)
