@@ -801,8 +801,9 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     blocks = [-(-m // _STATE_BLOCK) for m in numels]
     for name, scales in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
         keep += _adamw_column(table, name, scales, blocks, [{torch.uint8}] * n, dev)[0]
-    written = np.concatenate([table[c] for c in ("param", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
-                                                 "exp_avg_sq_scale")])
+    stepped = table[table["grad"] != 0]
+    written = np.concatenate([stepped[c] for c in ("param", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
+                                                   "exp_avg_sq_scale")])
     written = np.sort(written[written != 0])
     if (written[1:] == written[:-1]).any():
         raise ValueError("a tensor that the step writes is listed twice (shared weights: list them once)")
