@@ -11,13 +11,15 @@ namespace sdc {
 constexpr uint64_t kAdamwMagic = 0x31766D6164414453ull;  // "SDAdamv1", little-endian
 
 // A tensor is cut into items of one round of loads of a workgroup each (a
-// multiple of the 128-element block of an 8-bit state); tensors of up to
-// kAdamwWaveElems elements are items of one wave.  One round, because what
+// multiple of the 128-element block of an 8-bit state).  One round, because what
 // hides the memory's latency here is the number of waves that load: longer
 // items measured 4921 / 5130 / 5200 us at 4096 / 16384 / 65536 elements, this size
-// 4826 us (0.96B fp32 weights).
+// 4826 us (0.96B fp32 weights).  Tensors of up to a wave's round are items of one
+// wave: with waves for up to 2048 / 1024 / 512 / 128 elements, lists of small
+// tensors measured 607 / 601 / 596 / 589 us (20,000 of up to 65536 elements) and 92 /
+// 86 / 83 / 82 us (4,000, 8-bit states); below a round a wave's lanes idle.
 constexpr uint64_t kAdamwItemElems = 2048;
-constexpr uint64_t kAdamwWaveElems = 2048;
+constexpr uint64_t kAdamwWaveElems = 512;
 
 // Elements that share one scale byte of an 8-bit state.
 constexpr uint32_t kStateBlock = 128;
