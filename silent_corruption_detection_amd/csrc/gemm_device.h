@@ -22,8 +22,10 @@
 //     over the 16 rows that one transposing read takes.  A group is two
 //     transposing 8-byte reads (each gives a lane four k of its column), which
 //     is what spares transposed copies of the weights, the inputs and dz.
-// Measured alone on random data, 256 x 256: 4096 x 32768 x 2048 (rows along k)
-// 431 us (1275 TFLOP/s), 2048 x 32768 x 4096 (k-major) 455 us (1210).
+// Measured, 256 x 256: 2048 x 128256 x 8192 (rows along k, with the softmax'
+// statistics) 3290 us (1310 TFLOP/s), the whole gradient of that size, two thirds
+// of it k-major products, 10.9 ms (1190 TFLOP/s).  Four waves of 128 x 128 instead, which read a third less from
+// LDS, measured 10 to 14 % slower: with one wave a SIMD nothing covers its waits.
 #pragma once
 
 #include "scan_device.h"
@@ -151,7 +153,8 @@ struct Side {
   static constexpr uint32_t kRow = 2 * ROWS;              // bytes of a k-major row
   static constexpr uint32_t kPass = THREADS * 16;         // bytes that one load of every thread fills
   static constexpr uint32_t kGranules = ROWS / 16 - 1;
-  static_assert(kLoads * THREADS == ROWS * 8 && (!KMAJOR || THREADS == 2 * ROWS), "the loads cover a step");
+  static constexpr uint32_t kPassK = THREADS * 8 / ROWS;  // k-major: rows of k that they fill
+  static_assert(kLoads * THREADS == ROWS * 8, "the loads cover a step");
   const unsigned char* p[kLoads];  // of the thread's loads of the next step
   uint64_t step;                   // bytes from one step to the next
   uint32_t limit;                  // k from here on reads as zero
@@ -170,7 +173,7 @@ struct Side {
       step = o.stride * kTileK;
 #pragma unroll
       for (uint32_t i = 0; i < kLoads; ++i) {
-        const uint32_t k = i * 16u + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
+        const uint32_t k = i * kPassK + k_in, f = (k & 3u) | ((k >> 3) & 3u) << 2;
         const uint32_t col = at0 + ((((t % (ROWS / 8)) >> 1) ^ (f & kGranules)) * 16u) + (t & 1u) * 8u;
         const uint32_t from = min(col, o.cols - 8u);
         p[i] = o.p + (uint64_t)(k0 + k) * o.stride + (uint64_t)from * 2u;
@@ -201,7 +204,7 @@ struct Side {
         const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
 #pragma unroll
         for (uint32_t i = 0; i < kLoads; ++i)
-          load_to_lds(k + k_in + (KMAJOR ? i * 16u : 0u) < limit ? p[i] : zero, base + i * kPass);
+          load_to_lds(k + k_in + (KMAJOR ? i * kPassK : 0u) < limit ? p[i] : zero, base + i * kPass);
       }
     } else if (AT == kAny && k + kTileK <= limit) {
 #pragma unroll
@@ -215,7 +218,7 @@ struct Side {
       const uint32_t back = past_end(k);
 #pragma unroll
       for (uint32_t i = 0; i < kLoads; ++i) {
-        const bool in = k + k_in + (KMAJOR ? i * 16u : 0u) < limit;
+        const bool in = k + k_in + (KMAJOR ? i * kPassK : 0u) < limit;
         held[i] = load16_any(in ? p[i] - back * 2u : zero);
         if (AT == kAny && !KMAJOR) held[i] = drop_elements(held[i], back);
       }
@@ -259,10 +262,16 @@ struct Side {
   }
 };
 
-// The products of a step from LDS at la and lb.
-template <class T, class S, class SA, class SB>
+// The products of a step from LDS at la and lb; during(s) is called between the
+// reads of half s of the step and their products: the next step's loads are
+// issued there, so that the LDS reads start right behind the barrier (2048 x 8192
+// x 128256: 3330 us; with the loads first 3760; with both halves read first 3450).
+// PRIO: the products go before other waves' work, which pays for k-major
+// operands only (with / without: the gradient of that size 10.9 ms / 11.2, its
+// loss, rows along k, 3390 us / 3330).
+template <class T, class S, bool PRIO, class SA, class SB, class F>
 __device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsigned char* la,
-                                          const unsigned char* lb, f32x4 (&acc)[S::I][S::J]) {
+                                          const unsigned char* lb, f32x4 (&acc)[S::I][S::J], F&& during) {
 #pragma unroll
   for (uint32_t s = 0; s < 2; ++s) {
     typename T::frag a[S::I], b[S::J];
@@ -270,10 +279,13 @@ __device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsi
     for (int j = 0; j < S::J; ++j) b[j] = sb.read(lb, j, s);
 #pragma unroll
     for (int i = 0; i < S::I; ++i) a[i] = sa.read(la, i, s);
+    during(s);
+    if constexpr (PRIO) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < S::I; ++i)
 #pragma unroll
       for (int j = 0; j < S::J; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
+    if constexpr (PRIO) __builtin_amdgcn_s_setprio(0);
   }
 }
 
@@ -317,7 +329,7 @@ __device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& 
       sa.fill(at_k + S::kDeep * kTileK, 0, ha[i]);
       sb.fill(at_k + S::kDeep * kTileK, 0, hb[i]);
       __builtin_amdgcn_sched_barrier(0);  // the loads go first
-      gemm_step<T, S>(sa, sb, lds + buf * S::kBuf, lds + buf * S::kBuf + S::kA, acc);
+      gemm_step<T, S, false>(sa, sb, lds + buf * S::kBuf, lds + buf * S::kBuf + S::kA, acc, [](uint32_t) {});
       buf ^= 1u;
       sa.settle(at_k + kTileK, ha[next], lds + buf * S::kBuf);
       sb.settle(at_k + kTileK, hb[next], lds + buf * S::kBuf + S::kA);
@@ -360,9 +372,12 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
       asm volatile("" ::: "memory");
-      if (k + kTileK < k1) fill(k + kTileK, buf ^ 1u);
       const unsigned char* la = lds + buf * S::kBuf;
-      gemm_step<T, S>(sa, sb, la, la + S::kA, acc);
+      gemm_step<T, S, AK>(sa, sb, la, la + S::kA, acc, [&](uint32_t s) {
+        if (k + kTileK >= k1) return;
+        if (s == 0) sa.fill(k + kTileK, lds0 + (buf ^ 1u) * S::kBuf, ha);
+        else sb.fill(k + kTileK, lds0 + (buf ^ 1u) * S::kBuf + S::kA, hb);
+      });
       if (k + kTileK < k1) sa.settle(k + kTileK, ha, lds + (buf ^ 1u) * S::kBuf);
     }
     __syncthreads();  // the buffers may be reused
