@@ -224,11 +224,14 @@ def _scan_stream(stream, device, made):
     return stream.cuda_stream
 
 
+_NO_GUARD = contextlib.nullcontext()
+
+
 def _device_guard(device):
     """Context in which `device` is the current device (launches and pointers
     belong to the current one); free when it already is."""
     if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _NO_GUARD
     return torch.cuda.device(device)
 
 
@@ -722,18 +725,9 @@ class AdamwPlan:
 
     def __init__(self, buf, info, tensors, device):
         self.buf, self.info, self.tensors, self.device = buf, info, tensors, device
-
-    @property
-    def n_tensors(self):
-        return self.info.n_tensors
-
-    @property
-    def n_groups(self):
-        return self.info.n_groups
-
-    @property
-    def total_elems(self):
-        return self.info.total_elems
+        # read once: every ctypes access adds to a step's host time
+        self.n_tensors, self.n_groups, self.total_elems = info.n_tensors, info.n_groups, info.total_elems
+        self._args = buf.data_ptr(), ctypes.byref(info)
 
 
 def _adamw_column(table, name, tensors, numels, dtypes, dev):
@@ -850,7 +844,7 @@ def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0
     rows: an int64 [n_tensors, 4] device tensor that receives the new weights'
     fingerprint rows."""
     dev = plan.device
-    _arg(groups, "groups", torch.float64, 5 * plan.info.n_groups, dev)
+    _arg(groups, "groups", torch.float64, 5 * plan.n_groups, dev)
     _arg(control, "control", torch.int64, 4, dev)
     if sq_total is not None:
         _arg(sq_total, "sq_total", torch.float64, 1, dev)
@@ -860,7 +854,7 @@ def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0
         _arg(rows, "rows", torch.int64, 4 * plan.n_tensors, dev)
     with _device_guard(dev):
         _check(_lib.sdc_adamw_step(
-            plan.buf.data_ptr(), ctypes.byref(plan.info), groups.data_ptr(), control.data_ptr(),
+            *plan._args, groups.data_ptr(), control.data_ptr(),
             None if sq_total is None else sq_total.data_ptr(), None if flag is None else flag.data_ptr(),
             max_norm, grad_scale, None if rows is None else rows.data_ptr(), _stream_handle(stream, dev)),
             "sdc_adamw_step")

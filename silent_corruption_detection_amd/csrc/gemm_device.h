@@ -4,8 +4,9 @@
 //
 // A workgroup computes an M x N tile of C (a Shape): 256 x 256 by 8 waves, 128 x
 // 128 or 64 x 64 by 4 where the larger tiles would be too few to fill the chip,
-// and 128 x 32 or 64 x 32 by 4 for few rows of B.  Wave (wm, wn) holds M / WM rows and N / WN columns
-// of it as I x J groups of 16 x 16 (for 256 x 256: 128 accumulator registers).
+// and 128 x 32 or 64 x 32 by 4 for few rows of B.  Wave (wm, wn) holds M / WM
+// rows and N / WN columns of it as I x J groups of 16 x 16 (for 256 x 256: 128
+// accumulator registers).
 // k advances 64 at a time through two LDS buffers (64 KiB each for 256 x 256):
 // the next buffer is filled by direct global-to-LDS loads (16 bytes a lane, no
 // registers) while the current one is multiplied.  Four buffers of 32 k instead
@@ -24,8 +25,11 @@
 //     is what spares transposed copies of the weights, the inputs and dz.
 // Measured, 256 x 256: 2048 x 128256 x 8192 (rows along k, with the softmax'
 // statistics) 3290 us (1310 TFLOP/s), the whole gradient of that size, two thirds
-// of it k-major products, 10.9 ms (1190 TFLOP/s).  Four waves of 128 x 128 instead, which read a third less from
-// LDS, measured 10 to 14 % slower: with one wave a SIMD nothing covers its waits.
+// of it k-major products, 10.9 ms (1190 TFLOP/s); MFMA units 62 % busy at 4096 x
+// 50304 x 2048.  Bound by LDS reads beside the products: a step of 256 x 256 x 64
+// reads 192 KiB and multiplies for 2048 cycles.  Four waves of 128 x 128 instead,
+// which read a third less, measured 10 to 14 % slower: with one wave a SIMD nothing
+// covers its waits.
 #pragma once
 
 #include "scan_device.h"

@@ -160,11 +160,17 @@ __device__ __forceinline__ float token_loss(const RowArgs& a, uint32_t n) {
     for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
   }
   float m = -__builtin_inff(), s = 0.0f;
-  for (uint32_t k = l; k < a.n_vt; k += 64) {
-    const float2 p = a.part[(uint64_t)n * a.n_vt + k];
-    const float M = __builtin_fmaxf(m, p.x);
-    s = s * rescale(m, M) + p.y * rescale(p.x, M);
-    m = M;
+  for (uint32_t k = l; k < a.n_vt; k += 512) {  // eight loads in flight
+    float2 p[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+      p[i] = k + 64u * i < a.n_vt ? a.part[(uint64_t)n * a.n_vt + k + 64u * i] : float2{-__builtin_inff(), 0.0f};
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const float M = __builtin_fmaxf(m, p[i].x);
+      s = s * rescale(m, M) + p[i].y * rescale(p[i].x, M);
+      m = M;
+    }
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
