@@ -579,7 +579,8 @@ int32_t sdc_cross_entropy(const sdc_head* h_head, void* d_ws, uint64_t ws_bytes,
  * precision; one of the two may be NULL and is then not computed.  d_lse: the
  * forward pass'.  d_row: as there, of the recomputed logits; with d_ref (the
  * forward pass' row) a difference under col_mask adds 1 to *d_mismatch
- * (required then; the caller clears it).
+ * (required then; the caller clears it).  Outputs and workspace must not
+ * overlap the head.
  * ASYNCHRONOUS on stream.  Errors as sdc_cross_entropy. */
 int32_t sdc_cross_entropy_grad(const sdc_head* h_head, const float* d_lse, const float* d_grad,
                                void* d_ws, uint64_t ws_bytes, void* d_dx, void* d_dw,

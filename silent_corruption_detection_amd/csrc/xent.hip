@@ -311,14 +311,14 @@ int32_t check_head(const sdc_head* h) {
 // (twice the operand bytes per operation) and 2 for 64 x 64.  Larger tiles win
 // where they fill whole rounds, smaller ones where they would leave CUs idle (a
 // CU takes about 27 GB/s from beyond its L2 whatever is in flight) or tiles half
-// empty.  Measured (loss, us, 128 / 256): 100 x 2048 x 50304 53 / 79, 300 x 1000
-// x 16000 33 / 43, 2000 x 512 x 8000 30 / 28, 800 x 2048 x 50304 188 / 232, 1500
-// x 4096 x 30000 370 / 332; (64 / 128): 755 x 5296 x 688 54 / 79, 100 x 2048 x
-// 8000 28 / 33, 64 x 8192 x 32000 142 / 154, 500 x 2048 x 10000 49 / 39, 64 x
-// 2048 x 50304 48 / 44.
+// empty.  Measured (loss, us, 64 / 128 / 256): 755 x 5296 x 688 60 / 83 / 133, 100 x
+// 2048 x 8000 29 / 35 / 55, 500 x 2048 x 10000 50 / 39 / 56, 100 x 2048 x 50304 58 /
+// 46 / 64, 300 x 1000 x 16000 39 / 30 / 38, 800 x 2048 x 50304 278 / 211 / 219, 2000 x
+// 512 x 8000 39 / 32 / 29, 1500 x 4096 x 30000 604 / 371 / 307.
 // Up to 32 tokens fit a tile of 32, whose few accumulators leave the registers
-// to keep several steps of loads in flight.  Measured against 128 x 128 (us): 5 x
-// 8190 x 128255 396 / 486, 32 x 1001 x 20001 25 / 37, 32 x 2048 x 50304 49 / 48.
+// to keep several steps of loads in flight.  Measured against 64 x 64 and 128 x
+// 128 (us): 5 x 8190 x 128255 391 / 434 / 567, 32 x 1001 x 20001 25 / 33 / 36, 32 x
+// 2048 x 50304 47 / 46 / 48.
 uint32_t logit_tile(uint64_t n, uint64_t vocab) {
   if (n <= kFew) return kFew;
   const auto cost = [&](uint32_t t, double each) {
@@ -345,8 +345,8 @@ uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
 // 256 x 256 tile, 3 of the smaller), over the workgroups that run at a time (one of
 // 256, or two of 128 a CU, whose steps take 0.575 of the time), or that of the
 // longest tile.  Measured (the whole gradient in us, 128 / 256): 4096 x 256 x
-// 12800 126 / 220, 600 x 1024 x 20000 109 / 137, 800 x 2048 x 50304 615 / 638,
-// 1500 x 4096 x 30000 1275 / 1085.
+// 12800 158 / 206, 600 x 1024 x 20000 122 / 123, 800 x 2048 x 50304 702 / 631,
+// 1500 x 4096 x 30000 1306 / 1055.
 uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
   const auto steps = [&](uint32_t t) {
     const double k_dw = (double)tiles(n, kTileK), k_dx = (double)tiles(rows, kTileK);
