@@ -577,7 +577,8 @@ int32_t sdc_cross_entropy(const sdc_head* h_head, void* d_ws, uint64_t ws_bytes,
  *   d_dx = dz w  (n x d, contiguous)      d_dw = dz^T x  (vocab x d, contiguous)
  * both of the head's dtype, summed in fp32 from dz rounded to that type's
  * precision; one of the two may be NULL and is then not computed.  d_lse: the
- * forward pass'.  d_row: as there, of the recomputed logits; with d_ref (the
+ * forward pass'; as an fp32 number it is off by up to |lse| 2^-24, and exp(z -
+ * lse) by that factor, as fp32 logits of that size are themselves.  d_row: as there, of the recomputed logits; with d_ref (the
  * forward pass' row) a difference under col_mask adds 1 to *d_mismatch
  * (required then; the caller clears it).  Outputs and workspace must not
  * overlap the head.

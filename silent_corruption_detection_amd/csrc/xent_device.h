@@ -73,9 +73,15 @@ typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ bool has_target(int64_t t, uint64_t vocab) { return (uint64_t)t < vocab; }
 
+// exp(x).  What it is called for is a difference of logits, taken before the
+// factor log2(e): x log2(e) - M log2(e) would hold the rounding of M log2(e),
+// which is no longer small beside the difference from |M| of 1e5 on and passes
+// any exponent from 3e9 on.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
 // exp(m - M) of a running maximum m <= M, also where both are the same infinity
 __device__ __forceinline__ float rescale(float m, float M) {
-  return m == M ? 1.0f : __builtin_amdgcn_exp2f((m - M) * kLog2e);
+  return m == M ? 1.0f : exp_of(m - M);
 }
 
 // ---- logit tiles ------------------------------------------------------------------
@@ -153,14 +159,14 @@ __global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs 
         if (m0 + at.row(i) + r < a.w.rows) m = __builtin_fmaxf(m, acc[i][j][r]);
     m = __builtin_fmaxf(m, __shfl_xor(m, 16));
     m = __builtin_fmaxf(m, __shfl_xor(m, 32));
-    const float c = (__builtin_isinf(m) ? 0.0f : m) * kLog2e;
+    const float shift = __builtin_isinf(m) ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < S::I; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (m0 + at.row(i) + r < a.w.rows)
-          s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
+          s += exp_of(acc[i][j][r] - shift);
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (at.lane < 16) half[at.wm * S::N + at.col(j)] = float2{m, s};
@@ -191,14 +197,14 @@ __global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a
   const uint32_t m0 = (id / a.nt) * S::M, n0 = (id % a.nt) * S::N;
   const Place<S> at;
   // what the epilogue needs of its tokens, in flight during the product
-  float c[S::J];
+  float lse[S::J];
   uint32_t hit[S::J];  // the target among the rows from at.row(0) on; kNone: no target
   constexpr uint32_t kNone = 0x80000000u;
 #pragma unroll
   for (int j = 0; j < S::J; ++j) {
     const uint32_t n = min(n0 + at.col(j), a.x.rows - 1u);
     const int64_t t = a.target[n];
-    c[j] = a.lse[n] * kLog2e;
+    lse[j] = a.lse[n];
     // at most 2^24 rows: the difference, also a negative one, is never kNone
     hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
   }
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a
       uint32_t b[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, -c[j]));
+        float p = exp_of(acc[i][j][r] - lse[j]);
         p = (p - (hit[j] == (uint32_t)(i * 16 + r) ? 1.0f : 0.0f)) * T::kDzScale;
         b[r] = T::bits(live && m0 + at.row(i) + r < a.w.rows ? p : 0.0f);
       }
