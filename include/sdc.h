@@ -560,7 +560,8 @@ int32_t sdc_cross_entropy_ws_bytes(const sdc_head* h_head, uint64_t* h_bytes, ui
 
 /* z = x w^T in fp32; per row n
  *   d_lse[n]   log sum_v exp z_nv
- *   d_loss[n]  d_lse[n] - z_n,target (0 without a target)
+ *   d_loss[n]  log sum_v exp z_nv - z_n,target, with the logit that is in the
+ *              sum (and in d_row), so never below 0 (0 without a target)
  *   *d_total   the losses' sum (added in double in a fixed order, rounded once)
  *   *d_count   rows with a target (NULL allowed)
  *   d_row      NULL, or (16-byte aligned) the fingerprint row of the n x vocab

@@ -69,7 +69,6 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t bits(float x) {
     return __builtin_bit_cast(unsigned short, (__bf16)x);
   }
-  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
 };
 
 struct Fp16 {
@@ -82,9 +81,6 @@ struct Fp16 {
   }
   static __device__ __forceinline__ uint32_t bits(float x) {
     return __builtin_bit_cast(unsigned short, (_Float16)x);
-  }
-  static __device__ __forceinline__ float value(uint32_t b) {
-    return (float)__builtin_bit_cast(_Float16, (unsigned short)b);
   }
 };
 

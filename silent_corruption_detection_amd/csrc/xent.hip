@@ -12,11 +12,12 @@
 // in memory: both passes can fingerprint the logits while they are in
 // registers.
 //
-// Forward: one launch of 256 x 256 logit tiles, each leaving its columns'
-// running maximum and sum of exponentials, one that merges a row's tiles and
-// takes the target's logit, one for the total.  The tiles are computed as
-// z^T (vocabulary down, tokens across), which puts 32 logits of one token
-// into each lane: a token's maximum and sum need two shuffles.
+// Forward: one launch of logit tiles, each leaving its columns' running maximum
+// and sum of exponentials and the targets' logits it holds, one that merges a
+// row's tiles into its loss, one for the total (one for both for few tokens).  The
+// tiles are computed as z^T (vocabulary down, tokens across), which puts 32 logits
+// of one token into each lane (256 x 256; 4 to 16 in the smaller tiles): a token's
+// maximum and sum need two shuffles.
 // Gradient: the vocabulary in pieces; per piece the logit tiles again, whose
 // epilogue writes dz (16-bit), then the two products of dz in one launch.  dx
 // is summed over pieces and splits in fp32 in a fixed order.  Bound by the
@@ -115,12 +116,10 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict_
 }
 
 // ---- row results -------------------------------------------------------------------
-// What the row kernels need of a head.
 struct RowArgs {
   const float2* part;  // [N][n_vt]
-  uint32_t n_vt, N, d;
-  const unsigned char *x, *w;
-  uint64_t x_stride, w_stride;  // bytes
+  const float* hit;    // the target's logit (rows with a target)
+  uint32_t n_vt, N;
   const int64_t* target;
   uint64_t vocab;
   float *loss, *lse;
@@ -128,38 +127,14 @@ struct RowArgs {
   uint64_t* count;
 };
 
-// Token n by one wave: merges its tiles' maxima and sums, and takes the
-// target's logit as a plain dot product (fp32, a fixed order).  Lane 0 stores;
-// every lane returns the loss.
-template <class T>
+// Token n by one wave: merges its tiles' maxima m and sums s.  The loss is
+// (m - z_target) + ln s, both at least 0 as s holds the maximum's 1: near zero it
+// keeps the digits that lse - z_target would lose to lse's size.  Lane 0
+// stores; every lane returns the loss.
 __device__ __forceinline__ float token_loss(const RowArgs& a, uint32_t n) {
   const uint32_t l = threadIdx.x & 63u;
-  const int64_t t = a.target[n];
-  const bool live = has_target(t, a.vocab);
-  float dot = 0.0f;
-  if (live) {
-    const unsigned char* p = a.x + (uint64_t)n * a.x_stride;
-    const unsigned char* q = a.w + (uint64_t)t * a.w_stride;
-    const auto add = [&](uint32_t u, uint32_t v) {
-      dot = __builtin_fmaf(T::value(u & 0xFFFFu), T::value(v & 0xFFFFu), dot);
-      dot = __builtin_fmaf(T::value(u >> 16), T::value(v >> 16), dot);
-    };
-    uint32_t c = l * 8u;
-#pragma unroll 4
-    for (; c + 8u <= a.d; c += 512u) {
-      const u32x4 u = load16_any(p + c * 2u), v = load16_any(q + c * 2u);
-      add(u.x, v.x);
-      add(u.y, v.y);
-      add(u.z, v.z);
-      add(u.w, v.w);
-    }
-    for (uint32_t e = 0; e < 7u; ++e)
-      if (c + e < a.d)
-        dot = __builtin_fmaf(T::value(*reinterpret_cast<const uint16_t*>(p + (c + e) * 2u)),
-                             T::value(*reinterpret_cast<const uint16_t*>(q + (c + e) * 2u)), dot);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) dot += __shfl_xor(dot, off);
-  }
+  const bool live = has_target(a.target[n], a.vocab);
+  const float hit = live ? a.hit[n] : 0.0f;
   float m = -__builtin_inff(), s = 0.0f;
   for (uint32_t k = l; k < a.n_vt; k += 512) {  // eight loads in flight
     float2 p[8];
@@ -179,20 +154,18 @@ __device__ __forceinline__ float token_loss(const RowArgs& a, uint32_t n) {
     s = s * rescale(m, M) + ps * rescale(pm, M);
     m = M;
   }
-  const float r = m + kLn2 * __builtin_amdgcn_logf(s), loss = live ? r - dot : 0.0f;
+  const float ln = kLn2 * __builtin_amdgcn_logf(s), loss = live ? (m - hit) + ln : 0.0f;
   if (l == 0) {
-    a.lse[n] = r;
+    a.lse[n] = m + ln;
     a.loss[n] = loss;
   }
   return loss;
 }
 
-// One wave a token: bound by its reads of x, of the targets' rows of W and of the
-// tiles' pairs (4096 x 2048 with 197 tiles: 10 us).
-template <class T>
+// One wave a token: bound by latency (4096 tokens with 197 tiles: 5.3 us).
 __global__ void __launch_bounds__(kBlock) lse_kernel(const RowArgs a) {
   const uint32_t n = wave_item_index();
-  if (n < a.N) token_loss<T>(a, n);
+  if (n < a.N) token_loss(a, n);
 }
 
 // total = sum of the losses (in double, thread t adding t, t + 1024, ..., then
@@ -229,14 +202,13 @@ __device__ __forceinline__ void store_total(const RowArgs& a, const float* loss)
 __global__ void __launch_bounds__(1024) loss_total_kernel(const RowArgs a) { store_total(a, a.loss); }
 
 // Few tokens: their losses and the total in one launch of one workgroup (one
-// token with 1002 tiles: 15 us; 19 with 387: 10).
+// token with 1002 tiles: 5.7 us; 19 with 387: 4.8).
 constexpr uint32_t kFewTokens = 32;
 
-template <class T>
 __global__ void __launch_bounds__(1024) few_tokens_kernel(const RowArgs a) {
   __shared__ float losses[kFewTokens];
   for (uint32_t n = threadIdx.x >> 6; n < a.N; n += 16) {
-    const float loss = token_loss<T>(a, n);
+    const float loss = token_loss(a, n);
     if ((threadIdx.x & 63u) == 0) losses[n] = loss;
   }
   __syncthreads();
@@ -408,7 +380,7 @@ Head plan_head(const sdc_head* h, bool grad) {
 }
 
 struct Layout {
-  uint64_t part, rows, xc, wc, xm, dz, dxp, end;
+  uint64_t part, hit, rows, xc, wc, xm, dz, dxp, end;
 };
 
 Layout layout_head(const Head& p, bool grad) {
@@ -422,13 +394,14 @@ Layout layout_head(const Head& p, bool grad) {
   o.rows = take(32ull * p.n_tiles);
   o.xc = take(p.copy_x ? 2ull * p.N * p.d_pad : 0);
   o.wc = take(p.copy_w ? 2ull * p.piece * p.d_pad : 0);
-  o.part = o.xm = o.dz = o.dxp = at;
+  o.part = o.hit = o.xm = o.dz = o.dxp = at;
   if (grad) {
     o.xm = take(2ull * p.N * p.d_pad);
     o.dz = take(2ull * p.N * p.piece);
     o.dxp = take(4ull * p.splits * p.N * p.d);
   } else {
     o.part = take(8ull * p.N * p.vt);
+    o.hit = take(4ull * p.N);
   }
   o.end = std::max<uint64_t>(at, 256);
   return o;
@@ -502,7 +475,9 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
   if (p.N > 0) {
     LogitArgs a = {};
     a.xcds = dev.xcds;
+    a.target = h->target;
     a.part = reinterpret_cast<float2*>(ws + o.part);
+    a.hit = reinterpret_cast<float*>(ws + o.hit);
     sdc_row* rows = reinterpret_cast<sdc_row*>(ws + o.rows);
     a.n_vt = p.vt;
     for (uint32_t k = 0; k < p.pieces; ++k) {
@@ -518,20 +493,17 @@ extern "C" int32_t sdc_cross_entropy(const sdc_head* h, void* d_ws, uint64_t ws_
       a.part += tiles(n, p.vtile);
     }
   }
-  const RowArgs r = {reinterpret_cast<const float2*>(ws + o.part), p.vt, p.N, p.d,
-                     static_cast<const unsigned char*>(h->x), static_cast<const unsigned char*>(h->w),
-                     2 * h->x_stride, 2 * h->w_stride, h->target, h->vocab, d_loss, d_lse, d_total, d_count};
-  st = for_dtype(h->dtype, [&](auto t) {
-    typedef decltype(t) T;
-    if (p.N <= kFewTokens) {
-      hipLaunchKernelGGL(few_tokens_kernel<T>, dim3(1), dim3(1024), 0, s, r);
-      return launch_status();
-    }
-    hipLaunchKernelGGL(lse_kernel<T>, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s, r);
-    if (int32_t e = launch_status()) return e;
+  const RowArgs r = {reinterpret_cast<const float2*>(ws + o.part), reinterpret_cast<const float*>(ws + o.hit), p.vt,
+                     p.N, h->target, h->vocab, d_loss, d_lse, d_total, d_count};
+  if (p.N <= kFewTokens) {
+    hipLaunchKernelGGL(few_tokens_kernel, dim3(1), dim3(1024), 0, s, r);
+    st = launch_status();
+  } else {
+    hipLaunchKernelGGL(lse_kernel, dim3((p.N + kWaves - 1) / kWaves), dim3(kBlock), 0, s, r);
+    if ((st = launch_status())) return st;
     hipLaunchKernelGGL(loss_total_kernel, dim3(1), dim3(1024), 0, s, r);
-    return launch_status();
-  });
+    st = launch_status();
+  }
   if (st) return st;
   if (d_row) return merge_logit_row(o, p, ws, nullptr, 0, d_row, nullptr, s);
   return SDC_OK;

@@ -19,11 +19,12 @@ struct LogitArgs {
   uint32_t nt;             // token tiles
   uint32_t n_tiles, xcds;
   uint64_t vocab;
-  // forward: [token][tile] maxima and sums
+  const int64_t* target;
+  // forward: [token][tile] maxima and sums, and the target's logit of each token
   float2* part;
   uint32_t n_vt;
+  float* hit;
   // gradient
-  const int64_t* target;
   const float* lse;
   uint16_t* dz;            // [x.rows][v_pad]
   uint32_t v_pad;
@@ -86,6 +87,17 @@ __device__ __forceinline__ float rescale(float m, float M) {
 
 // ---- logit tiles ------------------------------------------------------------------
 
+// The target of the token of a lane's column j, counted from the lane's first row
+// of the tile (at.row(0), vocabulary row `first`): logit (i, r) is the target's
+// where this is 16 i + r.  kNoTarget: none.  At most 2^24 rows, so a difference,
+// also a negative one, is never kNoTarget.
+constexpr uint32_t kNoTarget = 0x80000000u;
+template <class S>
+__device__ __forceinline__ uint32_t target_from(const LogitArgs& a, uint32_t n, uint32_t first) {
+  const int64_t t = a.target[min(n, a.x.rows - 1u)];
+  return has_target(t, a.vocab) && n < a.x.rows ? (uint32_t)t - first : kNoTarget;
+}
+
 // The tile's part of the fingerprint row of the fp32 logits [N][V].
 template <class S>
 __device__ __forceinline__ void tile_row(const f32x4 (&acc)[S::I][S::J], const LogitArgs& a, uint32_t m0,
@@ -138,16 +150,22 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[S::I][S::J], const L
 
 // Maximum m and sum of exp(z - m) of each token over the tile's vocabulary rows:
 // in a lane over its logits of the token, over the four lanes of its column by
-// two shuffles, over the waves through LDS.  Bound by the matrix cores; 4096 x
+// two shuffles, over the waves through LDS.  The lane that has the target's logit
+// stores it, so that the loss is made of the logits whose sum (and fingerprint)
+// was taken: a product of its own, summed in another order, would differ in the
+// last bits, and could exceed the largest logit.  Bound by the matrix cores; 4096 x
 // 50304 x 2048 takes 743 us (1135 TFLOP/s).
 template <class T, class S, RowsAt AT, bool ROW>
 __global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   const uint32_t id = xcd_run(blockIdx.x, a.n_tiles, a.xcds), vt = id / a.nt;
   const uint32_t m0 = vt * S::M, n0 = (id % a.nt) * S::N;
+  const Place<S> at;
+  uint32_t hit[S::J];  // read during the product
+#pragma unroll
+  for (int j = 0; j < S::J; ++j) hit[j] = target_from<S>(a, n0 + at.col(j), a.v0 + m0 + at.row(0));
   f32x4 acc[S::I][S::J];
   gemm_tile<T, S, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
-  const Place<S> at;
   float2* half = reinterpret_cast<float2*>(lds);  // [wm][token of the tile]
 #pragma unroll
   for (int j = 0; j < S::J; ++j) {
@@ -170,6 +188,14 @@ __global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs 
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
     if (at.lane < 16) half[at.wm * S::N + at.col(j)] = float2{m, s};
+    if (hit[j] < S::I * 16u && (hit[j] & 15u) < 4u && m0 + at.row(0) + hit[j] < a.w.rows) {
+      float z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::I; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z = hit[j] == (uint32_t)(i * 16 + r) ? acc[i][j][r] : z;
+      a.hit[n0 + at.col(j)] = z;
+    }
   }
   __syncthreads();
   if (threadIdx.x < S::N && n0 + threadIdx.x < a.x.rows) {
@@ -198,15 +224,11 @@ __global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a
   const Place<S> at;
   // what the epilogue needs of its tokens, in flight during the product
   float lse[S::J];
-  uint32_t hit[S::J];  // the target among the rows from at.row(0) on; kNone: no target
-  constexpr uint32_t kNone = 0x80000000u;
+  uint32_t hit[S::J];
 #pragma unroll
   for (int j = 0; j < S::J; ++j) {
-    const uint32_t n = min(n0 + at.col(j), a.x.rows - 1u);
-    const int64_t t = a.target[n];
-    lse[j] = a.lse[n];
-    // at most 2^24 rows: the difference, also a negative one, is never kNone
-    hit[j] = has_target(t, a.vocab) && n0 + at.col(j) < a.x.rows ? (uint32_t)t - (a.v0 + m0 + at.row(0)) : kNone;
+    lse[j] = a.lse[min(n0 + at.col(j), a.x.rows - 1u)];
+    hit[j] = target_from<S>(a, n0 + at.col(j), a.v0 + m0 + at.row(0));
   }
   f32x4 acc[S::I][S::J];
   gemm_tile<T, S, AT, false, false>(a.w, a.x, m0, n0, 0, a.K, lds, acc);
@@ -214,7 +236,7 @@ __global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a
   uint16_t* st = reinterpret_cast<uint16_t*>(lds);
 #pragma unroll
   for (int j = 0; j < S::J; ++j) {
-    const bool live = hit[j] != kNone;
+    const bool live = hit[j] != kNoTarget;
 #pragma unroll
     for (int i = 0; i < S::I; ++i) {
       uint32_t b[4];

@@ -1,6 +1,6 @@
 """GPU tests of the linear head's cross entropy at logits of any magnitude.
 
-Each logit is one product of two numbers of at most 8 significant bits, so it is
+In the first tests each logit is one product of two numbers of at most 8 significant bits, so it is
 exact in fp32, and what is tested is the softmax alone.  A row's largest logit
 stands so far above the others that its probability is 1 and theirs 0 to far
 below fp32: lse is that logit, rounded once (u = 2^-24 of it), and the gradient
@@ -112,3 +112,77 @@ def test_neighbouring_logits_of_a_million():
     want = 1e6 + torch.log(torch.tensor(16.0, dtype=torch.float64)).item()
     # ln 16 to a few u, then the rounding of the sum
     assert (lse.double() - want).abs().max().item() <= U * want + 1e-5
+
+
+SHAPES = [(5, 301), (70, 700), (400, 25011), (2000, 8000)]   # a tile of 32, 64, 128 and 256 tokens
+
+
+@pytest.mark.parametrize("n, v", SHAPES)
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_a_sure_row_loses_nothing(n, v, dtype):
+    """Rows of d = 3001 random elements whose target's logit is about 40, the others' about
+    +-1: the loss, below v exp(-35), is 0 in fp32.  It is taken from the logit that is in
+    the sum: one summed in another order would be off by some u 40 either way."""
+    d = 3001
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.empty(n, d, device=DEV).normal_(0, 1, generator=g).to(dtype)
+    w = torch.empty(v, d, device=DEV).normal_(0, d ** -0.5, generator=g).to(dtype)
+    t = torch.randperm(v, device=DEV, generator=g)[:min(n, v // 4)]
+    t = t.repeat(-(-n // len(t)))[:n]
+    first = torch.arange(len(t.unique()), device=DEV)        # rows that share a word share their x
+    for k in range(0, n, len(first)):
+        x[k:k + len(first)] = x[first][:min(len(first), n - k)]
+    w[t[first]] = (x[first].double() * (40 / x[first].double().square().sum(1, keepdim=True))).to(dtype)
+    z = x.double() @ w.double().t()
+    want = torch.nn.functional.cross_entropy(z, t, reduction="none")
+    assert want.max().item() < 1e-11
+    loss, lse, total = sdc.sdc_cross_entropy(x, w, t)
+    assert not loss.any() and total.item() == 0, (loss.min(), loss.max())
+    top = z.amax(1)
+    assert ((lse.double() - top).abs() <= (d + 8) * U * (x.double().abs() @ w.double().abs().t()).amax(1)).all()
+
+
+@pytest.mark.parametrize("n", [1, 33, 500])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_a_vocabulary_of_one(n, dtype):
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.empty(n, 777, device=DEV).normal_(0, 3, generator=g).to(dtype)
+    w = torch.empty(1, 777, device=DEV).normal_(0, 3, generator=g).to(dtype)
+    t = torch.zeros(n, dtype=torch.int64, device=DEV)
+    loss, lse, total = sdc.sdc_cross_entropy(x, w, t)
+    assert not loss.any() and total.item() == 0
+    dx, dw = sdc.sdc_cross_entropy_grad(x, w, t, lse, torch.ones(1, device=DEV))
+    assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("n, v", SHAPES)
+def test_equal_logits_of_a_million(n, v):
+    """All logits 1e6, exactly: the loss is ln v although lse, in fp32, has steps of 1/16."""
+    x = torch.zeros(n, 8, dtype=BF, device=DEV)
+    w = torch.zeros(v, 8, dtype=BF, device=DEV)
+    x[:, 0], w[:, 0] = 1000.0, 1000.0
+    t = torch.arange(n, device=DEV) * 7 % v
+    loss, _, _ = sdc.sdc_cross_entropy(x, w, t)
+    want = torch.log(torch.tensor(float(v), dtype=torch.float64)).item()
+    # a sum of ones below 2^24 is exact; the logarithm and its factor, 4 u
+    assert (loss.double() - want).abs().max().item() <= 4 * U * want
+
+
+def test_losses_are_never_below_zero():
+    """Random rows of large width, half of them nearly sure of their target."""
+    n, d, v = 300, 4097, 2000
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.empty(n, d, device=DEV).normal_(0, 1, generator=g).to(BF)
+    w = torch.empty(v, d, device=DEV).normal_(0, 0.01, generator=g).to(BF)
+    t = torch.randperm(v, device=DEV, generator=g)[:n]
+    for k in range(0, n, 2):
+        w[t[k]] = (x[k].double() * ((10 + k / 5) / x[k].double().square().sum())).to(BF)
+    z = x.double() @ w.double().t()
+    want = torch.nn.functional.cross_entropy(z, t, reduction="none")
+    loss, _, _ = sdc.sdc_cross_entropy(x, w, t)
+    assert (loss >= 0).all()
+    # each logit is off by ez, the exponentials' relative error is twice that and 2 u,
+    # 11 levels of sums (2000 words) and the logarithm near 1: 16 u
+    ez = ((d + 8) * U * (x.double().abs() @ w.double().abs().t())).amax(1)
+    assert ((loss.double() - want).abs() <= 2 * ez * (-torch.expm1(-want)).clamp(min=0) * 1.01 + 2 * ez * ez
+            + 16 * U * (1 + want)).all()
