@@ -59,6 +59,7 @@ class RecomputeAudit:
         self._recomputed_rows = self.recomputed.split(1)
         self._mismatch_at = self.mismatch.split(1)
         self.calls = [0] * n_segments
+        self._step = 0  # of begin_step: stored rows are the current step's
         self._ws = {}  # one scan workspace per stream: calls on a stream run in order
 
     def _workspace(self, t):
@@ -82,6 +83,7 @@ class RecomputeAudit:
         """Start a step: clears the counters (a fill kernel on the current stream)."""
         self.mismatch.zero_()
         self.calls = [0] * self.n
+        self._step += 1
 
     def wrap(self, fn, k):
         """fn(*args) -> a tensor, or a tuple/list of tensors (None entries are
@@ -119,14 +121,18 @@ class RecomputeAudit:
     def cross_entropy(self, k, x, w, target, reduction="mean"):
         """The loss of a linear head as segment k (see
         loss.linear_cross_entropy): the fingerprint row of its logits is stored,
-        and compared when the backward pass computes them again."""
+        and compared when the backward pass computes them again, which has to be
+        in the same step (a backward pass after the next begin_step() is refused)."""
         if not 0 <= k < self.n:
             raise IndexError(f"segment {k} out of range 0..{self.n - 1}")
         if self.calls[k]:
             raise RuntimeError(f"segment {k} ran before in this step (call begin_step())")
-        r = k * self.outputs
+        r, step = k * self.outputs, self._step
 
         def checked():
+            if self._step != step:
+                raise RuntimeError(f"segment {k}'s backward pass belongs to an earlier step, whose rows begin_step() "
+                                   "gave up")
             if self.calls[k] != 1:
                 raise RuntimeError(f"segment {k}'s backward pass ran again in one step (call begin_step())")
             self.calls[k] = 2
