@@ -71,3 +71,19 @@ def test_no_64_bit_shift_by_the_last_register(disassembly):
     bad = {k: shifts_at_the_end(v) for k, v in disassembly.items()}
     bad = {k: v for k, v in bad.items() if v}
     assert not bad, bad
+
+
+def test_m0_is_set_right_before_each_use(disassembly):
+    """Loads from memory to LDS take their address from m0, which inline assembly sets
+    and the compiler does not track: each has its own, set by the second
+    instruction before it, and nothing else reads or writes m0."""
+    loads = 0
+    for name, lines in disassembly.items():
+        code = [line.partition("//")[0].strip() for line in lines]
+        for k, line in enumerate(code):
+            if "lds" in line.split(" ")[0] and line.startswith(("global_load", "buffer_load")):
+                loads += 1
+                assert code[k - 1] == "s_nop 0" and code[k - 2].startswith("s_mov_b32 m0, s"), (name, code[k - 3:k + 1])
+            elif re.search(r"\bm0\b", line):
+                assert "global_load_lds" in code[k + 2], (name, line)
+    assert loads > 100
