@@ -423,7 +423,9 @@ int32_t sdc_confirm_verdict(const uint64_t* d_witness, const uint64_t* d_retry,
  * write the new weights' rows in the pass that computes them. */
 
 /* One tensor of the step; all pointers to device memory, contiguous, element
- * i of each belonging to element i of the others, none overlapping another.
+ * i of each belonging to element i of the others.  Nothing that a step writes
+ * may overlap another tensor of the list (what it only reads, gradients and
+ * tensors without one, may share memory).
  *   param       numel weights of param_dtype (SDC_F32, SDC_BF16 or SDC_F16).
  *   grad        gradients of grad_dtype (one of the same three, need not be
  *               param_dtype); NULL: the tensor and its states are left alone.
@@ -482,7 +484,7 @@ typedef struct {
 } sdc_adamw_info;
 
 /* Device bytes of the plan of h_tensors[0..n) with n_groups groups (1..65536).
- * Host only.  Errors as sdc_adamw_plan_build's argument checks. */
+ * Host only.  Errors as sdc_adamw_plan_build's argument checks, overlaps aside. */
 int32_t sdc_adamw_plan_bytes(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,
                              uint64_t* h_bytes);
 
@@ -490,7 +492,8 @@ int32_t sdc_adamw_plan_bytes(const sdc_adamw_tensor* h_tensors, uint64_t n, uint
  * aligned, owned by the caller).  The plan keeps the pointers and holds the
  * step's scratch: steps of one plan must not overlap in time.  SYNCHRONOUS.
  * Errors: SDC_ERR_INVALID (NULL, a group out of range, a master of an fp32
- * param, scale bytes that do not go with the state type), SDC_ERR_DTYPE,
+ * param, scale bytes that do not go with the state type, tensors that overlap),
+ * SDC_ERR_DTYPE,
  * SDC_ERR_ALIGN (a pointer not aligned to its element), SDC_ERR_RANGE (2^25
  * tensors, 2^48 elements), SDC_ERR_WORKSPACE, SDC_ERR_HIP. */
 int32_t sdc_adamw_plan_build(const sdc_adamw_tensor* h_tensors, uint64_t n, uint32_t n_groups,

@@ -763,6 +763,52 @@ def _adamw_column(table, name, tensors, numels, dtypes, dev):
     return ts, idx
 
 
+def _adamw_overlap(table):
+    """The first two entries of a filled table that overlap, of which a step
+    writes one: ((column, index), (column, index)), or None."""
+    live, n = table["grad"] != 0, table["numel"]
+    state = np.where(table["state_dtype"] == F32, n * 4, n)
+    blocks = (n + np.uint64(_STATE_BLOCK - 1)) // np.uint64(_STATE_BLOCK)
+    size = lambda code: np.where(code == F32, n * 4, n * 2)  # noqa: E731
+    columns = [("param", size(table["param_dtype"]), None), ("grad", size(table["grad_dtype"]), False),
+               ("exp_avg", state, True), ("exp_avg_sq", state, True), ("master", n * 4, True),
+               ("exp_avg_scale", blocks, True), ("exp_avg_sq_scale", blocks, True)]
+    # tensors without a gradient: their weights are read, for their rows, and nothing written
+    keep = [(table[c] != 0) & (n != 0) & (live | (c == "param")) for c, _, _ in columns]
+    index = [np.flatnonzero(k) for k in keep]
+    start = np.concatenate([table[c][k] for (c, _, _), k in zip(columns, index)])
+    end = start + np.concatenate([b[k] for (_, b, _), k in zip(columns, index)])
+    written = np.concatenate([live[k] if w is None else np.full(len(k), w) for (_, _, w), k in zip(columns, index)])
+    order = np.argsort(start, kind="stable")
+    start, end, written = start[order], end[order], written[order]
+    # each against the furthest end of those that begin before it
+    none = np.zeros(1, dtype=np.uint64)
+    reach = lambda which: np.concatenate([none, np.maximum.accumulate(np.where(which, end, 0))])[:-1]  # noqa: E731
+    to_written, to_read = reach(written), reach(~written)
+    bad = np.flatnonzero((start < to_written) | (written & (start < to_read)))
+    if not len(bad):
+        return None
+    k = bad[0]
+    before = np.flatnonzero((end[:k] > start[k]) & (written[:k] | written[k]))[-1]
+    first = np.cumsum([0] + [len(i) for i in index])
+
+    def entry(at):
+        c = int(np.searchsorted(first, at, side="right")) - 1
+        return columns[c][0], int(index[c][at - first[c]])
+    return tuple(sorted((entry(order[before]), entry(order[k])), key=lambda e: [c[0] for c in columns].index(e[0])))
+
+
+def _refuse_overlap(table):
+    """Names what the library refused for overlapping (it does not say which)."""
+    both = _adamw_overlap(table)
+    if both is None:
+        return
+    (a, i), (b, j) = both
+    if table[a][i] == table[b][j]:
+        raise ValueError(f"{a}[{i}] and {b}[{j}] are one tensor listed twice (shared weights: list them once)")
+    raise ValueError(f"{a}[{i}] and {b}[{j}] overlap, and the step writes one of them")
+
+
 def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_avg_scale=None,
                          exp_avg_sq_scale=None, group=None, n_groups=1, stream=None):
     """Plan of an AdamW step over a tensor list (synchronous; see
@@ -775,8 +821,8 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     None where the state is fp32).  master: fp32 weights behind 16-bit params
     (None: the param itself is updated).  group: parameter group of each
     tensor.  The plan keeps the tensors' addresses: gradients have to stay
-    where they are (zero them in place).  No tensor that the step writes may be
-    listed twice or overlap another."""
+    where they are (zero them in place).  Nothing that the step writes may be
+    listed twice or overlap another tensor of the list."""
     n = len(params)
     if not n:
         raise ValueError("the list is empty")
@@ -795,12 +841,6 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     blocks = [-(-m // _STATE_BLOCK) for m in numels]
     for name, scales in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
         keep += _adamw_column(table, name, scales, blocks, [{torch.uint8}] * n, dev)[0]
-    stepped = table[table["grad"] != 0]
-    written = np.concatenate([stepped[c] for c in ("param", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
-                                                   "exp_avg_sq_scale")])
-    written = np.sort(written[written != 0])
-    if (written[1:] == written[:-1]).any():
-        raise ValueError("a tensor that the step writes is listed twice (shared weights: list them once)")
     table["numel"] = numels
     table["param_dtype"] = table["grad_dtype"] = [_TORCH_DTYPE[p.dtype] for p in params]
     table["grad_dtype"][at] = [_TORCH_DTYPE[g.dtype] for g in gs]
@@ -816,8 +856,10 @@ def sdc_adamw_plan_build(params, grads, exp_avg, exp_avg_sq, master=None, exp_av
     info = _AdamwInfo()
     with _device_guard(dev):
         s = _scan_stream(stream, dev, [buf])
-        _check(_lib.sdc_adamw_plan_build(h, n, n_groups, buf.data_ptr(), buf.numel(), ctypes.byref(info), s),
-               "sdc_adamw_plan_build")
+        status = _lib.sdc_adamw_plan_build(h, n, n_groups, buf.data_ptr(), buf.numel(), ctypes.byref(info), s)
+    if status == -1:  # SDC_ERR_INVALID
+        _refuse_overlap(table)
+    _check(status, "sdc_adamw_plan_build")
     return AdamwPlan(buf, info, keep, dev)
 
 

@@ -156,6 +156,55 @@ int32_t layout_adamw(const sdc_adamw_tensor* t, uint64_t n, uint32_t n_groups, L
   return SDC_OK;
 }
 
+// Bytes of memory from start to end that a step reads or writes.
+struct MemSpan {
+  uint64_t start, end : 63, written : 1;
+  bool operator<(const MemSpan& o) const { return start < o.start; }
+};
+
+// Whether something that a step writes overlaps another tensor of the list: the
+// spans in order of their starts, against the furthest end of those before.  A
+// column of pointers is usually in order by itself, so columns are merged.
+bool overlapping(const sdc_adamw_tensor* t, uint64_t n) {
+  std::vector<MemSpan> spans;
+  const auto column = [&](auto&& place) {
+    const size_t first = spans.size();
+    for (uint64_t k = 0; k < n; ++k) {
+      const MemSpan s = place(t[k]);
+      if (t[k].numel && s.start) spans.push_back(s);
+    }
+    const auto mid = spans.begin() + (ptrdiff_t)first;
+    if (!std::is_sorted(mid, spans.end())) std::sort(mid, spans.end());
+    std::inplace_merge(spans.begin(), mid, spans.end());
+  };
+  const auto span = [](const void* p, uint64_t bytes, bool written) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(p);
+    return MemSpan{a, a + bytes, written};
+  };
+  typedef const sdc_adamw_tensor& Tensor;
+  // tensors without a gradient: their weights are read, for their rows
+  const auto state = [&](Tensor x, const void* p) {
+    return span(x.grad ? p : nullptr, x.numel * (x.state_dtype == SDC_F32 ? 4 : 1), true);
+  };
+  const auto scale = [&](Tensor x, const void* p) {
+    return span(x.grad ? p : nullptr, (x.numel + kStateBlock - 1) / kStateBlock, true);
+  };
+  column([&](Tensor x) { return span(x.param, x.numel * element_size(x.param_dtype), x.grad != nullptr); });
+  column([&](Tensor x) { return span(x.grad, x.numel * element_size(x.grad_dtype), false); });
+  column([&](Tensor x) { return state(x, x.exp_avg); });
+  column([&](Tensor x) { return state(x, x.exp_avg_sq); });
+  column([&](Tensor x) { return span(x.grad ? x.master : nullptr, x.numel * 4, true); });
+  column([&](Tensor x) { return scale(x, x.exp_avg_scale); });
+  column([&](Tensor x) { return scale(x, x.exp_avg_sq_scale); });
+  uint64_t read = 0, written = 0;  // furthest ends
+  for (const MemSpan& s : spans) {
+    if (s.start < written || (s.written && s.start < read)) return true;
+    uint64_t& end = s.written ? written : read;
+    end = std::max<uint64_t>(end, s.end);
+  }
+  return false;
+}
+
 void pack_adamw(const sdc_adamw_tensor* t, uint64_t n, const Layout& L, std::vector<unsigned char>& img) {
   img.assign(L.off.partials, 0);
   AdamwDesc* desc = reinterpret_cast<AdamwDesc*>(img.data() + L.off.desc);
@@ -234,10 +283,11 @@ extern "C" int32_t sdc_adamw_plan_build(const sdc_adamw_tensor* h_tensors, uint6
   Layout L;
   int32_t st = layout_adamw(h_tensors, n, n_groups, &L);
   if (st) return st;
-  if (plan_bytes < L.off.end) return SDC_ERR_WORKSPACE;
-  if (!aligned(d_plan, 16)) return SDC_ERR_ALIGN;
   std::vector<unsigned char> img;
   try {
+    if (overlapping(h_tensors, n)) return SDC_ERR_INVALID;
+    if (plan_bytes < L.off.end) return SDC_ERR_WORKSPACE;
+    if (!aligned(d_plan, 16)) return SDC_ERR_ALIGN;
     pack_adamw(h_tensors, n, L, img);
   } catch (...) {
     return SDC_ERR_RANGE;  // host allocation failed
