@@ -728,6 +728,7 @@ class AdamwPlan:
         # read once: every ctypes access adds to a step's host time
         self.n_tensors, self.n_groups, self.total_elems = info.n_tensors, info.n_groups, info.total_elems
         self._args = buf.data_ptr(), ctypes.byref(info)
+        self._made_on = _current_stream_handle(device)  # the stream that buf was allocated on
 
 
 def _adamw_column(table, name, tensors, numels, dtypes, dev):
@@ -895,11 +896,14 @@ def sdc_adamw_step(plan, groups, control, sq_total=None, flag=None, max_norm=0.0
     if rows is not None:
         _arg(rows, "rows", torch.int64, 4 * plan.n_tensors, dev)
     with _device_guard(dev):
+        s = _stream_handle(stream, dev)
+        if s != plan._made_on and not torch.cuda.is_current_stream_capturing():
+            # the step's scratch: a plan dropped now is freed after the step
+            plan.buf.record_stream(stream or torch.cuda.current_stream(dev))
         _check(_lib.sdc_adamw_step(
             *plan._args, groups.data_ptr(), control.data_ptr(),
             None if sq_total is None else sq_total.data_ptr(), None if flag is None else flag.data_ptr(),
-            max_norm, grad_scale, None if rows is None else rows.data_ptr(), _stream_handle(stream, dev)),
-            "sdc_adamw_step")
+            max_norm, grad_scale, None if rows is None else rows.data_ptr(), s), "sdc_adamw_step")
     return rows
 
 

@@ -1,5 +1,5 @@
-"""GPU tests of which lists an AdamW plan takes: what the step writes shares no
-memory, what it only reads may."""
+"""GPU tests of the memory of an AdamW plan: what the step writes shares none, what
+it only reads may, and the plan's own lives as long as a step that uses it."""
 import pytest
 import torch
 
@@ -55,3 +55,29 @@ def test_what_is_only_read_may_be_shared():
     # weights that a step writes are not those of a tensor without a gradient
     with pytest.raises(ValueError, match=r"param\[0\] and param\[1\]"):
         sdc.sdc_adamw_plan_build([p[0], p[0]], [grad, None], [m[0], m[1]], [v[0], v[1]])
+
+
+@pytest.mark.parametrize("current", [False, True])
+def test_a_plan_dropped_behind_a_step_on_another_stream(current):
+    """The plan holds the step's scratch, so its memory is not handed out before the
+    step has run, also where that is on another stream than the plan was made on."""
+    p, g, m, v = (torch.zeros(5_000_000, device=DEV) for _ in range(4))
+    plan = sdc.sdc_adamw_plan_build([p], [g], [m], [v])
+    groups = torch.tensor([[1e-2, 0.9, 0.99, 1e-8, 0.0]], dtype=torch.float64, device=DEV)
+    control = sdc.sdc_adamw_control(DEV)
+    at, size = plan.buf.data_ptr(), plan.buf.numel()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    if current:
+        with torch.cuda.stream(s):
+            sdc.sdc_adamw_step(plan, groups, control)
+    else:
+        sdc.sdc_adamw_step(plan, groups, control, stream=s)
+    del plan
+    again = torch.empty(size, dtype=torch.uint8, device=DEV)
+    running = not s.query()
+    torch.cuda.synchronize()
+    assert running and again.data_ptr() != at
+    assert control.tolist()[0] == 1
