@@ -334,7 +334,8 @@ uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
 constexpr uint32_t kLaunchTiles = 1u << 22;
 
 // grad: the sizes of the gradient's pieces; else those of the forward pass,
-// which needs pieces only for a copy of w or for more than kLaunchTiles tiles.
+// which needs pieces only for more than kLaunchTiles tiles (a copy of w, 16
+// bytes for each of less than 2^24 rows, is below kPieceBytes).
 Head plan_head(const sdc_head* h, bool grad) {
   Head p;
   p.N = (uint32_t)h->n;
@@ -354,9 +355,9 @@ Head plan_head(const sdc_head* h, bool grad) {
   // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
   // of that on, the one that needs the fewest rounds of 256 tiles.
   const uint32_t nt = p.nt, vt = p.vt;
-  const uint64_t col = (p.copy_w ? 2ull * p.d_pad : 0) + (grad ? 2ull * p.N : 0);
+  const uint64_t col = (p.copy_w ? 2ull * p.d_pad : 0) + 2ull * p.N;
   uint32_t most = vt;
-  if (col && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.vtile, 1);
+  if (grad && col * p.V > kPieceBytes) most = (uint32_t)std::max<uint64_t>(kPieceBytes / col / p.vtile, 1);
   most = std::min(most, std::max(kLaunchTiles / std::max(nt, 1u), 1u));
   uint32_t best = most;
   if (most < vt) {
