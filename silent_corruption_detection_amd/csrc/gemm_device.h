@@ -60,7 +60,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
   typedef bf16x8 frag;
-  static constexpr uint32_t kDtype = SDC_BF16;
   // dz is at most 1 in magnitude and bf16 has fp32's exponents
   static constexpr float kDzScale = 1.0f;
   static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {
@@ -73,7 +72,6 @@ struct Bf16 {
 
 struct Fp16 {
   typedef f16x8 frag;
-  static constexpr uint32_t kDtype = SDC_F16;
   // probabilities of 1e-5 would be subnormal in fp16: dz is held 2^15 times as large
   static constexpr float kDzScale = 32768.0f;
   static __device__ __forceinline__ f32x4 mfma(frag a, frag b, f32x4 c) {

@@ -26,7 +26,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         count = torch.empty(1, dtype=torch.int64, device=x.device)
         _, lse, total = sdc_cross_entropy(x, w, target, count=count, row=row)
         ctx.save_for_backward(x, w, target, lse, count)
-        ctx.mean, ctx.row, ctx.checked = mean, row, checked
+        ctx.mean, ctx.checked = mean, checked
         total = total[0]
         return total / count[0] if mean else total
 
