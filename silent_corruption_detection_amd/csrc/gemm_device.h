@@ -39,16 +39,17 @@ namespace {
 
 constexpr uint32_t kTileK = 64;  // k per LDS buffer
 
-template <uint32_t M_, uint32_t N_, uint32_t WM_, uint32_t WN_, uint32_t DEEP = 0>
+template <uint32_t M_, uint32_t N_, uint32_t WM_, uint32_t WN_, uint32_t DEEP = 0, bool LATE = false>
 struct Shape {
   static constexpr uint32_t M = M_, N = N_, WM = WM_, WN = WN_;
   static constexpr uint32_t kDeep = DEEP;  // steps in flight of gemm_tile_deep
+  static constexpr bool kLate = LATE;      // the next step's loads stand behind LDS reads (see gemm_step)
   static constexpr uint32_t kThreads = 64 * WM * WN;
   static constexpr int I = M / WM / 16, J = N / WN / 16;
   static constexpr uint32_t kA = M * kTileK * 2, kBuf = (M + N) * kTileK * 2;  // bytes of A, of both, of one k step
   static constexpr uint32_t kLds = 2 * kBuf;
 };
-typedef Shape<256, 256, 2, 4> BigTile;
+typedef Shape<256, 256, 2, 4, 0, true> BigTile;
 typedef Shape<128, 128, 2, 2> SmallTile;
 typedef Shape<64, 64, 2, 2> TinyTile;
 typedef Shape<128, 32, 4, 1, 3> FewTile;
@@ -269,12 +270,16 @@ struct Side {
 };
 
 // The products of a step from LDS at la and lb; during(s) is called between the
-// reads of half s of the step and their products: the next step's loads are
-// issued there, so that the LDS reads start right behind the barrier (2048 x 8192
-// x 128256: 3330 us; with the loads first 3760; with both halves read first 3450).
-// PRIO: the products go before other waves' work, which pays for k-major
-// operands only (with / without: the gradient of that size 10.9 ms / 11.2, its
-// loss, rows along k, 3390 us / 3330).
+// reads of half s of the step and their products.  Where one workgroup fills a CU
+// (kLate, 256 x 256) the next step's loads are issued there, so that the LDS reads
+// start right behind the barrier (2048 x 8192 x 128256: 3330 us; with the loads
+// first 3760; with both halves read first 3450), and the products of k-major
+// operands go before other waves' work (PRIO; with / without: the gradient of that
+// size 10.9 ms / 11.2; rows along k, the loss, 3390 us / 3330).  In the smaller
+// tiles another workgroup covers the reads, and both cost (loss, loads first / late:
+// 755 x 5296 x 688 49 us / 55, with the row 100 x 2048 x 50304 45 / 49 and 800 x
+// 2048 x 50304 199 / 226; gradient 4096 x 256 x 12800 128 / 142, 600 x 1024 x 20000
+// 102 / 113; 64 x 2048 x 50304 alone 41.6 / 40.7).
 template <class T, class S, bool PRIO, class SA, class SB, class F>
 __device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsigned char* la,
                                           const unsigned char* lb, f32x4 (&acc)[S::I][S::J], F&& during) {
@@ -379,8 +384,9 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
       __builtin_amdgcn_s_barrier();  // this buffer is whole, and everyone has left the other
       asm volatile("" ::: "memory");
       const unsigned char* la = lds + buf * S::kBuf;
-      gemm_step<T, S, AK>(sa, sb, la, la + S::kA, acc, [&](uint32_t s) {
-        if (k + kTileK >= k1) return;
+      if (!S::kLate && k + kTileK < k1) fill(k + kTileK, buf ^ 1u);
+      gemm_step<T, S, S::kLate && AK>(sa, sb, la, la + S::kA, acc, [&](uint32_t s) {
+        if (!S::kLate || k + kTileK >= k1) return;
         if (s == 0) sa.fill(k + kTileK, lds0 + (buf ^ 1u) * S::kBuf, ha);
         else sb.fill(k + kTileK, lds0 + (buf ^ 1u) * S::kBuf + S::kA, hb);
       });
