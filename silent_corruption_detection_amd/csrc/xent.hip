@@ -243,6 +243,11 @@ __global__ void __launch_bounds__(256) zero16_kernel(uint16_t* p, uint64_t n) {
 // ---- host ----------------------------------------------------------------------------
 constexpr uint64_t kPieceBytes = 256ull << 20;  // of the gradient's workspace that grows with the piece
 
+// CUs that the rules below fill.  The MI355X' number, not the current device's: tiles,
+// pieces and splits follow from the sizes alone, so the results' bits and the
+// workspace (asked for without a device) are the same on a part of the chip.
+constexpr uint32_t kCus = 256;
+
 constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
 
 struct Head {
@@ -278,7 +283,7 @@ int32_t check_head(const sdc_head* h) {
   return SDC_OK;
 }
 
-// The tile of the logits' product, from the rounds that 256 CUs take: a tile has
+// The tile of the logits' product, from the rounds that the CUs take: a tile has
 // the work of its share of a 256 x 256 one at 1.15 times the cost for 128 x 128
 // (twice the operand bytes per operation) and 2 for 64 x 64.  Larger tiles win
 // where they fill whole rounds, smaller ones where they would leave CUs idle (a
@@ -294,7 +299,7 @@ int32_t check_head(const sdc_head* h) {
 uint32_t logit_tile(uint64_t n, uint64_t vocab) {
   if (n <= kFew) return kFew;
   const auto cost = [&](uint32_t t, double each) {
-    return (double)(((uint64_t)tiles(n, t) * tiles(vocab, t) + 255) / 256) * each;
+    return (double)(((uint64_t)tiles(n, t) * tiles(vocab, t) + kCus - 1) / kCus) * each;
   };
   const double c256 = cost(256, 1.0), c128 = cost(128, 1.15 / 4), c64 = cost(64, 2.0 / 16);
   if (c64 < c128 && c64 < c256) return 64;
@@ -304,12 +309,12 @@ uint32_t logit_tile(uint64_t n, uint64_t vocab) {
 // Vocabulary rows of a tile of 32 tokens: 128, or 64 where those would leave CUs
 // idle.  Measured (loss, us, 64 / 128): 4 x 3312 x 8340 30 / 39, 10 x 4096 x
 // 24000 42 / 48, 10 x 4096 x 32768 53 / 51, 19 x 836 x 49450 37 / 32.
-uint32_t few_rows(uint64_t vocab) { return tiles(vocab, FewTile::M) < 256 ? FewTinyTile::M : FewTile::M; }
+uint32_t few_rows(uint64_t vocab) { return tiles(vocab, FewTile::M) < kCus ? FewTinyTile::M : FewTile::M; }
 
-// Parts that dx's sum over `rows` vocabulary rows is split into: 256 tiles.
+// Parts that dx's sum over `rows` vocabulary rows is split into: a tile for each CU.
 uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
   const uint32_t per = tiles(n, tile) * tiles(d, tile);
-  return std::max(1u, std::min(256u / std::max(per, 1u), tiles(rows, 256)));
+  return std::max(1u, std::min(kCus / std::max(per, 1u), tiles(rows, 256)));
 }
 
 // The tile of the gradient's two products over `rows` vocabulary rows: the
@@ -325,7 +330,7 @@ uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
     const double n_dw = (double)tiles(d, t) * tiles(rows, t), n_dx = (double)tiles(n, t) * tiles(d, t);
     const uint32_t splits = dx_splits(n, d, rows, t);
     const double all = n_dw * k_dw + n_dx * k_dx + (n_dw + n_dx * splits) * (t == 256 ? 6 : 3);
-    return std::max(all / (t == 256 ? 256 : 512), std::max(k_dw, k_dx / splits));
+    return std::max(all / (t == 256 ? kCus : 2 * kCus), std::max(k_dw, k_dx / splits));
   };
   return 0.575 * steps(128) < steps(256) ? 128u : 256u;
 }
@@ -353,7 +358,7 @@ Head plan_head(const sdc_head* h, bool grad) {
   p.nt = tiles(p.N, p.tile);
   p.vt = tiles(p.V, p.vtile);
   // The most rows whose dz (and copy) take kPieceBytes; of the sizes from half
-  // of that on, the one that needs the fewest rounds of 256 tiles.
+  // of that on, the one that needs the fewest rounds of a tile for each CU.
   const uint32_t nt = p.nt, vt = p.vt;
   const uint64_t col = (p.copy_w ? 2ull * p.d_pad : 0) + 2ull * p.N;
   uint32_t most = vt;
@@ -363,7 +368,7 @@ Head plan_head(const sdc_head* h, bool grad) {
   if (most < vt) {
     uint64_t least = ~0ull;
     for (uint32_t k = most; k >= (most + 1) / 2; --k) {
-      const auto rounds_of = [&](uint64_t rows) { return (rows * nt + 255) / 256; };
+      const auto rounds_of = [&](uint64_t rows) { return (rows * nt + kCus - 1) / kCus; };
       const uint64_t rounds = (vt / k) * rounds_of(k) + rounds_of(vt % k);
       if (rounds < least) {
         least = rounds;
