@@ -458,7 +458,7 @@ typedef struct {
 
 /* Hyperparameters of a parameter group, in device memory: the caller may
  * change them between steps (a learning-rate schedule), also between replays
- * of a captured step.  0 <= beta < 1, eps > 0. */
+ * of a captured step.  0 <= beta < 1, eps > 0 (below 2^-126 it counts as that). */
 typedef struct {
   double lr, beta1, beta2, eps, weight_decay;
 } sdc_adamw_group;

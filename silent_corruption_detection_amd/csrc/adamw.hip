@@ -60,8 +60,10 @@ __global__ void __launch_bounds__(64) adamw_gate_kernel(sdc_adamw_control* contr
   for (uint32_t k = threadIdx.x; k < n_groups; k += 64) {
     if (k >= 64) g = groups[k];
     const double2 p = powers(g.beta1, g.beta2, t);
+    // an eps below fp32's normal numbers has no fp32 reciprocal: m = v = 0 would give 0 Inf
+    const float eps = (float)g.eps < 0x1p-126f ? 0x1p-126f : (float)g.eps;
     coef[k] = AdamwCoef{(float)g.beta1, (float)(1.0 - g.beta1), (float)g.beta2, (float)(1.0 - g.beta2),
-                        (float)(g.lr / (1.0 - p.x)), (float)(1.0 / sqrt(1.0 - p.y)), (float)g.eps,
+                        (float)(g.lr / (1.0 - p.x)), (float)(1.0 / sqrt(1.0 - p.y)), eps,
                         (float)(1.0 - g.lr * g.weight_decay)};
   }
 }

@@ -81,3 +81,29 @@ def test_a_plan_dropped_behind_a_step_on_another_stream(current):
     torch.cuda.synchronize()
     assert running and again.data_ptr() != at
     assert control.tolist()[0] == 1
+
+
+@pytest.mark.parametrize("eps", [1e-46, 1e-40, 2.0 ** -127, 1e-30, 1e-8])
+@pytest.mark.parametrize("state", [32, 8])
+def test_elements_that_never_had_a_gradient_stay(state, eps):
+    """m = v = 0 moves nothing, however small eps is: eps above 0 but below fp32's normal
+    numbers has no reciprocal in fp32.  Elements with a gradient move by lr."""
+    n = 1000
+    g = torch.Generator(device=DEV).manual_seed(2)
+    p = torch.empty(n, device=DEV).normal_(generator=g)
+    grad = torch.empty(n, device=DEV).normal_(generator=g).sign()
+    grad[100:400] = 0
+    start = p.clone()
+    z = lambda k, t: torch.zeros(k, dtype=t, device=DEV)  # noqa: E731
+    if state == 32:
+        m, v, kw = z(n, torch.float32), z(n, torch.float32), {}
+    else:
+        m, v = (z(n, torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+        kw = dict(exp_avg_scale=[z(8, torch.uint8)], exp_avg_sq_scale=[z(8, torch.uint8)])
+    plan = sdc.sdc_adamw_plan_build([p], [grad], [m], [v], **kw)
+    groups = torch.tensor([[1e-2, 0.9, 0.99, eps, 0.0]], dtype=torch.float64, device=DEV)
+    sdc.sdc_adamw_step(plan, groups, sdc.sdc_adamw_control(DEV))
+    assert torch.equal(p[100:400], start[100:400])
+    # the update is lr, up to 20 roundings and eps
+    want = start.double() - 1e-2 * grad.double()
+    assert ((p.double() - want).abs() <= 20 * 2.0 ** -24 * (start.double().abs() + 1e-2) + 1e-2 * eps).all()
