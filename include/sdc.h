@@ -555,7 +555,10 @@ typedef struct {
  * sdc_cross_entropy_grad (h_grad_bytes); either may be NULL.  The gradient's
  * holds dz of one piece of the vocabulary (up to 256 MiB, or 256 rows' worth
  * where that is more), a copy of x and fp32 sums of dx; the loss' 8 bytes for
- * each row of x and 128 or 256 rows of w.  Host only.  Errors: SDC_ERR_INVALID
+ * each row of x and tile of 64 to 256 rows of w, and 4 for each row of x.  Both
+ * hold 32 bytes for each tile of logits, and copies of x (rows off 16-byte
+ * boundaries) and of w (rows of less than 8 elements) where those are needed.
+ * Host only.  Errors: SDC_ERR_INVALID
  * (NULL x, w or target, d or vocab 0, a stride below d, flags), SDC_ERR_DTYPE,
  * SDC_ERR_ALIGN (an element, or target, not aligned), SDC_ERR_RANGE (2^24
  * rows of x or w, about 2^47 logits, d 2^20, a stride of 2^40). */

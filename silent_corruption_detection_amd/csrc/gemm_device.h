@@ -23,10 +23,10 @@
 //     over the 16 rows that one transposing read takes.  A group is two
 //     transposing 8-byte reads (each gives a lane four k of its column), which
 //     is what spares transposed copies of the weights, the inputs and dz.
-// Measured, 256 x 256: 2048 x 128256 x 8192 (rows along k, with the softmax'
-// statistics) 3290 us (1310 TFLOP/s), the whole gradient of that size, two thirds
-// of it k-major products, 10.9 ms (1190 TFLOP/s); MFMA units 62 % busy at 4096 x
-// 50304 x 2048.  Bound by LDS reads beside the products: a step of 256 x 256 x 64
+// Measured, 256 x 256, back to back: 2048 x 128256 x 8192 (rows along k, with the
+// softmax' statistics) 3.3 to 3.4 ms (1.26 to 1.31 PFLOP/s), the whole gradient of
+// that size, two thirds of it k-major products, 10.9 to 11.1 ms (1.17 to 1.19); MFMA
+// units 60 % busy at 4096 x 50304 x 2048.  Bound by LDS reads beside the products: a step of 256 x 256 x 64
 // reads 192 KiB and multiplies for 2048 cycles.  Four waves of 128 x 128 instead,
 // which read a third less, measured 10 to 14 % slower: with one wave a SIMD nothing
 // covers its waits.
@@ -301,8 +301,8 @@ __device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsi
 }
 
 // gemm_tile for few rows of B, where a step lasts as long as the loads it waits
-// for: three steps of both operands are in flight, in registers, of which there
-// are plenty.  Same operations in the same order, so the same bits.  k1 is where
+// for: three steps (four in the 64-row tile) of both operands are in flight, in
+// registers, of which there are plenty.  Same operations in the same order, so the same bits.  k1 is where
 // the operands end.
 template <class T, class S>
 __device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,

@@ -162,7 +162,7 @@ __device__ __forceinline__ float token_loss(const RowArgs& a, uint32_t n) {
   return loss;
 }
 
-// One wave a token: bound by latency (4096 tokens with 197 tiles: 5.3 us).
+// One wave a token: bound by latency (4096 tokens with 197 tiles: 5.4 us).
 __global__ void __launch_bounds__(kBlock) lse_kernel(const RowArgs a) {
   const uint32_t n = wave_item_index();
   if (n < a.N) token_loss(a, n);
@@ -202,7 +202,7 @@ __device__ __forceinline__ void store_total(const RowArgs& a, const float* loss)
 __global__ void __launch_bounds__(1024) loss_total_kernel(const RowArgs a) { store_total(a, a.loss); }
 
 // Few tokens: their losses and the total in one launch of one workgroup (one
-// token with 1002 tiles: 5.7 us; 19 with 387: 4.8).
+// token with 1002 tiles: 6.0 us; 19 with 387: 4.8).
 constexpr uint32_t kFewTokens = 32;
 
 __global__ void __launch_bounds__(1024) few_tokens_kernel(const RowArgs a) {
@@ -288,14 +288,15 @@ int32_t check_head(const sdc_head* h) {
 // (twice the operand bytes per operation) and 2 for 64 x 64.  Larger tiles win
 // where they fill whole rounds, smaller ones where they would leave CUs idle (a
 // CU takes about 27 GB/s from beyond its L2 whatever is in flight) or tiles half
-// empty.  Measured (loss, us, 64 / 128 / 256): 755 x 5296 x 688 60 / 83 / 133, 100 x
-// 2048 x 8000 29 / 35 / 55, 500 x 2048 x 10000 50 / 39 / 56, 100 x 2048 x 50304 58 /
-// 46 / 64, 300 x 1000 x 16000 39 / 30 / 38, 800 x 2048 x 50304 278 / 211 / 219, 2000 x
-// 512 x 8000 39 / 32 / 29, 1500 x 4096 x 30000 604 / 371 / 307.
+// empty.  Measured (loss, us, 64 / 128 / 256): 755 x 5296 x 688 49 / 76 / 132, 100 x
+// 2048 x 8000 25 / 31 / 54, 500 x 2048 x 10000 46 / 38 / 56, 100 x 2048 x 50304 50 /
+// 40 / 60, 300 x 1000 x 16000 32 / 27 / 35, 800 x 2048 x 50304 248 / 183 / 211, 2000 x
+// 512 x 8000 37 / 30 / 26, 1500 x 4096 x 30000 646 / 352 / 303, 1000 x 1024 x 12000
+// 45 / 38 / 37 (takes 128), 64 x 2048 x 50304 42 / 40 / 59 (takes 64).
 // Up to 32 tokens fit a tile of 32, whose few accumulators leave the registers
 // to keep several steps of loads in flight.  Measured against 64 x 64 and 128 x
-// 128 (us): 5 x 8190 x 128255 391 / 434 / 567, 32 x 1001 x 20001 25 / 33 / 36, 32 x
-// 2048 x 50304 47 / 46 / 48.
+// 128 (us): 5 x 8190 x 128255 379 / 417 / 450, 32 x 1001 x 20001 21 / 25 / 33, 32 x
+// 2048 x 50304 42 / 42 / 41.
 uint32_t logit_tile(uint64_t n, uint64_t vocab) {
   if (n <= kFew) return kFew;
   const auto cost = [&](uint32_t t, double each) {
@@ -307,8 +308,8 @@ uint32_t logit_tile(uint64_t n, uint64_t vocab) {
 }
 
 // Vocabulary rows of a tile of 32 tokens: 128, or 64 where those would leave CUs
-// idle.  Measured (loss, us, 64 / 128): 4 x 3312 x 8340 30 / 39, 10 x 4096 x
-// 24000 42 / 48, 10 x 4096 x 32768 53 / 51, 19 x 836 x 49450 37 / 32.
+// idle.  Measured (loss, us, 64 / 128): 4 x 3312 x 8340 29 / 38, 10 x 4096 x
+// 24000 40 / 47, 10 x 4096 x 32768 48 / 46, 19 x 836 x 49450 28 / 26.
 uint32_t few_rows(uint64_t vocab) { return tiles(vocab, FewTile::M) < kCus ? FewTinyTile::M : FewTile::M; }
 
 // Parts that dx's sum over `rows` vocabulary rows is split into: a tile for each CU.
@@ -322,8 +323,9 @@ uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
 // 256 x 256 tile, 3 of the smaller), over the workgroups that run at a time (one of
 // 256, or two of 128 a CU, whose steps take 0.575 of the time), or that of the
 // longest tile.  Measured (the whole gradient in us, 128 / 256): 4096 x 256 x
-// 12800 158 / 206, 600 x 1024 x 20000 122 / 123, 800 x 2048 x 50304 702 / 631,
-// 1500 x 4096 x 30000 1306 / 1055.
+// 12800 145 / 193, 600 x 1024 x 20000 106 / 119, 256 x 4096 x 32000 312 / 317, 800 x
+// 2048 x 50304 611 / 611, 2048 x 1024 x 16000 211 / 206, 1037 x 1000 x 32003 268 /
+// 252, 1500 x 4096 x 30000 1185 / 1035.
 uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
   const auto steps = [&](uint32_t t) {
     const double k_dw = (double)tiles(n, kTileK), k_dx = (double)tiles(rows, kTileK);

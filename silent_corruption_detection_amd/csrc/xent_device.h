@@ -154,7 +154,7 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[S::I][S::J], const L
 // stores it, so that the loss is made of the logits whose sum (and fingerprint)
 // was taken: a product of its own, summed in another order, would differ in the
 // last bits, and could exceed the largest logit.  Bound by the matrix cores; 4096 x
-// 50304 x 2048 takes 743 us (1135 TFLOP/s).
+// 50304 x 2048 takes 828 us of a trace on average (1020 TFLOP/s; 876 with the row).
 template <class T, class S, RowsAt AT, bool ROW>
 __global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(S::kThreads) logit_lse_kernel(const LogitArgs 
 // own size, which the products average out), 0 for rows without a target and
 // in the padding.  It passes through LDS, so that it is stored in whole rows of
 // the tile.  Bound by the matrix cores: the two pieces of 4096 x 50304 x 2048 take
-// 854 us (990 TFLOP/s), a tenth of it the exponentials and the store.
+// 865 us of a trace on average (976 TFLOP/s; 943 us with the row), a tenth of it the
+// exponentials and the store.
 template <class T, class S, RowsAt AT, bool ROW>
 __global__ void __launch_bounds__(S::kThreads) logit_dz_kernel(const LogitArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
@@ -339,8 +340,8 @@ __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsig
 // Both products of dz (see ProductArgs).  dx's tile is dx^T (d down, tokens
 // across) over a split of the piece, so a lane stores four fp32 of one token; dW's
 // is dW^T over all tokens, stored through LDS in whole rows.  Bound by the matrix
-// cores: 4096 x 50304 x 2048 takes 1540 us (1100 TFLOP/s); 16 tokens x 128256 x
-// 8192 910 us (4.6 TB/s: W read and dW written once).
+// cores: 4096 x 50304 x 2048 takes 1537 us of a trace on average (1098 TFLOP/s); 16
+// tokens x 128256 x 8192 963 us (4.4 TB/s: W read and dW written once).
 template <class T, class S, RowsAt AT>
 __global__ void __launch_bounds__(S::kThreads) products_kernel(const ProductArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
