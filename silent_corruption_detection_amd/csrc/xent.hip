@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const float* __restrict_
 }
 
 // ---- row results -------------------------------------------------------------------
+// What the row kernels need of the logit tiles and of a head.
 struct RowArgs {
   const float2* part;  // [N][n_vt]
   const float* hit;    // the target's logit (rows with a target)
