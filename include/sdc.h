@@ -595,6 +595,145 @@ int32_t sdc_cross_entropy_grad(const sdc_head* h_head, const float* d_lse, const
                                const sdc_row* d_ref, uint32_t col_mask, sdc_row* d_row,
                                uint32_t* d_mismatch, sdc_stream_t stream);
 
+/* ---- softmax attention --------------------------------------------------------
+ * The other recomputed half of a transformer block.  Its gradient computes the
+ * scores again, which are never kept, and both passes can take their fingerprint
+ * where they are computed ([AEGIS] item 4).  No sum is made by atomics: results are
+ * bit-reproducible on one kind of device, as [BLOG] "Check 2" needs of a replay. */
+
+/* Queries, keys and values, and which keys a query attends.
+ *   q, k, v   elements of dtype (SDC_BF16 or SDC_F16): rows of `heads` heads of d
+ *             elements (contiguous; d a multiple of 8, at most 128).  The strides are
+ *             in elements: from one entry of the batch to the next, row to row, head to
+ *             head; each a multiple of 8 (where there is more than one), and the pointers
+ *             16-byte aligned.  heads_q is a multiple of heads_k: query head h has the keys
+ *             and values of head h / (heads_q / heads_k).
+ *   seq_q, seq_k
+ *             NULL: `batch` entries of len_q rows of q and len_k of k and v.  Else device
+ *             arrays of batch + 1 ascending offsets: sequence b has the rows seq[b] .. seq[b+1]
+ *             of the len_q (len_k) rows there are (offsets outside those count as the
+ *             nearest inside); rows of no sequence are not read and not written, and strides[0]
+ *             is not used.
+ *   scale     of the scores, finite and above 0.
+ *   causal    1: query i of a sequence with lq queries and lk keys attends keys up to
+ *             i + lk - lq (the last query attends all).
+ *   window    with causal: only the last `window` of those.  0: all.
+ *   flags     0.
+ * A query that attends no key has out 0, lse -inf and gives no gradient.  What keys and
+ * values hold where no query attends them has no effect, nor has what a query that does
+ * not attend a key holds on that key's gradient. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* seq_q;
+  const int32_t* seq_k;
+  uint64_t batch, len_q, len_k;
+  uint64_t heads_q, heads_k, d;
+  uint64_t q_stride[3], k_stride[3], v_stride[3];
+  uint64_t window;
+  float scale;
+  uint32_t causal;
+  uint32_t dtype;
+  uint32_t flags;
+} sdc_attn;
+
+/* Device workspace bytes of sdc_attention (h_bytes) and sdc_attention_grad
+ * (h_grad_bytes); either may be NULL.  They hold 32 bytes for each tile and split, the
+ * fp32 sums of splits (few queries with many keys; the gradient of few keys, at most
+ * 1024 workgroups' worth), and the gradient's 8 bytes for each query and head.  Host only.
+ * Errors: SDC_ERR_INVALID (NULL, no heads, heads_q no multiple of heads_k, scale, a window
+ * without causal, one seq without the other, flags), SDC_ERR_DTYPE, SDC_ERR_ALIGN,
+ * SDC_ERR_RANGE (d, 2^31 rows times heads, batch 2^24, a row stride of 2^23, another of
+ * 2^40, 2^19 tiles of 32 queries or 128 keys). */
+int32_t sdc_attention_ws_bytes(const sdc_attn* h_attn, uint64_t* h_bytes, uint64_t* h_grad_bytes);
+
+/* d_out = softmax(scale q k^T) v, [rows of q][heads_q][d], contiguous, of the dtype;
+ * d_lse [rows of q][heads_q] = log sum exp of the scaled scores.  Sums and softmax in fp32,
+ * probabilities rounded to the dtype's precision for the product with v.
+ *   d_row      NULL, or (16-byte aligned) the fingerprint row of the fp32 scores q k^T
+ *              (unscaled) [rows of q][heads_q][len_k], key j of its sequence in column j,
+ *              zero where not attended, as a scan of them in memory would give it.
+ * d_out, d_ws: 16-byte aligned; d_ws not reused before the call's work has completed.
+ * ASYNCHRONOUS on stream.  Errors as sdc_attention_ws_bytes, and SDC_ERR_WORKSPACE,
+ * SDC_ERR_HIP. */
+int32_t sdc_attention(const sdc_attn* h_attn, void* d_ws, uint64_t ws_bytes, void* d_out, float* d_lse,
+                      sdc_row* d_row, sdc_stream_t stream);
+
+/* Gradient for d_dout, the gradient of d_out (contiguous, as d_out), from the forward
+ * pass' d_out and d_lse.  With p = exp(scale q k^T - lse), delta = sum dout out:
+ *   d_dv = p^T dout   dz = p (dout v^T - delta)   d_dq = scale dz k   d_dk = scale dz^T q
+ * contiguous [rows][heads][d], of the dtype, summed in fp32 from p and dz rounded to its
+ * precision; the gradients of a head of keys are its query heads' sums.  d_dq, or d_dk and
+ * d_dv, may be NULL and are then not computed.  d_row: as there, of the recomputed scores;
+ * with d_ref (the forward pass' row) a difference under col_mask adds 1 to *d_mismatch
+ * (required then; the caller clears it), for each of the two launches that compute
+ * them.  Outputs and workspace must not overlap the inputs.  All pointers but d_lse and
+ * d_mismatch 16-byte aligned.
+ * ASYNCHRONOUS on stream.  Errors as sdc_attention. */
+int32_t sdc_attention_grad(const sdc_attn* h_attn, const void* d_out, const float* d_lse, const void* d_dout,
+                           void* d_ws, uint64_t ws_bytes, void* d_dq, void* d_dk, void* d_dv, const sdc_row* d_ref,
+                           uint32_t col_mask, sdc_row* d_row, uint32_t* d_mismatch, sdc_stream_t stream);
+
+/* ---- the gated feed-forward block ---------------------------------------------
+ * [AEGIS] item 4 compares a recomputed result with the original's fingerprint.
+ * The wide half of a transformer block is where activation checkpointing
+ * recomputes most: its gradient computes both projections again, which are never
+ * kept in memory, so their fingerprint is taken where they are computed.  Results
+ * are bit-reproducible on one kind of device. */
+
+enum { SDC_ACT_SILU = 0, SDC_ACT_GELU_TANH = 1 };
+
+/* Both projections of a gated feed-forward block and the rows they are applied to.
+ *   x       n rows of d elements of dtype (SDC_BF16 or SDC_F16), x_stride elements
+ *           apart.      w_gate, w_up   f rows likewise.
+ *   act     SDC_ACT_SILU: g / (1 + exp(-g)); SDC_ACT_GELU_TANH:
+ *           0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+typedef struct {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  uint64_t n, d, f;
+  uint64_t x_stride, w_gate_stride, w_up_stride;
+  uint32_t dtype;
+  uint32_t act;
+} sdc_ffn;
+
+/* Device workspace bytes of sdc_gated_ffn (h_bytes) and sdc_gated_ffn_grad
+ * (h_grad_bytes); either may be NULL.  Both hold 32 bytes for each tile of the
+ * projections, and copies of x (rows off 16-byte boundaries) and of the weights (rows
+ * of less than 8 elements) where those are needed; the gradient's also the two
+ * projections' gradients (4 n f bytes) and, where dx's sum is split, its parts in
+ * fp32.  Host only.  Errors: SDC_ERR_INVALID (NULL x or weights, d or f 0, a stride below
+ * d, act), SDC_ERR_DTYPE, SDC_ERR_ALIGN (an element not aligned), SDC_ERR_RANGE (2^24
+ * rows of x, f 2^23, d 2^20, a stride of 2^40, 2^22 tiles of 128 x 128 in n x 2 f or
+ * half of that in n x d or 2 f x d). */
+int32_t sdc_gated_ffn_ws_bytes(const sdc_ffn* h_ffn, uint64_t* h_bytes, uint64_t* h_grad_bytes);
+
+/* d_h = act(x w_gate^T) * (x w_up^T), n x f, contiguous, of the block's dtype;
+ * sums and activation in fp32, rounded once.
+ *   d_row      NULL, or (16-byte aligned) the fingerprint row of the fp32 projections
+ *              [n][2][f] (gate, up), as a scan of them in memory would give it.
+ * d_ws: 16-byte aligned, not reused before the call's work has completed.
+ * ASYNCHRONOUS on stream.  Errors as sdc_gated_ffn_ws_bytes, and SDC_ERR_WORKSPACE,
+ * SDC_ERR_HIP. */
+int32_t sdc_gated_ffn(const sdc_ffn* h_ffn, void* d_ws, uint64_t ws_bytes, void* d_h, sdc_row* d_row,
+                      sdc_stream_t stream);
+
+/* Gradient for d_dh, the gradient of d_h (n rows of f elements of the block's dtype,
+ * dh_stride elements apart), with g and u the projections:
+ *   dg = dh u act'(g), du = dh act(g)
+ *   d_dx = dg w_gate + du w_up (n x d)   d_dw_gate = dg^T x, d_dw_up = du^T x (f x d)
+ * contiguous, of the block's dtype, summed in fp32 from dg and du rounded to that type.
+ * d_dx, or both weights' gradients, may be NULL and are then not computed.  d_row: as
+ * there, of the recomputed projections; with d_ref (the forward pass' row) a difference
+ * under col_mask adds 1 to *d_mismatch (required then; the caller clears it).  Outputs
+ * and workspace must not overlap the inputs.
+ * ASYNCHRONOUS on stream.  Errors as sdc_gated_ffn. */
+int32_t sdc_gated_ffn_grad(const sdc_ffn* h_ffn, const void* d_dh, uint64_t dh_stride, void* d_ws, uint64_t ws_bytes,
+                           void* d_dx, void* d_dw_gate, void* d_dw_up, const sdc_row* d_ref, uint32_t col_mask,
+                           sdc_row* d_row, uint32_t* d_mismatch, sdc_stream_t stream);
+
 /* ---- measurement ----------------------------------------------------------- */
 
 /* Streaming-read reference (no passage of the pages defines it: it measures

@@ -29,6 +29,8 @@ __all__ = [
     "sdc_read_sum_ws_bytes", "sdc_read_sum",
     "AdamwPlan", "sdc_adamw_plan_build", "sdc_adamw_control", "sdc_adamw_step",
     "sdc_cross_entropy_ws_bytes", "sdc_cross_entropy", "sdc_cross_entropy_grad",
+    "sdc_attention_ws_bytes", "sdc_attention", "sdc_attention_grad",
+    "sdc_gated_ffn_ws_bytes", "sdc_gated_ffn", "sdc_gated_ffn_grad",
 ]
 
 # The in-tree build; SDC_LIB_PATH may name another build of the same sources
@@ -107,6 +109,12 @@ def _load():
         "sdc_cross_entropy_ws_bytes": [P, P, P],
         "sdc_cross_entropy": [P, P, U64, P, P, P, P, P, P],
         "sdc_cross_entropy_grad": [P, P, P, P, U64, P, P, P, U32, P, P, P],
+        "sdc_attention_ws_bytes": [P, P, P],
+        "sdc_attention": [P, P, U64, P, P, P, P],
+        "sdc_attention_grad": [P, P, P, P, P, U64, P, P, P, P, U32, P, P, P],
+        "sdc_gated_ffn_ws_bytes": [P, P, P],
+        "sdc_gated_ffn": [P, P, U64, P, P, P],
+        "sdc_gated_ffn_grad": [P, P, U64, P, U64, P, P, P, P, U32, P, P, P],
         "sdc_adamw_plan_bytes": [P, U64, U32, P],
         "sdc_adamw_plan_build": [P, U64, U32, P, U64, P, P],
         "sdc_adamw_step": [P, P, P, P, P, P, F64, F64, P, P],
@@ -1036,3 +1044,274 @@ def sdc_cross_entropy_grad(x, w, target, lse, grad, dx=None, dw=None, row=None, 
             None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), ref_p, col_mask,
             None if row is None else row.data_ptr(), mis_p, s), "sdc_cross_entropy_grad")
     return dx, dw
+
+
+def _row_args(row, ref, mismatch, dev, made):
+    """(row, ref, mismatch) pointers of a recomputed tensor's fingerprint; a row
+    that only the comparison needs is allocated."""
+    if ref is not None and row is None:
+        row = torch.empty((1, 4), dtype=torch.int64, device=dev)
+        made.append(row)
+    if row is not None:
+        _arg(row, "row", torch.int64, 4, dev)
+    ref_p, mis_p = _ref_args(ref, mismatch, dev)
+    return None if row is None else row.data_ptr(), ref_p, mis_p
+
+
+def _op_ws(ws, name, desc, dev, grad, made):
+    """The workspace of a call, allocated where the caller gives none."""
+    need = ctypes.c_uint64(0)
+    args = (None, ctypes.byref(need)) if grad else (ctypes.byref(need), None)
+    _check(getattr(_lib, name)(ctypes.byref(desc), *args), name)
+    if ws is not None:
+        return _arg(ws, "ws", torch.uint8, need.value, dev)
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    made.append(ws)
+    return ws
+
+
+def _op_out(t, name, shape, dtype, dev, made, zero=False):
+    """A contiguous output, the caller's or a new one."""
+    if t is None:
+        t = (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=dev)
+        made.append(t)
+        return t
+    _arg(t, name, dtype, 0, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, is {tuple(t.shape)}")
+    return t
+
+
+# ---- softmax attention ---------------------------------------------------------------
+class _Attn(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "seq_q", "seq_k")]
+                + [(n, ctypes.c_uint64) for n in ("batch", "len_q", "len_k", "heads_q", "heads_k", "d")]
+                + [(n, ctypes.c_uint64 * 3) for n in ("q_stride", "k_stride", "v_stride")]
+                + [("window", ctypes.c_uint64), ("scale", ctypes.c_float), ("causal", ctypes.c_uint32),
+                   ("dtype", ctypes.c_uint32), ("flags", ctypes.c_uint32)])
+
+
+_ATTN_ROW_STRIDE = 1 << 23  # of a row, in elements
+
+
+def _attn_rows(t, name, dims):
+    """A tensor of heads as the library takes it (a copy where its heads are not
+    contiguous or not at 16-byte boundaries)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-D tensor")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
+    if t.get_device() < 0:
+        raise ValueError(f"{name} is not on a GPU")
+    steps = [s for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    if (t.shape[-1] > 1 and t.stride(-1) != 1) or t.data_ptr() % 16 or any(s % 8 for s in steps) or (
+            t.shape[-3] > 1 and t.stride(-3) >= _ATTN_ROW_STRIDE):
+        t = t.contiguous()
+        if t.data_ptr() % 16:  # a contiguous view into the middle of a buffer
+            t = t.clone()
+    return t
+
+
+def _attn(q, k, v, causal, window, scale, seq_q, seq_k):
+    """(sdc_attn, device, [q, k, v] as it points into them)"""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be [batch, rows, heads, d], or [rows, heads, d] with seq_q and seq_k")
+    dims = q.dim()
+    kept = [_attn_rows(t, n, dims) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    dev = _cuda_device(q.get_device())
+    if (seq_q is None) != (seq_k is None) or (seq_q is None) != (dims == 4):
+        raise ValueError("packed sequences need 3-D tensors and both seq_q and seq_k, a batch 4-D ones and neither")
+    for t, n in ((k, "k"), (v, "v")):
+        if t.dtype != q.dtype or not _on_device(t, dev):
+            raise ValueError(f"{n} must be {q.dtype} on {dev}, is {t.dtype} on {t.device}")
+    if k.shape != v.shape or k.shape[-1] != q.shape[-1] or (dims == 4 and k.shape[0] != q.shape[0]):
+        raise ValueError(f"shapes do not go together: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    if k.shape[-2] == 0 or q.shape[-2] == 0 or q.shape[-2] % k.shape[-2]:
+        raise ValueError(f"{q.shape[-2]} heads of queries cannot share {k.shape[-2]} of keys")
+    if q.shape[-1] % 8 or not 8 <= q.shape[-1] <= 128:
+        raise ValueError(f"heads must have a multiple of 8 elements, at most 128, not {q.shape[-1]}")
+    if window < 0 or (window and not causal):
+        raise ValueError("a window must not be negative and needs causal")
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    batch = q.shape[0]
+    if seq_q is not None:
+        batch = seq_q.numel() - 1
+        if batch < 0 or seq_k.numel() != batch + 1:
+            raise ValueError("seq_q and seq_k need one offset more than there are sequences")
+        _arg(seq_q, "seq_q", torch.int32, batch + 1, dev)
+        _arg(seq_k, "seq_k", torch.int32, batch + 1, dev)
+    step = ctypes.c_uint64 * 3
+    strides = [step(*((t.stride() if dims == 4 else (0,) + t.stride())[:3])) for t in kept]
+    desc = _Attn(*(t.data_ptr() for t in kept), None if seq_q is None else seq_q.data_ptr(),
+                 None if seq_k is None else seq_k.data_ptr(), batch, q.shape[-3], k.shape[-3], q.shape[-2], k.shape[-2],
+                 q.shape[-1], *strides, int(window), scale, 1 if causal else 0, _TORCH_DTYPE[q.dtype], 0)
+    return desc, dev, kept
+
+
+def sdc_attention_ws_bytes(q, k, v, causal=False, window=0, scale=None, seq_q=None, seq_k=None):
+    """(forward, gradient) workspace bytes of this attention."""
+    h, _, _ = _attn(q, k, v, causal, window, scale, seq_q, seq_k)
+    f, g = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(_lib.sdc_attention_ws_bytes(ctypes.byref(h), ctypes.byref(f), ctypes.byref(g)), "sdc_attention_ws_bytes")
+    return f.value, g.value
+
+
+def sdc_attention(q, k, v, causal=False, window=0, scale=None, seq_q=None, seq_k=None, out=None, lse=None, row=None,
+                  ws=None, stream=None):
+    """(out, lse): softmax attention, whose scores are not kept (asynchronous; see
+    include/sdc.h).
+
+    q: [batch, rows, heads, d], k, v: [batch, keys, heads, d] with as many or fewer
+    heads, bfloat16 or float16, any strides (heads that are not contiguous, or off
+    16-byte boundaries, are copied).  Or packed sequences: [rows, heads, d] with seq_q,
+    seq_k, int32 offsets on the device (one more than sequences, ascending).  causal: the last query attends all
+    keys, the one before it all but one, ...; window: only the last `window` of those.
+    scale: of the scores, 1 / sqrt(d) by default.
+
+    out: of q's shape and dtype; lse: fp32, log sum exp of each query's scaled scores
+    (-inf, and out 0, for a query without keys).  Rows of no packed sequence are zero
+    in new outputs and left as they are in given ones.  row: an int64 [1, 4] tensor that
+    receives the scores' fingerprint row.  ws: a uint8 workspace
+    (sdc_attention_ws_bytes), else one is allocated."""
+    h, dev, kept = _attn(q, k, v, causal, window, scale, seq_q, seq_k)
+    made = [t for t, given in zip(kept, (q, k, v)) if t is not given]
+    packed = seq_q is not None
+    out = _op_out(out, "out", q.shape, q.dtype, dev, made, zero=packed)
+    lse = _op_out(lse, "lse", q.shape[:-1], torch.float32, dev, made, zero=packed)
+    row_p, _, _ = _row_args(row, None, None, dev, made)
+    ws = _op_ws(ws, "sdc_attention_ws_bytes", h, dev, False, made)
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_attention(ctypes.byref(h), ws.data_ptr(), ws.numel(), out.data_ptr(), lse.data_ptr(), row_p, s),
+               "sdc_attention")
+    return out, lse
+
+
+def sdc_attention_grad(q, k, v, out, lse, dout, causal=False, window=0, scale=None, seq_q=None, seq_k=None, dq=None,
+                       dk=None, dv=None, row=None, ref=None, mismatch=None, col_mask=COL_ALL, ws=None, stream=None,
+                       need_dq=True, need_dkv=True):
+    """(dq, dk, dv): the gradient for dout, the gradient of `out`, from the scores
+    computed again (asynchronous; see include/sdc.h).
+
+    out, lse: the forward pass'.  dq, dk, dv: contiguous outputs of q's, k's and v's shape
+    and dtype (allocated by default; None for those that need_dq / need_dkv leaves out;
+    rows of no packed sequence as for sdc_attention).  row: receives the recomputed
+    scores' fingerprint row.  ref, mismatch: the forward pass' row and an int32 [1] counter
+    that a difference under col_mask adds to, once for each of the two launches (for dq and
+    for dk, dv) that compute the scores."""
+    h, dev, kept = _attn(q, k, v, causal, window, scale, seq_q, seq_k)
+    made = [t for t, given in zip(kept, (q, k, v)) if t is not given]
+    packed = seq_q is not None
+    if dout.shape != q.shape or dout.dtype != q.dtype or not _on_device(dout, dev):
+        raise ValueError(f"dout must be {q.dtype} {tuple(q.shape)} on {dev}, is {dout.dtype} {tuple(dout.shape)} on "
+                         f"{dout.device}")
+    if not dout.is_contiguous() or dout.data_ptr() % 16:
+        dout = dout.clone(memory_format=torch.contiguous_format)
+        made.append(dout)
+    _op_out(out, "out", q.shape, q.dtype, dev, made)
+    _op_out(lse, "lse", q.shape[:-1], torch.float32, dev, made)
+    if not need_dq and not need_dkv:
+        raise ValueError("there is nothing to compute")
+    if need_dq:
+        dq = _op_out(dq, "dq", q.shape, q.dtype, dev, made, zero=packed)
+    if need_dkv:
+        dk = _op_out(dk, "dk", k.shape, k.dtype, dev, made, zero=packed)
+        dv = _op_out(dv, "dv", v.shape, v.dtype, dev, made, zero=packed)
+    row_p, ref_p, mis_p = _row_args(row, ref, mismatch, dev, made)
+    ws = _op_ws(ws, "sdc_attention_ws_bytes", h, dev, True, made)
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_attention_grad(
+            ctypes.byref(h), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), ws.data_ptr(), ws.numel(),
+            dq.data_ptr() if need_dq else None, dk.data_ptr() if need_dkv else None,
+            dv.data_ptr() if need_dkv else None, ref_p, col_mask, row_p, mis_p, s), "sdc_attention_grad")
+    return dq if need_dq else None, dk if need_dkv else None, dv if need_dkv else None
+
+
+# ---- the gated feed-forward block ------------------------------------------------------
+class _Ffn(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w_gate", "w_up")]
+                + [(n, ctypes.c_uint64) for n in ("n", "d", "f", "x_stride", "w_gate_stride", "w_up_stride")]
+                + [("dtype", ctypes.c_uint32), ("act", ctypes.c_uint32)])
+
+
+_ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _ffn(x, w_gate, w_up, act):
+    """(sdc_ffn, device, [x, w_gate, w_up] as it points into them)"""
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}")
+    kept = [_head_rows(t, n) for t, n in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up"))]
+    dev = _cuda_device(x.get_device())
+    for t, n in ((w_gate, "w_gate"), (w_up, "w_up")):
+        if t.dtype != x.dtype or t.shape[1] != x.shape[1] or t.shape != w_gate.shape:
+            raise ValueError(f"{n} must be {x.dtype} {(w_gate.shape[0], x.shape[1])}, is {t.dtype} {tuple(t.shape)}")
+        if not _on_device(t, dev):
+            raise ValueError(f"{n} must be on {dev}, not {t.device}")
+    return (_Ffn(*(t.data_ptr() for t in kept), x.shape[0], x.shape[1], w_gate.shape[0],
+                 *(_row_stride(t) for t in kept), _TORCH_DTYPE[x.dtype], _ACTS[act]), dev, kept)
+
+
+def sdc_gated_ffn_ws_bytes(x, w_gate, w_up, act="silu"):
+    """(forward, gradient) workspace bytes of this block."""
+    b, _, _ = _ffn(x, w_gate, w_up, act)
+    f, g = ctypes.c_uint64(0), ctypes.c_uint64(0)
+    _check(_lib.sdc_gated_ffn_ws_bytes(ctypes.byref(b), ctypes.byref(f), ctypes.byref(g)), "sdc_gated_ffn_ws_bytes")
+    return f.value, g.value
+
+
+def sdc_gated_ffn(x, w_gate, w_up, act="silu", out=None, row=None, ws=None, stream=None):
+    """act(x w_gate^T) * (x w_up^T), [n, f], of x's dtype: the projections are not
+    kept (asynchronous; see include/sdc.h).
+
+    x: [n, d], w_gate, w_up: [f, d], bfloat16 or float16, rows contiguous (any row
+    stride; the two may be halves of one matrix).  act: "silu" or "gelu_tanh".  row: an
+    int64 [1, 4] tensor that receives the fp32 projections' fingerprint row.  ws: a uint8
+    workspace (sdc_gated_ffn_ws_bytes), else one is allocated."""
+    b, dev, kept = _ffn(x, w_gate, w_up, act)
+    made = [t for t, given in zip(kept, (x, w_gate, w_up)) if t is not given]
+    out = _op_out(out, "out", (x.shape[0], w_gate.shape[0]), x.dtype, dev, made)
+    row_p, _, _ = _row_args(row, None, None, dev, made)
+    ws = _op_ws(ws, "sdc_gated_ffn_ws_bytes", b, dev, False, made)
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_gated_ffn(ctypes.byref(b), ws.data_ptr(), ws.numel(), out.data_ptr(), row_p, s),
+               "sdc_gated_ffn")
+    return out
+
+
+def sdc_gated_ffn_grad(x, w_gate, w_up, dh, act="silu", dx=None, dw_gate=None, dw_up=None, row=None, ref=None,
+                       mismatch=None, col_mask=COL_ALL, ws=None, stream=None, need_dx=True, need_dw=True):
+    """(dx, dw_gate, dw_up): the gradient for dh, the gradient of the block's output, from
+    the projections computed again (asynchronous; see include/sdc.h).
+
+    dx, dw_gate, dw_up: contiguous outputs of the inputs' shapes and dtype (allocated by
+    default; None for those that need_dx / need_dw leaves out).  row: receives the
+    recomputed projections' fingerprint row.  ref, mismatch: the forward pass' row and an
+    int32 [1] counter that a difference under col_mask adds 1 to."""
+    b, dev, kept = _ffn(x, w_gate, w_up, act)
+    made = [t for t, given in zip(kept, (x, w_gate, w_up)) if t is not given]
+    given, dh = dh, _head_rows(dh, "dh")
+    if dh is not given:
+        made.append(dh)
+    if dh.dtype != x.dtype or tuple(dh.shape) != (x.shape[0], w_gate.shape[0]) or not _on_device(dh, dev):
+        raise ValueError(f"dh must be {x.dtype} {(x.shape[0], w_gate.shape[0])} on {dev}, is {dh.dtype} "
+                         f"{tuple(dh.shape)} on {dh.device}")
+    if not need_dx and not need_dw:
+        raise ValueError("there is nothing to compute")
+    if need_dx:
+        dx = _op_out(dx, "dx", x.shape, x.dtype, dev, made)
+    if need_dw:
+        dw_gate = _op_out(dw_gate, "dw_gate", w_gate.shape, x.dtype, dev, made)
+        dw_up = _op_out(dw_up, "dw_up", w_up.shape, x.dtype, dev, made)
+    row_p, ref_p, mis_p = _row_args(row, ref, mismatch, dev, made)
+    ws = _op_ws(ws, "sdc_gated_ffn_ws_bytes", b, dev, True, made)
+    with _device_guard(dev):
+        s = _scan_stream(stream, dev, made)
+        _check(_lib.sdc_gated_ffn_grad(
+            ctypes.byref(b), dh.data_ptr(), _row_stride(dh), ws.data_ptr(), ws.numel(),
+            dx.data_ptr() if need_dx else None, dw_gate.data_ptr() if need_dw else None,
+            dw_up.data_ptr() if need_dw else None, ref_p, col_mask, row_p, mis_p, s), "sdc_gated_ffn_grad")
+    return dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None

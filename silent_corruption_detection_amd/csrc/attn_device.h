@@ -1,0 +1,480 @@
+// attn_device.h -- the tiled kernels of softmax attention (csrc/attn.hip says what
+// they compute) and what they share.
+//
+// Rows and columns.  The queries of the G heads that share a head of keys are one
+// matrix of lq G rows, r = token G + head, so a tile of keys in LDS serves all of them
+// and a few tokens of many heads still fill a tile.  Products are 32 x 32 x 16 MFMA of
+// 16-bit operands into fp32:
+//   forward, dq   S^T = K Q^T: keys down, queries across.  A lane holds 16 of a
+//                 query's 32 keys (the lane 32 further on the other 16), so a query's
+//                 maximum and sum are in-lane but for one exchange of halves.
+//   dk, dv        S = Q K^T: queries down, keys across.
+// The result of such a product has, in lane (column, half), element r of row
+//   8 (r >> 2) + 4 half + (r & 3);
+// as the right operand of the next product, whose sum runs over those rows, a lane
+// has to give 8 rows of every 16, and the sum's order is free as long as the left
+// operand has the same: so a lane's elements 0 .. 7 and 8 .. 15, converted, are the
+// two operands, without an exchange, and the left operand is read transposed from
+// LDS in that order (two reads of four rows of a column each).
+//
+// LDS holds rows of 64 (128) elements, 128 (256) bytes, as direct loads write them;
+// the 16-byte chunks of a row are permuted by an exclusive or with swizzle(row), so
+// that both kinds of reads, rows' chunks (16 rows, one chunk) and transposed ones (8
+// rows, four chunks), fall on all banks alike.
+#pragma once
+
+#include "tile_device.h"
+
+namespace sdc {
+
+struct AttnArgs {
+  const unsigned char *q, *k, *v;
+  uint64_t q_batch, k_batch, v_batch;  // bytes from one entry of the batch to the next
+  uint64_t q_head, k_head, v_head;
+  uint32_t q_row, k_row, v_row;
+  const int32_t *seq_q, *seq_k;        // packed sequences' first rows, or null
+  uint32_t batch, len_q, len_k;        // rows of an entry, or of all packed sequences
+  uint32_t hq, hk, G, d;
+  uint32_t g_mul, g_shift;             // r / G = r g_mul >> g_shift for r below 2^31
+  uint32_t causal, window;             // window 0: none
+  float scale, c;                      // c = scale log2(e)
+  uint32_t tiles;                      // of an entry (packed: of all, at most)
+  uint32_t units;                      // tiles x heads of keys (x entries)
+  uint32_t splits;
+  uint64_t kw;                         // columns of the scores that the fingerprint row describes
+  sdc_row* rows;                       // one partial row per workgroup, or null
+  uint16_t* out;
+  float* lse;                          // [rows][hq]
+  float* part;                         // splits: their sums, [hk][rows G][split][d]
+  float2* part_ml;                     // and their reference exponents and sums of exponentials
+  // gradient
+  const unsigned char* dout;           // contiguous, as out
+  const float *l2, *delta;             // [hk][rows G]: lse log2(e) (less kPShift), sum dout out
+  const float* norms;                  // fp16: kNormParts largest sums of squares of rows of dout, and as many of v
+  uint16_t *dq, *dk, *dv;
+  float *part_k, *part_v;              // splits of the queries: [split][rows of keys][hk][d]
+};
+
+struct AttnLaunch {
+  uint32_t dtype;
+  uint32_t waves;  // of 32 queries (keys, for dk and dv)
+};
+int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
+int32_t launch_attn_dq(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
+int32_t launch_attn_dkv(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
+
+// Workgroups of the gradient's first launch, at most, and so parts of fp16's norms.
+constexpr uint32_t kNormParts = 512;
+
+// Rows (of keys; of queries for dk and dv) of a tile in LDS.
+constexpr uint32_t kAttnTile = 64;
+
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// fp16: probabilities are held 2^14 times as large (at most 2^14), out of the subnormals
+template <class T> constexpr float kPShift = 0.0f;
+template <> constexpr float kPShift<Fp16> = 14.0f;
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// Row of element r of a 32 x 32 result in a lane of half `half`.
+__device__ __forceinline__ constexpr uint32_t element_row(uint32_t r, uint32_t half) {
+  return 8u * (r >> 2) + 4u * half + (r & 3u);
+}
+
+// A value and the one of the lane 32 further on (or back).
+__device__ __forceinline__ float both_max(float x) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float both_sum(float x) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Elements 8 h .. 8 h + 7 of a result as an operand, rounded to nearest.
+template <class T>
+__device__ __forceinline__ typename T::frag operand(const f32x16& x, int h) {
+  union {
+    uint32_t w[4];
+    typename T::frag f;
+  } u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.w[i] = T::bits(x[8 * h + 2 * i]) | T::bits(x[8 * h + 2 * i + 1]) << 16;
+  return u.f;
+}
+
+// ---- sequences -------------------------------------------------------------------
+
+// The part of the batch that a workgroup works on.
+struct Place32 {
+  uint32_t seq, tile, head;
+  uint32_t q0, k0;   // first rows in the batch
+  int32_t lq, lk;
+  bool live;
+};
+
+__device__ __forceinline__ uint32_t seq_at(const int32_t* s, uint32_t i, uint32_t rows) {
+  const int32_t x = s[i];
+  return x < 0 ? 0u : min((uint32_t)x, rows);
+}
+
+// Whether a row lies in one of the sequences (whose offsets ascend).
+__device__ __forceinline__ bool in_sequences(const int32_t* s, uint32_t batch, uint32_t rows, uint32_t row) {
+  uint32_t lo = 0, hi = batch;  // sequences lo .. begin at or before row
+  if (row < seq_at(s, 0, rows)) return false;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (seq_at(s, mid, rows) <= row) lo = mid;
+    else hi = mid;
+  }
+  return row < seq_at(s, batch, rows);
+}
+
+// Unit -> sequence, tile, head of keys.  Heads run fastest, then sequences, and later
+// tiles, which attend more keys under a causal mask, come first.  For packed sequences
+// the tiles are counted from their offsets, 64 sequences at a time; there may be fewer
+// than units.  KEYS: tiles of `rows` keys (the first come first), else of `rows` queries
+// of G heads.
+template <bool KEYS>
+__device__ __forceinline__ Place32 place_of(const AttnArgs& a, uint32_t unit, uint32_t rows) {
+  Place32 p;
+  p.head = unit % a.hk;
+  uint32_t j = unit / a.hk;
+  p.live = true;
+  if (!a.seq_q) {
+    p.seq = j % a.batch;
+    j /= a.batch;
+    p.tile = KEYS ? j : a.tiles - 1u - j;
+    p.q0 = p.seq * a.len_q;
+    p.k0 = p.seq * a.len_k;
+    p.lq = (int32_t)a.len_q;
+    p.lk = (int32_t)a.len_k;
+    return p;
+  }
+  const uint32_t lane = threadIdx.x & 63u;
+  const int32_t* s = KEYS ? a.seq_k : a.seq_q;
+  const uint32_t all = KEYS ? a.len_k : a.len_q, each = KEYS ? 1u : a.G;
+  p.live = false;
+  p.seq = p.tile = 0;
+  for (uint32_t b = 0; b < a.batch; b += 64) {
+    uint32_t n = 0;
+    if (b + lane < a.batch) {
+      const uint32_t lo = seq_at(s, b + lane, all), hi = seq_at(s, b + lane + 1u, all);
+      n = hi > lo ? (uint32_t)(((uint64_t)(hi - lo) * each + rows - 1u) / rows) : 0u;
+    }
+    uint32_t sum = n;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const uint32_t x = __shfl_up(sum, off);
+      if ((int)lane >= off) sum += x;
+    }
+    const uint64_t past = __ballot(sum > j);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const uint32_t end = __shfl(sum, at), mine = __shfl(n, at), i = j - (end - mine);
+      p.seq = b + (uint32_t)at;
+      p.tile = KEYS ? i : mine - 1u - i;
+      p.live = true;
+      break;
+    }
+    j -= __shfl(sum, 63);
+  }
+  p.seq = __builtin_amdgcn_readfirstlane(p.seq);
+  p.tile = __builtin_amdgcn_readfirstlane(p.tile);
+  const uint32_t q0 = seq_at(a.seq_q, p.seq, a.len_q), q1 = seq_at(a.seq_q, p.seq + 1u, a.len_q);
+  const uint32_t k0 = seq_at(a.seq_k, p.seq, a.len_k), k1 = seq_at(a.seq_k, p.seq + 1u, a.len_k);
+  p.q0 = __builtin_amdgcn_readfirstlane(q0);
+  p.k0 = __builtin_amdgcn_readfirstlane(k0);
+  p.lq = (int32_t)__builtin_amdgcn_readfirstlane(q1 > q0 ? q1 - q0 : 0u);
+  p.lk = (int32_t)__builtin_amdgcn_readfirstlane(k1 > k0 ? k1 - k0 : 0u);
+  return p;
+}
+
+__device__ __forceinline__ uint32_t token_of(const AttnArgs& a, uint32_t r) {
+  return (uint32_t)(((uint64_t)r * a.g_mul) >> a.g_shift);
+}
+
+// Keys [lo, hi) that token t attends.
+__device__ __forceinline__ int32_t keys_end(const AttnArgs& a, const Place32& p, int32_t t) {
+  return a.causal ? min(t + 1 + p.lk - p.lq, p.lk) : p.lk;
+}
+__device__ __forceinline__ int32_t keys_begin(const AttnArgs& a, const Place32& p, int32_t t) {
+  return a.window ? max((int32_t)max((int64_t)t + 1 + p.lk - p.lq - (int64_t)a.window, (int64_t)0), 0) : 0;
+}
+
+// Address of row r of the queries (or, contiguous, of dout and out) of a head of keys.
+__device__ __forceinline__ const unsigned char* query_row(const AttnArgs& a, const Place32& p, uint32_t r) {
+  const uint32_t t = token_of(a, r), g = r - t * a.G;
+  const uint64_t row = a.seq_q ? (uint64_t)(p.q0 + t) : (uint64_t)t;
+  return a.q + (a.seq_q ? 0u : p.seq * a.q_batch) + row * a.q_row + (uint64_t)(p.head * a.G + g) * a.q_head;
+}
+__device__ __forceinline__ uint64_t flat_row(const AttnArgs& a, const Place32& p, uint32_t r) {
+  const uint32_t t = token_of(a, r), g = r - t * a.G;
+  return (uint64_t)(p.q0 + t) * a.hq + p.head * a.G + g;  // of [rows][hq]
+}
+__device__ __forceinline__ uint64_t grouped_row(const AttnArgs& a, const Place32& p, uint32_t r) {
+  const uint64_t all = (uint64_t)(a.seq_q ? a.len_q : a.batch * a.len_q) * a.G;
+  return (uint64_t)p.head * all + (uint64_t)p.q0 * a.G + r;  // of [hk][rows G]
+}
+__device__ __forceinline__ const unsigned char* key_rows(const AttnArgs& a, const Place32& p) {
+  return a.k + (a.seq_q ? (uint64_t)p.k0 * a.k_row : p.seq * a.k_batch) + p.head * a.k_head;
+}
+__device__ __forceinline__ const unsigned char* value_rows(const AttnArgs& a, const Place32& p) {
+  return a.v + (a.seq_q ? (uint64_t)p.k0 * a.v_row : p.seq * a.v_batch) + p.head * a.v_head;
+}
+
+// ---- tiles in LDS ----------------------------------------------------------------
+
+// 64 rows of up to 32 DB elements.
+template <int DB>
+struct Rows {
+  static constexpr uint32_t kRow = DB > 2 ? 256u : 128u;
+  static constexpr uint32_t kBytes = kAttnTile * kRow;
+  static constexpr uint32_t kChunks = kRow / 16u;
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+    return DB > 2 ? (row & 3u) << 2 | (row >> 2 & 3u) : (row >> 1 & 1u) << 2 | (row >> 2 & 3u);
+  }
+};
+
+// 16 bytes per lane from base + off to LDS at lds + 16 * lane (base, lds uniform); see load_to_lds.
+__device__ __forceinline__ void load_to_lds_from(const unsigned char* base, uint32_t off, uint32_t lds) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "m0", "memory");
+#pragma clang diagnostic pop
+}
+
+// 4 bytes per lane to LDS at lds + 4 * lane (lds uniform); see load_to_lds.
+__device__ __forceinline__ void load4_to_lds(const float* src, uint32_t lds) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, off"
+      :
+      : "s"(lds), "v"(src)
+      : "m0", "memory");
+#pragma clang diagnostic pop
+}
+
+// Fills a tile with rows of a matrix, all waves together: what lies past its last row
+// or past its width is zero, so that nothing there can reach a sum.
+template <int DB, int WAVES>
+struct TileLoader {
+  static constexpr uint32_t kRows = 1024u / Rows<DB>::kRow;            // of one load of a wave
+  static constexpr uint32_t kLoads = kAttnTile / kRows / WAVES;        // of a wave
+  static_assert(kLoads * kRows * WAVES == kAttnTile, "the loads cover a tile");
+  const unsigned char* base;  // of the matrix' first row
+  uint32_t stride, width;     // bytes
+  uint32_t row, off[kLoads];  // of the thread's first load
+  bool in;                    // whole rows
+
+  __device__ __forceinline__ uint32_t row_at(uint32_t i) const { return row + i * kRows * WAVES; }
+  __device__ __forceinline__ uint32_t chunk_at(uint32_t i) const {
+    return (threadIdx.x & (Rows<DB>::kChunks - 1u)) ^ Rows<DB>::swizzle(row_at(i));
+  }
+  __device__ __forceinline__ void init(const unsigned char* b, uint32_t row_bytes, uint32_t d) {
+    base = b;
+    stride = row_bytes;
+    width = 2u * d;
+    row = (threadIdx.x >> 6) * kRows + (threadIdx.x & 63u) / Rows<DB>::kChunks;
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; ++i) off[i] = row_at(i) * stride + chunk_at(i) * 16u;
+    in = width == Rows<DB>::kRow;
+  }
+  // Rows first .. first + 63, of `rows` rows, into LDS at byte `lds`.
+  __device__ __forceinline__ void fill(uint32_t first, uint32_t rows, uint32_t lds) const {
+    const uint32_t to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+    const unsigned char* at = base + (uint64_t)first * stride;
+    if (in && first + kAttnTile <= rows) {
+#pragma unroll
+      for (uint32_t i = 0; i < kLoads; ++i) load_to_lds_from(at, off[i], to + i * (1024u * WAVES));
+    } else {
+      const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+#pragma unroll
+      for (uint32_t i = 0; i < kLoads; ++i) {
+        const bool has = first + row_at(i) < rows && chunk_at(i) * 16u < width;
+        load_to_lds(has ? at + off[i] : zero, to + i * (1024u * WAVES));
+      }
+    }
+  }
+};
+
+// The queries' (dout's) rows, whose places follow from token and head.
+template <int DB, int WAVES>
+struct QueryLoader {
+  typedef TileLoader<DB, WAVES> Tile;
+  uint32_t row;
+  __device__ __forceinline__ void init() {
+    row = (threadIdx.x >> 6) * Tile::kRows + (threadIdx.x & 63u) / Rows<DB>::kChunks;
+  }
+  __device__ __forceinline__ void fill(const AttnArgs& a, const Place32& p, uint32_t first, uint32_t rows,
+                                       uint32_t lds_q, uint32_t lds_do) const {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+    const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+#pragma unroll
+    for (uint32_t i = 0; i < Tile::kLoads; ++i) {
+      const uint32_t at = row + i * Tile::kRows * WAVES, r = min(first + at, rows - 1u);
+      const uint32_t chunk = (threadIdx.x & (Rows<DB>::kChunks - 1u)) ^ Rows<DB>::swizzle(at);
+      const bool has = first + at < rows && chunk * 8u < a.d;
+      const unsigned char* q = query_row(a, p, r) + chunk * 16u;
+      const unsigned char* o = a.dout + flat_row(a, p, r) * (2u * a.d) + chunk * 16u;
+      load_to_lds(has ? q : zero, lds_q + to + i * (1024u * WAVES));
+      load_to_lds(has ? o : zero, lds_do + to + i * (1024u * WAVES));
+    }
+  }
+};
+
+// A lane's reads of a tile as the left operand.
+template <class T, int DB>
+struct TileReads {
+  uint32_t rows_off, cols_off;
+  __device__ __forceinline__ TileReads() {
+    const uint32_t lane = threadIdx.x & 63u, half = lane >> 5;
+    rows_off = (lane & 31u) * Rows<DB>::kRow + ((half ^ Rows<DB>::swizzle(lane & 31u)) << 4);
+    const uint32_t r = 4u * half + (lane >> 2 & 3u), chunk = (lane >> 4 & 1u) * 2u + (lane >> 1 & 1u);
+    cols_off = r * Rows<DB>::kRow + ((chunk ^ Rows<DB>::swizzle(r)) << 4) + (lane & 1u) * 8u;
+  }
+  // Rows 32 b .. of the tile, elements 16 s .. of each: the sum runs along the rows.
+  __device__ __forceinline__ typename T::frag row(const unsigned char* tile, int b, int s) const {
+    return *reinterpret_cast<const typename T::frag*>(tile + (rows_off ^ (uint32_t)s << 5) + b * (32u * Rows<DB>::kRow));
+  }
+  // Elements 32 m .. of each row, rows 16 s .. of the tile: the sum runs over the rows.
+  __device__ __forceinline__ typename T::frag column(const unsigned char* tile, int m, int s) const {
+    const unsigned char* q = tile + s * (16u * Rows<DB>::kRow);
+    const uint32_t at = cols_off ^ (uint32_t)m << 6;
+    union {
+      s16x4 half[2];
+      typename T::frag all;
+    } u;
+    // eight rows on, the swizzle's bit 1 is the other one
+    u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + at));
+    u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + (at ^ 32u) + 8u * Rows<DB>::kRow));
+    return u.all;
+  }
+};
+
+// A row of a matrix as the right operand of a product along it: elements 16 s + 8 half ..
+template <class T, int DB>
+__device__ __forceinline__ void load_row(const unsigned char* p, bool has, uint32_t d, typename T::frag (&f)[2 * DB]) {
+  const uint32_t half = threadIdx.x >> 5 & 1u;
+#pragma unroll
+  for (int s = 0; s < 2 * DB; ++s) {
+    const uint32_t e = 16u * s + 8u * half;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (has && e < d) v = *reinterpret_cast<const u32x4*>(p + 2u * e);
+    f[s] = __builtin_bit_cast(typename T::frag, v);
+  }
+}
+
+// Whether the tile holds an infinity or NaN.
+template <class T, int DB>
+__device__ __forceinline__ bool tile_nonfinite(const unsigned char* tile) {
+  constexpr uint32_t one = std::is_same<T, Bf16>::value ? 0x00800080u : 0x04000400u;  // of the exponent's last bit
+  uint32_t bad = 0;
+  for (uint32_t at = (threadIdx.x & 63u) * 16u; at < Rows<DB>::kBytes; at += 1024u) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(tile + at);
+    bad |= ((v.x & 0x7FFF7FFFu) + one) | ((v.y & 0x7FFF7FFFu) + one) | ((v.z & 0x7FFF7FFFu) + one) |
+           ((v.w & 0x7FFF7FFFu) + one);
+  }
+  return __any((bad & 0x80008000u) != 0u);
+}
+
+// acc[m] += X^T P for 32 rows (block b) of a tile that holds infinities or NaN, over the
+// pairs that attend only: zero times what a masked row holds is not zero.  Rare, so row by
+// row.  has: bit r: element r of the lane's column attends.
+template <class T, int DB>
+__device__ __forceinline__ void product_by_rows(f32x16 (&acc)[DB], const unsigned char* tile, int b, const f32x16& p,
+                                             uint32_t has) {
+  const uint32_t lane = threadIdx.x & 63u, half = lane >> 5;
+  for (int r = 0; r < 16; ++r) {
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine = i == r ? T::value(T::bits(p[i])) : mine;
+    for (uint32_t h = 0; h < 2; ++h) {
+      const float x = __shfl(mine, (lane & 31u) + 32u * h);
+      const bool on = __shfl(has, (lane & 31u) + 32u * h) >> r & 1u;
+      const uint32_t row = 32u * b + element_row(r, h);
+#pragma unroll
+      for (int m = 0; m < DB; ++m)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t col = 32u * m + element_row(e, half);
+          const uint32_t at = row * Rows<DB>::kRow + (((col >> 3) ^ Rows<DB>::swizzle(row)) << 4) + (col & 7u) * 2u;
+          const float y = T::value(*reinterpret_cast<const uint16_t*>(tile + at));
+          if (on) acc[m][e] += x * y;
+        }
+    }
+  }
+}
+
+// Four 16-bit values of consecutive elements.
+template <class T>
+__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = uint2{T::bits(a) | T::bits(b) << 16, T::bits(c) | T::bits(d) << 16};
+}
+
+// fp16: the power of two, less kPShift's, that dS = p (dP - delta) is held times: |dP| and
+// |delta| are at most the product of the largest norms of a row of dout and of v, so 2^14
+// over twice that keeps dS below fp16's largest number and as far as can be from its
+// subnormals.  bf16 has fp32's exponents.
+template <class T>
+__device__ __forceinline__ int grad_shift(const AttnArgs& a) {
+  if constexpr (std::is_same<T, Bf16>::value) return 0;
+  float x = 0.0f, y = 0.0f;
+  for (uint32_t i = threadIdx.x & 63u; i < kNormParts; i += 64) {
+    x = __builtin_fmaxf(x, a.norms[i]);
+    y = __builtin_fmaxf(y, a.norms[kNormParts + i]);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    x = __builtin_fmaxf(x, __shfl_xor(x, off));
+    y = __builtin_fmaxf(y, __shfl_xor(y, off));
+  }
+  const float bits = 0.5f * (__builtin_amdgcn_logf(x) + __builtin_amdgcn_logf(y)) + 1.0f;  // log2 of the bound
+  const float e = __builtin_floorf(14.0f - bits);
+  return __builtin_amdgcn_readfirstlane((int)__builtin_fminf(__builtin_fmaxf(e, -60.0f), 60.0f));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Own loads have landed, own LDS accesses are done, and everyone's.
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The part of the scores' fingerprint row that a 32 x 32 block of raw scores gives.
+// first: index, from 1, of element 0's score; step: from one row of the block to the next;
+// has: which elements attend.
+__device__ __forceinline__ void block_row(Lane& ln, const f32x16& z, uint64_t first, uint64_t step, uint32_t has) {
+  uint64_t s = 0, ws = 0;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const uint32_t x = has >> r & 1u ? __float_as_uint(z[r]) : 0u;
+    s += x;
+    ws += (uint64_t)element_row(r, 0) * x;
+    ln.x ^= x;
+    ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+  }
+  ln.s += s;
+  ln.w += ws * step + first * s;
+}
+
+}  // namespace
+}  // namespace sdc

@@ -1,0 +1,225 @@
+// attn_dkv.hip -- the keys' and values' gradients of softmax attention (csrc/attn.hip)
+// for gfx950.
+#include "attn_device.h"
+
+namespace sdc {
+namespace {
+
+// A workgroup of W waves takes 32 W keys, a wave 32 of them, keeps them and their values
+// in registers and streams the queries that attend them, of all heads that share them,
+// and their rows of dout past them in tiles of 64, so that the sums over queries and over
+// heads are one, in a fixed order.  Per block of 32 queries: S = Q K^T, dP = dout V^T, p and
+// dS as for dq; then dv^T += dout^T p and dk^T += Q^T dS.  p and dS are rounded to 16 bits (off
+// by half a step of their own size, which the sums average out).
+//
+// SPLIT: the queries in a.splits parts, each leaving fp32 sums.
+template <class T, int DB, int W, bool ROW, bool SPLIT>
+__global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  typedef Rows<DB> L;
+  constexpr uint32_t kBuf = 2u * L::kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
+  const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
+  const Place32 p = place_of<true>(a, unit, 32u * W);
+  Lane ln;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u, half = lane >> 5;
+  const int32_t wg0 = (int32_t)(p.tile * (32u * W)), key0 = wg0 + (int32_t)wave * 32;
+  if (p.live && wg0 < p.lk) {
+    const int32_t key = key0 + (int32_t)(lane & 31u), at_key = min(key, p.lk - 1), R = p.lq * (int32_t)a.G;
+    typename T::frag k[2 * DB], v[2 * DB];
+    load_row<T, DB>(key_rows(a, p) + (uint64_t)at_key * a.k_row, key < p.lk, a.d, k);
+    load_row<T, DB>(value_rows(a, p) + (uint64_t)at_key * a.v_row, key < p.lk, a.d, v);
+    // rows [first, last) of the queries attend key x
+    const auto first_row = [&](int32_t x) {
+      return a.causal ? (int32_t)min((int64_t)max(x - (p.lk - p.lq), 0) * a.G, (int64_t)R) : 0;
+    };
+    const auto last_row = [&](int32_t x) {
+      return a.window ? (int32_t)max(min(((int64_t)x - (p.lk - p.lq) + a.window) * a.G, (int64_t)R), (int64_t)0) : R;
+    };
+    const int32_t lo = first_row(at_key), hi = key < p.lk ? last_row(at_key) : 0;
+    const int32_t wg_last = min(wg0 + 32 * W - 1, p.lk - 1), w_last = min(key0 + 31, p.lk - 1);
+    const int32_t wg_begin = first_row(wg0), wg_end = last_row(wg_last);
+    const bool idle = key0 >= p.lk;
+    const int32_t begin = first_row(min(key0, p.lk - 1)), end = idle ? 0 : last_row(w_last);
+    const int32_t from = first_row(w_last), to = key0 + 31 < p.lk ? last_row(key0) : 0;  // all of the wave's keys
+    int32_t t0 = wg_begin / (int32_t)kAttnTile, t1 = max((wg_end + (int32_t)kAttnTile - 1) / (int32_t)kAttnTile, t0);
+    if constexpr (SPLIT) {
+      const int32_t each = (t1 - t0 + (int32_t)a.splits - 1) / (int32_t)a.splits;
+      t0 = min(t0 + (int32_t)split * each, t1);
+      t1 = min(t0 + each, t1);
+    }
+    const int shift = grad_shift<T>(a);
+    const float f = power_of_two(shift - (int)kPShift<T>);
+    f32x16 dk[DB], dv[DB];
+#pragma unroll
+    for (int m = 0; m < DB; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dk[m][e] = dv[m][e] = 0.0f;
+    const TileReads<T, DB> at;
+    QueryLoader<DB, W> lq;
+    lq.init();
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    const float *l2 = a.l2 + grouped_row(a, p, 0), *delta = a.delta + grouped_row(a, p, 0);
+    const auto fill = [&](int32_t t, uint32_t buf) {
+      const uint32_t r = (uint32_t)t * kAttnTile, base = lds0 + buf * kBuf;
+      lq.fill(a, p, r, (uint32_t)R, base, base + L::kBytes);
+      const uint32_t row = min(r + lane, (uint32_t)R - 1u);
+      if (wave == 0) load4_to_lds(l2 + row, base + 2u * L::kBytes);
+      if (wave == W - 1) load4_to_lds(delta + row, base + 2u * L::kBytes + 4u * kAttnTile);
+    };
+    if (t0 < t1) fill(t0, 0);
+    uint32_t buf = 0;
+    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
+      tile_barrier();  // this buffer is whole, and everyone has left the other
+      if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+      const int32_t q0 = t * (int32_t)kAttnTile;
+      if (q0 >= end || q0 + (int32_t)kAttnTile <= begin) continue;
+      const bool masked = q0 < from || q0 + (int32_t)kAttnTile > to;
+      const unsigned char *qt = lds + buf * kBuf, *dt = qt + L::kBytes;
+      const float *lt = reinterpret_cast<const float*>(dt + L::kBytes), *et = lt + kAttnTile;
+      const bool by_rows = masked && (tile_nonfinite<T, DB>(qt) || tile_nonfinite<T, DB>(dt));
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) {
+          s = mfma32(at.row(qt, n, i), k[i], s);
+          dp = mfma32(at.row(dt, n, i), v[i], dp);
+        }
+        uint32_t has = 0xFFFFu;
+        if (masked) {
+          has = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int32_t r = q0 + 32 * n + (int32_t)element_row(e, half);
+            if (r >= lo && r < hi) has |= 1u << e;
+          }
+        }
+        if constexpr (ROW) {
+          // the rows of a block are not evenly spaced where heads are grouped
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int32_t r = q0 + 32 * n + (int32_t)element_row(4 * g + e, half);
+              if (!(has >> (4 * g + e) & 1u)) continue;
+              const uint32_t x = __float_as_uint(s[4 * g + e]);
+              ln.s += x;
+              ln.w += (flat_row(a, p, (uint32_t)r) * a.kw + (uint32_t)key + 1u) * x;
+              ln.x ^= x;
+              ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+            }
+        }
+        f32x16 ds;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 lse = *reinterpret_cast<const f32x4*>(lt + 32 * n + 8 * g + 4 * half);
+          const f32x4 del = *reinterpret_cast<const f32x4*>(et + 32 * n + 8 * g + 4 * half);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * g + e], a.c, -lse[e]));
+            s[4 * g + e] = pr;
+            ds[4 * g + e] = pr * (dp[4 * g + e] - del[e]);
+            if constexpr (kPShift<T> != 0.0f) ds[4 * g + e] *= f;
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!(has >> e & 1u)) s[e] = ds[e] = 0.0f;
+        }
+        if (by_rows) {
+          product_by_rows<T, DB>(dv, dt, n, s, has);
+          product_by_rows<T, DB>(dk, qt, n, ds, has);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const typename T::frag w = operand<T>(s, i), x = operand<T>(ds, i);
+#pragma unroll
+          for (int m = 0; m < DB; ++m) {
+            dv[m] = mfma32(at.column(dt, m, 2 * n + i), w, dv[m]);
+            dk[m] = mfma32(at.column(qt, m, 2 * n + i), x, dk[m]);
+          }
+        }
+      }
+    }
+    if (key < p.lk) {
+      const float gk = a.scale * power_of_two(-shift), gv = power_of_two(-(int)kPShift<T>);
+      const uint64_t row = (uint64_t)(p.k0 + (uint32_t)key) * a.hk + p.head;
+      const uint64_t all = (uint64_t)(a.seq_k ? a.len_k : a.batch * a.len_k) * a.hk;
+#pragma unroll
+      for (int m = 0; m < DB; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = 32u * m + 8u * e + 4u * half;
+          if (x >= a.d) continue;
+          const f32x4 xk = {dk[m][4 * e] * gk, dk[m][4 * e + 1] * gk, dk[m][4 * e + 2] * gk, dk[m][4 * e + 3] * gk};
+          const f32x4 xv = {dv[m][4 * e] * gv, dv[m][4 * e + 1] * gv, dv[m][4 * e + 2] * gv, dv[m][4 * e + 3] * gv};
+          if constexpr (SPLIT) {
+            const uint64_t to_part = (split * all + row) * a.d + x;
+            *reinterpret_cast<f32x4*>(a.part_k + to_part) = xk;
+            *reinterpret_cast<f32x4*>(a.part_v + to_part) = xv;
+          } else {
+            store4<T>(a.dk + row * a.d + x, xk.x, xk.y, xk.z, xk.w);
+            store4<T>(a.dv + row * a.d + x, xv.x, xv.y, xv.z, xv.w);
+          }
+        }
+    }
+  }
+  if constexpr (ROW) store_tile_row<W>(ln, a.rows + blockIdx.x);
+}
+
+// dk and dv: the splits' sums, in split order.  Eight elements a thread; rows outside every
+// sequence have none.
+template <class T>
+__global__ void __launch_bounds__(256) attn_dkv_finish_kernel(const AttnArgs a, uint64_t rows) {
+  const uint64_t all = rows * a.hk * a.d, at = ((uint64_t)blockIdx.x * 256u + threadIdx.x) * 8u;
+  if (at >= all) return;
+  if (a.seq_k) {
+    const uint32_t row = (uint32_t)(at / ((uint64_t)a.hk * a.d));
+    if (!in_sequences(a.seq_k, a.batch, a.len_k, row)) return;
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const float* part = (v ? a.part_v : a.part_k) + at;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+    for (uint32_t k = 0; k < a.splits; ++k) {
+      x += *reinterpret_cast<const f32x4*>(part + k * all);
+      y += *reinterpret_cast<const f32x4*>(part + k * all + 4);
+    }
+    uint16_t* out = (v ? a.dv : a.dk) + at;
+    store4<T>(out, x.x, x.y, x.z, x.w);
+    store4<T>(out + 4, y.x, y.y, y.z, y.w);
+  }
+}
+
+}  // namespace
+
+int32_t launch_attn_dkv(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
+  return for_dtype(l.dtype, [&](auto type) {
+    typedef decltype(type) T;
+    const auto shape = [&](auto db) {
+      constexpr int DB = decltype(db)::value, W = 4;
+      const dim3 grid(a.units * a.splits), block(64 * W);
+      constexpr uint32_t bytes = 2u * (2u * Rows<DB>::kBytes + 2u * kAttnTile * 4u);
+      const bool split = a.splits > 1;
+      if (a.rows && split) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, true>), grid, block, bytes, s, a);
+      else if (a.rows) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, false>), grid, block, bytes, s, a);
+      else if (split) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, false, true>), grid, block, bytes, s, a);
+      else hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, false, false>), grid, block, bytes, s, a);
+      return launch_status();
+    };
+    int32_t st = a.d <= 64   ? shape(std::integral_constant<int, 2>())
+                 : a.d <= 96 ? shape(std::integral_constant<int, 3>())
+                             : shape(std::integral_constant<int, 4>());
+    if (st || a.splits == 1) return st;
+    const uint64_t rows = a.seq_k ? a.len_k : (uint64_t)a.batch * a.len_k;
+    hipLaunchKernelGGL(attn_dkv_finish_kernel<T>, dim3((uint32_t)((rows * a.hk * a.d / 8 + 255) / 256)), dim3(256), 0, s,
+                       a, rows);
+    return launch_status();
+  });
+}
+
+}  // namespace sdc

@@ -1,0 +1,142 @@
+// attn_dq.hip -- the queries' gradient of softmax attention (csrc/attn.hip) for gfx950.
+#include "attn_device.h"
+
+namespace sdc {
+namespace {
+
+// As the forward pass, a workgroup of W waves takes 32 W queries of a head of keys and
+// streams the keys they attend past them.  A wave keeps its queries and their rows of
+// dout in registers, and per block of 32 keys computes S^T = K Q^T and dP^T = V dout^T, the
+// probabilities p = exp2(s c - lse log2(e)), dS = p (dP - delta), and adds K^T dS^T to
+// dq^T.  dS is the one thing rounded to 16 bits on the way (off by half a step of its own
+// size, which the sum over keys averages out).
+template <class T, int DB, int W, bool ROW>
+__global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  typedef Rows<DB> L;
+  const Place32 p = place_of<false>(a, blockIdx.x, 32u * W);
+  Lane ln;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u, half = lane >> 5;
+  const uint32_t R = (uint32_t)p.lq * a.G, wg0 = p.tile * (32u * W), r0 = wg0 + wave * 32u;
+  if (p.live && R != 0) {
+    typename T::frag q[2 * DB], dout[2 * DB];
+    const uint32_t r = r0 + (lane & 31u), c = min(r, R - 1u);
+    const uint64_t flat = flat_row(a, p, c);
+    load_row<T, DB>(query_row(a, p, c), r < R, a.d, q);
+    load_row<T, DB>(a.dout + flat * (2u * a.d), r < R, a.d, dout);
+    const float l2 = a.l2[grouped_row(a, p, c)], delta = a.delta[grouped_row(a, p, c)];
+    const int32_t mine = (int32_t)token_of(a, c), lo = keys_begin(a, p, mine), hi = keys_end(a, p, mine);
+    const auto token = [&](uint32_t x) { return (int32_t)token_of(a, min(x, R - 1u)); };
+    const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * W - 1u));
+    const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 31u));
+    const int32_t from = keys_begin(a, p, token(r0 + 31u)), to = keys_end(a, p, token(r0));
+    const int32_t t0 = wg_begin / (int32_t)kAttnTile, t1 = (wg_end + (int32_t)kAttnTile - 1) / (int32_t)kAttnTile;
+    const int shift = grad_shift<T>(a);
+    const float f = power_of_two(shift - (int)kPShift<T>);
+    f32x16 acc[DB];
+#pragma unroll
+    for (int m = 0; m < DB; ++m)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
+    const TileReads<T, DB> at;
+    TileLoader<DB, W> lk, lv;
+    lk.init(key_rows(a, p), a.k_row, a.d);
+    lv.init(value_rows(a, p), a.v_row, a.d);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    const auto fill = [&](int32_t t, uint32_t buf) {
+      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes));
+      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
+    };
+    if (t0 < t1) fill(t0, 0);
+    uint32_t buf = 0;
+    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
+      tile_barrier();  // this buffer is whole, and everyone has left the other
+      if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+      const int32_t k0 = t * (int32_t)kAttnTile;
+      if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;
+      const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
+      const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
+      const bool by_rows = masked && tile_nonfinite<T, DB>(kt);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * DB; ++i) {
+          s = mfma32(at.row(kt, n, i), q[i], s);
+          dp = mfma32(at.row(vt, n, i), dout[i], dp);
+        }
+        uint32_t has = 0xFFFFu;
+        if (masked) {
+          has = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int32_t key = k0 + 32 * n + (int32_t)element_row(e, half);
+            if (key >= lo && key < hi) has |= 1u << e;
+          }
+        }
+        if constexpr (ROW)
+          block_row(ln, s, flat * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u, 1u, r < R ? has : 0u);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.c, -l2));
+          s[e] = pr * (dp[e] - delta);
+          if constexpr (kPShift<T> != 0.0f) s[e] *= f;
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!(has >> e & 1u)) s[e] = 0.0f;
+        }
+        if (by_rows) {
+          product_by_rows<T, DB>(acc, kt, n, s, has);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const typename T::frag w = operand<T>(s, i);
+#pragma unroll
+          for (int m = 0; m < DB; ++m) acc[m] = mfma32(at.column(kt, m, 2 * n + i), w, acc[m]);
+        }
+      }
+    }
+    if (r < R) {
+      const float g = a.scale * power_of_two(-shift);
+      uint16_t* out = a.dq + flat * a.d;
+#pragma unroll
+      for (int m = 0; m < DB; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = 32u * m + 8u * e + 4u * half;
+          if (x < a.d)
+            store4<T>(out + x, acc[m][4 * e] * g, acc[m][4 * e + 1] * g, acc[m][4 * e + 2] * g, acc[m][4 * e + 3] * g);
+        }
+    }
+  }
+  if constexpr (ROW) store_tile_row<W>(ln, a.rows + blockIdx.x);
+}
+
+}  // namespace
+
+int32_t launch_attn_dq(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
+  return for_dtype(l.dtype, [&](auto type) {
+    typedef decltype(type) T;
+    const auto launch = [&](auto db, auto waves) {
+      constexpr int DB = decltype(db)::value, W = decltype(waves)::value;
+      const dim3 grid(a.units), block(64 * W);
+      constexpr uint32_t bytes = 4u * Rows<DB>::kBytes;
+      if (a.rows) hipLaunchKernelGGL((attn_dq_kernel<T, DB, W, true>), grid, block, bytes, s, a);
+      else hipLaunchKernelGGL((attn_dq_kernel<T, DB, W, false>), grid, block, bytes, s, a);
+      return launch_status();
+    };
+    const auto shape = [&](auto db) {
+      return l.waves == 1 ? launch(db, std::integral_constant<int, 1>()) : launch(db, std::integral_constant<int, 4>());
+    };
+    return a.d <= 64   ? shape(std::integral_constant<int, 2>())
+           : a.d <= 96 ? shape(std::integral_constant<int, 3>())
+                       : shape(std::integral_constant<int, 4>());
+  });
+}
+
+}  // namespace sdc

@@ -1,0 +1,291 @@
+// attn_fwd.hip -- the forward pass of softmax attention (csrc/attn.hip) for gfx950.
+#include "attn_device.h"
+
+namespace sdc {
+namespace {
+
+// A workgroup of W waves takes 32 QB W queries of a head of keys, a wave 32 QB of them,
+// and streams the keys they attend past them in tiles of 64 (two buffers in LDS, the next
+// filled by direct loads while this one is multiplied).  The queries stay in registers, as
+// do the sums of values: out^T = V^T P^T with a query per lane, so its rescaling is one
+// factor a lane.
+//
+// The softmax runs on exponents z c = s scale log2(e), less a reference that a query
+// raises only when a tile's maximum passes it by more than 8: probabilities are then at
+// most 2^8, sums in fp32 are none the worse, and most tiles rescale nothing.  p =
+// exp2(s c - ref) as one fused operation is off by the rounding of ref alone, which is
+// ref itself: a factor that out and lse = (ref + log2 l) ln 2 share.  From |ref| of 2^20
+// on (SPLIT apart) the product's own rounding would show, and the difference of scores is taken first.
+//
+// SPLIT: the keys in a.splits parts, each leaving its unscaled sums, ref and l.
+template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
+__global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
+  extern __shared__ __align__(16) unsigned char lds[];
+  typedef Rows<DB> L;
+  const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
+  const Place32 p = place_of<false>(a, unit, 32u * QB * W);
+  Lane ln;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u, half = lane >> 5;
+  const uint32_t R = (uint32_t)p.lq * a.G, wg0 = p.tile * (32u * QB * W), r0 = wg0 + wave * (32u * QB);
+  if (p.live && R != 0) {
+    typename T::frag q[QB][2 * DB];
+    int32_t lo[QB], hi[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      const uint32_t r = r0 + 32u * b + (lane & 31u), c = min(r, R - 1u);
+      load_row<T, DB>(query_row(a, p, c), r < R, a.d, q[b]);
+      const int32_t t = (int32_t)token_of(a, c);
+      lo[b] = keys_begin(a, p, t);
+      hi[b] = keys_end(a, p, t);
+    }
+    // keys of the workgroup's, and of the wave's, queries: [begin, end), all attend [from, to)
+    const auto token = [&](uint32_t r) { return (int32_t)token_of(a, min(r, R - 1u)); };
+    const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * QB * W - 1u));
+    const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 32u * QB - 1u));
+    const int32_t from = keys_begin(a, p, token(r0 + 32u * QB - 1u)), to = keys_end(a, p, token(r0));
+    int32_t t0 = wg_begin / (int32_t)kAttnTile, t1 = max((wg_end + (int32_t)kAttnTile - 1) / (int32_t)kAttnTile, t0);
+    if constexpr (SPLIT) {
+      const int32_t each = (t1 - t0 + (int32_t)a.splits - 1) / (int32_t)a.splits;
+      t0 = min(t0 + (int32_t)split * each, t1);
+      t1 = min(t0 + each, t1);
+    }
+    f32x16 o[QB][DB];
+    float ref[QB], l[QB];
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      ref[b] = -__builtin_inff();
+      l[b] = 0.0f;
+#pragma unroll
+      for (int m = 0; m < DB; ++m)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[b][m][e] = 0.0f;
+    }
+    const TileReads<T, DB> at;
+    TileLoader<DB, W> lk, lv;
+    lk.init(key_rows(a, p), a.k_row, a.d);
+    lv.init(value_rows(a, p), a.v_row, a.d);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    const auto fill = [&](int32_t t, uint32_t buf) {
+      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes));
+      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
+    };
+    if (t0 < t1) fill(t0, 0);
+    uint32_t buf = 0;
+    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
+      tile_barrier();  // this buffer is whole, and everyone has left the other
+      if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+      const int32_t k0 = t * (int32_t)kAttnTile;
+      if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;  // none of the wave's
+      const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
+      const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
+      f32x16 s[QB][2];
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[b][n][e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const typename T::frag f = at.row(kt, n, i);
+#pragma unroll
+          for (int b = 0; b < QB; ++b) s[b][n] = mfma32(f, q[b][i], s[b][n]);
+        }
+      uint32_t has[QB][2];
+#pragma unroll
+      for (int b = 0; b < QB; ++b)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          has[b][n] = 0xFFFFu;
+          if (masked) {
+            has[b][n] = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int32_t key = k0 + 32 * n + (int32_t)element_row(e, half);
+              if (key >= lo[b] && key < hi[b]) has[b][n] |= 1u << e;
+            }
+          }
+        }
+      if constexpr (ROW) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+          const uint32_t r = r0 + 32u * b + (lane & 31u);
+          const uint64_t row = flat_row(a, p, min(r, R - 1u)) * a.kw + (uint32_t)k0 + 4u * half + 1u;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) block_row(ln, s[b][n], row + 32u * n, 1u, r < R ? has[b][n] : 0u);
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (!(has[b][n] >> e & 1u)) s[b][n][e] = -__builtin_inff();
+      }
+#pragma unroll
+      for (int b = 0; b < QB; ++b) {
+        float top = s[b][0][0];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[b][n][e]);
+        top = both_max(top) * a.c;
+        if (__any(top > ref[b] + 8.0f)) {
+          const float was = ref[b];
+          ref[b] = __builtin_fmaxf(was, top);
+          const float f = was == ref[b] ? 1.0f : __builtin_amdgcn_exp2f(was - ref[b]);
+          l[b] *= f;
+#pragma unroll
+          for (int m = 0; m < DB; ++m)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[b][m][e] *= f;
+        }
+        const float base = ref[b] == -__builtin_inff() ? 0.0f : ref[b];
+        if (!__any(__builtin_fabsf(base) >= 0x1p20f)) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              s[b][n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][n][e], a.c, -base));
+        } else {
+          const float score = base / a.c;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][n][e] = __builtin_amdgcn_exp2f((s[b][n][e] - score) * a.c);
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum += s[b][n][e];
+        l[b] += sum;
+      }
+      if (masked && tile_nonfinite<T, DB>(vt)) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) product_by_rows<T, DB>(o[b], vt, n, s[b][n], has[b][n]);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        typename T::frag w[QB];
+#pragma unroll
+        for (int b = 0; b < QB; ++b) w[b] = operand<T>(s[b][i >> 1], i & 1);
+#pragma unroll
+        for (int m = 0; m < DB; ++m) {
+          const typename T::frag f = at.column(vt, m, i);
+#pragma unroll
+          for (int b = 0; b < QB; ++b) o[b][m] = mfma32(f, w[b], o[b][m]);
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < QB; ++b) {
+      const uint32_t r = r0 + 32u * b + (lane & 31u);
+      const float sum = both_sum(l[b]);
+      if (r >= R) continue;
+      if constexpr (SPLIT) {
+        const uint64_t row = grouped_row(a, p, r) * a.splits + split;
+        if (half == 0) a.part_ml[row] = float2{ref[b], sum};
+        float* out = a.part + row * a.d;
+#pragma unroll
+        for (int m = 0; m < DB; ++m)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t e = 32u * m + 8u * g + 4u * half;
+            if (e < a.d)
+              *reinterpret_cast<f32x4*>(out + e) =
+                  f32x4{o[b][m][4 * g], o[b][m][4 * g + 1], o[b][m][4 * g + 2], o[b][m][4 * g + 3]};
+          }
+      } else {
+        // a query that attends nothing: out 0, lse -inf
+        const bool none = ref[b] == -__builtin_inff() && !(sum != sum);
+        const float f = none ? 0.0f : 1.0f / sum;
+        const uint64_t row = flat_row(a, p, r);
+        if (half == 0) a.lse[row] = none ? -__builtin_inff() : (ref[b] + __builtin_amdgcn_logf(sum)) * kLn2;
+        uint16_t* out = a.out + row * a.d;
+#pragma unroll
+        for (int m = 0; m < DB; ++m)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t e = 32u * m + 8u * g + 4u * half;
+            if (e < a.d)
+              store4<T>(out + e, o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f,
+                        o[b][m][4 * g + 3] * f);
+          }
+      }
+    }
+  }
+  if constexpr (ROW) store_tile_row<W>(ln, a.rows + blockIdx.x);
+}
+
+// Joins the splits of a row: out = sum_k 2^(ref_k - ref) o_k / sum_k 2^(ref_k - ref) l_k, in
+// split order.  A wave per row; rows outside every sequence have none.
+template <class T>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, uint64_t rows) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint64_t n = (uint64_t)blockIdx.x * 4u + (threadIdx.x >> 6);  // of [rows][hq]
+  if (n >= rows * a.hq) return;
+  const uint64_t row = n / a.hq;
+  const uint32_t head = (uint32_t)(n % a.hq);
+  if (a.seq_q && !in_sequences(a.seq_q, a.batch, a.len_q, (uint32_t)row)) return;
+  const uint64_t at = ((head / a.G) * rows * a.G + row * a.G + head % a.G) * a.splits;
+  float ref = -__builtin_inff(), sum = 0.0f;
+  for (uint32_t k = 0; k < a.splits; ++k) ref = __builtin_fmaxf(ref, a.part_ml[at + k].x);
+  const float base = ref == -__builtin_inff() ? 0.0f : ref;
+  float x[2] = {0.0f, 0.0f};
+#pragma unroll 4
+  for (uint32_t k = 0; k < a.splits; ++k) {
+    const float2 ml = a.part_ml[at + k];
+    const float f = __builtin_amdgcn_exp2f(ml.x - base);
+    sum += ml.y * f;
+    const float* part = a.part + (at + k) * a.d;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 64u * i < a.d) x[i] += part[lane + 64u * i] * f;
+  }
+  const bool none = ref == -__builtin_inff() && !(sum != sum);
+  if (lane == 0) a.lse[n] = none ? -__builtin_inff() : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64u * i < a.d) a.out[n * a.d + lane + 64u * i] = (uint16_t)T::bits(none ? 0.0f : x[i] / sum);
+}
+
+}  // namespace
+
+int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
+  return for_dtype(l.dtype, [&](auto type) {
+    typedef decltype(type) T;
+    const auto launch = [&](auto db, auto waves, auto blocks) {
+      constexpr int DB = decltype(db)::value, W = decltype(waves)::value, QB = decltype(blocks)::value;
+      const dim3 grid(a.units * a.splits), block(64 * W);
+      constexpr uint32_t bytes = 4u * Rows<DB>::kBytes;
+      const bool split = a.splits > 1;
+      if (a.rows && split) hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, true, true>), grid, block, bytes, s, a);
+      else if (a.rows) hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, true, false>), grid, block, bytes, s, a);
+      else if (split) hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, false, true>), grid, block, bytes, s, a);
+      else hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, false, false>), grid, block, bytes, s, a);
+      return launch_status();
+    };
+    const auto shape = [&](auto db) {
+      std::integral_constant<int, 1> one;
+      if (l.waves == 1) return launch(db, one, one);
+      return launch(db, std::integral_constant<int, 4>(), one);
+    };
+    int32_t st = a.d <= 64   ? shape(std::integral_constant<int, 2>())
+                 : a.d <= 96 ? shape(std::integral_constant<int, 3>())
+                             : shape(std::integral_constant<int, 4>());
+    if (st || a.splits == 1) return st;
+    const uint64_t rows = a.seq_q ? a.len_q : (uint64_t)a.batch * a.len_q;
+    hipLaunchKernelGGL(attn_join_kernel<T>, dim3((uint32_t)((rows * a.hq + 3) / 4)), dim3(256), 0, s, a, rows);
+    return launch_status();
+  });
+}
+
+}  // namespace sdc

@@ -1,5 +1,5 @@
-// gemm_device.h -- the matrix-product tile of the cross-entropy head for
-// gfx950: C[m][n] = sum_k A(m, k) B(n, k) for 16-bit operands whose rows are
+// gemm_device.h -- the matrix-product tile of the cross-entropy head and the gated
+// feed-forward block for gfx950: C[m][n] = sum_k A(m, k) B(n, k) for 16-bit operands whose rows are
 // contiguous either in k or, "k-major", in m (n), accumulated in fp32 by MFMA.
 //
 // A workgroup computes an M x N tile of C (a Shape): 256 x 256 by 8 waves, 128 x
@@ -69,6 +69,7 @@ struct Bf16 {
   static __device__ __forceinline__ uint32_t bits(float x) {
     return __builtin_bit_cast(unsigned short, (__bf16)x);
   }
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
 };
 
 struct Fp16 {
@@ -81,6 +82,9 @@ struct Fp16 {
   static __device__ __forceinline__ uint32_t bits(float x) {
     return __builtin_bit_cast(unsigned short, (_Float16)x);
   }
+  static __device__ __forceinline__ float value(uint32_t bits) {
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+  }
 };
 
 // An operand with `rows` rows (of C's index, or, k-major, of k), `stride` bytes
@@ -91,6 +95,24 @@ struct Operand {
   uint64_t stride;
   uint32_t rows, cols;
 };
+
+// Two matrices as one operand A: rows in turns of 16, one's rows 16 k .. 16 k + 15
+// and then the other's, so that the groups 2 i and 2 i + 1 of a wave hold the same
+// rows of the two.
+struct Paired {
+  Operand a, b;
+};
+
+// Address of row `r` of a tile whose first row is at0; rows past the last are the last.
+__device__ __forceinline__ const unsigned char* row_of(const Operand& o, uint32_t at0, uint32_t r) {
+  return o.p + (uint64_t)min(at0 + r, o.rows - 1u) * o.stride;
+}
+__device__ __forceinline__ const unsigned char* row_of(const Paired& o, uint32_t at0, uint32_t r) {
+  const uint32_t row = min(((at0 + r) >> 5) * 16u + (r & 15u), o.a.rows - 1u);
+  return r & 16u ? o.b.p + (uint64_t)row * o.b.stride : o.a.p + (uint64_t)row * o.a.stride;
+}
+__device__ __forceinline__ uint32_t cols_of(const Operand& o) { return o.cols; }
+__device__ __forceinline__ uint32_t cols_of(const Paired& o) { return o.a.cols; }
 
 // Where a thread's accumulators stand in the tile: element r of acc[i][j] is
 // C[row(i) + r][col(j)].
@@ -172,7 +194,8 @@ struct Side {
   // at0: first row of C's index; base: LDS row (rows along k) or granule
   // (k-major) of the wave's first group.  Rows along k past the operand's last
   // are read as the last, chunks past a k-major one's columns as its last eight.
-  __device__ __forceinline__ void init(const Operand& o, uint32_t at0, uint32_t base, uint32_t k0) {
+  template <class O>
+  __device__ __forceinline__ void init(const O& o, uint32_t at0, uint32_t base, uint32_t k0) {
     const uint32_t t = threadIdx.x, lane = t & 63u;
     if constexpr (KMAJOR) {
       limit = o.rows;
@@ -189,13 +212,13 @@ struct Side {
       const uint32_t g = lane >> 4, r = (lane >> 2) & 3u, f = r | g << 2;
       off = (8u * g + r) * kRow + ((base ^ (f & kGranules)) << 5) + (lane & 3u) * 8u;
     } else {
-      limit = o.cols;
+      limit = cols_of(o);
       const uint32_t q = (t & 7u) ^ ((t >> 3) & 7u);
       k_in = q * 8u;
       step = kTileK * 2u;
 #pragma unroll
       for (uint32_t i = 0; i < kLoads; ++i)
-        p[i] = o.p + (uint64_t)min(at0 + i * (THREADS / 8) + (t >> 3), o.rows - 1u) * o.stride + (uint64_t)(k0 + k_in) * 2u;
+        p[i] = row_of(o, at0, i * (THREADS / 8) + (t >> 3)) + (uint64_t)(k0 + k_in) * 2u;
       off = (base + (lane & 15u)) * 128u + (((lane >> 4) ^ (lane & 7u)) << 4);
     }
   }
@@ -304,8 +327,8 @@ __device__ __forceinline__ void gemm_step(const SA& sa, const SB& sb, const unsi
 // for: three steps (four in the 64-row tile) of both operands are in flight, in
 // registers, of which there are plenty.  Same operations in the same order, so the same bits.  k1 is where
 // the operands end.
-template <class T, class S>
-__device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
+template <class T, class S, class OA>
+__device__ __forceinline__ void gemm_tile_deep(const OA& A, const Operand& B, uint32_t m0, uint32_t n0,
                                                uint32_t k0, uint32_t k1, unsigned char* lds,
                                                f32x4 (&acc)[S::I][S::J]) {
   const Place<S> at;
@@ -351,13 +374,13 @@ __device__ __forceinline__ void gemm_tile_deep(const Operand& A, const Operand& 
 
 // Sum over k in [k0, k1) (k0 a multiple of 64) of the tile at row m0 of A's
 // index and n0 of B's.  What the tile holds past either's last means nothing.
-// AAT: how A's rows lie; B's lie at 16-byte boundaries.
-template <class T, class S, RowsAt AAT, bool AK, bool BK>
-__device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, uint32_t m0, uint32_t n0,
+// AAT: how A's rows lie; B's lie at 16-byte boundaries.  ADD: onto what acc holds.
+template <class T, class S, RowsAt AAT, bool AK, bool BK, bool ADD = false, class OA = Operand>
+__device__ __forceinline__ void gemm_tile(const OA& A, const Operand& B, uint32_t m0, uint32_t n0,
                                           uint32_t k0, uint32_t k1, unsigned char* lds,
                                           f32x4 (&acc)[S::I][S::J]) {
   if constexpr (AAT == kDeep) {
-    static_assert(!AK && !BK, "rows along k");
+    static_assert(!AK && !BK && !ADD, "rows along k, a whole sum");
     gemm_tile_deep<T, S>(A, B, m0, n0, k0, k1, lds, acc);
   } else {
     const Place<S> at;
@@ -366,10 +389,12 @@ __device__ __forceinline__ void gemm_tile(const Operand& A, const Operand& B, ui
     sa.init(A, m0, at.wm * (S::M / S::WM) / (AK ? 16u : 1u), k0);
     sb.init(B, n0, at.wn * (S::N / S::WN) / (BK ? 16u : 1u), k0);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    if constexpr (!ADD) {
 #pragma unroll
-    for (int i = 0; i < S::I; ++i)
+      for (int i = 0; i < S::I; ++i)
 #pragma unroll
-      for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < S::J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     u32x4 ha[sa.kLoads], hb[sb.kLoads];  // ha: kAny, A's loads of the next step; hb is not used
     const auto fill = [&](uint32_t k, uint32_t buf) {
       sa.fill(k, lds0 + buf * S::kBuf, ha);

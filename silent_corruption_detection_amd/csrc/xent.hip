@@ -32,19 +32,7 @@ namespace sdc {
 namespace {
 
 // ---- copies of operands ---------------------------------------------------------
-// Copies the R x C matrix src (rows `stride` bytes apart, elements at any even
-// address) to dst [R][c_pad], zeros from column C on.  mask: rows whose target
-// is outside [0, vocab) become zeros, whatever they hold.  A wave copies part of a
-// row; 4096 x 2048 takes 8.3 us (4 TB/s).
-struct PackArgs {
-  const unsigned char* src;
-  uint64_t stride;
-  uint32_t R, C, c_pad;
-  uint16_t* dst;
-  const int64_t* mask;
-  uint64_t vocab;
-};
-
+// A wave copies part of a row; 4096 x 2048 takes 8.3 us (4 TB/s).
 constexpr uint32_t kPackCols = 2048;  // of one wave: four loads of 16 bytes in flight
 
 template <bool VEC>
@@ -75,6 +63,8 @@ __global__ void __launch_bounds__(kBlock) pack_kernel(const PackArgs a) {
   }
 }
 
+}  // namespace
+
 int32_t launch_pack(const PackArgs& a, hipStream_t s) {
   const bool vec = a.C % 8 == 0 && a.stride % 16 == 0 && reinterpret_cast<uintptr_t>(a.src) % 16 == 0;
   const dim3 grid((a.R + kWaves - 1) / kWaves, (a.c_pad + kPackCols - 1) / kPackCols);
@@ -82,6 +72,8 @@ int32_t launch_pack(const PackArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL(pack_kernel<false>, grid, dim3(kBlock), 0, s, a);
   return launch_status();
 }
+
+namespace {
 
 // ---- dx's sum ---------------------------------------------------------------------
 // dx = grad * the splits' sum, in split order; 0 for rows without a target.
@@ -241,48 +233,21 @@ __global__ void __launch_bounds__(256) zero16_kernel(uint16_t* p, uint64_t n) {
   for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < n; i += gridDim.x * 256ull) p[i] = 0;
 }
 
-// ---- host ----------------------------------------------------------------------------
-constexpr uint64_t kPieceBytes = 256ull << 20;  // of the gradient's workspace that grows with the piece
+}  // namespace
 
-// CUs that the rules below fill.  The MI355X' number, not the current device's: tiles,
-// pieces and splits follow from the sizes alone, so the results' bits and the
-// workspace (asked for without a device) are the same on a part of the chip.
-constexpr uint32_t kCus = 256;
-
-constexpr uint64_t up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
-
-struct Head {
-  uint32_t N, d, V, d_pad;
-  uint32_t tile, vtile;  // tokens (256, 128, 64 or kFew) and vocabulary rows of the logits' tiles
-  uint32_t nt, vt;       // tiles of the tokens, of the whole vocabulary
-  uint32_t ptile;        // 256 or 128, of the gradient's products
-  bool copy_x, copy_w;   // the operand needs an aligned copy
-  bool any;              // w's rows are read where they lie, off 16-byte boundaries
-  uint32_t piece;        // vocabulary rows of a piece
-  uint32_t pieces;
-  uint32_t splits;       // of dx's sum over a piece
-  uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
-};
-
-// Tokens of the tiles for few of them.
-constexpr uint32_t kFew = FewTile::N;
-
-uint32_t tiles(uint64_t n, uint32_t tile) { return (uint32_t)((n + tile - 1) / tile); }
-
-int32_t check_head(const sdc_head* h) {
-  if (h == nullptr) return SDC_ERR_INVALID;
-  if (h->dtype != SDC_BF16 && h->dtype != SDC_F16) return SDC_ERR_DTYPE;
-  if (h->d == 0 || h->vocab == 0 || h->flags != 0) return SDC_ERR_INVALID;
-  if (h->n > 0 && (h->x == nullptr || h->target == nullptr)) return SDC_ERR_INVALID;
-  if (h->w == nullptr || h->x_stride < h->d || h->w_stride < h->d) return SDC_ERR_INVALID;
-  if (reinterpret_cast<uintptr_t>(h->x) % 2 || reinterpret_cast<uintptr_t>(h->w) % 2 ||
-      reinterpret_cast<uintptr_t>(h->target) % 8)
-    return SDC_ERR_ALIGN;
-  if (h->n >= 1ull << 24 || h->d >= 1ull << 20 || h->vocab >= 1ull << 24 || h->x_stride >= 1ull << 40 ||
-      h->w_stride >= 1ull << 40 || (uint64_t)tiles(h->n, 256) * (tiles(h->vocab, 256) + 4096) >= 1ull << 31)
-    return SDC_ERR_RANGE;
-  return SDC_OK;
+int32_t launch_merge_tile_rows(const sdc_row* parts, uint32_t n, const sdc_row* ref, uint32_t col_mask, sdc_row* row,
+                               uint32_t* mismatch, hipStream_t s) {
+  hipLaunchKernelGGL(logit_row_kernel, dim3(1), dim3(64), 0, s, parts, n, ref, col_mask, row, mismatch);
+  return launch_status();
 }
+
+int32_t launch_zero16(uint16_t* p, uint64_t n, hipStream_t s) {
+  hipLaunchKernelGGL(zero16_kernel, dim3(1024), dim3(256), 0, s, p, n);
+  return launch_status();
+}
+
+// ---- host ----------------------------------------------------------------------------
+uint32_t tiles(uint64_t n, uint32_t tile) { return (uint32_t)((n + tile - 1) / tile); }
 
 // The tile of the logits' product, from the rounds that the CUs take: a tile has
 // the work of its share of a 256 x 256 one at 1.15 times the cost for 128 x 128
@@ -313,6 +278,38 @@ uint32_t logit_tile(uint64_t n, uint64_t vocab) {
 // 24000 40 / 47, 10 x 4096 x 32768 48 / 46, 19 x 836 x 49450 28 / 26.
 uint32_t few_rows(uint64_t vocab) { return tiles(vocab, FewTile::M) < kCus ? FewTinyTile::M : FewTile::M; }
 
+namespace {
+
+constexpr uint64_t kPieceBytes = 256ull << 20;  // of the gradient's workspace that grows with the piece
+
+struct Head {
+  uint32_t N, d, V, d_pad;
+  uint32_t tile, vtile;  // tokens (256, 128, 64 or kFew) and vocabulary rows of the logits' tiles
+  uint32_t nt, vt;       // tiles of the tokens, of the whole vocabulary
+  uint32_t ptile;        // 256 or 128, of the gradient's products
+  bool copy_x, copy_w;   // the operand needs an aligned copy
+  bool any;              // w's rows are read where they lie, off 16-byte boundaries
+  uint32_t piece;        // vocabulary rows of a piece
+  uint32_t pieces;
+  uint32_t splits;       // of dx's sum over a piece
+  uint32_t n_tiles;      // logit tiles over the whole vocabulary, piece by piece
+};
+
+int32_t check_head(const sdc_head* h) {
+  if (h == nullptr) return SDC_ERR_INVALID;
+  if (h->dtype != SDC_BF16 && h->dtype != SDC_F16) return SDC_ERR_DTYPE;
+  if (h->d == 0 || h->vocab == 0 || h->flags != 0) return SDC_ERR_INVALID;
+  if (h->n > 0 && (h->x == nullptr || h->target == nullptr)) return SDC_ERR_INVALID;
+  if (h->w == nullptr || h->x_stride < h->d || h->w_stride < h->d) return SDC_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(h->x) % 2 || reinterpret_cast<uintptr_t>(h->w) % 2 ||
+      reinterpret_cast<uintptr_t>(h->target) % 8)
+    return SDC_ERR_ALIGN;
+  if (h->n >= 1ull << 24 || h->d >= 1ull << 20 || h->vocab >= 1ull << 24 || h->x_stride >= 1ull << 40 ||
+      h->w_stride >= 1ull << 40 || (uint64_t)tiles(h->n, 256) * (tiles(h->vocab, 256) + 4096) >= 1ull << 31)
+    return SDC_ERR_RANGE;
+  return SDC_OK;
+}
+
 // Parts that dx's sum over `rows` vocabulary rows is split into: a tile for each CU.
 uint32_t dx_splits(uint64_t n, uint64_t d, uint64_t rows, uint32_t tile) {
   const uint32_t per = tiles(n, tile) * tiles(d, tile);
@@ -337,9 +334,6 @@ uint32_t product_tile(uint64_t n, uint64_t d, uint64_t rows) {
   };
   return 0.575 * steps(128) < steps(256) ? 128u : 256u;
 }
-
-// Tiles of one launch: a grid has fewer than 2^32 threads.
-constexpr uint32_t kLaunchTiles = 1u << 22;
 
 // grad: the sizes of the gradient's pieces; else those of the forward pass,
 // which needs pieces only for more than kLaunchTiles tiles (a copy of w, 16
@@ -445,9 +439,7 @@ int32_t piece_operands(const sdc_head* h, const Head& p, const Layout& o, unsign
 
 int32_t merge_logit_row(const Layout& o, const Head& p, unsigned char* ws, const sdc_row* ref, uint32_t mask,
                         sdc_row* row, uint32_t* mismatch, hipStream_t s) {
-  hipLaunchKernelGGL(logit_row_kernel, dim3(1), dim3(64), 0, s, reinterpret_cast<const sdc_row*>(ws + o.rows),
-                     p.n_tiles, ref, mask, row, mismatch);
-  return launch_status();
+  return launch_merge_tile_rows(reinterpret_cast<const sdc_row*>(ws + o.rows), p.n_tiles, ref, mask, row, mismatch, s);
 }
 
 }  // namespace
@@ -542,10 +534,7 @@ extern "C" int32_t sdc_cross_entropy_grad(const sdc_head* h, const float* d_lse,
   hipStream_t s = as_stream(stream);
   unsigned char* ws = static_cast<unsigned char*>(d_ws);
   if (p.N == 0) {
-    if (d_dw)
-      hipLaunchKernelGGL(zero16_kernel, dim3(1024), dim3(256), 0, s, static_cast<uint16_t*>(d_dw),
-                         (uint64_t)p.V * p.d);
-    if ((st = launch_status())) return st;
+    if (d_dw && (st = launch_zero16(static_cast<uint16_t*>(d_dw), (uint64_t)p.V * p.d, s))) return st;
     return d_row ? merge_logit_row(o, p, ws, d_ref, col_mask, d_row, d_mismatch, s) : SDC_OK;
   }
   // x without what rows that have no target hold: dz is zero there, but 0 * NaN is not

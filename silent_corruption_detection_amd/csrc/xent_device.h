@@ -4,11 +4,7 @@
 // few rows of x (csrc/xent_few.hip).
 #pragma once
 
-#include <algorithm>
-#include <type_traits>
-
-#include "fingerprint_device.h"
-#include "gemm_device.h"
+#include "tile_device.h"
 
 namespace sdc {
 
@@ -62,16 +58,6 @@ int32_t launch_products_any(const HeadLaunch& h, const ProductArgs& x, hipStream
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-// 16-bit elements of a staged row of M, padded off the banks
-template <class S>
-constexpr uint32_t stage_row() { return S::M + 8; }
-template <class S>
-constexpr uint32_t lds_bytes() { return std::max(S::kLds, S::N * stage_row<S>() * 2); }
-static_assert(lds_bytes<BigTile>() + 1024 <= 160u * 1024u, "one workgroup fits a CU");
-
-typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
-
 __device__ __forceinline__ bool has_target(int64_t t, uint64_t vocab) { return (uint64_t)t < vocab; }
 
 // exp(x).  What it is called for is a difference of logits, taken before the
@@ -123,29 +109,7 @@ __device__ __forceinline__ void tile_row(const f32x4 (&acc)[S::I][S::J], const L
     ln.s += s;
     ln.w += ws + ((uint64_t)n * a.vocab + a.v0 + m0 + at.row(0) + 1u) * s;
   }
-  wave_reduce(ln);
-  constexpr int kW = S::kThreads / 64;
-  __shared__ uint64_t waves[4][kW];
-  const uint32_t wave = threadIdx.x >> 6;
-  if (at.lane == 0) {
-    waves[0][wave] = ln.s;
-    waves[1][wave] = ln.w;
-    waves[2][wave] = ln.x;
-    waves[3][wave] = ln.nf;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int i = 1; i < kW; ++i) {
-      ln.s += waves[0][i];
-      ln.w += waves[1][i];
-      ln.x ^= waves[2][i];
-      ln.nf += waves[3][i];
-    }
-    ulonglong2* d = reinterpret_cast<ulonglong2*>(out);
-    d[0] = ulonglong2{ln.s, ln.w};
-    d[1] = ulonglong2{ln.x, ln.nf};
-  }
+  store_tile_row<S::kThreads / 64>(ln, out);
 }
 
 // Maximum m and sum of exp(z - m) of each token over the tile's vocabulary rows:
@@ -328,12 +292,7 @@ __device__ __forceinline__ void dw_tile(const ProductArgs& a, uint32_t id, unsig
     const uint32_t v = n0 + k, c = m0 + ch;
     if (v >= a.rows || c >= a.d) continue;
     uint16_t* p = a.dw + (uint64_t)v * a.d + c;
-    const uint16_t* s = st + k * stage_row<S>() + ch;
-    if (c + 8u <= a.d) {
-      *reinterpret_cast<u32x4_at2*>(p) = *reinterpret_cast<const u32x4*>(s);
-    } else {
-      for (uint32_t e = 0; c + e < a.d; ++e) p[e] = s[e];
-    }
+    store8(p, st + k * stage_row<S>() + ch, a.d - c);
   }
 }
 
@@ -347,12 +306,6 @@ __global__ void __launch_bounds__(S::kThreads) products_kernel(const ProductArgs
   extern __shared__ __align__(16) unsigned char lds[];
   if (blockIdx.x < a.n_dx) dx_tile<T, S, AT>(a, xcd_run(blockIdx.x, a.n_dx, a.xcds), lds);
   else dw_tile<T, S>(a, xcd_run(blockIdx.x - a.n_dx, a.n_dw, a.xcds), lds);
-}
-
-// f(type)
-template <class F>
-int32_t for_dtype(uint32_t dtype, F&& f) {
-  return dtype == SDC_BF16 ? f(Bf16()) : f(Fp16());
 }
 
 // f(type, shape) of the logits' product; tile: rows of the shape.  kDeep has the
