@@ -664,7 +664,9 @@ int32_t sdc_attention(const sdc_attn* h_attn, void* d_ws, uint64_t ws_bytes, voi
  * pass' d_out and d_lse.  With p = exp(scale q k^T - lse), delta = sum dout out:
  *   d_dv = p^T dout   dz = p (dout v^T - delta)   d_dq = scale dz k   d_dk = scale dz^T q
  * contiguous [rows][heads][d], of the dtype, summed in fp32 from p and dz rounded to its
- * precision; the gradients of a head of keys are its query heads' sums.  d_dq, or d_dk and
+ * precision; the gradients of a head of keys are its query heads' sums.  d_lse as an fp32
+ * number is off by up to |lse| 2^-24, and p by that factor, as fp32 scores of that size are
+ * themselves.  d_dq, or d_dk and
  * d_dv, may be NULL and are then not computed.  d_row: as there, of the recomputed scores;
  * with d_ref (the forward pass' row) a difference under col_mask adds 1 to *d_mismatch
  * (required then; the caller clears it), for each of the two launches that compute

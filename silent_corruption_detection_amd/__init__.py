@@ -1117,10 +1117,10 @@ def _attn(q, k, v, causal, window, scale, seq_q, seq_k):
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [batch, rows, heads, d], or [rows, heads, d] with seq_q and seq_k")
     dims = q.dim()
-    kept = [_attn_rows(t, n, dims) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    dev = _cuda_device(q.get_device())
     if (seq_q is None) != (seq_k is None) or (seq_q is None) != (dims == 4):
         raise ValueError("packed sequences need 3-D tensors and both seq_q and seq_k, a batch 4-D ones and neither")
+    kept = [_attn_rows(t, n, dims) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    dev = _cuda_device(q.get_device())
     for t, n in ((k, "k"), (v, "v")):
         if t.dtype != q.dtype or not _on_device(t, dev):
             raise ValueError(f"{n} must be {q.dtype} on {dev}, is {t.dtype} on {t.device}")

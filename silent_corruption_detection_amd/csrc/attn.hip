@@ -303,7 +303,8 @@ extern "C" int32_t sdc_attention_grad(const sdc_attn* h, const void* d_out, cons
   int32_t st = check_attn(h);
   if (st) return st;
   const Attn p = plan_attn(h);
-  if (d_ws == nullptr || (d_dk == nullptr) != (d_dv == nullptr) || (d_dq == nullptr && d_dk == nullptr) ||
+  if (d_ws == nullptr || (d_dk == nullptr) != (d_dv == nullptr) ||
+      (p.rows_q > 0 && p.rows_k > 0 && d_dq == nullptr && d_dk == nullptr) ||
       (p.rows_q > 0 && (d_out == nullptr || d_lse == nullptr || d_dout == nullptr)))
     return SDC_ERR_INVALID;
   if (d_ref != nullptr && (d_row == nullptr || d_mismatch == nullptr || col_mask == 0 || (col_mask & ~15u)))

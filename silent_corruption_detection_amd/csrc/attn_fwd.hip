@@ -4,20 +4,28 @@
 namespace sdc {
 namespace {
 
+// lse from the largest score (or one near it) and the sum of exponentials less its reference.
+__device__ __forceinline__ float log_sum(float top, float scale, float sum, float off) {
+  return __builtin_fmaf(top, scale, (__builtin_amdgcn_logf(sum) - off) * kLn2);
+}
+
 // A workgroup of W waves takes 32 QB W queries of a head of keys, a wave 32 QB of them,
 // and streams the keys they attend past them in tiles of 64 (two buffers in LDS, the next
 // filled by direct loads while this one is multiplied).  The queries stay in registers, as
 // do the sums of values: out^T = V^T P^T with a query per lane, so its rescaling is one
 // factor a lane.
 //
-// The softmax runs on exponents z c = s scale log2(e), less a reference that a query
-// raises only when a tile's maximum passes it by more than 8: probabilities are then at
-// most 2^8, sums in fp32 are none the worse, and most tiles rescale nothing.  p =
-// exp2(s c - ref) as one fused operation is off by the rounding of ref alone, which is
-// ref itself: a factor that out and lse = (ref + log2 l) ln 2 share.  From |ref| of 2^20
-// on (SPLIT apart) the product's own rounding would show, and the difference of scores is taken first.
+// The softmax runs on exponents s c, c = scale log2(e), less a reference: base, the rounded
+// product of c and a score m that a query raises only when a tile's maximum passes it by
+// more than 8 / c.  Probabilities are then at most 2^8, sums in fp32 are none the worse, and
+// most tiles rescale nothing.  s c - base is one fused operation, exact but for its own
+// rounding, so that base's rounding is no error but a factor 2^d, d = m c - base, that out's
+// sums and l share.  From |base| of 2^27 on (kFarOut) that factor could overflow: there the
+// difference of scores comes first and the reference is m c itself.
 //
-// SPLIT: the keys in a.splits parts, each leaving its unscaled sums, ref and l.
+// SPLIT: the keys in a.splits parts, each leaving its unscaled sums, m and l.
+constexpr float kFarOut = 0x1p27f;
+
 template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
@@ -50,11 +58,11 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
       t1 = min(t0 + each, t1);
     }
     f32x16 o[QB][DB];
-    float ref[QB], l[QB];
+    float top[QB], base[QB], off[QB], l[QB];  // m, base, d (0 far out) and the sum of exponentials
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-      ref[b] = -__builtin_inff();
-      l[b] = 0.0f;
+      top[b] = -__builtin_inff();
+      base[b] = off[b] = l[b] = 0.0f;
 #pragma unroll
       for (int m = 0; m < DB; ++m)
 #pragma unroll
@@ -128,35 +136,38 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
       }
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
-        float top = s[b][0][0];
+        float most = s[b][0][0];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[b][n][e]);
-        top = both_max(top) * a.c;
-        if (__any(top > ref[b] + 8.0f)) {
-          const float was = ref[b];
-          ref[b] = __builtin_fmaxf(was, top);
-          const float f = was == ref[b] ? 1.0f : __builtin_amdgcn_exp2f(was - ref[b]);
+          for (int e = 0; e < 16; ++e) most = __builtin_fmaxf(most, s[b][n][e]);
+        most = both_max(most);
+        if (__any(most > top[b] + 8.0f / a.c)) {
+          const float was = top[b], before = off[b];
+          top[b] = __builtin_fmaxf(was, most);
+          base[b] = top[b] == -__builtin_inff() ? 0.0f : top[b] * a.c;
+          off[b] = top[b] != -__builtin_inff() && __builtin_fabsf(base[b]) < kFarOut
+                       ? __builtin_fmaf(top[b], a.c, -base[b]) : 0.0f;
+          const float f =
+              was == top[b] ? 1.0f : __builtin_amdgcn_exp2f((was - top[b]) * a.c - before + off[b]);
           l[b] *= f;
 #pragma unroll
           for (int m = 0; m < DB; ++m)
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[b][m][e] *= f;
         }
-        const float base = ref[b] == -__builtin_inff() ? 0.0f : ref[b];
-        if (!__any(__builtin_fabsf(base) >= 0x1p20f)) {
+        if (!__any(__builtin_fabsf(base[b]) >= kFarOut)) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              s[b][n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][n][e], a.c, -base));
+              s[b][n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][n][e], a.c, -base[b]));
         } else {
-          const float score = base / a.c;
+          const float m = top[b] == -__builtin_inff() ? 0.0f : top[b];
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[b][n][e] = __builtin_amdgcn_exp2f((s[b][n][e] - score) * a.c);
+            for (int e = 0; e < 16; ++e) s[b][n][e] = __builtin_amdgcn_exp2f((s[b][n][e] - m) * a.c + off[b]);
         }
         float sum = 0.0f;
 #pragma unroll
@@ -192,7 +203,8 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
       if (r >= R) continue;
       if constexpr (SPLIT) {
         const uint64_t row = grouped_row(a, p, r) * a.splits + split;
-        if (half == 0) a.part_ml[row] = float2{ref[b], sum};
+        const float f = __builtin_amdgcn_exp2f(-off[b]);  // from base to m c
+        if (half == 0) a.part_ml[row] = float2{top[b], sum * f};
         float* out = a.part + row * a.d;
 #pragma unroll
         for (int m = 0; m < DB; ++m)
@@ -201,14 +213,14 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
             const uint32_t e = 32u * m + 8u * g + 4u * half;
             if (e < a.d)
               *reinterpret_cast<f32x4*>(out + e) =
-                  f32x4{o[b][m][4 * g], o[b][m][4 * g + 1], o[b][m][4 * g + 2], o[b][m][4 * g + 3]};
+                  f32x4{o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f, o[b][m][4 * g + 3] * f};
           }
       } else {
         // a query that attends nothing: out 0, lse -inf
-        const bool none = ref[b] == -__builtin_inff() && !(sum != sum);
+        const bool none = top[b] == -__builtin_inff() && !(sum != sum);
         const float f = none ? 0.0f : 1.0f / sum;
         const uint64_t row = flat_row(a, p, r);
-        if (half == 0) a.lse[row] = none ? -__builtin_inff() : (ref[b] + __builtin_amdgcn_logf(sum)) * kLn2;
+        if (half == 0) a.lse[row] = none ? -__builtin_inff() : log_sum(top[b], a.scale, sum, off[b]);
         uint16_t* out = a.out + row * a.d;
 #pragma unroll
         for (int m = 0; m < DB; ++m)
@@ -225,7 +237,7 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
   if constexpr (ROW) store_tile_row<W>(ln, a.rows + blockIdx.x);
 }
 
-// Joins the splits of a row: out = sum_k 2^(ref_k - ref) o_k / sum_k 2^(ref_k - ref) l_k, in
+// Joins the splits of a row: out = sum_k f_k o_k / sum_k f_k l_k with f_k = 2^((m_k - m) c), in
 // split order.  A wave per row; rows outside every sequence have none.
 template <class T>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, uint64_t rows) {
@@ -236,22 +248,22 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, uint64
   const uint32_t head = (uint32_t)(n % a.hq);
   if (a.seq_q && !in_sequences(a.seq_q, a.batch, a.len_q, (uint32_t)row)) return;
   const uint64_t at = ((head / a.G) * rows * a.G + row * a.G + head % a.G) * a.splits;
-  float ref = -__builtin_inff(), sum = 0.0f;
-  for (uint32_t k = 0; k < a.splits; ++k) ref = __builtin_fmaxf(ref, a.part_ml[at + k].x);
-  const float base = ref == -__builtin_inff() ? 0.0f : ref;
+  float top = -__builtin_inff(), sum = 0.0f;
+  for (uint32_t k = 0; k < a.splits; ++k) top = __builtin_fmaxf(top, a.part_ml[at + k].x);
+  const float m = top == -__builtin_inff() ? 0.0f : top;
   float x[2] = {0.0f, 0.0f};
 #pragma unroll 4
   for (uint32_t k = 0; k < a.splits; ++k) {
     const float2 ml = a.part_ml[at + k];
-    const float f = __builtin_amdgcn_exp2f(ml.x - base);
+    const float f = __builtin_amdgcn_exp2f((ml.x - m) * a.c);
     sum += ml.y * f;
     const float* part = a.part + (at + k) * a.d;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (lane + 64u * i < a.d) x[i] += part[lane + 64u * i] * f;
   }
-  const bool none = ref == -__builtin_inff() && !(sum != sum);
-  if (lane == 0) a.lse[n] = none ? -__builtin_inff() : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
+  const bool none = top == -__builtin_inff() && !(sum != sum);
+  if (lane == 0) a.lse[n] = none ? -__builtin_inff() : log_sum(top, a.scale, sum, 0.0f);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     if (lane + 64u * i < a.d) a.out[n * a.d + lane + 64u * i] = (uint16_t)T::bits(none ? 0.0f : x[i] / sum);

@@ -227,7 +227,7 @@ extern "C" int32_t sdc_gated_ffn_grad(const sdc_ffn* b, const void* d_dh, uint64
                                       sdc_stream_t stream) {
   int32_t st = check_ffn(b);
   if (st) return st;
-  if (d_ws == nullptr || (d_dx == nullptr && d_dw_gate == nullptr) || (d_dw_gate == nullptr) != (d_dw_up == nullptr) ||
+  if (d_ws == nullptr || (b->n > 0 && d_dx == nullptr && d_dw_gate == nullptr) || (d_dw_gate == nullptr) != (d_dw_up == nullptr) ||
       (b->n > 0 && d_dh == nullptr) || dh_stride < b->f)
     return SDC_ERR_INVALID;
   if (d_ref != nullptr && (d_row == nullptr || d_mismatch == nullptr || col_mask == 0 || (col_mask & ~15u)))

@@ -28,12 +28,15 @@ A segment that was not recomputed is reported in `result()["not_recomputed"]`.
 with a large vocabulary: the loss of a linear head whose logits are computed in
 the forward pass, never kept, and computed again in the backward pass.  Both
 passes fingerprint them where they are computed; a difference is counted and
-reported like any other segment's.
+reported like any other segment's.  `RecomputeAudit.attention` and
+`RecomputeAudit.gated_ffn` are the same for the halves of a block whose scores and
+projections their backward passes compute again.
 """
 import torch
 
 from . import (COL_ALL, _current_stream_handle, rows_numpy, sdc_fingerprint_diff, sdc_fingerprint_tensor,
                sdc_tensor_ws_bytes)
+from .block import attention, gated_ffn
 from .loss import linear_cross_entropy
 
 
@@ -123,6 +126,25 @@ class RecomputeAudit:
         loss.linear_cross_entropy): the fingerprint row of its logits is stored,
         and compared when the backward pass computes them again, which has to be
         in the same step (a backward pass after the next begin_step() is refused)."""
+        return self._recomputing(k, lambda row, checked: linear_cross_entropy(x, w, target, reduction, row, checked))
+
+    def attention(self, k, q, key, value, causal=False, window=0, scale=None, seq_q=None, seq_k=None):
+        """Softmax attention as segment k (see block.attention): its scores' fingerprint
+        row is stored, and compared when the backward pass computes them again, which has to
+        be in the same step.  A call inside a checkpointed function runs twice in a step:
+        audit that function with wrap() instead."""
+        return self._recomputing(k, lambda row, checked: attention(q, key, value, causal, window, scale, seq_q, seq_k,
+                                                                   row, checked))
+
+    def gated_ffn(self, k, x, w_gate, w_up, act="silu"):
+        """The gated feed-forward block as segment k (see block.gated_ffn): as attention,
+        with both projections' row."""
+        return self._recomputing(k, lambda row, checked: gated_ffn(x, w_gate, w_up, act, row, checked))
+
+    def _recomputing(self, k, run):
+        """run(row, checked) as segment k: an operator that leaves the row of what it
+        computes in `row` and, when its backward pass computes that again, compares under
+        the arguments that checked() returns."""
         if not 0 <= k < self.n:
             raise IndexError(f"segment {k} out of range 0..{self.n - 1}")
         if self.calls[k]:
@@ -139,9 +161,9 @@ class RecomputeAudit:
             return dict(row=self._recomputed_rows[r], ref=self._original_rows[r], mismatch=self._mismatch_at[k],
                         col_mask=self.col_mask)
 
-        loss = linear_cross_entropy(x, w, target, reduction, row=self._original_rows[r], checked=checked)
+        out = run(self._original_rows[r], checked)
         self.calls[k] = 1
-        return loss
+        return out
 
     def result(self):
         """After backward (synchronises): segments whose recomputation differed
