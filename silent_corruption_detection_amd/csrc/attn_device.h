@@ -57,7 +57,7 @@ struct AttnArgs {
 
 struct AttnLaunch {
   uint32_t dtype;
-  uint32_t waves;  // of 32 queries (keys, for dk and dv)
+  uint32_t waves, blocks;  // waves of a workgroup, blocks of 32 queries of a wave
 };
 int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
 int32_t launch_attn_dq(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
@@ -102,13 +102,9 @@ __device__ __forceinline__ float both_sum(float x) {
 // Elements 8 h .. 8 h + 7 of a result as an operand, rounded to nearest.
 template <class T>
 __device__ __forceinline__ typename T::frag operand(const f32x16& x, int h) {
-  union {
-    uint32_t w[4];
-    typename T::frag f;
-  } u;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) u.w[i] = T::bits(x[8 * h + 2 * i]) | T::bits(x[8 * h + 2 * i + 1]) << 16;
-  return u.f;
+  typedef float f32x8 __attribute__((ext_vector_type(8)));
+  const f32x8 y = {x[8 * h], x[8 * h + 1], x[8 * h + 2], x[8 * h + 3], x[8 * h + 4], x[8 * h + 5], x[8 * h + 6], x[8 * h + 7]};
+  return __builtin_convertvector(y, typename T::frag);
 }
 
 // ---- sequences -------------------------------------------------------------------
@@ -395,32 +391,26 @@ __device__ __forceinline__ bool tile_nonfinite(const unsigned char* tile) {
   return __any((bad & 0x80008000u) != 0u);
 }
 
-// acc[m] += X^T P for 32 rows (block b) of a tile that holds infinities or NaN, over the
-// pairs that attend only: zero times what a masked row holds is not zero.  Rare, so row by
-// row.  has: bit r: element r of the lane's column attends.
-template <class T, int DB>
-__device__ __forceinline__ void product_by_rows(f32x16 (&acc)[DB], const unsigned char* tile, int b, const f32x16& p,
-                                             uint32_t has) {
-  const uint32_t lane = threadIdx.x & 63u, half = lane >> 5;
-  for (int r = 0; r < 16; ++r) {
-    float mine = 0.0f;
+// sum_e x_e y_e of two rows.
+template <class T>
+__device__ __forceinline__ float dot_rows(const unsigned char* x, const unsigned char* y, uint32_t d) {
+  float s = 0.0f;
+  for (uint32_t e = 0; e < d; e += 8) {
+    const u32x4 u = *reinterpret_cast<const u32x4*>(x + 2u * e), v = *reinterpret_cast<const u32x4*>(y + 2u * e);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mine = i == r ? T::value(T::bits(p[i])) : mine;
-    for (uint32_t h = 0; h < 2; ++h) {
-      const float x = __shfl(mine, (lane & 31u) + 32u * h);
-      const bool on = __shfl(has, (lane & 31u) + 32u * h) >> r & 1u;
-      const uint32_t row = 32u * b + element_row(r, h);
-#pragma unroll
-      for (int m = 0; m < DB; ++m)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t col = 32u * m + element_row(e, half);
-          const uint32_t at = row * Rows<DB>::kRow + (((col >> 3) ^ Rows<DB>::swizzle(row)) << 4) + (col & 7u) * 2u;
-          const float y = T::value(*reinterpret_cast<const uint16_t*>(tile + at));
-          if (on) acc[m][e] += x * y;
-        }
-    }
+    for (int i = 0; i < 4; ++i)
+      s += T::value(u[i] & 0xFFFFu) * T::value(v[i] & 0xFFFFu) + T::value(u[i] >> 16) * T::value(v[i] >> 16);
   }
+  return s;
+}
+
+// x[i] += w times elements lane and lane + 64 of a row.
+template <class T>
+__device__ __forceinline__ void add_row(float (&x)[2], float w, const unsigned char* row, uint32_t d) {
+  const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64u * i < d) x[i] += w * T::value(reinterpret_cast<const uint16_t*>(row)[lane + 64u * i]);
 }
 
 // Four 16-bit values of consecutive elements.

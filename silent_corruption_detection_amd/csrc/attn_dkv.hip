@@ -5,6 +5,45 @@
 namespace sdc {
 namespace {
 
+// One key's and value's gradient by a wave, over the queries [first, last): for the tiles
+// that a mask cuts and that hold an infinity or NaN among their queries or rows of dout, where
+// zero times what a masked query holds would not be zero.  row: of dk and dv; part: the
+// split's first row.
+template <class T, bool SPLIT>
+__device__ __forceinline__ void dkv_row(const AttnArgs& a, const Place32& p, int32_t key, int32_t first, int32_t last,
+                                        uint64_t row, uint64_t part) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const unsigned char *k = key_rows(a, p) + (uint64_t)key * a.k_row, *v = value_rows(a, p) + (uint64_t)key * a.v_row;
+  const auto dout = [&](int32_t r) { return a.dout + flat_row(a, p, (uint32_t)r) * (2u * a.d); };
+  float xk[2] = {0.0f, 0.0f}, xv[2] = {0.0f, 0.0f};
+  for (int32_t q0 = first; q0 < last; q0 += 64) {
+    const int32_t r = q0 + (int32_t)lane;
+    float w = 0.0f, dw = 0.0f;
+    if (r < last) {
+      const float s = dot_rows<T>(query_row(a, p, (uint32_t)r), k, a.d);
+      w = __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.c, -(a.l2[grouped_row(a, p, (uint32_t)r)] + kPShift<T>)));
+      dw = w * (dot_rows<T>(dout(r), v, a.d) - a.delta[grouped_row(a, p, (uint32_t)r)]);
+    }
+    const int32_t n = min(last - q0, 64);
+    for (int32_t j = 0; j < n; ++j) {
+      add_row<T>(xv, __shfl(w, j), dout(q0 + j), a.d);
+      add_row<T>(xk, __shfl(dw, j), query_row(a, p, (uint32_t)(q0 + j)), a.d);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t e = lane + 64u * i;
+    if (e >= a.d) continue;
+    if constexpr (SPLIT) {
+      a.part_k[(part + row) * a.d + e] = xk[i] * a.scale;
+      a.part_v[(part + row) * a.d + e] = xv[i];
+    } else {
+      a.dk[row * a.d + e] = (uint16_t)T::bits(xk[i] * a.scale);
+      a.dv[row * a.d + e] = (uint16_t)T::bits(xv[i]);
+    }
+  }
+}
+
 // A workgroup of W waves takes 32 W keys, a wave 32 of them, keeps them and their values
 // in registers and streams the queries that attend them, of all heads that share them,
 // and their rows of dout past them in tiles of 64, so that the sums over queries and over
@@ -14,7 +53,7 @@ namespace {
 //
 // SPLIT: the queries in a.splits parts, each leaving fp32 sums.
 template <class T, int DB, int W, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   typedef Rows<DB> L;
   constexpr uint32_t kBuf = 2u * L::kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
@@ -67,6 +106,7 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
       if (wave == W - 1) load4_to_lds(delta + row, base + 2u * L::kBytes + 4u * kAttnTile);
     };
     if (t0 < t1) fill(t0, 0);
+    bool redo = false;
     uint32_t buf = 0;
     for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
@@ -76,7 +116,7 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
       const bool masked = q0 < from || q0 + (int32_t)kAttnTile > to;
       const unsigned char *qt = lds + buf * kBuf, *dt = qt + L::kBytes;
       const float *lt = reinterpret_cast<const float*>(dt + L::kBytes), *et = lt + kAttnTile;
-      const bool by_rows = masked && (tile_nonfinite<T, DB>(qt) || tile_nonfinite<T, DB>(dt));
+      if (masked) redo |= tile_nonfinite<T, DB>(qt) || tile_nonfinite<T, DB>(dt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         f32x16 s, dp;
@@ -87,29 +127,18 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
           s = mfma32(at.row(qt, n, i), k[i], s);
           dp = mfma32(at.row(dt, n, i), v[i], dp);
         }
-        uint32_t has = 0xFFFFu;
-        if (masked) {
-          has = 0;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int32_t r = q0 + 32 * n + (int32_t)element_row(e, half);
-            if (r >= lo && r < hi) has |= 1u << e;
-          }
-        }
+        const uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
         if constexpr (ROW) {
           // the rows of a block are not evenly spaced where heads are grouped
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int32_t r = q0 + 32 * n + (int32_t)element_row(4 * g + e, half);
-              if (!(has >> (4 * g + e) & 1u)) continue;
-              const uint32_t x = __float_as_uint(s[4 * g + e]);
-              ln.s += x;
-              ln.w += (flat_row(a, p, (uint32_t)r) * a.kw + (uint32_t)key + 1u) * x;
-              ln.x ^= x;
-              ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
-            }
+          for (int e = 0; e < 16; ++e) {
+            if (masked && first + element_row(e, 0) >= all) continue;
+            const uint32_t r = (uint32_t)q0 + 32u * n + element_row(e, half), x = __float_as_uint(s[e]);
+            ln.s += x;
+            ln.w += (flat_row(a, p, r) * a.kw + (uint32_t)key + 1u) * x;
+            ln.x ^= x;
+            ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+          }
         }
         f32x16 ds;
 #pragma unroll
@@ -127,12 +156,7 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (!(has >> e & 1u)) s[e] = ds[e] = 0.0f;
-        }
-        if (by_rows) {
-          product_by_rows<T, DB>(dv, dt, n, s, has);
-          product_by_rows<T, DB>(dk, qt, n, ds, has);
-          continue;
+            if (first + element_row(e, 0) >= all) s[e] = ds[e] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -145,10 +169,15 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
         }
       }
     }
-    if (key < p.lk) {
+    const uint64_t key_row = (uint64_t)(p.k0 + (uint32_t)key) * a.hk + p.head;
+    const uint64_t all_rows = (uint64_t)(a.seq_k ? a.len_k : a.batch * a.len_k) * a.hk;
+    if (redo) {
+      for (int32_t x = key0; x < min(key0 + 32, p.lk); ++x)
+        dkv_row<T, SPLIT>(a, p, x, max(first_row(x), t0 * (int32_t)kAttnTile),
+                          min(last_row(x), t1 * (int32_t)kAttnTile), (uint64_t)(p.k0 + (uint32_t)x) * a.hk + p.head,
+                          split * all_rows);
+    } else if (key < p.lk) {
       const float gk = a.scale * power_of_two(-shift), gv = power_of_two(-(int)kPShift<T>);
-      const uint64_t row = (uint64_t)(p.k0 + (uint32_t)key) * a.hk + p.head;
-      const uint64_t all = (uint64_t)(a.seq_k ? a.len_k : a.batch * a.len_k) * a.hk;
 #pragma unroll
       for (int m = 0; m < DB; ++m)
 #pragma unroll
@@ -158,12 +187,12 @@ __global__ void __launch_bounds__(64 * W) attn_dkv_kernel(const AttnArgs a) {
           const f32x4 xk = {dk[m][4 * e] * gk, dk[m][4 * e + 1] * gk, dk[m][4 * e + 2] * gk, dk[m][4 * e + 3] * gk};
           const f32x4 xv = {dv[m][4 * e] * gv, dv[m][4 * e + 1] * gv, dv[m][4 * e + 2] * gv, dv[m][4 * e + 3] * gv};
           if constexpr (SPLIT) {
-            const uint64_t to_part = (split * all + row) * a.d + x;
+            const uint64_t to_part = (split * all_rows + key_row) * a.d + x;
             *reinterpret_cast<f32x4*>(a.part_k + to_part) = xk;
             *reinterpret_cast<f32x4*>(a.part_v + to_part) = xv;
           } else {
-            store4<T>(a.dk + row * a.d + x, xk.x, xk.y, xk.z, xk.w);
-            store4<T>(a.dv + row * a.d + x, xv.x, xv.y, xv.z, xv.w);
+            store4<T>(a.dk + key_row * a.d + x, xk.x, xk.y, xk.z, xk.w);
+            store4<T>(a.dv + key_row * a.d + x, xv.x, xv.y, xv.z, xv.w);
           }
         }
     }

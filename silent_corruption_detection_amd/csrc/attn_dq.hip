@@ -4,6 +4,33 @@
 namespace sdc {
 namespace {
 
+// One query's gradient by a wave: for the tiles that a mask cuts and that hold an infinity or
+// NaN among their keys, where zero times what a masked key holds would not be zero.
+template <class T>
+__device__ __forceinline__ void dq_row(const AttnArgs& a, const Place32& p, uint32_t r) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const int32_t t = (int32_t)token_of(a, r), lo = keys_begin(a, p, t), hi = keys_end(a, p, t);
+  const uint64_t flat = flat_row(a, p, r);
+  const unsigned char *q = query_row(a, p, r), *dout = a.dout + flat * (2u * a.d);
+  const unsigned char *k = key_rows(a, p), *v = value_rows(a, p);
+  const float l2 = a.l2[grouped_row(a, p, r)] + kPShift<T>, delta = a.delta[grouped_row(a, p, r)];
+  float x[2] = {0.0f, 0.0f};
+  for (int32_t k0 = lo; k0 < hi; k0 += 64) {
+    const int32_t key = k0 + (int32_t)lane;
+    float w = 0.0f;
+    if (key < hi) {
+      const float s = dot_rows<T>(q, k + (uint64_t)key * a.k_row, a.d);
+      w = __builtin_amdgcn_exp2f(__builtin_fmaf(s, a.c, -l2)) *
+          (dot_rows<T>(dout, v + (uint64_t)key * a.v_row, a.d) - delta);
+    }
+    const int32_t n = min(hi - k0, 64);
+    for (int32_t j = 0; j < n; ++j) add_row<T>(x, __shfl(w, j), k + (uint64_t)(k0 + j) * a.k_row, a.d);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 64u * i < a.d) a.dq[flat * a.d + lane + 64u * i] = (uint16_t)T::bits(x[i] * a.scale);
+}
+
 // As the forward pass, a workgroup of W waves takes 32 W queries of a head of keys and
 // streams the keys they attend past them.  A wave keeps its queries and their rows of
 // dout in registers, and per block of 32 keys computes S^T = K Q^T and dP^T = V dout^T, the
@@ -11,7 +38,7 @@ namespace {
 // dq^T.  dS is the one thing rounded to 16 bits on the way (off by half a step of its own
 // size, which the sum over keys averages out).
 template <class T, int DB, int W, bool ROW>
-__global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   typedef Rows<DB> L;
   const Place32 p = place_of<false>(a, blockIdx.x, 32u * W);
@@ -48,6 +75,7 @@ __global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
       lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
     };
     if (t0 < t1) fill(t0, 0);
+    bool redo = false;
     uint32_t buf = 0;
     for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
@@ -56,7 +84,7 @@ __global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
       if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;
       const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
       const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
-      const bool by_rows = masked && tile_nonfinite<T, DB>(kt);
+      if (masked) redo |= tile_nonfinite<T, DB>(kt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         f32x16 s, dp;
@@ -67,17 +95,16 @@ __global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
           s = mfma32(at.row(kt, n, i), q[i], s);
           dp = mfma32(at.row(vt, n, i), dout[i], dp);
         }
-        uint32_t has = 0xFFFFu;
-        if (masked) {
-          has = 0;
+        const uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
+        if constexpr (ROW) {
+          uint32_t has = 0xFFFFu;
+          if (masked) {
+            has = 0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int32_t key = k0 + 32 * n + (int32_t)element_row(e, half);
-            if (key >= lo && key < hi) has |= 1u << e;
+            for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
           }
-        }
-        if constexpr (ROW)
           block_row(ln, s, flat * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u, 1u, r < R ? has : 0u);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], a.c, -l2));
@@ -87,11 +114,7 @@ __global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (!(has >> e & 1u)) s[e] = 0.0f;
-        }
-        if (by_rows) {
-          product_by_rows<T, DB>(acc, kt, n, s, has);
-          continue;
+            s[e] = first + element_row(e, 0) < all ? s[e] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -101,7 +124,10 @@ __global__ void __launch_bounds__(64 * W) attn_dq_kernel(const AttnArgs a) {
         }
       }
     }
-    if (r < R) {
+    if (redo) {
+      const uint32_t rows = min(r0 + 32u, R);
+      for (uint32_t x = r0; x < rows; ++x) dq_row<T>(a, p, x);
+    } else if (r < R) {
       const float g = a.scale * power_of_two(-shift);
       uint16_t* out = a.dq + flat * a.d;
 #pragma unroll

@@ -9,6 +9,48 @@ __device__ __forceinline__ float log_sum(float top, float scale, float sum, floa
   return __builtin_fmaf(top, scale, (__builtin_amdgcn_logf(sum) - off) * kLn2);
 }
 
+// One query by a wave, over the keys it attends in [first, last): for the tiles that a mask
+// cuts and that hold an infinity or NaN among their values, where zero times what a masked
+// key holds would not be zero.
+template <class T, bool SPLIT>
+__device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, uint32_t r, int32_t first, int32_t last,
+                                         uint32_t split) {
+  const uint32_t lane = threadIdx.x & 63u;
+  const int32_t t = (int32_t)token_of(a, r), lo = max(keys_begin(a, p, t), first), hi = min(keys_end(a, p, t), last);
+  const unsigned char *q = query_row(a, p, r), *k = key_rows(a, p), *v = value_rows(a, p);
+  float top = -__builtin_inff();
+  for (int32_t k0 = lo; k0 < hi; k0 += 64) {
+    const int32_t key = k0 + (int32_t)lane;
+    if (key < hi) top = __builtin_fmaxf(top, dot_rows<T>(q, k + (uint64_t)key * a.k_row, a.d));
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+  const float m = top == -__builtin_inff() ? 0.0f : top;
+  float sum = 0.0f, x[2] = {0.0f, 0.0f};
+  for (int32_t k0 = lo; k0 < hi; k0 += 64) {
+    const int32_t key = k0 + (int32_t)lane;
+    float w = 0.0f;
+    if (key < hi) w = __builtin_amdgcn_exp2f((dot_rows<T>(q, k + (uint64_t)key * a.k_row, a.d) - m) * a.c);
+    sum += w;
+    const int32_t n = min(hi - k0, 64);
+    for (int32_t j = 0; j < n; ++j) add_row<T>(x, __shfl(w, j), v + (uint64_t)(k0 + j) * a.v_row, a.d);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+  const bool none = top == -__builtin_inff() && !(sum != sum);
+  const uint64_t row = SPLIT ? grouped_row(a, p, r) * a.splits + split : flat_row(a, p, r);
+  if (lane == 0) {
+    if constexpr (SPLIT) a.part_ml[row] = float2{top, sum};
+    else a.lse[row] = none ? -__builtin_inff() : log_sum(top, a.scale, sum, 0.0f);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (lane + 64u * i >= a.d) continue;
+    if constexpr (SPLIT) a.part[row * a.d + lane + 64u * i] = x[i];
+    else a.out[row * a.d + lane + 64u * i] = (uint16_t)T::bits(none ? 0.0f : x[i] / sum);
+  }
+}
+
 // A workgroup of W waves takes 32 QB W queries of a head of keys, a wave 32 QB of them,
 // and streams the keys they attend past them in tiles of 64 (two buffers in LDS, the next
 // filled by direct loads while this one is multiplied).  The queries stay in registers, as
@@ -27,7 +69,7 @@ __device__ __forceinline__ float log_sum(float top, float scale, float sum, floa
 constexpr float kFarOut = 0x1p27f;
 
 template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   typedef Rows<DB> L;
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
@@ -68,6 +110,12 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[b][m][e] = 0.0f;
     }
+    const float rise = 8.0f / a.c;
+    const auto score_row = [&](int b, int n, const f32x16& z, int32_t k0, uint32_t has) {
+      const uint32_t r = r0 + 32u * b + (lane & 31u);
+      const uint64_t row = flat_row(a, p, min(r, R - 1u)) * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u;
+      block_row(ln, z, row, 1u, r < R ? has : 0u);
+    };
     const TileReads<T, DB> at;
     TileLoader<DB, W> lk, lv;
     lk.init(key_rows(a, p), a.k_row, a.d);
@@ -78,13 +126,13 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
       lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
     };
     if (t0 < t1) fill(t0, 0);
+    bool redo = false;
     uint32_t buf = 0;
     for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
       const int32_t k0 = t * (int32_t)kAttnTile;
       if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;  // none of the wave's
-      const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
       const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
       f32x16 s[QB][2];
 #pragma unroll
@@ -101,38 +149,32 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
 #pragma unroll
           for (int b = 0; b < QB; ++b) s[b][n] = mfma32(f, q[b][i], s[b][n]);
         }
-      uint32_t has[QB][2];
-#pragma unroll
-      for (int b = 0; b < QB; ++b)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          has[b][n] = 0xFFFFu;
-          if (masked) {
-            has[b][n] = 0;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int32_t key = k0 + 32 * n + (int32_t)element_row(e, half);
-              if (key >= lo[b] && key < hi[b]) has[b][n] |= 1u << e;
-            }
-          }
-        }
-      if constexpr (ROW) {
-#pragma unroll
-        for (int b = 0; b < QB; ++b) {
-          const uint32_t r = r0 + 32u * b + (lane & 31u);
-          const uint64_t row = flat_row(a, p, min(r, R - 1u)) * a.kw + (uint32_t)k0 + 4u * half + 1u;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) block_row(ln, s[b][n], row + 32u * n, 1u, r < R ? has[b][n] : 0u);
-        }
-      }
-      if (masked) {
+      if (k0 < from || k0 + (int32_t)kAttnTile > to) {  // cut by a mask for some query
 #pragma unroll
         for (int b = 0; b < QB; ++b)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo[b]);
+            const uint32_t all = (uint32_t)max(hi[b] - lo[b], 0);
+            uint32_t has = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (!(has[b][n] >> e & 1u)) s[b][n][e] = -__builtin_inff();
+            for (int e = 0; e < 16; ++e) {
+              const bool on = first + element_row(e, 0) < all;
+              if constexpr (ROW) has |= on ? 1u << e : 0u;
+              else s[b][n][e] = on ? s[b][n][e] : -__builtin_inff();
+            }
+            if constexpr (ROW) {
+              score_row(b, n, s[b][n], k0, has);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[b][n][e] = has >> e & 1u ? s[b][n][e] : -__builtin_inff();
+            }
+          }
+        redo |= tile_nonfinite<T, DB>(vt);
+      } else if constexpr (ROW) {
+#pragma unroll
+        for (int b = 0; b < QB; ++b)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) score_row(b, n, s[b][n], k0, 0xFFFFu);
       }
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
@@ -142,7 +184,7 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) most = __builtin_fmaxf(most, s[b][n][e]);
         most = both_max(most);
-        if (__any(most > top[b] + 8.0f / a.c)) {
+        if (__any(most > top[b] + rise)) {
           const float was = top[b], before = off[b];
           top[b] = __builtin_fmaxf(was, most);
           base[b] = top[b] == -__builtin_inff() ? 0.0f : top[b] * a.c;
@@ -176,13 +218,6 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
           for (int e = 0; e < 16; ++e) sum += s[b][n][e];
         l[b] += sum;
       }
-      if (masked && tile_nonfinite<T, DB>(vt)) {
-#pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) product_by_rows<T, DB>(o[b], vt, n, s[b][n], has[b][n]);
-        continue;
-      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         typename T::frag w[QB];
@@ -196,41 +231,47 @@ __global__ void __launch_bounds__(64 * W) attn_kernel(const AttnArgs a) {
         }
       }
     }
+    if (redo) {
+      const uint32_t rows = min(r0 + 32u * QB, R);
+      for (uint32_t r = r0; r < rows; ++r)
+        attn_row<T, SPLIT>(a, p, r, t0 * (int32_t)kAttnTile, t1 * (int32_t)kAttnTile, split);
+    } else {
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      const uint32_t r = r0 + 32u * b + (lane & 31u);
-      const float sum = both_sum(l[b]);
-      if (r >= R) continue;
-      if constexpr (SPLIT) {
-        const uint64_t row = grouped_row(a, p, r) * a.splits + split;
-        const float f = __builtin_amdgcn_exp2f(-off[b]);  // from base to m c
-        if (half == 0) a.part_ml[row] = float2{top[b], sum * f};
-        float* out = a.part + row * a.d;
+      for (int b = 0; b < QB; ++b) {
+        const uint32_t r = r0 + 32u * b + (lane & 31u);
+        const float sum = both_sum(l[b]);
+        if (r >= R) continue;
+        if constexpr (SPLIT) {
+          const uint64_t row = grouped_row(a, p, r) * a.splits + split;
+          const float f = __builtin_amdgcn_exp2f(-off[b]);  // from base to m c
+          if (half == 0) a.part_ml[row] = float2{top[b], sum * f};
+          float* out = a.part + row * a.d;
 #pragma unroll
-        for (int m = 0; m < DB; ++m)
+          for (int m = 0; m < DB; ++m)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t e = 32u * m + 8u * g + 4u * half;
-            if (e < a.d)
-              *reinterpret_cast<f32x4*>(out + e) =
-                  f32x4{o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f, o[b][m][4 * g + 3] * f};
-          }
-      } else {
-        // a query that attends nothing: out 0, lse -inf
-        const bool none = top[b] == -__builtin_inff() && !(sum != sum);
-        const float f = none ? 0.0f : 1.0f / sum;
-        const uint64_t row = flat_row(a, p, r);
-        if (half == 0) a.lse[row] = none ? -__builtin_inff() : log_sum(top[b], a.scale, sum, off[b]);
-        uint16_t* out = a.out + row * a.d;
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t e = 32u * m + 8u * g + 4u * half;
+              if (e < a.d)
+                *reinterpret_cast<f32x4*>(out + e) =
+                    f32x4{o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f, o[b][m][4 * g + 3] * f};
+            }
+        } else {
+          // a query that attends nothing: out 0, lse -inf
+          const bool none = top[b] == -__builtin_inff() && !(sum != sum);
+          const float f = none ? 0.0f : 1.0f / sum;
+          const uint64_t row = flat_row(a, p, r);
+          if (half == 0) a.lse[row] = none ? -__builtin_inff() : log_sum(top[b], a.scale, sum, off[b]);
+          uint16_t* out = a.out + row * a.d;
 #pragma unroll
-        for (int m = 0; m < DB; ++m)
+          for (int m = 0; m < DB; ++m)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t e = 32u * m + 8u * g + 4u * half;
-            if (e < a.d)
-              store4<T>(out + e, o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f,
-                        o[b][m][4 * g + 3] * f);
-          }
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t e = 32u * m + 8u * g + 4u * half;
+              if (e < a.d)
+                store4<T>(out + e, o[b][m][4 * g] * f, o[b][m][4 * g + 1] * f, o[b][m][4 * g + 2] * f,
+                          o[b][m][4 * g + 3] * f);
+            }
+        }
       }
     }
   }
@@ -288,6 +329,7 @@ int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto shape = [&](auto db) {
       std::integral_constant<int, 1> one;
       if (l.waves == 1) return launch(db, one, one);
+      if (l.blocks == 2) return launch(db, std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
       return launch(db, std::integral_constant<int, 4>(), one);
     };
     int32_t st = a.d <= 64   ? shape(std::integral_constant<int, 2>())
