@@ -17,10 +17,11 @@
 // two operands, without an exchange, and the left operand is read transposed from
 // LDS in that order (two reads of four rows of a column each).
 //
-// LDS holds rows of 64 (128) elements, 128 (256) bytes, as direct loads write them;
-// the 16-byte chunks of a row are permuted by an exclusive or with swizzle(row), so
-// that both kinds of reads, rows' chunks (16 rows, one chunk) and transposed ones (8
-// rows, four chunks), fall on all banks alike.
+// LDS holds a tile of 64 rows in groups of 32 elements: 64 pieces of 64 bytes, as direct
+// loads write them (16 rows a load), whose four 16-byte chunks are permuted by an exclusive or
+// with (row >> 2) & 3.  Both kinds of reads, a chunk of 16 rows and, transposed, four chunks of 8
+// rows, then fall on all banks alike, and a read's address is one of two registers and a
+// constant, whichever group, block or step it takes.
 #pragma once
 
 #include "tile_device.h"
@@ -87,6 +88,15 @@ __device__ __forceinline__ f32x16 mfma32(f16x8 a, f16x8 b, f32x16 c) {
 // Row of element r of a 32 x 32 result in a lane of half `half`.
 __device__ __forceinline__ constexpr uint32_t element_row(uint32_t r, uint32_t half) {
   return 8u * (r >> 2) + 4u * half + (r & 3u);
+}
+
+// x, which every lane of the wave has, in a scalar register.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ const unsigned char* uniform(const unsigned char* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = (uint32_t)uniform((int32_t)(uint32_t)x), hi = (uint32_t)uniform((int32_t)(uint32_t)(x >> 32));
+  return reinterpret_cast<const unsigned char*>((uint64_t)hi << 32 | lo);
 }
 
 // A value and the one of the lane 32 further on (or back).
@@ -230,15 +240,10 @@ __device__ __forceinline__ const unsigned char* value_rows(const AttnArgs& a, co
 // ---- tiles in LDS ----------------------------------------------------------------
 
 // 64 rows of up to 32 DB elements.
+constexpr uint32_t kGroup = kAttnTile * 64u;  // bytes of 32 elements of each
 template <int DB>
-struct Rows {
-  static constexpr uint32_t kRow = DB > 2 ? 256u : 128u;
-  static constexpr uint32_t kBytes = kAttnTile * kRow;
-  static constexpr uint32_t kChunks = kRow / 16u;
-  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    return DB > 2 ? (row & 3u) << 2 | (row >> 2 & 3u) : (row >> 1 & 1u) << 2 | (row >> 2 & 3u);
-  }
-};
+constexpr uint32_t tile_bytes() { return DB * kGroup; }
+__device__ __forceinline__ uint32_t chunk_swizzle(uint32_t row) { return row >> 2 & 3u; }
 
 // 16 bytes per lane from base + off to LDS at lds + 16 * lane (base, lds uniform); see load_to_lds.
 __device__ __forceinline__ void load_to_lds_from(const unsigned char* base, uint32_t off, uint32_t lds) {
@@ -256,6 +261,7 @@ __device__ __forceinline__ void load_to_lds_from(const unsigned char* base, uint
 
 // 4 bytes per lane to LDS at lds + 4 * lane (lds uniform); see load_to_lds.
 __device__ __forceinline__ void load4_to_lds(const float* src, uint32_t lds) {
+  lds = (uint32_t)uniform((int32_t)lds);
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
   asm volatile(
@@ -272,95 +278,104 @@ __device__ __forceinline__ void load4_to_lds(const float* src, uint32_t lds) {
 // or past its width is zero, so that nothing there can reach a sum.
 template <int DB, int WAVES>
 struct TileLoader {
-  static constexpr uint32_t kRows = 1024u / Rows<DB>::kRow;            // of one load of a wave
-  static constexpr uint32_t kLoads = kAttnTile / kRows / WAVES;        // of a wave
-  static_assert(kLoads * kRows * WAVES == kAttnTile, "the loads cover a tile");
+  static constexpr uint32_t kBlocks = 4 / WAVES;  // of 16 rows, of a wave
+  static_assert(kBlocks * WAVES == 4, "the waves' rows cover a tile");
   const unsigned char* base;  // of the matrix' first row
   uint32_t stride, width;     // bytes
-  uint32_t row, off[kLoads];  // of the thread's first load
-  bool in;                    // whole rows
+  uint32_t row, at, off;      // of the lane within 16 rows: row, byte of its chunk, both from base
+  bool in;                    // whole groups
 
-  __device__ __forceinline__ uint32_t row_at(uint32_t i) const { return row + i * kRows * WAVES; }
-  __device__ __forceinline__ uint32_t chunk_at(uint32_t i) const {
-    return (threadIdx.x & (Rows<DB>::kChunks - 1u)) ^ Rows<DB>::swizzle(row_at(i));
-  }
   __device__ __forceinline__ void init(const unsigned char* b, uint32_t row_bytes, uint32_t d) {
+    const uint32_t lane = threadIdx.x & 63u;
     base = b;
     stride = row_bytes;
     width = 2u * d;
-    row = (threadIdx.x >> 6) * kRows + (threadIdx.x & 63u) / Rows<DB>::kChunks;
-#pragma unroll
-    for (uint32_t i = 0; i < kLoads; ++i) off[i] = row_at(i) * stride + chunk_at(i) * 16u;
-    in = width == Rows<DB>::kRow;
+    row = lane >> 2;
+    at = ((lane & 3u) ^ chunk_swizzle(row)) * 16u;
+    off = row * stride + at;
+    in = width == 64u * DB;
   }
   // Rows first .. first + 63, of `rows` rows, into LDS at byte `lds`.
   __device__ __forceinline__ void fill(uint32_t first, uint32_t rows, uint32_t lds) const {
-    const uint32_t to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
-    const unsigned char* at = base + (uint64_t)first * stride;
-    if (in && first + kAttnTile <= rows) {
+    const uint32_t block = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kBlocks;
+    const bool whole = in && first + kAttnTile <= rows;
 #pragma unroll
-      for (uint32_t i = 0; i < kLoads; ++i) load_to_lds_from(at, off[i], to + i * (1024u * WAVES));
-    } else {
-      const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+    for (uint32_t i = 0; i < kBlocks; ++i) {
+      const uint32_t r = first + (block + i) * 16u, to = (uint32_t)uniform((int32_t)(lds + (block + i) * 1024u));
+      const unsigned char* from = uniform(base + (uint64_t)r * stride);
+      if (whole) {
 #pragma unroll
-      for (uint32_t i = 0; i < kLoads; ++i) {
-        const bool has = first + row_at(i) < rows && chunk_at(i) * 16u < width;
-        load_to_lds(has ? at + off[i] : zero, to + i * (1024u * WAVES));
+        for (uint32_t m = 0; m < DB; ++m) load_to_lds_from(from + m * 64u, off, to + m * kGroup);
+      } else {
+        const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+#pragma unroll
+        for (uint32_t m = 0; m < DB; ++m)
+          load_to_lds(r + row < rows && m * 64u + at < width ? from + m * 64u + off : zero, to + m * kGroup);
       }
     }
   }
 };
 
-// The queries' (dout's) rows, whose places follow from token and head.
+// The queries' and dout's rows, whose places follow from token and head.
 template <int DB, int WAVES>
 struct QueryLoader {
-  typedef TileLoader<DB, WAVES> Tile;
-  uint32_t row;
-  __device__ __forceinline__ void init() {
-    row = (threadIdx.x >> 6) * Tile::kRows + (threadIdx.x & 63u) / Rows<DB>::kChunks;
-  }
+  static_assert(WAVES == 4, "a wave has 16 rows of a tile");
   __device__ __forceinline__ void fill(const AttnArgs& a, const Place32& p, uint32_t first, uint32_t rows,
                                        uint32_t lds_q, uint32_t lds_do) const {
-    const uint32_t to = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024u;
+    lds_q = (uint32_t)uniform((int32_t)lds_q);
+    lds_do = (uint32_t)uniform((int32_t)lds_do);
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r = first + wave * 16u + (lane >> 2), at = ((lane & 3u) ^ chunk_swizzle(lane >> 2)) * 16u;
     const unsigned char* zero = reinterpret_cast<const unsigned char*>(&g_zero16);
+    const unsigned char* q = query_row(a, p, min(r, rows - 1u)) + at;
+    const unsigned char* o = a.dout + flat_row(a, p, min(r, rows - 1u)) * (2u * a.d) + at;
+    const bool whole = a.d == 32u * DB && first + kAttnTile <= rows;
 #pragma unroll
-    for (uint32_t i = 0; i < Tile::kLoads; ++i) {
-      const uint32_t at = row + i * Tile::kRows * WAVES, r = min(first + at, rows - 1u);
-      const uint32_t chunk = (threadIdx.x & (Rows<DB>::kChunks - 1u)) ^ Rows<DB>::swizzle(at);
-      const bool has = first + at < rows && chunk * 8u < a.d;
-      const unsigned char* q = query_row(a, p, r) + chunk * 16u;
-      const unsigned char* o = a.dout + flat_row(a, p, r) * (2u * a.d) + chunk * 16u;
-      load_to_lds(has ? q : zero, lds_q + to + i * (1024u * WAVES));
-      load_to_lds(has ? o : zero, lds_do + to + i * (1024u * WAVES));
+    for (uint32_t m = 0; m < DB; ++m) {
+      const bool has = whole || (r < rows && m * 64u + at < 2u * a.d);
+      load_to_lds(has ? q + m * 64u : zero, lds_q + wave * 1024u + m * kGroup);
+      load_to_lds(has ? o + m * 64u : zero, lds_do + wave * 1024u + m * kGroup);
     }
   }
 };
 
-// A lane's reads of a tile as the left operand.
-template <class T, int DB>
+// A lane's reads of the tile at LDS byte `tile` as the left operand.
+template <class T>
 struct TileReads {
-  uint32_t rows_off, cols_off;
-  __device__ __forceinline__ TileReads() {
+  uint32_t row0, row1, col0, col1;
+  __device__ __forceinline__ explicit TileReads(uint32_t tile) {
     const uint32_t lane = threadIdx.x & 63u, half = lane >> 5;
-    rows_off = (lane & 31u) * Rows<DB>::kRow + ((half ^ Rows<DB>::swizzle(lane & 31u)) << 4);
+    const uint32_t rows = (lane & 31u) * 64u + ((half ^ chunk_swizzle(lane & 31u)) << 4);
     const uint32_t r = 4u * half + (lane >> 2 & 3u), chunk = (lane >> 4 & 1u) * 2u + (lane >> 1 & 1u);
-    cols_off = r * Rows<DB>::kRow + ((chunk ^ Rows<DB>::swizzle(r)) << 4) + (lane & 1u) * 8u;
+    const uint32_t cols = r * 64u + ((chunk ^ chunk_swizzle(r)) << 4) + (lane & 1u) * 8u;
+    row0 = tile + rows;
+    row1 = tile + (rows ^ 32u);
+    col0 = tile + cols;
+    col1 = tile + (cols ^ 32u) + 512u;  // eight rows on, the swizzle's bit 1 is the other one
+  }
+  // The same of the tile `by` bytes on.
+  __device__ __forceinline__ void move(uint32_t by) {
+    row0 += by;
+    row1 += by;
+    col0 += by;
+    col1 += by;
+    // kept as they are: a read's constant then fits its instruction
+    asm volatile("" : "+v"(row0), "+v"(row1), "+v"(col0), "+v"(col1));
   }
   // Rows 32 b .. of the tile, elements 16 s .. of each: the sum runs along the rows.
-  __device__ __forceinline__ typename T::frag row(const unsigned char* tile, int b, int s) const {
-    return *reinterpret_cast<const typename T::frag*>(tile + (rows_off ^ (uint32_t)s << 5) + b * (32u * Rows<DB>::kRow));
+  // tile: bytes to another one, a constant.
+  __device__ __forceinline__ typename T::frag row(uint32_t tile, int b, int s) const {
+    return *(const SDC_LDS typename T::frag*)(uintptr_t)((s & 1 ? row1 : row0) + (tile + (s >> 1) * kGroup + b * 2048u));
   }
   // Elements 32 m .. of each row, rows 16 s .. of the tile: the sum runs over the rows.
-  __device__ __forceinline__ typename T::frag column(const unsigned char* tile, int m, int s) const {
-    const unsigned char* q = tile + s * (16u * Rows<DB>::kRow);
-    const uint32_t at = cols_off ^ (uint32_t)m << 6;
+  __device__ __forceinline__ typename T::frag column(uint32_t tile, int m, int s) const {
+    const uint32_t by = tile + m * kGroup + s * 1024u;
     union {
       s16x4 half[2];
       typename T::frag all;
     } u;
-    // eight rows on, the swizzle's bit 1 is the other one
-    u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + at));
-    u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(q + (at ^ 32u) + 8u * Rows<DB>::kRow));
+    u.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(uintptr_t)(col0 + by));
+    u.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SDC_LDS s16x4*)(uintptr_t)(col1 + by));
     return u.all;
   }
 };
@@ -383,7 +398,7 @@ template <class T, int DB>
 __device__ __forceinline__ bool tile_nonfinite(const unsigned char* tile) {
   constexpr uint32_t one = std::is_same<T, Bf16>::value ? 0x00800080u : 0x04000400u;  // of the exponent's last bit
   uint32_t bad = 0;
-  for (uint32_t at = (threadIdx.x & 63u) * 16u; at < Rows<DB>::kBytes; at += 1024u) {
+  for (uint32_t at = (threadIdx.x & 63u) * 16u; at < tile_bytes<DB>(); at += 1024u) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(tile + at);
     bad |= ((v.x & 0x7FFF7FFFu) + one) | ((v.y & 0x7FFF7FFFu) + one) | ((v.z & 0x7FFF7FFFu) + one) |
            ((v.w & 0x7FFF7FFFu) + one);

@@ -53,10 +53,10 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& a, const Place32& p, int
 //
 // SPLIT: the queries in a.splits parts, each leaving fp32 sums.
 template <class T, int DB, int W, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
-  typedef Rows<DB> L;
-  constexpr uint32_t kBuf = 2u * L::kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
+  constexpr uint32_t kBytes = tile_bytes<DB>();
+  constexpr uint32_t kBuf = 2u * kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
   const Place32 p = place_of<true>(a, unit, 32u * W);
   Lane ln;
@@ -93,29 +93,28 @@ __global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const
     for (int m = 0; m < DB; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) dk[m][e] = dv[m][e] = 0.0f;
-    const TileReads<T, DB> at;
     QueryLoader<DB, W> lq;
-    lq.init();
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    TileReads<T> at(lds0);
     const float *l2 = a.l2 + grouped_row(a, p, 0), *delta = a.delta + grouped_row(a, p, 0);
     const auto fill = [&](int32_t t, uint32_t buf) {
       const uint32_t r = (uint32_t)t * kAttnTile, base = lds0 + buf * kBuf;
-      lq.fill(a, p, r, (uint32_t)R, base, base + L::kBytes);
+      lq.fill(a, p, r, (uint32_t)R, base, base + kBytes);
       const uint32_t row = min(r + lane, (uint32_t)R - 1u);
-      if (wave == 0) load4_to_lds(l2 + row, base + 2u * L::kBytes);
-      if (wave == W - 1) load4_to_lds(delta + row, base + 2u * L::kBytes + 4u * kAttnTile);
+      if (wave == 0) load4_to_lds(l2 + row, base + 2u * kBytes);
+      if (wave == W - 1) load4_to_lds(delta + row, base + 2u * kBytes + 4u * kAttnTile);
     };
     if (t0 < t1) fill(t0, 0);
     bool redo = false;
     uint32_t buf = 0;
-    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
+    for (int32_t t = t0; t < t1; ++t, at.move(buf ? 0u - kBuf : kBuf), buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
       const int32_t q0 = t * (int32_t)kAttnTile;
       if (q0 >= end || q0 + (int32_t)kAttnTile <= begin) continue;
       const bool masked = q0 < from || q0 + (int32_t)kAttnTile > to;
-      const unsigned char *qt = lds + buf * kBuf, *dt = qt + L::kBytes;
-      const float *lt = reinterpret_cast<const float*>(dt + L::kBytes), *et = lt + kAttnTile;
+      const unsigned char *qt = lds + buf * kBuf, *dt = qt + kBytes;
+      const float *lt = reinterpret_cast<const float*>(dt + kBytes), *et = lt + kAttnTile;
       if (masked) redo |= tile_nonfinite<T, DB>(qt) || tile_nonfinite<T, DB>(dt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -124,10 +123,10 @@ __global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const
         for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) {
-          s = mfma32(at.row(qt, n, i), k[i], s);
-          dp = mfma32(at.row(dt, n, i), v[i], dp);
+          s = mfma32(at.row(0, n, i), k[i], s);
+          dp = mfma32(at.row(kBytes, n, i), v[i], dp);
         }
-        const uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
+        uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
         if constexpr (ROW) {
           // the rows of a block are not evenly spaced where heads are grouped
 #pragma unroll
@@ -154,6 +153,7 @@ __global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const
           }
         }
         if (masked) {
+          asm volatile("" : "+v"(first));  // so that this stays a branch: no selects for the other tiles
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (first + element_row(e, 0) >= all) s[e] = ds[e] = 0.0f;
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(64 * W, DB == 4 ? 1 : 2) attn_dkv_kernel(const
           const typename T::frag w = operand<T>(s, i), x = operand<T>(ds, i);
 #pragma unroll
           for (int m = 0; m < DB; ++m) {
-            dv[m] = mfma32(at.column(dt, m, 2 * n + i), w, dv[m]);
-            dk[m] = mfma32(at.column(qt, m, 2 * n + i), x, dk[m]);
+            dv[m] = mfma32(at.column(kBytes, m, 2 * n + i), w, dv[m]);
+            dk[m] = mfma32(at.column(0, m, 2 * n + i), x, dk[m]);
           }
         }
       }
@@ -232,7 +232,7 @@ int32_t launch_attn_dkv(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto shape = [&](auto db) {
       constexpr int DB = decltype(db)::value, W = 4;
       const dim3 grid(a.units * a.splits), block(64 * W);
-      constexpr uint32_t bytes = 2u * (2u * Rows<DB>::kBytes + 2u * kAttnTile * 4u);
+      constexpr uint32_t bytes = 2u * (2u * tile_bytes<DB>() + 2u * kAttnTile * 4u);
       const bool split = a.splits > 1;
       if (a.rows && split) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, true>), grid, block, bytes, s, a);
       else if (a.rows) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, false>), grid, block, bytes, s, a);

@@ -40,7 +40,7 @@ __device__ __forceinline__ void dq_row(const AttnArgs& a, const Place32& p, uint
 template <class T, int DB, int W, bool ROW>
 __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
-  typedef Rows<DB> L;
+  constexpr uint32_t kBytes = tile_bytes<DB>();
   const Place32 p = place_of<false>(a, blockIdx.x, 32u * W);
   Lane ln;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63u, half = lane >> 5;
@@ -65,25 +65,25 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
     for (int m = 0; m < DB; ++m)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[m][e] = 0.0f;
-    const TileReads<T, DB> at;
     TileLoader<DB, W> lk, lv;
     lk.init(key_rows(a, p), a.k_row, a.d);
     lv.init(value_rows(a, p), a.v_row, a.d);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    TileReads<T> at(lds0);
     const auto fill = [&](int32_t t, uint32_t buf) {
-      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes));
-      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
+      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes));
+      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes) + kBytes);
     };
     if (t0 < t1) fill(t0, 0);
     bool redo = false;
     uint32_t buf = 0;
-    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
+    for (int32_t t = t0; t < t1; ++t, at.move(buf ? 0u - 2u * kBytes : 2u * kBytes), buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
       const int32_t k0 = t * (int32_t)kAttnTile;
       if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;
       const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
-      const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
+      const unsigned char* kt = lds + buf * (2u * kBytes);
       if (masked) redo |= tile_nonfinite<T, DB>(kt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
@@ -92,10 +92,10 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
         for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) {
-          s = mfma32(at.row(kt, n, i), q[i], s);
-          dp = mfma32(at.row(vt, n, i), dout[i], dp);
+          s = mfma32(at.row(0, n, i), q[i], s);
+          dp = mfma32(at.row(kBytes, n, i), dout[i], dp);
         }
-        const uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
+        uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
         if constexpr (ROW) {
           uint32_t has = 0xFFFFu;
           if (masked) {
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
           if constexpr (kPShift<T> != 0.0f) s[e] *= f;
         }
         if (masked) {
+          asm volatile("" : "+v"(first));  // so that this stays a branch: no selects for the other tiles
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             s[e] = first + element_row(e, 0) < all ? s[e] : 0.0f;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
         for (int i = 0; i < 2; ++i) {
           const typename T::frag w = operand<T>(s, i);
 #pragma unroll
-          for (int m = 0; m < DB; ++m) acc[m] = mfma32(at.column(kt, m, 2 * n + i), w, acc[m]);
+          for (int m = 0; m < DB; ++m) acc[m] = mfma32(at.column(0, m, 2 * n + i), w, acc[m]);
         }
       }
     }
@@ -151,7 +152,7 @@ int32_t launch_attn_dq(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto launch = [&](auto db, auto waves) {
       constexpr int DB = decltype(db)::value, W = decltype(waves)::value;
       const dim3 grid(a.units), block(64 * W);
-      constexpr uint32_t bytes = 4u * Rows<DB>::kBytes;
+      constexpr uint32_t bytes = 4u * tile_bytes<DB>();
       if (a.rows) hipLaunchKernelGGL((attn_dq_kernel<T, DB, W, true>), grid, block, bytes, s, a);
       else hipLaunchKernelGGL((attn_dq_kernel<T, DB, W, false>), grid, block, bytes, s, a);
       return launch_status();

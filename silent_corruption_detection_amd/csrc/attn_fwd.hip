@@ -71,7 +71,7 @@ constexpr float kFarOut = 0x1p27f;
 template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
-  typedef Rows<DB> L;
+  constexpr uint32_t kBytes = tile_bytes<DB>();
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
   const Place32 p = place_of<false>(a, unit, 32u * QB * W);
   Lane ln;
@@ -116,24 +116,41 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
       const uint64_t row = flat_row(a, p, min(r, R - 1u)) * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u;
       block_row(ln, z, row, 1u, r < R ? has : 0u);
     };
-    const TileReads<T, DB> at;
     TileLoader<DB, W> lk, lv;
     lk.init(key_rows(a, p), a.k_row, a.d);
     lv.init(value_rows(a, p), a.v_row, a.d);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
+    TileReads<T> at(lds0);
     const auto fill = [&](int32_t t, uint32_t buf) {
-      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes));
-      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * L::kBytes) + L::kBytes);
+      lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes));
+      lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes) + kBytes);
     };
+    t0 = uniform(t0);
+    t1 = uniform(t1);
     if (t0 < t1) fill(t0, 0);
     bool redo = false;
     uint32_t buf = 0;
-    for (int32_t t = t0; t < t1; ++t, buf ^= 1u) {
-      tile_barrier();  // this buffer is whole, and everyone has left the other
+    // On to tile t: this buffer is whole, everyone has left the other, the next is filled.
+    const auto enter = [&](int32_t t) {
+      tile_barrier();
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+    };
+    const auto leave = [&] {
+      at.move(buf ? 0u - 2u * kBytes : 2u * kBytes);
+      buf ^= 1u;
+    };
+    // the wave's own tiles, [tw, te), and before and after them those of others of the workgroup
+    const int32_t te = uniform(min(max((end + (int32_t)kAttnTile - 1) / (int32_t)kAttnTile, t0), t1));
+    const int32_t tw = uniform(min(max(begin / (int32_t)kAttnTile, t0), te));
+    int32_t t = t0;
+    for (; t < tw; ++t) {
+      enter(t);
+      leave();
+    }
+    for (; t < te; ++t) {
+      enter(t);
       const int32_t k0 = t * (int32_t)kAttnTile;
-      if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;  // none of the wave's
-      const unsigned char *kt = lds + buf * (2u * L::kBytes), *vt = kt + L::kBytes;
+      const unsigned char* vt = lds + buf * (2u * kBytes) + kBytes;
       f32x16 s[QB][2];
 #pragma unroll
       for (int b = 0; b < QB; ++b)
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
       for (int i = 0; i < 2 * DB; ++i)
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const typename T::frag f = at.row(kt, n, i);
+          const typename T::frag f = at.row(0, n, i);
 #pragma unroll
           for (int b = 0; b < QB; ++b) s[b][n] = mfma32(f, q[b][i], s[b][n]);
         }
@@ -225,11 +242,16 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
         for (int b = 0; b < QB; ++b) w[b] = operand<T>(s[b][i >> 1], i & 1);
 #pragma unroll
         for (int m = 0; m < DB; ++m) {
-          const typename T::frag f = at.column(vt, m, i);
+          const typename T::frag f = at.column(kBytes, m, i);
 #pragma unroll
           for (int b = 0; b < QB; ++b) o[b][m] = mfma32(f, w[b], o[b][m]);
         }
       }
+      leave();
+    }
+    for (; t < t1; ++t) {
+      enter(t);
+      leave();
     }
     if (redo) {
       const uint32_t rows = min(r0 + 32u * QB, R);
@@ -318,7 +340,7 @@ int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto launch = [&](auto db, auto waves, auto blocks) {
       constexpr int DB = decltype(db)::value, W = decltype(waves)::value, QB = decltype(blocks)::value;
       const dim3 grid(a.units * a.splits), block(64 * W);
-      constexpr uint32_t bytes = 4u * Rows<DB>::kBytes;
+      constexpr uint32_t bytes = 4u * tile_bytes<DB>();
       const bool split = a.splits > 1;
       if (a.rows && split) hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, true, true>), grid, block, bytes, s, a);
       else if (a.rows) hipLaunchKernelGGL((attn_kernel<T, DB, W, QB, true, false>), grid, block, bytes, s, a);
