@@ -72,6 +72,9 @@ constexpr uint32_t kAttnTile = 64;
 
 namespace {
 
+// For lambdas that several places call.
+#define SDC_INLINE __attribute__((always_inline))
+
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // fp16: probabilities are held 2^14 times as large (at most 2^14), out of the subnormals
@@ -465,9 +468,8 @@ __device__ __forceinline__ void tile_barrier() {
 }
 
 // The part of the scores' fingerprint row that a 32 x 32 block of raw scores gives.
-// first: index, from 1, of element 0's score; step: from one row of the block to the next;
-// has: which elements attend.
-__device__ __forceinline__ void block_row(Lane& ln, const f32x16& z, uint64_t first, uint64_t step, uint32_t has) {
+// first: index, from 1, of element 0's score; has: which elements attend.
+__device__ __forceinline__ void block_row(Lane& ln, const f32x16& z, uint64_t first, uint32_t has) {
   uint64_t s = 0, ws = 0;
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
@@ -476,9 +478,10 @@ __device__ __forceinline__ void block_row(Lane& ln, const f32x16& z, uint64_t fi
     ws += (uint64_t)element_row(r, 0) * x;
     ln.x ^= x;
     ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+    if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // in turn: all at once would not fit the registers
   }
   ln.s += s;
-  ln.w += ws * step + first * s;
+  ln.w += ws + first * s;
 }
 
 }  // namespace

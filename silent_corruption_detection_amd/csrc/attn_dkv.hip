@@ -14,7 +14,7 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& a, const Place32& p, int
                                         uint64_t row, uint64_t part) {
   const uint32_t lane = threadIdx.x & 63u;
   const unsigned char *k = key_rows(a, p) + (uint64_t)key * a.k_row, *v = value_rows(a, p) + (uint64_t)key * a.v_row;
-  const auto dout = [&](int32_t r) { return a.dout + flat_row(a, p, (uint32_t)r) * (2u * a.d); };
+  const auto dout = [&](int32_t r) SDC_INLINE { return a.dout + flat_row(a, p, (uint32_t)r) * (2u * a.d); };
   float xk[2] = {0.0f, 0.0f}, xv[2] = {0.0f, 0.0f};
   for (int32_t q0 = first; q0 < last; q0 += 64) {
     const int32_t r = q0 + (int32_t)lane;
@@ -68,10 +68,10 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
     load_row<T, DB>(key_rows(a, p) + (uint64_t)at_key * a.k_row, key < p.lk, a.d, k);
     load_row<T, DB>(value_rows(a, p) + (uint64_t)at_key * a.v_row, key < p.lk, a.d, v);
     // rows [first, last) of the queries attend key x
-    const auto first_row = [&](int32_t x) {
+    const auto first_row = [&](int32_t x) SDC_INLINE {
       return a.causal ? (int32_t)min((int64_t)max(x - (p.lk - p.lq), 0) * a.G, (int64_t)R) : 0;
     };
-    const auto last_row = [&](int32_t x) {
+    const auto last_row = [&](int32_t x) SDC_INLINE {
       return a.window ? (int32_t)max(min(((int64_t)x - (p.lk - p.lq) + a.window) * a.G, (int64_t)R), (int64_t)0) : R;
     };
     const int32_t lo = first_row(at_key), hi = key < p.lk ? last_row(at_key) : 0;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
     TileReads<T> at(lds0);
     const float *l2 = a.l2 + grouped_row(a, p, 0), *delta = a.delta + grouped_row(a, p, 0);
-    const auto fill = [&](int32_t t, uint32_t buf) {
+    const auto fill = [&](int32_t t, uint32_t buf) SDC_INLINE {
       const uint32_t r = (uint32_t)t * kAttnTile, base = lds0 + buf * kBuf;
       lq.fill(a, p, r, (uint32_t)R, base, base + kBytes);
       const uint32_t row = min(r + lane, (uint32_t)R - 1u);

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
     load_row<T, DB>(a.dout + flat * (2u * a.d), r < R, a.d, dout);
     const float l2 = a.l2[grouped_row(a, p, c)], delta = a.delta[grouped_row(a, p, c)];
     const int32_t mine = (int32_t)token_of(a, c), lo = keys_begin(a, p, mine), hi = keys_end(a, p, mine);
-    const auto token = [&](uint32_t x) { return (int32_t)token_of(a, min(x, R - 1u)); };
+    const auto token = [&](uint32_t x) SDC_INLINE { return (int32_t)token_of(a, min(x, R - 1u)); };
     const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * W - 1u));
     const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 31u));
     const int32_t from = keys_begin(a, p, token(r0 + 31u)), to = keys_end(a, p, token(r0));
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
     lv.init(value_rows(a, p), a.v_row, a.d);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
     TileReads<T> at(lds0);
-    const auto fill = [&](int32_t t, uint32_t buf) {
+    const auto fill = [&](int32_t t, uint32_t buf) SDC_INLINE {
       lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes));
       lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes) + kBytes);
     };
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
 #pragma unroll
             for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
           }
-          block_row(ln, s, flat * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u, 1u, r < R ? has : 0u);
+          block_row(ln, s, flat * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u, r < R ? has : 0u);
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {

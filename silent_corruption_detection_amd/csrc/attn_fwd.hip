@@ -69,7 +69,7 @@ __device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, ui
 constexpr float kFarOut = 0x1p27f;
 
 template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, W * QB == 4 && !ROW ? 2 : 1) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   constexpr uint32_t kBytes = tile_bytes<DB>();
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
       hi[b] = keys_end(a, p, t);
     }
     // keys of the workgroup's, and of the wave's, queries: [begin, end), all attend [from, to)
-    const auto token = [&](uint32_t r) { return (int32_t)token_of(a, min(r, R - 1u)); };
+    const auto token = [&](uint32_t r) SDC_INLINE { return (int32_t)token_of(a, min(r, R - 1u)); };
     const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * QB * W - 1u));
     const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 32u * QB - 1u));
     const int32_t from = keys_begin(a, p, token(r0 + 32u * QB - 1u)), to = keys_end(a, p, token(r0));
@@ -111,17 +111,19 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
         for (int e = 0; e < 16; ++e) o[b][m][e] = 0.0f;
     }
     const float rise = 8.0f / a.c;
-    const auto score_row = [&](int b, int n, const f32x16& z, int32_t k0, uint32_t has) {
-      const uint32_t r = r0 + 32u * b + (lane & 31u);
-      const uint64_t row = flat_row(a, p, min(r, R - 1u)) * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u;
-      block_row(ln, z, row, 1u, r < R ? has : 0u);
+    uint64_t first_score[QB];  // of the lane's query, from 1
+#pragma unroll
+    for (int b = 0; b < QB; ++b)
+      first_score[b] = flat_row(a, p, min(r0 + 32u * b + (lane & 31u), R - 1u)) * a.kw + 4u * half + 1u;
+    const auto score_row = [&](int b, int n, const f32x16& z, int32_t k0, uint32_t has) SDC_INLINE {
+      block_row(ln, z, first_score[b] + (uint32_t)(k0 + 32 * n), r0 + 32u * b + (lane & 31u) < R ? has : 0u);
     };
     TileLoader<DB, W> lk, lv;
     lk.init(key_rows(a, p), a.k_row, a.d);
     lv.init(value_rows(a, p), a.v_row, a.d);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(SDC_LDS unsigned char*)lds;
     TileReads<T> at(lds0);
-    const auto fill = [&](int32_t t, uint32_t buf) {
+    const auto fill = [&](int32_t t, uint32_t buf) SDC_INLINE {
       lk.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes));
       lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes) + kBytes);
     };
@@ -131,11 +133,11 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
     bool redo = false;
     uint32_t buf = 0;
     // On to tile t: this buffer is whole, everyone has left the other, the next is filled.
-    const auto enter = [&](int32_t t) {
+    const auto enter = [&](int32_t t) SDC_INLINE {
       tile_barrier();
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
     };
-    const auto leave = [&] {
+    const auto leave = [&]() SDC_INLINE {
       at.move(buf ? 0u - 2u * kBytes : 2u * kBytes);
       buf ^= 1u;
     };
@@ -147,11 +149,13 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
       enter(t);
       leave();
     }
-    for (; t < te; ++t) {
-      enter(t);
+    // Two loops in one another, the outer for the tiles that raise a reference: the inner
+    // one, which nearly all tiles take, then has no branch around the sums of values, which
+    // would cost a copy of them each time.  An inner turn goes from a tile's scores to the next's.
+    f32x16 s[QB][2];
+    float most[QB];
+    const auto scores = [&]() SDC_INLINE {
       const int32_t k0 = t * (int32_t)kAttnTile;
-      const unsigned char* vt = lds + buf * (2u * kBytes) + kBytes;
-      f32x16 s[QB][2];
 #pragma unroll
       for (int b = 0; b < QB; ++b)
 #pragma unroll
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
               for (int e = 0; e < 16; ++e) s[b][n][e] = has >> e & 1u ? s[b][n][e] : -__builtin_inff();
             }
           }
-        redo |= tile_nonfinite<T, DB>(vt);
+        redo |= tile_nonfinite<T, DB>(lds + buf * (2u * kBytes) + kBytes);
       } else if constexpr (ROW) {
 #pragma unroll
         for (int b = 0; b < QB; ++b)
@@ -195,59 +199,79 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const
       }
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
-        float most = s[b][0][0];
+        most[b] = s[b][0][0];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) most = __builtin_fmaxf(most, s[b][n][e]);
-        most = both_max(most);
-        if (__any(most > top[b] + rise)) {
-          const float was = top[b], before = off[b];
-          top[b] = __builtin_fmaxf(was, most);
-          base[b] = top[b] == -__builtin_inff() ? 0.0f : top[b] * a.c;
-          off[b] = top[b] != -__builtin_inff() && __builtin_fabsf(base[b]) < kFarOut
-                       ? __builtin_fmaf(top[b], a.c, -base[b]) : 0.0f;
-          const float f =
-              was == top[b] ? 1.0f : __builtin_amdgcn_exp2f((was - top[b]) * a.c - before + off[b]);
-          l[b] *= f;
+          for (int e = 0; e < 16; ++e) most[b] = __builtin_fmaxf(most[b], s[b][n][e]);
+        most[b] = both_max(most[b]);
+      }
+    };
+    if (t < te) {
+      enter(t);
+      scores();
+    }
+    while (t < te) {
+      bool far_out = false;
 #pragma unroll
-          for (int m = 0; m < DB; ++m)
+      for (int b = 0; b < QB; ++b) {
+        const float was = top[b], before = off[b];
+        top[b] = most[b] > was + rise ? most[b] : was;
+        base[b] = top[b] == -__builtin_inff() ? 0.0f : top[b] * a.c;
+        const bool near = __builtin_fabsf(base[b]) < kFarOut;
+        off[b] = top[b] != -__builtin_inff() && near ? __builtin_fmaf(top[b], a.c, -base[b]) : 0.0f;
+        const float f = was == top[b] ? 1.0f : __builtin_amdgcn_exp2f((was - top[b]) * a.c - before + off[b]);
+        far_out |= __any(!near);
+        l[b] *= f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[b][m][e] *= f;
-        }
-        if (!__any(__builtin_fabsf(base[b]) >= kFarOut)) {
+        for (int m = 0; m < DB; ++m)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[b][m][e] *= f;
+      }
+      bool raise;
+      do {
+#pragma unroll
+        for (int b = 0; b < QB; ++b) {
+          if (!far_out) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                s[b][n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][n][e], a.c, -base[b]));
+          } else {
+            const float m = top[b] == -__builtin_inff() ? 0.0f : top[b];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[b][n][e] = __builtin_amdgcn_exp2f((s[b][n][e] - m) * a.c + off[b]);
+          }
+          float sum = 0.0f;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              s[b][n][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][n][e], a.c, -base[b]));
-        } else {
-          const float m = top[b] == -__builtin_inff() ? 0.0f : top[b];
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[b][n][e] = __builtin_amdgcn_exp2f((s[b][n][e] - m) * a.c + off[b]);
+            for (int e = 0; e < 16; ++e) sum += s[b][n][e];
+          l[b] += sum;
         }
-        float sum = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int i = 0; i < 4; ++i) {
+          typename T::frag w[QB];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sum += s[b][n][e];
-        l[b] += sum;
-      }
+          for (int b = 0; b < QB; ++b) w[b] = operand<T>(s[b][i >> 1], i & 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        typename T::frag w[QB];
+          for (int m = 0; m < DB; ++m) {
+            const typename T::frag f = at.column(kBytes, m, i);
 #pragma unroll
-        for (int b = 0; b < QB; ++b) w[b] = operand<T>(s[b][i >> 1], i & 1);
-#pragma unroll
-        for (int m = 0; m < DB; ++m) {
-          const typename T::frag f = at.column(kBytes, m, i);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][m] = mfma32(f, w[b], o[b][m]);
+            for (int b = 0; b < QB; ++b) o[b][m] = mfma32(f, w[b], o[b][m]);
+          }
         }
-      }
-      leave();
+        leave();
+        if (++t >= te) break;
+        enter(t);
+        scores();
+        raise = false;
+#pragma unroll
+        for (int b = 0; b < QB; ++b) raise |= __any(most[b] > top[b] + rise);
+      } while (!raise);
     }
     for (; t < t1; ++t) {
       enter(t);
