@@ -467,21 +467,49 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The part of the scores' fingerprint row that a 32 x 32 block of raw scores gives.
-// first: index, from 1, of element 0's score; has: which elements attend.
-__device__ __forceinline__ void block_row(Lane& ln, const f32x16& z, uint64_t first, uint32_t has) {
-  uint64_t s = 0, ws = 0;
+// The part of the scores' fingerprint row that a lane has of a tile: sums of the raw scores'
+// 16-bit halves, and weighted by their rows within the tile (and tokens, for dk and dv), in 32
+// bits: at most 32 elements of weight below 64.  One dot product of halves does what a 64-bit
+// addition or multiplication takes two to four issues for (8192 tokens, 64/8 heads of 128:
+// the forward pass with its row 1.16 ms where it took 2.72).
+struct ScoreSums {
+  uint32_t lo = 0, hi = 0, wlo = 0, whi = 0, x = 0;
+  float odd = 0.0f;  // 0, or NaN where a score was infinite or NaN
+};
+
+// Adds a 32 x 32 block, rows 32 n .. of the tile counted from the lane's first; has: which
+// elements attend (all: all do).
+__device__ __forceinline__ void add_scores(ScoreSums& c, const f32x16& z, int n, bool all, uint32_t has) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const uint32_t x = has >> r & 1u ? __float_as_uint(z[r]) : 0u;
-    s += x;
-    ws += (uint64_t)element_row(r, 0) * x;
-    ln.x ^= x;
-    ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
-    if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // in turn: all at once would not fit the registers
+    const uint32_t bits = __float_as_uint(z[r]), x = all || (has >> r & 1u) ? bits : 0u;
+    const uint32_t w = 32u * n + element_row(r, 0);
+    c.lo = udot2(x, 1u, c.lo);
+    c.hi = udot2(x, 1u << 16, c.hi);
+    if (w != 0) {
+      c.wlo = udot2(x, w, c.wlo);
+      c.whi = udot2(x, w << 16, c.whi);
+    }
+    c.x ^= x;
+    c.odd = __builtin_fmaf(__uint_as_float(x), 0.0f, c.odd);
   }
+}
+
+__device__ __forceinline__ uint32_t nonfinite_scores(const f32x16& z, bool all, uint32_t has) {
+  uint32_t n = 0;
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    n += (all || (has >> r & 1u)) && !(__builtin_fabsf(z[r]) < __builtin_inff()) ? 1u : 0u;
+  return n;
+}
+
+// Joins a tile's sums; first: index, from 1, of the lane's first score of the tile, step: of
+// the next row.
+__device__ __forceinline__ void join_scores(Lane& ln, const ScoreSums& c, uint64_t first, uint64_t step) {
+  const uint64_t s = c.lo + ((uint64_t)c.hi << 16);
   ln.s += s;
-  ln.w += ws + first * s;
+  ln.w += first * s + step * (c.wlo + ((uint64_t)c.whi << 16));
+  ln.x ^= c.x;
 }
 
 }  // namespace

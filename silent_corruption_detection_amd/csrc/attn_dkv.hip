@@ -128,15 +128,38 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
         }
         uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
         if constexpr (ROW) {
-          // the rows of a block are not evenly spaced where heads are grouped
+          // row r = token G + head of the queries is row token hq + head of the scores', so
+          // token (hq - G) + r: the sums weighted by r and, where heads are grouped, by token
+          uint32_t has = 0xFFFFu;
+          if (masked) {
+            has = 0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (masked && first + element_row(e, 0) >= all) continue;
-            const uint32_t r = (uint32_t)q0 + 32u * n + element_row(e, half), x = __float_as_uint(s[e]);
-            ln.s += x;
-            ln.w += (flat_row(a, p, r) * a.kw + (uint32_t)key + 1u) * x;
-            ln.x ^= x;
-            ln.nf += ((x & 0x7F800000u) + 0x00800000u) >> 31;
+            for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
+          }
+          if (key < p.lk) {
+            ScoreSums c;
+            if (masked) add_scores(c, s, 0, false, has);
+            else add_scores(c, s, 0, true, has);
+            const uint32_t row = (uint32_t)q0 + 32u * n + 4u * half;
+            const uint64_t at_row = (uint64_t)p.q0 * a.hq + p.head * a.G + row;
+            join_scores(ln, c, at_row * a.kw + (uint32_t)key + 1u, a.kw);
+            if (a.hq != a.G) {
+              const uint32_t token = token_of(a, row);
+              uint32_t tlo = c.wlo, thi = c.whi;
+              if (a.G != 1) {
+                tlo = thi = 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const uint32_t x = has >> e & 1u ? __float_as_uint(s[e]) : 0u;
+                  const uint32_t w = token_of(a, row + element_row(e, 0)) - token;
+                  tlo = udot2(x, w, tlo);
+                  thi = udot2(x, w << 16, thi);
+                }
+              }
+              ln.w += (uint64_t)(a.hq - a.G) * a.kw *
+                      ((uint64_t)token * (c.lo + ((uint64_t)c.hi << 16)) + tlo + ((uint64_t)thi << 16));
+            }
+            if (c.odd != c.odd) ln.nf += nonfinite_scores(s, false, has);
           }
         }
         f32x16 ds;

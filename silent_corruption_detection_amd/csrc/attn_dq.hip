@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
     const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 31u));
     const int32_t from = keys_begin(a, p, token(r0 + 31u)), to = keys_end(a, p, token(r0));
     const int32_t t0 = wg_begin / (int32_t)kAttnTile, t1 = (wg_end + (int32_t)kAttnTile - 1) / (int32_t)kAttnTile;
+    const uint64_t first_score = flat * a.kw + 4u * half + 1u;  // of the lane's query, from 1
     const int shift = grad_shift<T>(a);
     const float f = power_of_two(shift - (int)kPShift<T>);
     f32x16 acc[DB];
@@ -103,7 +104,13 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
 #pragma unroll
             for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
           }
-          block_row(ln, s, flat * a.kw + (uint32_t)k0 + 32u * n + 4u * half + 1u, r < R ? has : 0u);
+          if (r < R) {
+            ScoreSums c;
+            if (masked) add_scores(c, s, 0, false, has);
+            else add_scores(c, s, 0, true, has);
+            join_scores(ln, c, first_score + (uint32_t)(k0 + 32 * n), 1u);
+            if (c.odd != c.odd) ln.nf += nonfinite_scores(s, false, has);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {

@@ -69,7 +69,7 @@ __device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, ui
 constexpr float kFarOut = 0x1p27f;
 
 template <class T, int DB, int W, int QB, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W, W * QB == 4 && !ROW ? 2 : 1) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, W * QB == 4 ? 2 : 1) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   constexpr uint32_t kBytes = tile_bytes<DB>();
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
@@ -115,8 +115,15 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 && !ROW ? 2 : 1) attn_kern
 #pragma unroll
     for (int b = 0; b < QB; ++b)
       first_score[b] = flat_row(a, p, min(r0 + 32u * b + (lane & 31u), R - 1u)) * a.kw + 4u * half + 1u;
-    const auto score_row = [&](int b, int n, const f32x16& z, int32_t k0, uint32_t has) SDC_INLINE {
-      block_row(ln, z, first_score[b] + (uint32_t)(k0 + 32 * n), r0 + 32u * b + (lane & 31u) < R ? has : 0u);
+    // the tile's part of the row; has: which of the scores attend (cut tiles)
+    const auto score_row = [&](int b, const f32x16 (&z)[2], int32_t k0, bool all, const uint32_t (&has)[2])
+                               SDC_INLINE {
+      if (r0 + 32u * b + (lane & 31u) >= R) return;
+      ScoreSums c;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) add_scores(c, z[n], n, all, has[n]);
+      join_scores(ln, c, first_score[b] + (uint32_t)k0, 1u);
+      if (c.odd != c.odd) ln.nf += nonfinite_scores(z[0], all, has[0]) + nonfinite_scores(z[1], all, has[1]);
     };
     TileLoader<DB, W> lk, lv;
     lk.init(key_rows(a, p), a.k_row, a.d);
@@ -172,30 +179,24 @@ __global__ void __launch_bounds__(64 * W, W * QB == 4 && !ROW ? 2 : 1) attn_kern
         }
       if (k0 < from || k0 + (int32_t)kAttnTile > to) {  // cut by a mask for some query
 #pragma unroll
-        for (int b = 0; b < QB; ++b)
+        for (int b = 0; b < QB; ++b) {
+          const uint32_t first = (uint32_t)(k0 + 4 * (int32_t)half - lo[b]), all = (uint32_t)max(hi[b] - lo[b], 0);
+          uint32_t has[2] = {0, 0};
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo[b]);
-            const uint32_t all = (uint32_t)max(hi[b] - lo[b], 0);
-            uint32_t has = 0;
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const bool on = first + element_row(e, 0) < all;
-              if constexpr (ROW) has |= on ? 1u << e : 0u;
-              else s[b][n][e] = on ? s[b][n][e] : -__builtin_inff();
-            }
-            if constexpr (ROW) {
-              score_row(b, n, s[b][n], k0, has);
+            for (int e = 0; e < 16; ++e) has[n] |= first + 32u * n + element_row(e, 0) < all ? 1u << e : 0u;
+          if constexpr (ROW) score_row(b, s[b], k0, false, has);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) s[b][n][e] = has >> e & 1u ? s[b][n][e] : -__builtin_inff();
-            }
-          }
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[b][n][e] = has[n] >> e & 1u ? s[b][n][e] : -__builtin_inff();
+        }
         redo |= tile_nonfinite<T, DB>(lds + buf * (2u * kBytes) + kBytes);
       } else if constexpr (ROW) {
+        const uint32_t has[2] = {0xFFFFu, 0xFFFFu};
 #pragma unroll
-        for (int b = 0; b < QB; ++b)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) score_row(b, n, s[b][n], k0, 0xFFFFu);
+        for (int b = 0; b < QB; ++b) score_row(b, s[b], k0, true, has);
       }
 #pragma unroll
       for (int b = 0; b < QB; ++b) {
