@@ -116,9 +116,7 @@ constexpr uint32_t kMaxUnits = 1u << 23;  // a grid has fewer than 2^32 threads
 struct Attn {
   uint64_t rows_q, rows_k;
   uint32_t waves;                       // of the forward pass' and dq's workgroups
-  uint32_t blocks;                      // of 32 queries of a wave of the forward pass
-  uint32_t tiles_q, units_q, splits;    // of the forward pass; splits of its keys
-  uint32_t tiles_dq, units_dq;
+  uint32_t tiles_q, units_q, splits;    // splits: of the forward pass' keys
   uint32_t tiles_k, units_k, splits_k;  // of dk and dv: splits of the queries
 };
 
@@ -172,17 +170,11 @@ Attn plan_attn(const sdc_attn* h) {
   const uint64_t len_q = packed ? (h->len_q + some - 1) / some : h->len_q;
   const uint64_t len_k = packed ? (h->len_k + some - 1) / some : h->len_k;
   p.waves = len_q * G <= 32 ? 1 : 4;
-  p.blocks = p.waves == 4 && getenv("ATTN_B") ? atoi(getenv("ATTN_B")) : 1;
-  const uint32_t rows = 32 * p.waves * p.blocks, extra = packed ? (uint32_t)h->batch : 0;
-  const auto tiles_of = [&](uint32_t each) {
-    return packed ? (uint32_t)(h->len_q * G / each) + extra : tiles(h->len_q * G, each);
-  };
-  p.tiles_q = tiles_of(rows);
-  p.tiles_dq = tiles_of(32 * p.waves);
+  const uint32_t rows = 32 * p.waves, extra = packed ? (uint32_t)h->batch : 0;
+  p.tiles_q = packed ? (uint32_t)(h->len_q * G / rows) + extra : tiles(h->len_q * G, rows);
   p.tiles_k = packed ? (uint32_t)(h->len_k / 128) + extra : tiles(h->len_k, 128);
   const uint32_t each = (uint32_t)h->heads_k * (packed ? 1u : (uint32_t)h->batch);
   p.units_q = p.tiles_q * each;
-  p.units_dq = p.tiles_dq * each;
   p.units_k = p.tiles_k * each;
   // Enough workgroups for two a CU, of at least four tiles of keys
   uint64_t keys = len_k;
@@ -209,7 +201,7 @@ AttnLayout layout_attn(const sdc_attn* h, const Attn& p, bool grad) {
     return here;
   };
   const uint64_t q = p.rows_q * h->heads_q, k = p.rows_k * h->heads_k;
-  o.rows = take(32ull * (grad ? (uint64_t)p.units_dq + (uint64_t)p.units_k * p.splits_k + 1
+  o.rows = take(32ull * (grad ? (uint64_t)p.units_q + (uint64_t)p.units_k * p.splits_k + 1
                               : (uint64_t)p.units_q * p.splits));
   o.part = take(!grad && p.splits > 1 ? 4ull * p.splits * q * h->d : 0);
   o.ml = take(!grad && p.splits > 1 ? 8ull * p.splits * q : 0);
@@ -299,7 +291,7 @@ extern "C" int32_t sdc_attention(const sdc_attn* h, void* d_ws, uint64_t ws_byte
     a.lse = d_lse;
     a.part = reinterpret_cast<float*>(ws + o.part);
     a.part_ml = reinterpret_cast<float2*>(ws + o.ml);
-    if ((st = launch_attn(AttnLaunch{h->dtype, p.waves, p.blocks}, a, s))) return st;
+    if ((st = launch_attn(AttnLaunch{h->dtype, p.waves}, a, s))) return st;
   }
   return d_row ? launch_merge_tile_rows(rows, p.units_q * p.splits, nullptr, 0, d_row, nullptr, s) : SDC_OK;
 }
@@ -325,7 +317,7 @@ extern "C" int32_t sdc_attention_grad(const sdc_attn* h, const void* d_out, cons
   if (ws_bytes < o.end) return SDC_ERR_WORKSPACE;
   hipStream_t s = as_stream(stream);
   unsigned char* ws = static_cast<unsigned char*>(d_ws);
-  sdc_row *rows_q = reinterpret_cast<sdc_row*>(ws + o.rows), *rows_k = rows_q + p.units_dq;
+  sdc_row *rows_q = reinterpret_cast<sdc_row*>(ws + o.rows), *rows_k = rows_q + p.units_q;
   const uint32_t n_rows_k = p.units_k * p.splits_k;
   AttnArgs a = attn_args(h);
   a.dout = static_cast<const unsigned char*>(d_dout);
@@ -345,7 +337,7 @@ extern "C" int32_t sdc_attention_grad(const sdc_attn* h, const void* d_out, cons
   a.l2 = l2;
   a.delta = delta;
   a.norms = norms;
-  const bool keys = d_dk != nullptr && p.units_k > 0, queries = d_dq != nullptr && p.units_dq > 0;
+  const bool keys = d_dk != nullptr && p.units_k > 0, queries = d_dq != nullptr && p.units_q > 0;
   if (keys) {
     a.tiles = p.tiles_k;
     a.units = p.units_k;
@@ -355,21 +347,21 @@ extern "C" int32_t sdc_attention_grad(const sdc_attn* h, const void* d_out, cons
     a.dv = static_cast<uint16_t*>(d_dv);
     a.part_k = reinterpret_cast<float*>(ws + o.part_k);
     a.part_v = reinterpret_cast<float*>(ws + o.part_v);
-    if ((st = launch_attn_dkv(AttnLaunch{h->dtype, 4, 1}, a, s))) return st;
+    if ((st = launch_attn_dkv(AttnLaunch{h->dtype, 4}, a, s))) return st;
   }
   if (queries) {
-    a.tiles = p.tiles_dq;
-    a.units = p.units_dq;
+    a.tiles = p.tiles_q;
+    a.units = p.units_q;
     a.splits = 1;
     a.rows = d_row ? rows_q : nullptr;
     a.dq = static_cast<uint16_t*>(d_dq);
-    if ((st = launch_attn_dq(AttnLaunch{h->dtype, p.waves, 1}, a, s))) return st;
+    if ((st = launch_attn_dq(AttnLaunch{h->dtype, p.waves}, a, s))) return st;
   }
   if (!d_row) return SDC_OK;
   // both launches compute the scores; d_row is dk's and dv's where those ran
   if (queries && keys &&
-      (st = launch_merge_tile_rows(rows_q, p.units_dq, d_ref, col_mask, rows_k + n_rows_k, d_mismatch, s)))
+      (st = launch_merge_tile_rows(rows_q, p.units_q, d_ref, col_mask, rows_k + n_rows_k, d_mismatch, s)))
     return st;
   return keys ? launch_merge_tile_rows(rows_k, n_rows_k, d_ref, col_mask, d_row, d_mismatch, s)
-              : launch_merge_tile_rows(rows_q, queries ? p.units_dq : 0, d_ref, col_mask, d_row, d_mismatch, s);
+              : launch_merge_tile_rows(rows_q, queries ? p.units_q : 0, d_ref, col_mask, d_row, d_mismatch, s);
 }

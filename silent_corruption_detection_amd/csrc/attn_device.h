@@ -58,7 +58,7 @@ struct AttnArgs {
 
 struct AttnLaunch {
   uint32_t dtype;
-  uint32_t waves, blocks;  // waves of a workgroup, blocks of 32 queries of a wave
+  uint32_t waves;  // of 32 queries (keys, for dk and dv)
 };
 int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
 int32_t launch_attn_dq(const AttnLaunch& l, const AttnArgs& a, hipStream_t s);
@@ -356,14 +356,21 @@ struct TileReads {
     col0 = tile + cols;
     col1 = tile + (cols ^ 32u) + 512u;  // eight rows on, the swizzle's bit 1 is the other one
   }
-  // The same of the tile `by` bytes on.
-  __device__ __forceinline__ void move(uint32_t by) {
+  // The same of the tile `by` bytes on.  (Kept as they are: a read's constant then fits its
+  // instruction.)
+  __device__ __forceinline__ void move_rows(uint32_t by) {
     row0 += by;
     row1 += by;
+    asm volatile("" : "+v"(row0), "+v"(row1));
+  }
+  __device__ __forceinline__ void move_columns(uint32_t by) {
     col0 += by;
     col1 += by;
-    // kept as they are: a read's constant then fits its instruction
-    asm volatile("" : "+v"(row0), "+v"(row1), "+v"(col0), "+v"(col1));
+    asm volatile("" : "+v"(col0), "+v"(col1));
+  }
+  __device__ __forceinline__ void move(uint32_t by) {
+    move_rows(by);
+    move_columns(by);
   }
   // Rows 32 b .. of the tile, elements 16 s .. of each: the sum runs along the rows.
   // tile: bytes to another one, a constant.

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
           for (int e = 0; e < 16; ++e)
             if (first + element_row(e, 0) >= all) s[e] = ds[e] = 0.0f;
         }
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const typename T::frag w = operand<T>(s, i), x = operand<T>(ds, i);
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
             dk[m] = mfma32(at.column(0, m, 2 * n + i), x, dk[m]);
           }
         }
+        __builtin_amdgcn_s_setprio(0);
       }
     }
     const uint64_t key_row = (uint64_t)(p.k0 + (uint32_t)key) * a.hk + p.head;
