@@ -44,6 +44,12 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& a, const Place32& p, int
   }
 }
 
+// Fragments of its keys that a wave holds in registers; for heads of 128 all would be one more than
+// there are registers for, and a spilled one waits for all loads in flight, the next
+// tile's among them: the lane's own slot in LDS does not (see below for what it gave).
+template <int DB>
+constexpr int dkv_held() { return DB == 4 ? 5 : 2 * DB; }
+
 // A workgroup of W waves takes 32 W keys, a wave 32 of them, keeps them and their values
 // in registers and streams the queries that attend them, of all heads that share them,
 // and their rows of dout past them in tiles of 64, so that the sums over queries and over
@@ -57,6 +63,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   constexpr uint32_t kBytes = tile_bytes<DB>();
   constexpr uint32_t kBuf = 2u * kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
+  constexpr int kHeld = dkv_held<DB>();
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
   const Place32 p = place_of<true>(a, unit, 32u * W);
   Lane ln;
@@ -104,6 +111,10 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
       if (wave == 0) load4_to_lds(l2 + row, base + 2u * kBytes);
       if (wave == W - 1) load4_to_lds(delta + row, base + 2u * kBytes + 4u * kAttnTile);
     };
+    const uint32_t put = lds0 + 2u * kBuf + threadIdx.x * 16u;  // the lane's fragments of its key that LDS holds
+#pragma unroll
+    for (int i = kHeld; i < 2 * DB; ++i)
+      *(SDC_LDS typename T::frag*)(uintptr_t)(put + (i - kHeld) * 16u * 64u * W) = k[i];
     if (t0 < t1) fill(t0, 0);
     bool redo = false;
     uint32_t buf = 0;
@@ -123,7 +134,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
         for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) {
-          s = mfma32(at.row(0, n, i), k[i], s);
+          s = mfma32(at.row(0, n, i), i < kHeld ? k[i] : *(const SDC_LDS typename T::frag*)(uintptr_t)(put + (i - kHeld) * 16u * 64u * W), s);
           dp = mfma32(at.row(kBytes, n, i), v[i], dp);
         }
         uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
@@ -257,7 +268,7 @@ int32_t launch_attn_dkv(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto shape = [&](auto db) {
       constexpr int DB = decltype(db)::value, W = 4;
       const dim3 grid(a.units * a.splits), block(64 * W);
-      constexpr uint32_t bytes = 2u * (2u * tile_bytes<DB>() + 2u * kAttnTile * 4u);
+      constexpr uint32_t bytes = 2u * (2u * tile_bytes<DB>() + 2u * kAttnTile * 4u) + (2 * DB - dkv_held<DB>()) * 1024u * W;
       const bool split = a.splits > 1;
       if (a.rows && split) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, true>), grid, block, bytes, s, a);
       else if (a.rows) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, false>), grid, block, bytes, s, a);
