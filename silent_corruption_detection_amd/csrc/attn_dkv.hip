@@ -50,6 +50,9 @@ __device__ __forceinline__ void dkv_row(const AttnArgs& a, const Place32& p, int
 template <int DB>
 constexpr int dkv_held() { return DB == 4 ? 5 : 2 * DB; }
 
+template <int DB, bool ROW>
+constexpr uint32_t dkv_buffer() { return 2u * tile_bytes<DB>() + (ROW ? 3u : 2u) * kAttnTile * 4u; }
+
 // A workgroup of W waves takes 32 W keys, a wave 32 of them, keeps them and their values
 // in registers and streams the queries that attend them, of all heads that share them,
 // and their rows of dout past them in tiles of 64, so that the sums over queries and over
@@ -62,7 +65,7 @@ template <class T, int DB, int W, bool ROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   constexpr uint32_t kBytes = tile_bytes<DB>();
-  constexpr uint32_t kBuf = 2u * kBytes + 2u * kAttnTile * 4u;  // queries, dout, l2, delta
+  constexpr uint32_t kBuf = dkv_buffer<DB, ROW>();  // queries, dout, l2, delta, and with rows tokens
   constexpr int kHeld = dkv_held<DB>();
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
   const Place32 p = place_of<true>(a, unit, 32u * W);
@@ -110,6 +113,9 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
       const uint32_t row = min(r + lane, (uint32_t)R - 1u);
       if (wave == 0) load4_to_lds(l2 + row, base + 2u * kBytes);
       if (wave == W - 1) load4_to_lds(delta + row, base + 2u * kBytes + 4u * kAttnTile);
+      if (ROW && wave == 1)  // the rows' tokens, from the first's
+        *(SDC_LDS uint32_t*)(uintptr_t)(base + 2u * kBytes + 8u * kAttnTile + 4u * lane) =
+            token_of(a, r + lane) - token_of(a, r);
     };
     const uint32_t put = lds0 + 2u * kBuf + threadIdx.x * 16u;  // the lane's fragments of its key that LDS holds
 #pragma unroll
@@ -132,10 +138,16 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
         f32x16 s, dp;
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = dp[e] = 0.0f;
+        // with rows the scores first, all that the row takes of them next: both products and the
+        // row's sums at a time would not fit the registers
+        const auto key_frag = [&](int i) SDC_INLINE {
+          return i < kHeld ? k[i]
+                           : *(const SDC_LDS typename T::frag*)(uintptr_t)(put + (i - kHeld) * 16u * 64u * W);
+        };
 #pragma unroll
         for (int i = 0; i < 2 * DB; ++i) {
-          s = mfma32(at.row(0, n, i), i < kHeld ? k[i] : *(const SDC_LDS typename T::frag*)(uintptr_t)(put + (i - kHeld) * 16u * 64u * W), s);
-          dp = mfma32(at.row(kBytes, n, i), v[i], dp);
+          s = mfma32(at.row(0, n, i), key_frag(i), s);
+          if constexpr (!ROW) dp = mfma32(at.row(kBytes, n, i), v[i], dp);
         }
         uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
         if constexpr (ROW) {
@@ -155,16 +167,19 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
             const uint64_t at_row = (uint64_t)p.q0 * a.hq + p.head * a.G + row;
             join_scores(ln, c, at_row * a.kw + (uint32_t)key + 1u, a.kw);
             if (a.hq != a.G) {
-              const uint32_t token = token_of(a, row);
+              const uint32_t token = token_of(a, a.G != 1 ? (uint32_t)q0 : row);
               uint32_t tlo = c.wlo, thi = c.whi;
               if (a.G != 1) {
                 tlo = thi = 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const uint32_t x = has >> e & 1u ? __float_as_uint(s[e]) : 0u;
-                  const uint32_t w = token_of(a, row + element_row(e, 0)) - token;
-                  tlo = udot2(x, w, tlo);
-                  thi = udot2(x, w << 16, thi);
+                for (int g = 0; g < 4; ++g) {
+                  const u32x4 w = *reinterpret_cast<const u32x4*>(et + kAttnTile + 32 * n + 8 * g + 4 * half);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t x = has >> (4 * g + e) & 1u ? __float_as_uint(s[4 * g + e]) : 0u;
+                    tlo = udot2(x, w[e], tlo);
+                    thi = udot2(x, w[e] << 16, thi);
+                  }
                 }
               }
               ln.w += (uint64_t)(a.hq - a.G) * a.kw *
@@ -172,6 +187,9 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
             }
             if (c.odd != c.odd) ln.nf += nonfinite_scores(s, false, has);
           }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < 2 * DB; ++i) dp = mfma32(at.row(kBytes, n, i), v[i], dp);
         }
         f32x16 ds;
 #pragma unroll
@@ -268,7 +286,8 @@ int32_t launch_attn_dkv(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto shape = [&](auto db) {
       constexpr int DB = decltype(db)::value, W = 4;
       const dim3 grid(a.units * a.splits), block(64 * W);
-      constexpr uint32_t bytes = 2u * (2u * tile_bytes<DB>() + 2u * kAttnTile * 4u) + (2 * DB - dkv_held<DB>()) * 1024u * W;
+      const uint32_t bytes =
+          2u * (a.rows ? dkv_buffer<DB, true>() : dkv_buffer<DB, false>()) + (2 * DB - dkv_held<DB>()) * 1024u * W;
       const bool split = a.splits > 1;
       if (a.rows && split) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, true>), grid, block, bytes, s, a);
       else if (a.rows) hipLaunchKernelGGL((attn_dkv_kernel<T, DB, W, true, false>), grid, block, bytes, s, a);
