@@ -176,11 +176,13 @@ Attn plan_attn(const sdc_attn* h) {
   const uint32_t each = (uint32_t)h->heads_k * (packed ? 1u : (uint32_t)h->batch);
   p.units_q = p.tiles_q * each;
   p.units_k = p.tiles_k * each;
-  // Enough workgroups for two a CU, of at least four tiles of keys
+  // Enough workgroups for two a CU (five of one wave), of at least four tiles of keys; at most
+  // 64, which is what the launch that joins them takes
   uint64_t keys = len_k;
   if (h->window) keys = std::min<uint64_t>(keys, h->window + rows / G + 1);
-  p.splits = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((2 * kCus) / std::max(p.units_q, 1u),
-                                                                tiles(keys, 4 * kAttnTile)));
+  p.splits = (uint32_t)std::max<uint64_t>(
+      1, std::min<uint64_t>({(p.waves == 1 ? 5 * kCus : 2 * kCus) / std::max(p.units_q, 1u), tiles(keys, 4 * kAttnTile),
+                             64}));
   uint64_t queries = len_q;
   if (h->window) queries = std::min<uint64_t>(queries, h->window + 128);
   p.splits_k = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((4 * kCus) / std::max(p.units_k, 1u),

@@ -73,14 +73,18 @@ __device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, ui
 // (1058 TFLOP/s at 8192 tokens without a mask).  Waves of 64 queries, which read LDS half as
 // often but leave one wave a SIMD, measured 20 % slower (1500 us against 1234).
 //
+// Few queries, one wave: one buffer, so that five workgroups fit a CU and cover each
+// other's loads (8 x 1 query of 32/8 heads against 8191 keys: 59 us with two buffers, ONE with one).
+//
 // SPLIT: the keys in a.splits parts, each leaving its unscaled sums, m and l.
 constexpr float kFarOut = 0x1p27f;
 
 template <class T, int DB, int W, bool ROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
   constexpr uint32_t kBytes = tile_bytes<DB>();
   constexpr int32_t kTile = (int32_t)kAttnTile;
+  constexpr bool kTwo = W > 1;  // buffers
   const uint32_t unit = SPLIT ? blockIdx.x / a.splits : blockIdx.x, split = SPLIT ? blockIdx.x % a.splits : 0u;
   const Place32 p = place_of<false>(a, unit, 32u * W);
   Lane ln;
@@ -121,13 +125,22 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_kernel(const Attn
       lv.fill((uint32_t)(t * kTile), (uint32_t)p.lk, lds0 + to_buf * (2u * kBytes) + kBytes);
     };
     // On to tile t: this buffer is whole, everyone has left the other, the next is filled.
+    // One buffer: the wave has left it; its own loads fill it.
     const auto enter = [&](int32_t t) SDC_INLINE {
-      tile_barrier();
-      if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+      if constexpr (kTwo) {
+        tile_barrier();
+        if (t + 1 < t1) fill(t + 1, buf ^ 1u);
+      } else {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fill(t, 0);
+        tile_barrier();
+      }
     };
     const auto leave = [&]() SDC_INLINE {
-      at.move(buf ? 0u - 2u * kBytes : 2u * kBytes);
-      buf ^= 1u;
+      if constexpr (kTwo) {
+        at.move(buf ? 0u - 2u * kBytes : 2u * kBytes);
+        buf ^= 1u;
+      }
     };
     // A tile's scores, what the row takes of them, the masked ones as -inf; the largest of
     // the lane's query.
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_kernel(const Attn
     t1 = uniform(t1);
     const int32_t te = uniform(min(max((end + kTile - 1) / kTile, t0), t1));
     const int32_t tw = uniform(min(max(begin / kTile, t0), te));
-    if (t0 < t1) fill(t0, 0);
+    if (kTwo && t0 < t1) fill(t0, 0);
     int32_t t = t0;
     for (; t < tw; ++t) {
       enter(t);
@@ -278,19 +291,29 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a, uint64
   const uint32_t head = (uint32_t)(n % a.hq);
   if (a.seq_q && !in_sequences(a.seq_q, a.batch, a.len_q, (uint32_t)row)) return;
   const uint64_t at = ((head / a.G) * rows * a.G + row * a.G + head % a.G) * a.splits;
-  float top = -__builtin_inff(), sum = 0.0f;
-  for (uint32_t k = 0; k < a.splits; ++k) top = __builtin_fmaxf(top, a.part_ml[at + k].x);
-  const float m = top == -__builtin_inff() ? 0.0f : top;
-  float x[2] = {0.0f, 0.0f};
-#pragma unroll 4
-  for (uint32_t k = 0; k < a.splits; ++k) {
-    const float2 ml = a.part_ml[at + k];
-    const float f = __builtin_amdgcn_exp2f((ml.x - m) * a.c);
-    sum += ml.y * f;
-    const float* part = a.part + (at + k) * a.d;
+  // the splits' factors, one a lane (at most 64)
+  const float2 ml = lane < a.splits ? a.part_ml[at + lane] : float2{-__builtin_inff(), 0.0f};
+  float top = ml.x;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 64u * i < a.d) x[i] += part[lane + 64u * i] * f;
+  for (int o = 32; o > 0; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+  const float m = top == -__builtin_inff() ? 0.0f : top;
+  const float mine = __builtin_amdgcn_exp2f((ml.x - m) * a.c);
+  float x[2] = {0.0f, 0.0f}, sum = 0.0f;
+  for (uint32_t k = 0; k < a.splits; k += 8) {  // eight splits' loads in flight
+    float v[8][2];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i)
+        v[j][i] = k + j < a.splits && lane + 64u * i < a.d ? a.part[(at + k + j) * a.d + lane + 64u * i] : 0.0f;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      if (k + j >= a.splits) break;
+      const float f = __shfl(mine, k + j);
+      sum += __shfl(ml.y, k + j) * f;
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) x[i] += v[j][i] * f;
+    }
   }
   const bool none = top == -__builtin_inff() && !(sum != sum);
   if (lane == 0) a.lse[n] = none ? -__builtin_inff() : log_sum(top, a.scale, sum, 0.0f);
@@ -307,7 +330,7 @@ int32_t launch_attn(const AttnLaunch& l, const AttnArgs& a, hipStream_t s) {
     const auto launch = [&](auto db, auto waves) {
       constexpr int DB = decltype(db)::value, W = decltype(waves)::value;
       const dim3 grid(a.units * a.splits), block(64 * W);
-      constexpr uint32_t bytes = 4u * tile_bytes<DB>();
+      constexpr uint32_t bytes = (W > 1 ? 4u : 2u) * tile_bytes<DB>();
       const bool split = a.splits > 1;
       if (a.rows && split) hipLaunchKernelGGL((attn_kernel<T, DB, W, true, true>), grid, block, bytes, s, a);
       else if (a.rows) hipLaunchKernelGGL((attn_kernel<T, DB, W, true, false>), grid, block, bytes, s, a);
