@@ -11,6 +11,7 @@ Function names are those of the C ABI.
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -1062,7 +1063,7 @@ def _op_ws(ws, name, desc, dev, grad, made):
     """The workspace of a call, allocated where the caller gives none."""
     need = ctypes.c_uint64(0)
     args = (None, ctypes.byref(need)) if grad else (ctypes.byref(need), None)
-    _check(getattr(_lib, name)(ctypes.byref(desc), *args), name)
+    _check(getattr(_lib, name)(desc, *args), name)
     if ws is not None:
         return _arg(ws, "ws", torch.uint8, need.value, dev)
     ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
@@ -1091,69 +1092,76 @@ class _Attn(ctypes.Structure):
                    ("dtype", ctypes.c_uint32), ("flags", ctypes.c_uint32)])
 
 
+# the same packed at once: filling a ctypes structure field by field costs 6 us a call
+_ATTN = struct.Struct("=21QfIII")
+assert _ATTN.size == ctypes.sizeof(_Attn)
 _ATTN_ROW_STRIDE = 1 << 23  # of a row, in elements
 
 
 def _attn_rows(t, name, dims):
-    """A tensor of heads as the library takes it (a copy where its heads are not
-    contiguous or not at 16-byte boundaries)."""
+    """(a tensor of heads as the library takes it, its strides but the last): a copy where
+    its heads are not contiguous or not at 16-byte boundaries."""
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise ValueError(f"{name} must be a {dims}-D tensor")
     if t.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
     if t.get_device() < 0:
         raise ValueError(f"{name} is not on a GPU")
-    steps = [s for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
-    if (t.shape[-1] > 1 and t.stride(-1) != 1) or t.data_ptr() % 16 or any(s % 8 for s in steps) or (
-            t.shape[-3] > 1 and t.stride(-3) >= _ATTN_ROW_STRIDE):
-        t = t.contiguous()
-        if t.data_ptr() % 16:  # a contiguous view into the middle of a buffer
-            t = t.clone()
-    return t
+    *outer, row, head, last = t.stride() if dims == 4 else (0,) + t.stride()
+    if last != 1 or t.data_ptr() % 16 or (outer[0] | row | head) % 8 or row >= _ATTN_ROW_STRIDE:
+        # of one entry, row or element a stride means nothing
+        steps = [s for n, s in zip(t.shape, t.stride()) if n > 1]
+        if not (t.shape[-1] == 1 or last == 1) or t.data_ptr() % 16 or any(s % 8 for s in steps[:-1]) or (
+                t.shape[-3] > 1 and row >= _ATTN_ROW_STRIDE):
+            t = t.contiguous()
+            if t.data_ptr() % 16:  # a contiguous view into the middle of a buffer
+                t = t.clone()
+            *outer, row, head, last = t.stride() if dims == 4 else (0,) + t.stride()
+    return t, (outer[0], row, head)
 
 
 def _attn(q, k, v, causal, window, scale, seq_q, seq_k):
-    """(sdc_attn, device, [q, k, v] as it points into them)"""
+    """(sdc_attn as bytes, device, [q, k, v] as it points into them)"""
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be [batch, rows, heads, d], or [rows, heads, d] with seq_q and seq_k")
     dims = q.dim()
     if (seq_q is None) != (seq_k is None) or (seq_q is None) != (dims == 4):
         raise ValueError("packed sequences need 3-D tensors and both seq_q and seq_k, a batch 4-D ones and neither")
-    kept = [_attn_rows(t, n, dims) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    (q1, sq), (k1, sk), (v1, sv) = _attn_rows(q, "q", dims), _attn_rows(k, "k", dims), _attn_rows(v, "v", dims)
     dev = _cuda_device(q.get_device())
+    dtype, qs, ks = q.dtype, q.shape, k.shape
     for t, n in ((k, "k"), (v, "v")):
-        if t.dtype != q.dtype or not _on_device(t, dev):
-            raise ValueError(f"{n} must be {q.dtype} on {dev}, is {t.dtype} on {t.device}")
-    if k.shape != v.shape or k.shape[-1] != q.shape[-1] or (dims == 4 and k.shape[0] != q.shape[0]):
-        raise ValueError(f"shapes do not go together: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    if k.shape[-2] == 0 or q.shape[-2] == 0 or q.shape[-2] % k.shape[-2]:
-        raise ValueError(f"{q.shape[-2]} heads of queries cannot share {k.shape[-2]} of keys")
-    if q.shape[-1] % 8 or not 8 <= q.shape[-1] <= 128:
-        raise ValueError(f"heads must have a multiple of 8 elements, at most 128, not {q.shape[-1]}")
+        if t.dtype != dtype or not _on_device(t, dev):
+            raise ValueError(f"{n} must be {dtype} on {dev}, is {t.dtype} on {t.device}")
+    if ks != v.shape or ks[-1] != qs[-1] or (dims == 4 and ks[0] != qs[0]):
+        raise ValueError(f"shapes do not go together: q {tuple(qs)}, k {tuple(ks)}, v {tuple(v.shape)}")
+    d, heads_q, heads_k = qs[-1], qs[-2], ks[-2]
+    if heads_k == 0 or heads_q == 0 or heads_q % heads_k:
+        raise ValueError(f"{heads_q} heads of queries cannot share {heads_k} of keys")
+    if d % 8 or not 8 <= d <= 128:
+        raise ValueError(f"heads must have a multiple of 8 elements, at most 128, not {d}")
     if window < 0 or (window and not causal):
         raise ValueError("a window must not be negative and needs causal")
     if scale is None:
-        scale = q.shape[-1] ** -0.5
-    batch = q.shape[0]
+        scale = d ** -0.5
+    batch, pq, pk = qs[0], 0, 0
     if seq_q is not None:
         batch = seq_q.numel() - 1
         if batch < 0 or seq_k.numel() != batch + 1:
             raise ValueError("seq_q and seq_k need one offset more than there are sequences")
         _arg(seq_q, "seq_q", torch.int32, batch + 1, dev)
         _arg(seq_k, "seq_k", torch.int32, batch + 1, dev)
-    step = ctypes.c_uint64 * 3
-    strides = [step(*((t.stride() if dims == 4 else (0,) + t.stride())[:3])) for t in kept]
-    desc = _Attn(*(t.data_ptr() for t in kept), None if seq_q is None else seq_q.data_ptr(),
-                 None if seq_k is None else seq_k.data_ptr(), batch, q.shape[-3], k.shape[-3], q.shape[-2], k.shape[-2],
-                 q.shape[-1], *strides, int(window), scale, 1 if causal else 0, _TORCH_DTYPE[q.dtype], 0)
-    return desc, dev, kept
+        pq, pk = seq_q.data_ptr(), seq_k.data_ptr()
+    desc = _ATTN.pack(q1.data_ptr(), k1.data_ptr(), v1.data_ptr(), pq, pk, batch, qs[-3], ks[-3], heads_q, heads_k, d,
+                      *sq, *sk, *sv, window, scale, 1 if causal else 0, _TORCH_DTYPE[dtype], 0)
+    return desc, dev, (q1, k1, v1)
 
 
 def sdc_attention_ws_bytes(q, k, v, causal=False, window=0, scale=None, seq_q=None, seq_k=None):
     """(forward, gradient) workspace bytes of this attention."""
     h, _, _ = _attn(q, k, v, causal, window, scale, seq_q, seq_k)
     f, g = ctypes.c_uint64(0), ctypes.c_uint64(0)
-    _check(_lib.sdc_attention_ws_bytes(ctypes.byref(h), ctypes.byref(f), ctypes.byref(g)), "sdc_attention_ws_bytes")
+    _check(_lib.sdc_attention_ws_bytes(h, ctypes.byref(f), ctypes.byref(g)), "sdc_attention_ws_bytes")
     return f.value, g.value
 
 
@@ -1183,7 +1191,7 @@ def sdc_attention(q, k, v, causal=False, window=0, scale=None, seq_q=None, seq_k
     ws = _op_ws(ws, "sdc_attention_ws_bytes", h, dev, False, made)
     with _device_guard(dev):
         s = _scan_stream(stream, dev, made)
-        _check(_lib.sdc_attention(ctypes.byref(h), ws.data_ptr(), ws.numel(), out.data_ptr(), lse.data_ptr(), row_p, s),
+        _check(_lib.sdc_attention(h, ws.data_ptr(), ws.numel(), out.data_ptr(), lse.data_ptr(), row_p, s),
                "sdc_attention")
     return out, lse
 
@@ -1223,7 +1231,7 @@ def sdc_attention_grad(q, k, v, out, lse, dout, causal=False, window=0, scale=No
     with _device_guard(dev):
         s = _scan_stream(stream, dev, made)
         _check(_lib.sdc_attention_grad(
-            ctypes.byref(h), out.data_ptr(), lse.data_ptr(), dout.data_ptr(), ws.data_ptr(), ws.numel(),
+            h, out.data_ptr(), lse.data_ptr(), dout.data_ptr(), ws.data_ptr(), ws.numel(),
             dq.data_ptr() if need_dq else None, dk.data_ptr() if need_dkv else None,
             dv.data_ptr() if need_dkv else None, ref_p, col_mask, row_p, mis_p, s), "sdc_attention_grad")
     return dq if need_dq else None, dk if need_dkv else None, dv if need_dkv else None
@@ -1236,11 +1244,13 @@ class _Ffn(ctypes.Structure):
                 + [("dtype", ctypes.c_uint32), ("act", ctypes.c_uint32)])
 
 
+_FFN = struct.Struct("=9QII")
+assert _FFN.size == ctypes.sizeof(_Ffn)
 _ACTS = {"silu": 0, "gelu_tanh": 1}
 
 
 def _ffn(x, w_gate, w_up, act):
-    """(sdc_ffn, device, [x, w_gate, w_up] as it points into them)"""
+    """(sdc_ffn as bytes, device, [x, w_gate, w_up] as it points into them)"""
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, not {act!r}")
     kept = [_head_rows(t, n) for t, n in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up"))]
@@ -1250,15 +1260,15 @@ def _ffn(x, w_gate, w_up, act):
             raise ValueError(f"{n} must be {x.dtype} {(w_gate.shape[0], x.shape[1])}, is {t.dtype} {tuple(t.shape)}")
         if not _on_device(t, dev):
             raise ValueError(f"{n} must be on {dev}, not {t.device}")
-    return (_Ffn(*(t.data_ptr() for t in kept), x.shape[0], x.shape[1], w_gate.shape[0],
-                 *(_row_stride(t) for t in kept), _TORCH_DTYPE[x.dtype], _ACTS[act]), dev, kept)
+    return (_FFN.pack(*(t.data_ptr() for t in kept), x.shape[0], x.shape[1], w_gate.shape[0],
+                      *(_row_stride(t) for t in kept), _TORCH_DTYPE[x.dtype], _ACTS[act]), dev, kept)
 
 
 def sdc_gated_ffn_ws_bytes(x, w_gate, w_up, act="silu"):
     """(forward, gradient) workspace bytes of this block."""
     b, _, _ = _ffn(x, w_gate, w_up, act)
     f, g = ctypes.c_uint64(0), ctypes.c_uint64(0)
-    _check(_lib.sdc_gated_ffn_ws_bytes(ctypes.byref(b), ctypes.byref(f), ctypes.byref(g)), "sdc_gated_ffn_ws_bytes")
+    _check(_lib.sdc_gated_ffn_ws_bytes(b, ctypes.byref(f), ctypes.byref(g)), "sdc_gated_ffn_ws_bytes")
     return f.value, g.value
 
 
@@ -1277,7 +1287,7 @@ def sdc_gated_ffn(x, w_gate, w_up, act="silu", out=None, row=None, ws=None, stre
     ws = _op_ws(ws, "sdc_gated_ffn_ws_bytes", b, dev, False, made)
     with _device_guard(dev):
         s = _scan_stream(stream, dev, made)
-        _check(_lib.sdc_gated_ffn(ctypes.byref(b), ws.data_ptr(), ws.numel(), out.data_ptr(), row_p, s),
+        _check(_lib.sdc_gated_ffn(b, ws.data_ptr(), ws.numel(), out.data_ptr(), row_p, s),
                "sdc_gated_ffn")
     return out
 
@@ -1311,7 +1321,7 @@ def sdc_gated_ffn_grad(x, w_gate, w_up, dh, act="silu", dx=None, dw_gate=None, d
     with _device_guard(dev):
         s = _scan_stream(stream, dev, made)
         _check(_lib.sdc_gated_ffn_grad(
-            ctypes.byref(b), dh.data_ptr(), _row_stride(dh), ws.data_ptr(), ws.numel(),
+            b, dh.data_ptr(), _row_stride(dh), ws.data_ptr(), ws.numel(),
             dx.data_ptr() if need_dx else None, dw_gate.data_ptr() if need_dw else None,
             dw_up.data_ptr() if need_dw else None, ref_p, col_mask, row_p, mis_p, s), "sdc_gated_ffn_grad")
     return dx if need_dx else None, dw_gate if need_dw else None, dw_up if need_dw else None

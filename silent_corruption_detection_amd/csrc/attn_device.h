@@ -135,16 +135,9 @@ __device__ __forceinline__ uint32_t seq_at(const int32_t* s, uint32_t i, uint32_
   return x < 0 ? 0u : min((uint32_t)x, rows);
 }
 
-// Whether a row lies in one of the sequences (whose offsets ascend).
+// Whether a row lies in one of the sequences, whose offsets ascend.
 __device__ __forceinline__ bool in_sequences(const int32_t* s, uint32_t batch, uint32_t rows, uint32_t row) {
-  uint32_t lo = 0, hi = batch;  // sequences lo .. begin at or before row
-  if (row < seq_at(s, 0, rows)) return false;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) / 2;
-    if (seq_at(s, mid, rows) <= row) lo = mid;
-    else hi = mid;
-  }
-  return row < seq_at(s, batch, rows);
+  return seq_at(s, 0, rows) <= row && row < seq_at(s, batch, rows);
 }
 
 // Unit -> sequence, tile, head of keys.  Heads run fastest, then sequences, and later
@@ -403,17 +396,18 @@ __device__ __forceinline__ void load_row(const unsigned char* p, bool has, uint3
   }
 }
 
-// Whether the tile holds an infinity or NaN.
-template <class T, int DB>
-__device__ __forceinline__ bool tile_nonfinite(const unsigned char* tile) {
+// Sets *found where the tile holds an infinity or NaN; each wave looks at its part.
+template <class T, int DB, int WAVES>
+__device__ __forceinline__ void find_nonfinite(const unsigned char* tile, uint32_t* found) {
   constexpr uint32_t one = std::is_same<T, Bf16>::value ? 0x00800080u : 0x04000400u;  // of the exponent's last bit
   uint32_t bad = 0;
-  for (uint32_t at = (threadIdx.x & 63u) * 16u; at < tile_bytes<DB>(); at += 1024u) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(tile + at);
+#pragma unroll
+  for (uint32_t i = 0; i < tile_bytes<DB>() / (1024u * WAVES); ++i) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(tile + (i * 64u * WAVES + threadIdx.x) * 16u);
     bad |= ((v.x & 0x7FFF7FFFu) + one) | ((v.y & 0x7FFF7FFFu) + one) | ((v.z & 0x7FFF7FFFu) + one) |
            ((v.w & 0x7FFF7FFFu) + one);
   }
-  return __any((bad & 0x80008000u) != 0u);
+  if (__any((bad & 0x80008000u) != 0u)) *found = 1u;
 }
 
 // sum_e x_e y_e of two rows.

@@ -64,6 +64,7 @@ constexpr uint32_t dkv_buffer() { return 2u * tile_bytes<DB>() + (ROW ? 3u : 2u)
 template <class T, int DB, int W, bool ROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
+  __shared__ uint32_t found;  // an infinity or NaN among the queries or rows of dout of a tile that a mask cuts
   constexpr uint32_t kBytes = tile_bytes<DB>();
   constexpr uint32_t kBuf = dkv_buffer<DB, ROW>();  // queries, dout, l2, delta, and with rows tokens
   constexpr int kHeld = dkv_held<DB>();
@@ -122,17 +123,22 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
     for (int i = kHeld; i < 2 * DB; ++i)
       *(SDC_LDS typename T::frag*)(uintptr_t)(put + (i - kHeld) * 16u * 64u * W) = k[i];
     if (t0 < t1) fill(t0, 0);
-    bool redo = false;
+    // cut by a mask for some key of the workgroup
+    const int32_t wg_from = first_row(wg_last), wg_to = wg0 + 32 * W <= p.lk ? last_row(wg0) : 0;
+    if (threadIdx.x == 0) found = 0;
     uint32_t buf = 0;
     for (int32_t t = t0; t < t1; ++t, at.move(buf ? 0u - kBuf : kBuf), buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
       const int32_t q0 = t * (int32_t)kAttnTile;
+      const unsigned char *qt = lds + buf * kBuf, *dt = qt + kBytes;
+      if (q0 < wg_from || q0 + (int32_t)kAttnTile > wg_to) {
+        find_nonfinite<T, DB, W>(qt, &found);
+        find_nonfinite<T, DB, W>(dt, &found);
+      }
       if (q0 >= end || q0 + (int32_t)kAttnTile <= begin) continue;
       const bool masked = q0 < from || q0 + (int32_t)kAttnTile > to;
-      const unsigned char *qt = lds + buf * kBuf, *dt = qt + kBytes;
       const float *lt = reinterpret_cast<const float*>(dt + kBytes), *et = lt + kAttnTile;
-      if (masked) redo |= tile_nonfinite<T, DB>(qt) || tile_nonfinite<T, DB>(dt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         f32x16 s, dp;
@@ -225,7 +231,8 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
     }
     const uint64_t key_row = (uint64_t)(p.k0 + (uint32_t)key) * a.hk + p.head;
     const uint64_t all_rows = (uint64_t)(a.seq_k ? a.len_k : a.batch * a.len_k) * a.hk;
-    if (redo) {
+    __syncthreads();  // found is
+    if (found) {
       for (int32_t x = key0; x < min(key0 + 32, p.lk); ++x)
         dkv_row<T, SPLIT>(a, p, x, max(first_row(x), t0 * (int32_t)kAttnTile),
                           min(last_row(x), t1 * (int32_t)kAttnTile), (uint64_t)(p.k0 + (uint32_t)x) * a.hk + p.head,

@@ -40,6 +40,7 @@ __device__ __forceinline__ void dq_row(const AttnArgs& a, const Place32& p, uint
 template <class T, int DB, int W, bool ROW>
 __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
+  __shared__ uint32_t found;  // an infinity or NaN among the keys of a tile that a mask cuts
   constexpr uint32_t kBytes = tile_bytes<DB>();
   const Place32 p = place_of<false>(a, blockIdx.x, 32u * W);
   Lane ln;
@@ -76,16 +77,17 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
       lv.fill((uint32_t)t * kAttnTile, (uint32_t)p.lk, lds0 + buf * (2u * kBytes) + kBytes);
     };
     if (t0 < t1) fill(t0, 0);
-    bool redo = false;
+    // cut by a mask for some query of the workgroup
+    const int32_t wg_from = keys_begin(a, p, token(wg0 + 32u * W - 1u)), wg_to = keys_end(a, p, token(wg0));
+    if (threadIdx.x == 0) found = 0;
     uint32_t buf = 0;
     for (int32_t t = t0; t < t1; ++t, at.move(buf ? 0u - 2u * kBytes : 2u * kBytes), buf ^= 1u) {
       tile_barrier();  // this buffer is whole, and everyone has left the other
       if (t + 1 < t1) fill(t + 1, buf ^ 1u);
       const int32_t k0 = t * (int32_t)kAttnTile;
+      if (k0 < wg_from || k0 + (int32_t)kAttnTile > wg_to) find_nonfinite<T, DB, W>(lds + buf * (2u * kBytes), &found);
       if (k0 >= end || k0 + (int32_t)kAttnTile <= begin) continue;
       const bool masked = k0 < from || k0 + (int32_t)kAttnTile > to;
-      const unsigned char* kt = lds + buf * (2u * kBytes);
-      if (masked) redo |= tile_nonfinite<T, DB>(kt);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         f32x16 s, dp;
@@ -132,7 +134,8 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
         }
       }
     }
-    if (redo) {
+    __syncthreads();  // found is
+    if (found) {
       const uint32_t rows = min(r0 + 32u, R);
       for (uint32_t x = r0; x < rows; ++x) dq_row<T>(a, p, x);
     } else if (r < R) {

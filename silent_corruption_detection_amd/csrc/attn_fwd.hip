@@ -82,6 +82,7 @@ constexpr float kFarOut = 0x1p27f;
 template <class T, int DB, int W, bool ROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) unsigned char lds[];
+  __shared__ uint32_t found;  // an infinity or NaN among the values of a tile that a mask cuts
   constexpr uint32_t kBytes = tile_bytes<DB>();
   constexpr int32_t kTile = (int32_t)kAttnTile;
   constexpr bool kTwo = W > 1;  // buffers
@@ -124,6 +125,9 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
       lk.fill((uint32_t)(t * kTile), (uint32_t)p.lk, lds0 + to_buf * (2u * kBytes));
       lv.fill((uint32_t)(t * kTile), (uint32_t)p.lk, lds0 + to_buf * (2u * kBytes) + kBytes);
     };
+    // cut by a mask for some query of the workgroup
+    const int32_t wg_from = keys_begin(a, p, token(wg0 + 32u * W - 1u)), wg_to = keys_end(a, p, token(wg0));
+    if (threadIdx.x == 0) found = 0;
     // On to tile t: this buffer is whole, everyone has left the other, the next is filled.
     // One buffer: the wave has left it; its own loads fill it.
     const auto enter = [&](int32_t t) SDC_INLINE {
@@ -135,6 +139,8 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
         fill(t, 0);
         tile_barrier();
       }
+      if (t * kTile < wg_from || t * kTile + kTile > wg_to)
+        find_nonfinite<T, DB, W>(lds + buf * (2u * kBytes) + kBytes, &found);
     };
     const auto leave = [&]() SDC_INLINE {
       if constexpr (kTwo) {
@@ -145,7 +151,6 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
     // A tile's scores, what the row takes of them, the masked ones as -inf; the largest of
     // the lane's query.
     f32x16 s[2];
-    bool redo = false;
     const auto scores = [&](int32_t t) SDC_INLINE {
       const int32_t k0 = t * kTile;
 #pragma unroll
@@ -176,7 +181,6 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[n][e] = has[n] >> e & 1u ? s[n][e] : -__builtin_inff();
-        redo |= tile_nonfinite<T, DB>(lds + buf * (2u * kBytes) + kBytes);
       } else if constexpr (ROW) {
         row(true, 0, 0);
       }
@@ -253,7 +257,8 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
       leave();
     }
     const float sum = both_sum(l);
-    if (redo) {
+    __syncthreads();  // found is
+    if (found) {
       const uint32_t rows = min(r0 + 32u, R);
       for (uint32_t x = r0; x < rows; ++x) attn_row<T, SPLIT>(a, p, x, t0 * kTile, t1 * kTile, split);
     } else if (r < R) {
