@@ -478,13 +478,12 @@ struct ScoreSums {
   float odd = 0.0f;  // 0, or NaN where a score was infinite or NaN
 };
 
-// Adds a 32 x 32 block, rows 32 n .. of the tile counted from the lane's first; has: which
-// elements attend (all: all do).
-__device__ __forceinline__ void add_scores(ScoreSums& c, const f32x16& z, int n, bool all, uint32_t has) {
+// Adds a 32 x 32 block, rows 32 n .. of the tile counted from the lane's first; scores that
+// do not attend are 0.
+__device__ __forceinline__ void add_scores(ScoreSums& c, const f32x16& z, int n) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    const uint32_t bits = __float_as_uint(z[r]), x = all || (has >> r & 1u) ? bits : 0u;
-    const uint32_t w = 32u * n + element_row(r, 0);
+    const uint32_t x = __float_as_uint(z[r]), w = 32u * n + element_row(r, 0);
     c.lo = udot2(x, 1u, c.lo);
     c.hi = udot2(x, 1u << 16, c.hi);
     if (w != 0) {
@@ -492,15 +491,14 @@ __device__ __forceinline__ void add_scores(ScoreSums& c, const f32x16& z, int n,
       c.whi = udot2(x, w << 16, c.whi);
     }
     c.x ^= x;
-    c.odd = __builtin_fmaf(__uint_as_float(x), 0.0f, c.odd);
+    c.odd = __builtin_fmaf(z[r], 0.0f, c.odd);
   }
 }
 
-__device__ __forceinline__ uint32_t nonfinite_scores(const f32x16& z, bool all, uint32_t has) {
+__device__ __forceinline__ uint32_t nonfinite_scores(const f32x16& z) {
   uint32_t n = 0;
 #pragma unroll
-  for (int r = 0; r < 16; ++r)
-    n += (all || (has >> r & 1u)) && !(__builtin_fabsf(z[r]) < __builtin_inff()) ? 1u : 0u;
+  for (int r = 0; r < 16; ++r) n += __builtin_fabsf(z[r]) < __builtin_inff() ? 0u : 1u;
   return n;
 }
 

@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
     const auto last_row = [&](int32_t x) SDC_INLINE {
       return a.window ? (int32_t)max(min(((int64_t)x - (p.lk - p.lq) + a.window) * a.G, (int64_t)R), (int64_t)0) : R;
     };
-    const int32_t lo = first_row(at_key), hi = key < p.lk ? last_row(at_key) : 0;
+    // the lane's key is attended by rows [lo, lo + span)
+    const int32_t lo = first_row(at_key);
+    const uint32_t span = (uint32_t)max((key < p.lk ? last_row(at_key) : 0) - lo, 0);
     const int32_t wg_last = min(wg0 + 32 * W - 1, p.lk - 1), w_last = min(key0 + 31, p.lk - 1);
     const int32_t wg_begin = first_row(wg0), wg_end = last_row(wg_last);
     const bool idle = key0 >= p.lk;
@@ -155,20 +157,17 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
           s = mfma32(at.row(0, n, i), key_frag(i), s);
           if constexpr (!ROW) dp = mfma32(at.row(kBytes, n, i), v[i], dp);
         }
-        uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
+        uint32_t first = (uint32_t)(q0 + 32 * n + 4 * (int32_t)half - lo);
         if constexpr (ROW) {
           // row r = token G + head of the queries is row token hq + head of the scores', so
           // token (hq - G) + r: the sums weighted by r and, where heads are grouped, by token
-          uint32_t has = 0xFFFFu;
           if (masked) {
-            has = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
+            for (int e = 0; e < 16; ++e) s[e] = first + element_row(e, 0) < span ? s[e] : 0.0f;
           }
           if (key < p.lk) {
             ScoreSums c;
-            if (masked) add_scores(c, s, 0, false, has);
-            else add_scores(c, s, 0, true, has);
+            add_scores(c, s, 0);
             const uint32_t row = (uint32_t)q0 + 32u * n + 4u * half;
             const uint64_t at_row = (uint64_t)p.q0 * a.hq + p.head * a.G + row;
             join_scores(ln, c, at_row * a.kw + (uint32_t)key + 1u, a.kw);
@@ -182,7 +181,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
                   const u32x4 w = *reinterpret_cast<const u32x4*>(et + kAttnTile + 32 * n + 8 * g + 4 * half);
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
-                    const uint32_t x = has >> (4 * g + e) & 1u ? __float_as_uint(s[4 * g + e]) : 0u;
+                    const uint32_t x = __float_as_uint(s[4 * g + e]);
                     tlo = udot2(x, w[e], tlo);
                     thi = udot2(x, w[e] << 16, thi);
                   }
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
               ln.w += (uint64_t)(a.hq - a.G) * a.kw *
                       ((uint64_t)token * (c.lo + ((uint64_t)c.hi << 16)) + tlo + ((uint64_t)thi << 16));
             }
-            if (c.odd != c.odd) ln.nf += nonfinite_scores(s, false, has);
+            if (c.odd != c.odd) ln.nf += nonfinite_scores(s);
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(64 * W, 2) attn_dkv_kernel(const AttnArgs a) {
           asm volatile("" : "+v"(first));  // so that this stays a branch: no selects for the other tiles
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (first + element_row(e, 0) >= all) s[e] = ds[e] = 0.0f;
+            if (first + element_row(e, 0) >= span) s[e] = ds[e] = 0.0f;
         }
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll

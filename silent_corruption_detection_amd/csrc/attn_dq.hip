@@ -53,7 +53,9 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
     load_row<T, DB>(query_row(a, p, c), r < R, a.d, q);
     load_row<T, DB>(a.dout + flat * (2u * a.d), r < R, a.d, dout);
     const float l2 = a.l2[grouped_row(a, p, c)], delta = a.delta[grouped_row(a, p, c)];
-    const int32_t mine = (int32_t)token_of(a, c), lo = keys_begin(a, p, mine), hi = keys_end(a, p, mine);
+    // the lane's query attends keys [lo, lo + span)
+    const int32_t mine = (int32_t)token_of(a, c), lo = keys_begin(a, p, mine);
+    const uint32_t span = (uint32_t)max(keys_end(a, p, mine) - lo, 0);
     const auto token = [&](uint32_t x) SDC_INLINE { return (int32_t)token_of(a, min(x, R - 1u)); };
     const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * W - 1u));
     const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 31u));
@@ -98,20 +100,17 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
           s = mfma32(at.row(0, n, i), q[i], s);
           dp = mfma32(at.row(kBytes, n, i), dout[i], dp);
         }
-        uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
+        uint32_t first = (uint32_t)(k0 + 32 * n + 4 * (int32_t)half - lo);
         if constexpr (ROW) {
-          uint32_t has = 0xFFFFu;
           if (masked) {
-            has = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) has |= first + element_row(e, 0) < all ? 1u << e : 0u;
+            for (int e = 0; e < 16; ++e) s[e] = first + element_row(e, 0) < span ? s[e] : 0.0f;
           }
           if (r < R) {
             ScoreSums c;
-            if (masked) add_scores(c, s, 0, false, has);
-            else add_scores(c, s, 0, true, has);
+            add_scores(c, s, 0);
             join_scores(ln, c, first_score + (uint32_t)(k0 + 32 * n), 1u);
-            if (c.odd != c.odd) ln.nf += nonfinite_scores(s, false, has);
+            if (c.odd != c.odd) ln.nf += nonfinite_scores(s);
           }
         }
 #pragma unroll
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(64 * W, W == 4 ? 2 : 1) attn_dq_kernel(const A
           asm volatile("" : "+v"(first));  // so that this stays a branch: no selects for the other tiles
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            s[e] = first + element_row(e, 0) < all ? s[e] : 0.0f;
+            s[e] = first + element_row(e, 0) < span ? s[e] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

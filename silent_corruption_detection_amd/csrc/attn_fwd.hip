@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
     typename T::frag q[2 * DB];
     load_row<T, DB>(query_row(a, p, mine), r < R, a.d, q);
     const auto token = [&](uint32_t x) SDC_INLINE { return (int32_t)token_of(a, min(x, R - 1u)); };
-    const int32_t lo = keys_begin(a, p, token(mine)), hi = keys_end(a, p, token(mine));
+    // the lane's query attends keys [lo, lo + span)
+    const int32_t lo = keys_begin(a, p, token(mine));
+    const uint32_t span = (uint32_t)max(keys_end(a, p, token(mine)) - lo, 0);
     // keys of the workgroup's, and of the wave's, queries: [begin, end), all attend [from, to)
     const int32_t wg_begin = keys_begin(a, p, token(wg0)), wg_end = keys_end(a, p, token(wg0 + 32u * W - 1u));
     const int32_t begin = keys_begin(a, p, token(r0)), end = keys_end(a, p, token(r0 + 31u));
@@ -161,29 +163,25 @@ __global__ void __launch_bounds__(64 * W, 2) attn_kernel(const AttnArgs a) {
       for (int i = 0; i < 2 * DB; ++i)
 #pragma unroll
         for (int n = 0; n < 2; ++n) s[n] = mfma32(at.row(0, n, i), q[i], s[n]);
-      const auto row = [&](bool all, uint32_t has0, uint32_t has1) SDC_INLINE {
-        if (r >= R) return;
-        ScoreSums c;
-        add_scores(c, s[0], 0, all, has0);
-        add_scores(c, s[1], 1, all, has1);
-        join_scores(ln, c, first_score + (uint32_t)k0, 1u);
-        if (c.odd != c.odd) ln.nf += nonfinite_scores(s[0], all, has0) + nonfinite_scores(s[1], all, has1);
+      const bool cut = k0 < from || k0 + kTile > to;  // by a mask, for some query of the wave
+      const uint32_t first = (uint32_t)(k0 + 4 * (int32_t)half - lo);
+      const auto mask = [&](float with) SDC_INLINE {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[n][e] = first + 32u * n + element_row(e, 0) < span ? s[n][e] : with;
       };
-      if (k0 < from || k0 + kTile > to) {  // cut by a mask for some query
-        const uint32_t first = (uint32_t)(k0 + 4 * (int32_t)half - lo), all = (uint32_t)max(hi - lo, 0);
-        uint32_t has[2] = {0, 0};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) has[n] |= first + 32u * n + element_row(e, 0) < all ? 1u << e : 0u;
-        if constexpr (ROW) row(false, has[0], has[1]);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[n][e] = has[n] >> e & 1u ? s[n][e] : -__builtin_inff();
-      } else if constexpr (ROW) {
-        row(true, 0, 0);
+      if constexpr (ROW) {
+        if (cut) mask(0.0f);
+        if (r < R) {
+          ScoreSums c;
+          add_scores(c, s[0], 0);
+          add_scores(c, s[1], 1);
+          join_scores(ln, c, first_score + (uint32_t)k0, 1u);
+          if (c.odd != c.odd) ln.nf += nonfinite_scores(s[0]) + nonfinite_scores(s[1]);
+        }
       }
+      if (cut) mask(-__builtin_inff());
       float most = s[0][0];
 #pragma unroll
       for (int n = 0; n < 2; ++n)
