@@ -185,8 +185,13 @@ Attn plan_attn(const sdc_attn* h) {
                              64}));
   uint64_t queries = len_q;
   if (h->window) queries = std::min<uint64_t>(queries, h->window + 128);
-  p.splits_k = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((4 * kCus) / std::max(p.units_k, 1u),
-                                                                  tiles(queries * G, 8 * kAttnTile)));
+  // Key tiles: two workgroups a CU, and twice that, so that the short sums that a causal mask
+  // leaves even out, where a split still has 64 tiles of queries: its fp32 sums are written
+  // and read again.  Measured (dk and dv in us, one split / two; two / four): 8192 tokens, 64/8
+  // heads of 128 3105 / 2068, 2 x 4096, 16/4 heads of 80 323 / 255, but 2 x 2048, 16 heads of 128 114 /
+  // 126.
+  const uint32_t tiles_of_q = tiles(queries * G, kAttnTile), units = std::max(p.units_k, 1u);
+  p.splits_k = std::max(1u, std::min({4 * kCus / units, std::max(2 * kCus / units, tiles_of_q / 64), tiles_of_q / 8}));
   return p;
 }
 

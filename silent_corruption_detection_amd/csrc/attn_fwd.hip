@@ -74,7 +74,7 @@ __device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, ui
 // often but leave one wave a SIMD, measured 20 % slower (1500 us against 1234).
 //
 // Few queries, one wave: one buffer, so that five workgroups fit a CU and cover each
-// other's loads (8 x 1 query of 32/8 heads against 8191 keys: 59 us with two buffers, ONE with one).
+// other's loads (8 x 1 query of 32/8 heads against 8191 keys: 59 us with two buffers, 55 with one).
 //
 // SPLIT: the keys in a.splits parts, each leaving its unscaled sums, m and l.
 constexpr float kFarOut = 0x1p27f;
