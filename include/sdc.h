@@ -1,7 +1,8 @@
 /*
  * sdc.h -- C ABI of libsdc.so, the MI355X (gfx950) integrity scan for
  * silent-data-corruption checks in data-parallel training, with the loss of a
- * linear head and the optimizer step between which the checks stand.
+ * linear head and the optimizer step between which the checks stand, and the
+ * two recomputed halves of a transformer block.
  *
  * What the library computes comes from these pages:
  *   [BLOG] AWS Machine Learning Blog, "Detecting and recovering from silent
@@ -35,7 +36,7 @@
  *     over raw bit patterns (floating-point data are never converted), so
  *     every row is exact and independent of launch shape and scheduling.
  *     Floating-point results (squared norms, the optimizer step, the loss of a
- *     linear head and its gradient) are summed in an order fixed by the plan or
+ *     linear head, attention, the feed-forward block and their gradients) are summed in an order fixed by the plan or
  *     the sizes, never by scheduling: a call repeated on the same inputs gives
  *     the same bits.
  *   - Functions are thread-safe.  Two scans that write the same output rows
@@ -614,7 +615,7 @@ int32_t sdc_cross_entropy_grad(const sdc_head* h_head, const float* d_lse, const
  *             of the len_q (len_k) rows there are (offsets outside those count as the
  *             nearest inside); rows of no sequence are not read and not written, and strides[0]
  *             is not used.
- *   scale     of the scores, finite and above 0.
+ *   scale     of the scores, from 2^-64 to 2^64.
  *   causal    1: query i of a sequence with lq queries and lk keys attends keys up to
  *             i + lk - lq (the last query attends all).
  *   window    with causal: only the last `window` of those.  0: all.
@@ -645,7 +646,7 @@ typedef struct {
  * Errors: SDC_ERR_INVALID (NULL, no heads, heads_q no multiple of heads_k, scale, a window
  * without causal, one seq without the other, flags), SDC_ERR_DTYPE, SDC_ERR_ALIGN,
  * SDC_ERR_RANGE (d, 2^31 rows times heads, batch 2^24, a row stride of 2^23, another of
- * 2^40, 2^19 tiles of 32 queries or 128 keys). */
+ * 2^40, 2^23 tiles of 32 queries or 128 keys). */
 int32_t sdc_attention_ws_bytes(const sdc_attn* h_attn, uint64_t* h_bytes, uint64_t* h_grad_bytes);
 
 /* d_out = softmax(scale q k^T) v, [rows of q][heads_q][d], contiguous, of the dtype;
@@ -654,7 +655,8 @@ int32_t sdc_attention_ws_bytes(const sdc_attn* h_attn, uint64_t* h_bytes, uint64
  *   d_row      NULL, or (16-byte aligned) the fingerprint row of the fp32 scores q k^T
  *              (unscaled) [rows of q][heads_q][len_k], key j of its sequence in column j,
  *              zero where not attended, as a scan of them in memory would give it.
- * d_out, d_ws: 16-byte aligned; d_ws not reused before the call's work has completed.
+ * d_out, d_ws: 16-byte aligned; neither may overlap the inputs, and d_ws is not reused before
+ * the call's work has completed.
  * ASYNCHRONOUS on stream.  Errors as sdc_attention_ws_bytes, and SDC_ERR_WORKSPACE,
  * SDC_ERR_HIP. */
 int32_t sdc_attention(const sdc_attn* h_attn, void* d_ws, uint64_t ws_bytes, void* d_out, float* d_lse,

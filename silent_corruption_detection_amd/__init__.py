@@ -1,6 +1,6 @@
 """Python binding of libsdc.so -- the MI355X integrity scan for silent data
-corruption checks, the loss of a linear head and the optimizer step (see
-include/sdc.h for the C ABI and the semantics).
+corruption checks, the loss of a linear head, the optimizer step, attention and
+the gated feed-forward block (see include/sdc.h for the C ABI and the semantics).
 
 Argument marshalling only: every computation runs in the library's HIP
 kernels.  PyTorch provides device memory and streams.  Importing this module
@@ -1144,6 +1144,8 @@ def _attn(q, k, v, causal, window, scale, seq_q, seq_k):
         raise ValueError("a window must not be negative and needs causal")
     if scale is None:
         scale = d ** -0.5
+    if not 2.0 ** -64 <= scale <= 2.0 ** 64:
+        raise ValueError(f"scale must be between 2^-64 and 2^64, not {scale}")
     batch, pq, pk = qs[0], 0, 0
     if seq_q is not None:
         batch = seq_q.numel() - 1

@@ -19,8 +19,6 @@
 // them, then dk and dv (csrc/attn_dkv.hip), dq (csrc/attn_dq.hip).  Bound by the matrix
 // cores and, beside them, LDS reads and the vector units' exponentials; few queries by
 // reading keys and values.
-#include <cmath>
-
 #include "attn_device.h"
 
 namespace sdc {
@@ -124,7 +122,7 @@ int32_t check_attn(const sdc_attn* h) {
   if (h == nullptr) return SDC_ERR_INVALID;
   if (h->dtype != SDC_BF16 && h->dtype != SDC_F16) return SDC_ERR_DTYPE;
   if (h->flags != 0 || h->causal > 1 || h->d == 0 || h->heads_k == 0 || h->heads_q == 0 ||
-      h->heads_q % h->heads_k != 0 || (h->window != 0 && !h->causal) || !(h->scale > 0.0f) || !std::isfinite(h->scale) ||
+      h->heads_q % h->heads_k != 0 || (h->window != 0 && !h->causal) || !(h->scale >= 0x1p-64f && h->scale <= 0x1p64f) ||
       (h->seq_q == nullptr) != (h->seq_k == nullptr))
     return SDC_ERR_INVALID;
   if (h->d % 8 != 0 || h->d > 128) return SDC_ERR_RANGE;
@@ -153,8 +151,8 @@ int32_t check_attn(const sdc_attn* h) {
   }
   if (reinterpret_cast<uintptr_t>(h->seq_q) % 4 || reinterpret_cast<uintptr_t>(h->seq_k) % 4) return SDC_ERR_ALIGN;
   // one tile of 32 queries, or of 128 keys, for each row at least
-  if (rows_q * h->heads_q / 32 + h->batch * h->heads_k * 2 >= kMaxUnits / 16 ||
-      rows_k * h->heads_k / 128 + h->batch * h->heads_k * 2 >= kMaxUnits / 16)
+  if (rows_q * h->heads_q / 32 + h->batch * h->heads_k * 2 >= kMaxUnits ||
+      rows_k * h->heads_k / 128 + h->batch * h->heads_k * 2 >= kMaxUnits)
     return SDC_ERR_RANGE;
   return SDC_OK;
 }

@@ -41,7 +41,7 @@ BAD_ATTN = [
     (dict(q=0), INVALID), (dict(k=0), INVALID), (dict(v=0), INVALID), (dict(d=0), INVALID), (dict(heads_q=0), INVALID),
     (dict(heads_k=0), INVALID), (dict(heads_k=3), INVALID), (dict(heads_q=1), INVALID), (dict(window=5), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=math.inf), INVALID),
-    (dict(scale=math.nan), INVALID), (dict(seq_q=0x4000), INVALID), (dict(seq_k=0x4000), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=1e-30), INVALID), (dict(scale=1e30), INVALID), (dict(seq_q=0x4000), INVALID), (dict(seq_k=0x4000), INVALID),
     (dict(d=60), RANGE), (dict(d=136), RANGE), (dict(batch=1 << 24), RANGE), (dict(len_q=1 << 31), RANGE),
     (dict(len_k=1 << 30), RANGE), (dict(batch=1 << 20, len_q=1 << 20), RANGE), (dict(heads_q=1 << 20, heads_k=1), RANGE),
     (dict(batch=1 << 23, len_q=1, len_k=1), RANGE), (dict(q=0x1008), ALIGN), (dict(k=0x2002), ALIGN), (dict(v=0x3008), ALIGN),
