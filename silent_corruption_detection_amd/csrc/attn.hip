@@ -26,7 +26,8 @@ namespace {
 
 // l2 and delta of every query, and for fp16 the largest sums of squares of the rows of
 // dout and v (of finite ones, in sequences: others have no say in what fp16 can hold).  16
-// lanes a row; bound by reading dout and out.
+// lanes a row; bound by reading dout and out (8192 tokens, 64 heads of 128: 268 MB in
+// 44 us, right after the passes that wrote them).
 template <class T>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a, const uint16_t* __restrict__ out,
                                                          const float* __restrict__ lse, uint64_t rows_q,
@@ -167,20 +168,29 @@ Attn plan_attn(const sdc_attn* h) {
   const uint64_t some = std::max<uint64_t>(h->batch, 1);
   const uint64_t len_q = packed ? (h->len_q + some - 1) / some : h->len_q;
   const uint64_t len_k = packed ? (h->len_k + some - 1) / some : h->len_k;
-  p.waves = len_q * G <= 32 ? 1 : 4;
-  const uint32_t rows = 32 * p.waves, extra = packed ? (uint32_t)h->batch : 0;
-  p.tiles_q = packed ? (uint32_t)(h->len_q * G / rows) + extra : tiles(h->len_q * G, rows);
-  p.tiles_k = packed ? (uint32_t)(h->len_k / 128) + extra : tiles(h->len_k, 128);
-  const uint32_t each = (uint32_t)h->heads_k * (packed ? 1u : (uint32_t)h->batch);
-  p.units_q = p.tiles_q * each;
-  p.units_k = p.tiles_k * each;
-  // Enough workgroups for two a CU (five of one wave), of at least four tiles of keys; at most
-  // 64, which is what the launch that joins them takes
-  uint64_t keys = len_k;
-  if (h->window) keys = std::min<uint64_t>(keys, h->window + rows / G + 1);
-  p.splits = (uint32_t)std::max<uint64_t>(
-      1, std::min<uint64_t>({(p.waves == 1 ? 5 * kCus : 2 * kCus) / std::max(p.units_q, 1u), tiles(keys, 4 * kAttnTile),
-                             64}));
+  const uint64_t each = h->heads_k * (packed ? 1 : h->batch);
+  // Enough workgroups to fill the chip, of at least four tiles of keys; at most 64 for a tile
+  // of queries, which is what the launch that joins them takes.
+  const auto with_waves = [&](uint32_t waves, uint32_t per_cu) {
+    const uint32_t rows = 32 * waves;
+    const uint64_t keys = h->window ? std::min<uint64_t>(len_k, h->window + rows / G + 1) : len_k;
+    p.waves = waves;
+    p.tiles_q = packed ? (uint32_t)(h->len_q * G / rows + h->batch) : tiles(h->len_q * G, rows);
+    p.units_q = (uint32_t)(p.tiles_q * each);
+    p.splits = (uint32_t)std::max<uint64_t>(
+        1, std::min<uint64_t>({per_cu * kCus / std::max(p.units_q, 1u), tiles(keys, 4 * kAttnTile), 64}));
+  };
+  // Up to 32 rows of queries: workgroups of one wave, whose single buffer is 8 kB for each 32
+  // elements of a row, as many of them as run on a CU at once.  8 sequences of 8191 keys, 32/8
+  // heads, one query each, with 4 / 5 / 6 / 8 of them a CU: 62.6 / 71.1 / 67.5 / 66.3 us with
+  // heads of 128, 48.6 / 50.9 / 45.9 / 49.2 of 80 and (8192 keys) 41.7 / 36.4 / 36.9 / 43.8 of
+  // 64.  Where even the splits leave fewer than three of them a CU, four waves that share the
+  // loads of a tile hide more of their latency: one sequence of 8191 keys 22.8 -> 21.5 us, of
+  // 65536 keys 71.0 -> 66.4; but 128 sequences of 2048 keys take 206 us so, and 197 with one.
+  if (len_q * G <= 32) with_waves(1, h->d > 96 ? 4 : 6);
+  if (len_q * G > 32 || (uint64_t)p.units_q * p.splits < 3 * kCus) with_waves(4, 2);
+  p.tiles_k = packed ? (uint32_t)(h->len_k / 128) + (uint32_t)h->batch : tiles(h->len_k, 128);
+  p.units_k = (uint32_t)(p.tiles_k * each);
   uint64_t queries = len_q;
   if (h->window) queries = std::min<uint64_t>(queries, h->window + 128);
   // Key tiles: two workgroups a CU, and twice that, so that the short sums that a causal mask

@@ -67,14 +67,16 @@ __device__ __forceinline__ void attn_row(const AttnArgs& a, const Place32& p, ui
 //
 // Two loops in one another, the outer for the tiles that raise a reference: the inner one,
 // which nearly all tiles take, then has no branch around the sums of values, which would cost
-// a copy of them each time (1218 -> 1163 us at 8192 tokens, 64/8 heads of 128, causal).
+// a copy of them each time (8192 tokens, causal: 1163 us against 1218 when it was built).
 //
 // Bound by the matrix cores and the vector units beside them, which two waves a SIMD overlap
-// (1058 TFLOP/s at 8192 tokens without a mask).  Waves of 64 queries, which read LDS half as
-// often but leave one wave a SIMD, measured 20 % slower (1500 us against 1234).
+// (8192 tokens, 64/8 heads of 128: 1041 us causal, 2017 us and 1090 TFLOP/s without a mask,
+// the matrix cores 53 % busy).  Waves of 64 queries, which read LDS half as
+// often but leave one wave a SIMD, measured 20 to 50 % slower; the next tile's scores between
+// this one's exponentials and products, which takes two sets of scores in registers, 45 %.
 //
-// Few queries, one wave: one buffer, so that five workgroups fit a CU and cover each
-// other's loads (8 x 1 query of 32/8 heads against 8191 keys: 59 us with two buffers, 55 with one).
+// Few queries, one wave: one buffer, so that four workgroups or more fit a CU and cover each
+// other's loads (8 x 1 query of 32/8 heads against 8191 keys, this launch: 59 us with two buffers, 55 with one).
 //
 // SPLIT: the keys in a.splits parts, each leaving its unscaled sums, m and l.
 constexpr float kFarOut = 0x1p27f;

@@ -78,7 +78,9 @@ int32_t check_ffn(const sdc_ffn* b) {
 // for each 64 of its k and some for its epilogue (6 steps of a 256 x 256 tile, 3 of a 128 x
 // 128 one, whose steps take 0.575 of the time with two workgroups a CU); dx's are the
 // longest, and are split as far as one of them would outlast the whole work's share of
-// a CU.
+// a CU.  Measured (bf16, us of the whole gradient with 256 / 128): 256 x 1024 x 4096 39.8 /
+// 35.3, 1037 x 1000 x 2731 65.2 / 70.7, 1024 x 2048 x 8192 195 / 211, 4096 x 2048 x 8192 702 /
+// 819; the rule takes the faster each time.
 void plan_products(Ffn* p) {
   const double steps_f = tiles(p->f, kTileK), steps_n = tiles(p->N, kTileK);
   double best = 0.0;

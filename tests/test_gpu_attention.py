@@ -485,3 +485,47 @@ def test_long_cache_past_32_bit_offsets():
     got = sdc.sdc_attention(q, k, v, True)
     want = sdc.sdc_attention(q, k.contiguous(), v.contiguous(), True)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+MANY = [  # single tokens and few queries of many sequences: one wave each, with and without splits
+    (100, 1, 70, 8, 8, 128, True, 0), (8, 2, 3301, 16, 8, 128, True, 0), (32, 1, 1500, 16, 8, 64, False, 0),
+    (100, 3, 400, 16, 8, 40, True, 90), (50, 5, 66, 32, 16, 96, True, 0), (100, 1, 1, 8, 8, 72, True, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("b, lq, lk, hq, hk, d, causal, window", MANY)
+def test_few_queries_of_many_sequences(b, lq, lk, hq, hk, d, causal, window, dtype):
+    say(f"case many {b} {lq} {lk} {hq} {hk} {d} {causal} {window} {dtype}")
+    q, k, v, do = make(b, lq, lk, hq, hk, d, dtype, seed=b + lk + d)
+    out, lse, dq, *_ = check(q, k, v, do, causal, window)
+    rows = torch.zeros(2, 4, dtype=torch.int64, device=DEV)
+    again = sdc.sdc_attention(q, k, v, causal, window, row=rows[0])
+    grads = sdc.sdc_attention_grad(q, k, v, out, lse, do, causal, window, row=rows[1])
+    torch.cuda.synchronize()
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse) and torch.equal(grads[0], dq)
+    assert torch.equal(rows[0], rows[1])
+
+
+def test_few_queries_of_many_packed_sequences():
+    lengths = torch.randint(0, 4, (450,), generator=torch.Generator().manual_seed(21)).tolist()
+    keys = torch.randint(0, 90, (450,), generator=torch.Generator().manual_seed(22)).tolist()
+    sq, sk = [0], [0]
+    for a, b in zip(lengths, keys):
+        sq.append(sq[-1] + a)
+        sk.append(sk[-1] + b)
+    q, k, v, do = (t[0] for t in make(1, sq[-1], sk[-1], 4, 2, 128, BF, seed=23))
+    check(q, k, v, do, True, seq=(sq, sk))
+
+
+@pytest.mark.parametrize("hold", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("b, lk", [(100, 151), (8, 3301)])
+def test_masked_places_of_few_queries_of_many_sequences(hold, b, lk):
+    """The last key is attended by the last query only: the first's results are those without it."""
+    q, k, v, do = make(b, 2, lk, 16, 8, 128, BF, seed=24)
+    k2, v2 = k.clone(), v.clone()
+    k2[:, -1], v2[:, -1] = hold, hold
+    out, lse = sdc.sdc_attention(q, k2, v2, True)
+    torch.cuda.synchronize()
+    for i in range(b):
+        for name, (x, tol) in exact(q[i], k[i], v[i], do[i], True, 0, 128 ** -0.5).items():
+            close({"out": out, "lse": lse}[name][i][:1], x[:1], tol[:1], (name, i))
